@@ -79,6 +79,11 @@ typedef enum { SSD_F32 = 0, SSD_BF16 = 1 } ssd_dtype_t;
 #define SSD_FLAG_BAD_HISTORY 128u /* backup: hist_len outside [0, hist_stride]: taken as 0  */
 #define SSD_FLAG_BAD_RATE 256u    /* plan: p_hit outside [0, 1] or e_hit < 0 / not finite:  */
                                   /* clamped into [0, 1], taken as 0                        */
+#define SSD_FLAG_BAD_VALUE 512u   /* 8-bit cache: a value that is not finite (stored as NaN), or a block   */
+                                  /* scale that is negative or not finite (append: taken as 0; attention:  */
+                                  /* the block's keys are hidden)                                          */
+#define SSD_FLAG_NO_BLOCKS 1024u  /* block tables: the free blocks do not suffice; the sequence keeps its  */
+                                  /* blocks as they are                                                    */
 
 /* Human-readable name of a status code (static string). */
 const char *ssd_status_string(ssd_status_t st);
@@ -488,6 +493,130 @@ ssd_status_t ssd_fallback_plan(const float *p_hit, const float *e_hit, int B, do
                                double T_p, int nopt, const double *T_b, const double *e_miss,
                                double *time, double *tokens, double *throughput, double *speedup,
                                int32_t *best, uint32_t *status, ssd_stream_t s);
+
+/*
+ * The 8-bit cache of the branch decode
+ * ------------------------------------
+ * The calls below are the decode step's cache work with keys and values held
+ * in 8 bits: block tables kept on the GPU, rotary positions at the nodes'
+ * depths, the append that quantises, and the attention that reads the codes.
+ * A cache is k_cache, v_cache [num_blocks, Hkv, 16, d] of e4m3 codes (1 sign,
+ * 4 exponent, 3 mantissa bits; largest value 448; 0x7F and 0xFF are NaN) with
+ * k_scale, v_scale [num_blocks, Hkv] fp32: a code c of block n and head h
+ * stands for c * scale[n, h].  Scales are finite and >= 0; the ones that
+ * ssd_kv_append_q8 writes are powers of two.
+ *
+ * ssd_block_table_update: the block tables of B sequences grown or shrunk to
+ * given lengths without a host round trip: room for a tree's nodes before a
+ * round, the accepted tokens alone after it, nothing for a finished request.
+ *   len [B] int32, reserve >= 0: sequence b gets ceil((len[b] + reserve) / 16)
+ *           blocks; len[b] < 0 gives all its blocks back.
+ *   block_table [B, maxb], pages [B] int32 (blocks held; entries 0 .. pages-1
+ *           of a row are valid), updated in place; released entries become -1.
+ *   ring [num_blocks], pool [4] int32: the free block ids ring[(pool[0] + i) %
+ *           num_blocks], 0 <= i < pool[1]; pool[2] is the call's own and 0
+ *           between calls; pool[3] is unused.  Initially e.g. ring[i] = i,
+ *           pool = {0, num_blocks, 0, 0}, pages = 0, block_table = -1.
+ *   slots [B, S] int32 (or NULL, S = 0): slot of logical position len[b] + i,
+ *           block * 16 + position % 16, or -1 where the sequence holds no
+ *           block for it (len[b] < 0 included).
+ * Blocks are taken from the front of the ring in (sequence, position) order
+ * and given back at its end in the same order, so a released block is not
+ * handed out in the same call.  When the free blocks run out, the sequences
+ * whose running total of new blocks exceeds them keep the blocks they have
+ * (NO_BLOCKS).  A length beyond 16 maxb - reserve, a pages entry outside [0,
+ * maxb] (clamped) and a pool outside its range (taken as empty) set
+ * BAD_PREFIX; such a length leaves the sequence as it is.
+ * num_blocks <= 2^27 (slots are 32 bits), B <= 65536.  One launch; calls that share
+ * a pool must not overlap on the GPU.
+ */
+ssd_status_t ssd_block_table_update(const int32_t *len, int reserve, int B, int32_t *block_table,
+                                    int maxb, int32_t *pages, int32_t *ring, int64_t num_blocks,
+                                    int32_t *pool, int32_t *slots, int S, uint32_t *status,
+                                    ssd_stream_t s);
+
+/*
+ * ssd_rope_frequencies (host only): the rotation per position of each of the
+ * rot/2 pairs, theta_i = base^(-2i/rot), as a fraction of a turn in 64-bit
+ * fixed point (turns[i] = round(theta_i / 2 pi * 2^64), host uint64[rot/2]),
+ * so that position * turns[i] mod 2^64 is the angle at any position without
+ * loss.  factor > 1 scales for a context that many times longer: with
+ * original_len = 0 every theta is divided by it; else by parts: pairs that
+ * turn more than `fast` times in original_len positions keep theta, those
+ * that turn fewer than `slow` times are divided by factor, a linear ramp over
+ * the pair index between, and *mscale = 0.1 ln(factor) + 1 (else 1).
+ * rot even, 2 <= rot <= 1024, base > 1, factor >= 1, fast > slow > 0.
+ *
+ * ssd_tree_rope: rotary positions of the queries and keys of the S tokens at
+ * tree nodes node0 .. node0+S-1.  Token i of sequence b stands at position
+ * prefix_len[b] + depth, depth = the number of proper ancestors of node
+ * node0 + i in parent [B, N]; parent = NULL (N = 0): a chain, depth = node0 +
+ * i.  With x the head's first rot elements (the others are copied) and pair i
+ * = (x[i], x[i + rot/2]), or (x[2i], x[2i+1]) if interleaved, at angle phi:
+ *   (a, b) -> mscale * (a cos phi - b sin phi, a sin phi + b cos phi).
+ * q, k: element (b, i, h, e) at base + b*seq_stride + i*tok_stride + h*d + e
+ * (strides in elements), Hq and Hkv heads, fp32 or bf16; q_out, k_out alike
+ * with strides of their own; an output may be its input (same address and
+ * strides), any other overlap is not allowed.  Hkv = 0 (k NULL) or Hq = 0 (q
+ * NULL) leaves that operand out.  turns: DEVICE uint64[rot/2].  The angle is
+ * reduced exactly, the rotation is fp32, rounded once.  A negative prefix counts
+ * as 0 (BAD_PREFIX); a parent outside [-1, m-1] ends the path (BAD_TREE).
+ * rot even, 2 <= rot <= d <= 512; node0 + S <= N <= 128 with a tree.
+ */
+ssd_status_t ssd_rope_frequencies(int rot, double base, double factor, double original_len,
+                                  double fast, double slow, uint64_t *turns, float *mscale);
+ssd_status_t ssd_tree_rope(const void *q, int64_t q_seq_stride, int64_t q_tok_stride, void *q_out,
+                           int64_t qo_seq_stride, int64_t qo_tok_stride, const void *k,
+                           int64_t k_seq_stride, int64_t k_tok_stride, void *k_out,
+                           int64_t ko_seq_stride, int64_t ko_tok_stride, ssd_dtype_t dt,
+                           const uint64_t *turns, int rot, int interleaved, float mscale,
+                           const int32_t *prefix_len, const int32_t *parent, int N, int node0, int B,
+                           int S, int Hq, int Hkv, int d, uint32_t *status, ssd_stream_t s);
+
+/*
+ * ssd_kv_append_q8: ssd_kv_append into the 8-bit cache.  k_new, v_new bf16:
+ * row (b, i, h) at base + b*seq_stride + i*tok_stride + h*d (strides in
+ * elements, multiples of 8; 16-byte aligned bases).  count [B] int32 (or
+ * NULL: S): rows i >= count[b] are not written (a padded batch); a count
+ * outside [0, S] is clamped and sets BAD_PREFIX.  Per block and head
+ *   need = the smallest power of two s >= 2^-100 with max|finite new rows| <= 448 s,
+ *   scale' = max(scale, need) if the block holds rows before the new ones
+ *            (positions below prefix_len[b] + node0), else need;
+ *   new rows: code = e4m3(x / scale'), rounded to nearest even; a value that
+ *            is not finite becomes NaN (0x7F, BAD_VALUE);
+ *   rows before the new ones: code = e4m3(code * scale / scale') when the
+ *            scale grew (exact for powers of two but for underflow);
+ *   rows behind the new ones: left as they were (their values are void).
+ * BAD_PREFIX and BAD_BLOCK as in ssd_kv_append.  d in {64, 128}.  The blocks
+ * that one call writes are distinct (a block belongs to one sequence).
+ */
+ssd_status_t ssd_kv_append_q8(const void *k_new, int64_t k_seq_stride, int64_t k_tok_stride,
+                              const void *v_new, int64_t v_seq_stride, int64_t v_tok_stride,
+                              void *k_cache, void *v_cache, float *k_scale, float *v_scale,
+                              const int32_t *block_table, int maxb, int64_t num_blocks,
+                              const int32_t *prefix_len, const int32_t *count, int node0, int B,
+                              int S, int Hkv, int d, uint32_t *status, ssd_stream_t s);
+
+/*
+ * ssd_branch_attention_q8: ssd_branch_attention over the 8-bit cache:
+ *     out = softmax(scale * q (k_scale k)^T + mask) (v_scale v),
+ * same arguments, limits and flags otherwise.  A row that sees no key (its
+ * blocks are bad) gives 0 and lse = -inf.  A block scale that is negative or
+ * not finite hides its block (BAD_VALUE); v scales below 2^-100 count as 0.
+ * A NaN code of a key reaches the rows that see the key, in v only its
+ * element; what hidden positions hold does not matter.  A query row with a
+ * value that is not finite gives NaN.  Workspace:
+ * ssd_attention_q8_workspace_size() bytes, 256-byte aligned, for splitting
+ * long key ranges; NULL or short: not split, same result, slower.
+ */
+size_t ssd_attention_q8_workspace_size(int B, int Nq, int Hq, int Hkv, int d);
+ssd_status_t ssd_branch_attention_q8(const void *q, const void *k_cache, const void *v_cache,
+                                     const float *k_scale, const float *v_scale,
+                                     const int32_t *block_table, int maxb, int64_t num_blocks,
+                                     const int32_t *prefix_len, const int32_t *parent, int B, int N,
+                                     int Nq, int Hq, int Hkv, int d, float scale, void *out,
+                                     float *lse, uint32_t *status, void *ws, size_t ws_bytes,
+                                     ssd_stream_t s);
 
 #ifdef __cplusplus
 }

@@ -26,6 +26,8 @@ FLAG_BAD_BLOCK = 32
 FLAG_BAD_PREFIX = 64
 FLAG_BAD_HISTORY = 128
 FLAG_BAD_RATE = 256
+FLAG_BAD_VALUE = 512
+FLAG_NO_BLOCKS = 1024
 
 EXPORTS = ("ssd_status_string", "ssd_fanout_split", "ssd_workspace_size", "ssd_set_timing_events", "ssd_set_trace",
            "ssd_saguaro_sample",
@@ -33,7 +35,8 @@ EXPORTS = ("ssd_status_string", "ssd_fanout_split", "ssd_workspace_size", "ssd_s
            "ssd_predict_outcomes", "ssd_cache_lookup", "ssd_round", "ssd_round_analytics",
            "ssd_attention_workspace_size", "ssd_branch_attention", "ssd_ngram_backup",
            "ssd_fallback_plan", "ssd_fill_sample", "ssd_kv_append", "ssd_tree_verify",
-           "ssd_round_pipelined")
+           "ssd_round_pipelined", "ssd_block_table_update", "ssd_rope_frequencies", "ssd_tree_rope",
+           "ssd_kv_append_q8", "ssd_attention_q8_workspace_size", "ssd_branch_attention_q8")
 
 _lib = None
 
@@ -126,6 +129,21 @@ def _declare(lib):
     lib.ssd_fallback_plan.argtypes = [_vp, _vp, _i, _d, _d, _i, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
                                       _vp, _vp]
     lib.ssd_fallback_plan.restype = _i
+    lib.ssd_block_table_update.argtypes = [_vp, _i, _i, _vp, _i, _vp, _vp, _i64, _vp, _vp, _i, _vp, _vp]
+    lib.ssd_block_table_update.restype = _i
+    lib.ssd_rope_frequencies.argtypes = [_i, _d, _d, _d, _d, _d, _vp, _vp]
+    lib.ssd_rope_frequencies.restype = _i
+    lib.ssd_tree_rope.argtypes = ([_vp, _i64, _i64] * 4 + [_i, _vp, _i, _i, _f, _vp, _vp]
+                                  + [_i] * 7 + [_vp, _vp])
+    lib.ssd_tree_rope.restype = _i
+    lib.ssd_kv_append_q8.argtypes = ([_vp, _i64, _i64] * 2 + [_vp] * 5 + [_i, _i64, _vp, _vp]
+                                     + [_i] * 5 + [_vp, _vp])
+    lib.ssd_kv_append_q8.restype = _i
+    lib.ssd_attention_q8_workspace_size.argtypes = [_i] * 5
+    lib.ssd_attention_q8_workspace_size.restype = _sz
+    lib.ssd_branch_attention_q8.argtypes = ([_vp] * 6 + [_i, _i64, _vp, _vp] + [_i] * 6
+                                            + [_f, _vp, _vp, _vp, _vp, _sz, _vp])
+    lib.ssd_branch_attention_q8.restype = _i
 
 
 # ---------------------------------------------------------------------------
@@ -442,3 +460,155 @@ def ssd_tree_verify(target, draft, V, T, parent, tokens, u_acc, u_bonus, accept_
         _ptr(target, strided=True), _ptr(draft, strided=True), dt, ss, rs, B, N1 - 1, int(V), float(T), _ptr(parent, torch.int32),
         _ptr(tokens, torch.int32), _ptr(u_acc, torch.float32), _ptr(u_bonus, torch.float32), _ptr(accept_len, torch.int32), _ptr(path, torch.int32), _ptr(bonus, torch.int32),
         _ptr(out_tokens, torch.int32), _ptr(resid_mass, torch.float32), _ptr(status, torch.int32), _stream(stream)))
+
+
+# ---------------------------------------------------------------------------
+# the 8-bit cache of the branch decode
+# ---------------------------------------------------------------------------
+def _dense(x, dtype, shape, what):
+    """Address of a dense tensor of the given dtype and shape (None passes through)."""
+    if x is None:
+        return None
+    if x.dtype != dtype or tuple(x.shape) != shape or not x.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous {dtype} tensor of shape {shape}, got {x.dtype} {tuple(x.shape)}")
+    return x.data_ptr()
+
+
+def _codes(x, shape, what):
+    if x.dtype not in (torch.float8_e4m3fn, torch.uint8):
+        raise ValueError(f"{what} must hold e4m3 codes (float8_e4m3fn or uint8), got {x.dtype}")
+    return _dense(x, x.dtype, shape, what)
+
+
+def _rows(x, dtype, shape, what):
+    """Address and (sequence, token) strides of [B, S, H, d] rows whose heads are dense."""
+    if x.dtype != dtype or tuple(x.shape) != shape:
+        raise ValueError(f"{what} must be a {dtype} tensor of shape {shape}, got {x.dtype} {tuple(x.shape)}")
+    ss, ts, hs, es = x.stride()
+    if (es != 1 and shape[3] > 1) or (hs != shape[3] and shape[2] > 1):
+        raise ValueError(f"{what}: the heads of a token must be contiguous")
+    return x.data_ptr(), ss if shape[0] > 1 else 0, ts if shape[1] > 1 else 0
+
+
+def _launch(call, fn, device, stream, *args):
+    """Call ``fn(*args, stream)`` with ``device`` (the tensors') current."""
+    if device.type != "cuda":
+        raise ValueError("tensors passed to the library must live on a CUDA device")
+    if stream is not None:
+        s = stream.cuda_stream
+    else:
+        s = torch._C._cuda_getCurrentRawStream(device.index)
+    if device.index == torch._C._cuda_getDevice():
+        code = fn(*args, s)
+    else:
+        with torch.cuda.device(device):
+            code = fn(*args, s)
+    if code != SSD_OK:
+        _check(call, code)
+
+
+def _same_device(device, *tensors):
+    for x in tensors:
+        if x is not None and x.device != device:
+            raise ValueError(f"all tensors of a call must live on one device, got {device} and {x.device}")
+
+
+def ssd_block_table_update(length, reserve, block_table, pages, ring, pool, slots=None, status=None, stream=None):
+    """Grow or shrink the block tables [B, maxb] in place so that sequence b
+    holds ceil((length[b] + reserve) / 16) blocks (none where length[b] < 0),
+    taking from and giving back to the free ring; ``slots`` [B, S] gets the
+    slots of the positions from length[b] on."""
+    B, maxb = block_table.shape
+    n = ring.shape[0]
+    S = 0 if slots is None else slots.shape[1]
+    i32 = torch.int32
+    _same_device(block_table.device, length, pages, ring, pool, slots, status)
+    _launch("ssd_block_table_update", load().ssd_block_table_update, block_table.device, stream,
+            _dense(length, i32, (B,), "length"), int(reserve), B, _dense(block_table, i32, (B, maxb), "block_table"),
+            maxb, _dense(pages, i32, (B,), "pages"), _dense(ring, i32, (n,), "ring"), n,
+            _dense(pool, i32, (4,), "pool"), _dense(slots, i32, (B, S), "slots"), S,
+            _dense(status, i32, (1,), "status"))
+
+
+def ssd_rope_frequencies(rot, base=10000.0, factor=1.0, original_len=0.0, fast=32.0, slow=1.0):
+    """(turns, mscale): the rotary frequencies of rot/2 pairs as 64-bit turn
+    fractions (int64 host tensor of the bits), scaled for a ``factor`` times
+    longer context (by parts with ``original_len`` > 0), and the magnitude."""
+    turns = torch.empty(max(int(rot) // 2, 1), dtype=torch.int64)
+    m = ctypes.c_float()
+    _check("ssd_rope_frequencies", load().ssd_rope_frequencies(
+        int(rot), float(base), float(factor), float(original_len), float(fast), float(slow),
+        turns.data_ptr(), ctypes.byref(m)))
+    return turns, m.value
+
+
+def ssd_tree_rope(q, k, turns, rot, prefix_len, q_out, k_out, parent=None, node0=0, interleaved=False, mscale=1.0,
+                  status=None, stream=None):
+    """Rotary positions of ``q`` [B, S, Hq, d] and ``k`` [B, S, Hkv, d] (bf16 or
+    fp32, heads contiguous; either may be None) at tree nodes node0.. of
+    ``parent`` [B, N], or of a chain; outputs may be the inputs."""
+    x = q if q is not None else k
+    B, S, _, d = x.shape
+    dt = SSD_F32 if x.dtype == torch.float32 else SSD_BF16
+    if dt == SSD_BF16 and x.dtype != torch.bfloat16:
+        raise ValueError(f"q and k must be float32 or bfloat16, got {x.dtype}")
+    Hq = 0 if q is None else q.shape[2]
+    Hkv = 0 if k is None else k.shape[2]
+    none = (None, 0, 0)
+    N = 0 if parent is None else parent.shape[1]
+    _same_device(x.device, q, k, q_out, k_out, turns, prefix_len, parent, status)
+    _launch("ssd_tree_rope", load().ssd_tree_rope, x.device, stream,
+            *(none if q is None else _rows(q, x.dtype, (B, S, Hq, d), "q")),
+            *(none if q is None else _rows(q_out, x.dtype, (B, S, Hq, d), "q_out")),
+            *(none if k is None else _rows(k, x.dtype, (B, S, Hkv, d), "k")),
+            *(none if k is None else _rows(k_out, x.dtype, (B, S, Hkv, d), "k_out")), dt,
+            _dense(turns, torch.int64, (int(rot) // 2,), "turns"), int(rot), int(bool(interleaved)), float(mscale),
+            _dense(prefix_len, torch.int32, (B,), "prefix_len"), _dense(parent, torch.int32, (B, N), "parent"), N,
+            int(node0), B, S, Hq, Hkv, d, _dense(status, torch.int32, (1,), "status"))
+
+
+def ssd_kv_append_q8(k_new, v_new, k_cache, v_cache, k_scale, v_scale, block_table, prefix_len, node0, count=None,
+                     status=None, stream=None):
+    """Quantise the rows ``k_new``/``v_new`` [B, S, Hkv, d] (bf16, heads
+    contiguous) into the 8-bit caches at tree nodes node0.. of every sequence
+    (rows i >= count[b] are left out)."""
+    B, S, Hkv, d = k_new.shape
+    nb = k_cache.shape[0]
+    maxb = block_table.shape[1]
+    i32, f32 = torch.int32, torch.float32
+    _same_device(k_cache.device, k_new, v_new, v_cache, k_scale, v_scale, block_table, prefix_len, count, status)
+    _launch("ssd_kv_append_q8", load().ssd_kv_append_q8, k_cache.device, stream,
+            *_rows(k_new, torch.bfloat16, (B, S, Hkv, d), "k_new"),
+            *_rows(v_new, torch.bfloat16, (B, S, Hkv, d), "v_new"),
+            _codes(k_cache, (nb, Hkv, 16, d), "k_cache"), _codes(v_cache, (nb, Hkv, 16, d), "v_cache"),
+            _dense(k_scale, f32, (nb, Hkv), "k_scale"), _dense(v_scale, f32, (nb, Hkv), "v_scale"),
+            _dense(block_table, i32, (B, maxb), "block_table"), maxb, nb, _dense(prefix_len, i32, (B,), "prefix_len"),
+            _dense(count, i32, (B,), "count"), int(node0), B, S, Hkv, d, _dense(status, i32, (1,), "status"))
+
+
+def ssd_attention_q8_workspace_size(B, Nq, Hq, Hkv, d) -> int:
+    return int(load().ssd_attention_q8_workspace_size(int(B), int(Nq), int(Hq), int(Hkv), int(d)))
+
+
+def ssd_branch_attention_q8(q, k_cache, v_cache, k_scale, v_scale, block_table, prefix_len, parent, out, lse=None,
+                            scale=None, status=None, ws=None, stream=None):
+    """ssd_branch_attention over the 8-bit caches [num_blocks, Hkv, 16, d] with
+    block scales [num_blocks, Hkv]."""
+    B, Nq, Hq, d = q.shape
+    nb, Hkv = k_scale.shape
+    N = parent.shape[1]
+    maxb = block_table.shape[1]
+    i32, f32, bf16 = torch.int32, torch.float32, torch.bfloat16
+    if scale is None:
+        scale = d ** -0.5
+    if ws is not None and (ws.dtype != torch.uint8 or not ws.is_contiguous()):
+        raise ValueError("ws must be a contiguous uint8 tensor")
+    _same_device(q.device, k_cache, v_cache, k_scale, v_scale, block_table, prefix_len, parent, out, lse, status, ws)
+    _launch("ssd_branch_attention_q8", load().ssd_branch_attention_q8, q.device, stream,
+            _dense(q, bf16, (B, Nq, Hq, d), "q"), _codes(k_cache, (nb, Hkv, 16, d), "k_cache"),
+            _codes(v_cache, (nb, Hkv, 16, d), "v_cache"), _dense(k_scale, f32, (nb, Hkv), "k_scale"),
+            _dense(v_scale, f32, (nb, Hkv), "v_scale"), _dense(block_table, i32, (B, maxb), "block_table"), maxb, nb,
+            _dense(prefix_len, i32, (B,), "prefix_len"), _dense(parent, i32, (B, N), "parent"), B, N, Nq, Hq, Hkv, d,
+            float(scale), _dense(out, bf16, (B, Nq, Hq, d), "out"), _dense(lse, f32, (B, Nq, Hq), "lse"),
+            _dense(status, i32, (1,), "status"), None if ws is None else ws.data_ptr(),
+            0 if ws is None else ws.numel())

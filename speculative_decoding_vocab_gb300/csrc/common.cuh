@@ -20,6 +20,8 @@ constexpr uint32_t kFlagBadBlock = 32u;
 constexpr uint32_t kFlagBadPrefix = 64u;
 constexpr uint32_t kFlagBadHistory = 128u;
 constexpr uint32_t kFlagBadRate = 256u;
+constexpr uint32_t kFlagBadValue = 512u;
+constexpr uint32_t kFlagNoBlocks = 1024u;
 
 // Upper bound on polls of an mbarrier before a wait gives up and reports
 // SSD_FLAG_WAIT_TIMEOUT (each poll may suspend the thread for a short,
