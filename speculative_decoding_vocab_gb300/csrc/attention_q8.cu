@@ -1,9 +1,35 @@
 // attention_q8.cu -- tree-masked decode attention over a paged K/V cache held
-// in 8 bits (e4m3 codes, one scale per block of 16 positions and KV head).
+// in 8 bits (e4m3 codes, one scale per block of 16 positions and KV head), on
+// the sm_103a tensor cores.
 //
-//   k_branch_attn_q8   one CTA per (sequence, query node, head): a thread per
-//                      key for the scores, a thread per element for the
-//                      output, an online softmax over tiles of 128 keys.
+// The codes go to the tensor cores as they are (kind::f8f6f4, fp32 sums); a
+// decode step has few query rows and many keys, so the keys take the MMA's
+// 128-wide side and the rows its N:
+//     S^T [128 keys x rows] = K8 Q^T,      O^T [d x rows] += V8^T P^T.
+// What 8 bits would lose of the bf16 queries and of the probabilities is kept
+// in a second term:
+//   q = 2^e (q1 + q2): e4m3 holds 4 significant bits, so q1 = e4m3(q) leaves a
+//     remainder of at most 4 bits, and q2 = e4m3(q - q1) is exact (bf16 has 8;
+//     below 2^-17 of the row's largest element the remainder is cut): two MMAs
+//     into the same S.
+//   p = p1 + p2 / 32 with p1 = e4m3(p), p2 = e4m3(32 (p - p1)): off by at most
+//     2^-8 p, as a bf16 p would be, or 2^-15 where p2 underflows; p1 and p2
+//     lie side by side in N and fill two accumulators, O = O1 + O2 / 32.
+// A key's thread (its TMEM lane) knows its block's scales: x = s * k_scale *
+// scale * 2^e, P = 2^(x - m + 6), and P * v_scale is what is split into p1 and p2.
+// m is the row's largest x + log2(v_scale) when it was last moved: it moves
+// (and O, l are rescaled) when some P * v_scale exceeds 2^8, two binades above
+// where it started, so p has at least 13 binades above 2^-7, where p2 is cut.
+// l sums the fp32 P, unrounded.
+//
+// Work split: the key tiles of all (sequence, KV head, row tile) are one line
+// of units, cut into equal pieces, one per CTA (one CTA per SM), whatever the
+// lengths are; a piece that covers part of an item leaves (O, m, l) in the
+// workspace and k_attn_q8_merge joins them.
+//
+// CTA: G groups of four softmax warps (NR rows each), a producer warp, an MMA
+// warp, two warps that prepare the next segment's rows (q1, q2, tree masks).
+#include <cuda.h>
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
@@ -12,146 +38,1021 @@
 
 #include "../../include/ssd.h"
 #include "common.cuh"
+#include "device_info.h"
 #include "e4m3.cuh"
+#include "tcgen05.cuh"
 
-namespace {
-
-using namespace ssd;
+namespace ssd {
+namespace q8 {
 
 constexpr int kPage = 16;
 constexpr int kMaxNodes = 128;
-constexpr int kKeys = 128;
+constexpr int kKeys = 128;                 // keys per tile (MMA M of S^T, K of O^T)
+constexpr int kPages = kKeys / kPage;      // 8
+constexpr float kBias = 6.f;               // P is at most 2^6 where m was taken ...
+constexpr float kGrow = 8.f;               // ... and m moves before it exceeds 2^8 (e4m3 ends at 448)
+constexpr float kUnset = 1e30f;            // -m + 6 of a row without a visible key so far: any key moves it
+constexpr int kMinChunk = 4;               // tiles of the smallest piece: below, joining costs more than it gives
+constexpr int kSmemBudget = 222 * 1024;
 
-struct AttnArgs {
+SSD_DEV void umma_f8(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t accum) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accum)
+      : "memory");
+}
+// Shared-memory matrix descriptor, 128-byte (D = 128 rows) or 64-byte swizzle;
+// sbo: bytes between groups of 8 rows; lbo: between column blocks of an MN-major
+// operand (0: the second block repeats the first).
+SSD_DEV uint64_t smem_desc(uint32_t saddr, uint32_t lbo, uint32_t sbo, uint32_t swizzle) {
+  return static_cast<uint64_t>((saddr >> 4) & 0x3FFFu) | static_cast<uint64_t>((lbo >> 4) & 0x3FFFu) << 16 |
+         static_cast<uint64_t>((sbo >> 4) & 0x3FFFu) << 32 | static_cast<uint64_t>(1u) << 46 |
+         static_cast<uint64_t>(swizzle) << 61;
+}
+constexpr uint32_t kSw128 = 2, kSw64 = 4;
+// Instruction descriptor: fp32 sums, e4m3 A and B, both K-major (mn = 0) or MN-major (mn = 1), M = 128
+__host__ __device__ constexpr uint32_t idesc_f8(int N, uint32_t mn) {
+  return (1u << 4) | (mn << 15) | (mn << 16) | (static_cast<uint32_t>(N >> 3) << 17) | (8u << 24);
+}
+// byte offset of (row r, byte c) in a block of 128-byte rows, 128-byte swizzled
+SSD_DEV uint32_t sw128(int r, int c) {
+  return (r >> 3) * 1024 + (r & 7) * 128 + ((((c >> 4) ^ (r & 7)) << 4) | (c & 15));
+}
+SSD_DEV uint32_t sw64(int r, int c) {  // 64-byte rows
+  const uint32_t o = r * 64 + c;
+  return o ^ (((o >> 7) & 3) << 4);
+}
+SSD_DEV void tma_load_3d(void *dst, const CUtensorMap *map, int x, int y, int z, uint64_t *bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], "
+      "[%5];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
+      : "memory");
+}
+// 16 columns of this thread's lane, waited for by tmem_wait16
+SSD_DEV void tmem_ld16_async(uint32_t taddr, float *v) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]),
+        "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15])
+      : "r"(taddr));
+}
+SSD_DEV void tmem_wait16(float *v) {  // orders the uses of v after the wait
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]),
+                 "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15])
+               :
+               : "memory");
+}
+SSD_DEV void bar_sync(int id, int n) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory"); }
+SSD_DEV bool bar_or(int id, int n, bool pred) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %1, 0;\n\t"
+      "bar.red.or.pred q, %2, %3, p;\n\tselp.u32 %0, 1, 0, q;\n\t}\n"
+      : "=r"(r)
+      : "r"(static_cast<uint32_t>(pred)), "r"(id), "r"(n)
+      : "memory");
+  return r != 0;
+}
+SSD_DEV uint32_t half2_of(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+SSD_DEV uint16_t e4m3_of_half2(uint32_t h) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(h));
+  return r;
+}
+SSD_DEV uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t r;
+  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+  return r;
+}
+SSD_DEV uint32_t hmul2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+SSD_DEV uint32_t pack16(uint16_t lo, uint16_t hi) {
+  uint32_t r;
+  asm("mov.b32 %0, {%1, %2};" : "=r"(r) : "h"(lo), "h"(hi));
+  return r;
+}
+
+// One value per 16 columns and lane -> the columns' maximum (or sum) over the
+// warp's lanes: five exchanges that halve the columns held (a fixed order).
+// Column (lane >> 1) & 15 ends in both lanes of a pair.
+template <bool SUM>
+SSD_DEV float warp_columns(float *v, int lane) {
+#pragma unroll
+  for (int s = 0; s < 4; ++s) {
+    const int o = 16 >> s, n = 8 >> s;
+    const bool up = (lane & o) != 0;
+#pragma unroll
+    for (int k = 0; k < n; ++k) {
+      const float keep = up ? v[k + n] : v[k], send = up ? v[k] : v[k + n];
+      const float got = __shfl_xor_sync(0xffffffffu, send, o);
+      v[k] = SUM ? __fadd_rn(keep, got) : fmaxf(keep, got);
+    }
+  }
+  const float got = __shfl_xor_sync(0xffffffffu, v[0], 1);
+  return SUM ? __fadd_rn(v[0], got) : fmaxf(v[0], got);
+}
+
+struct Args {
   const uint16_t *q;
-  const uint8_t *kc, *vc;
+  const uint8_t *vc;
   const float *ks, *vs;
   const int32_t *table;
   int maxb;
   int64_t num_blocks;
   const int32_t *prefix_len, *parent;
-  int N, Nq, Hq, Hkv, group;
+  int B, N, Nq, Hq, Hkv, group, nrows, mtiles, per_b;  // per_b: items of a sequence
+  uint32_t group_magic;                                // row / group = row * magic >> 16 (row < 4096)
+  int split;                                           // pieces may cut items
   float scale_log2;
   uint16_t *out;
   float *lse;
+  float *part_o;   // [CTA][2][rows][d]: a piece's first item (begun elsewhere), then its last (ended elsewhere)
+  float2 *part_ml;  // [CTA][2][rows] (m, l)
+  int4 *info;      // [CTA] what its last item still needs: {parts, sequence, item of the sequence, 0}
   uint32_t *status;
 };
 
-SSD_DEV float code_value(uint8_t c) {
-  float lo, hi;
-  half2_to_float(e4m3_to_half2(c), lo, hi);
-  return lo;
+SSD_DEV int keys_of(const Args &a, int b, int &L) {
+  L = max(a.prefix_len[b], 0);
+  const int64_t n = min(static_cast<int64_t>(L) + a.N, static_cast<int64_t>(a.maxb) * kPage);
+  return static_cast<int>(min(n, static_cast<int64_t>(0x7fffffff - kKeys)));
+}
+SSD_DEV int tiles_of(const Args &a, int b) {
+  int L;
+  return (keys_of(a, b, L) + kKeys - 1) / kKeys;
+}
+
+// A CTA's piece of the line of units.
+struct Piece {
+  int b;            // sequence of the first unit
+  int64_t off;      // units of that sequence before it
+  int64_t left;     // units of the piece
+  int64_t chunk;    // units of a full piece
+};
+
+// The segments of a piece: one item (or part of it) after the other.
+struct Segments {
+  int b, item, nt, nkeys, L, t0, t1;
+  int64_t left;
+  SSD_DEV bool first(const Args &a, const Piece &p) {
+    if (p.left <= 0) return false;
+    b = p.b;
+    left = p.left;
+    nkeys = keys_of(a, b, L);
+    nt = (nkeys + kKeys - 1) / kKeys;
+    item = static_cast<int>(p.off / nt);
+    t0 = static_cast<int>(p.off % nt);
+    if (!a.split && t0 > 0) {  // begun in the piece before, which takes it whole
+      left -= nt - t0;
+      return step(a);
+    }
+    return take(a);
+  }
+  SSD_DEV bool take(const Args &a) {
+    t1 = (a.split && left < nt - t0) ? t0 + static_cast<int>(left) : nt;
+    left -= t1 - t0;
+    return true;
+  }
+  SSD_DEV bool step(const Args &a) {
+    if (left <= 0) return false;
+    t0 = 0;
+    if (++item == a.per_b) {
+      item = 0;
+      ++b;
+      if (b >= a.B) return false;
+      nkeys = keys_of(a, b, L);
+      nt = (nkeys + kKeys - 1) / kKeys;
+    }
+    return take(a);
+  }
+};
+
+template <int D, int G, int NR>
+struct Cfg {
+  static constexpr int kRows = G * NR;                     // rows of a tile
+  static constexpr int kSoftWarps = 4 * G;
+  static constexpr int kTmaWarp = kSoftWarps, kMmaWarp = kSoftWarps + 1, kPrepWarp = kSoftWarps + 2;
+  static constexpr int kThreads = (kSoftWarps + 4) * 32;
+  static constexpr int kQTile = NR * 128;                  // q1 (or q2) of a group at D = 128; [q1 | q2] at D = 64
+  static constexpr int kQGroup = D == 128 ? 2 * kQTile : kQTile;
+  static constexpr int kQBuf = G * kQGroup;
+  static constexpr int kPBuf = kKeys * 128;                // a row per key: p1 [NR] then p2 [NR]
+  static constexpr int kNPB = G == 1 ? 2 : 1;              // P buffers of a group
+  static constexpr int kKV = kKeys * D;                    // K or V of a tile
+  static constexpr int kFixed = 2 * kQBuf + G * kNPB * kPBuf;
+  static constexpr int kFit = (kSmemBudget - kFixed) / (2 * kKV);
+  static constexpr int kStages = kFit > 8 ? 8 : kFit;
+  static_assert(kStages >= 2, "two stages at least");
+  static constexpr int kQ = 0, kP = 2 * kQBuf, kRing = kFixed;
+  static constexpr int kSmem = kFixed + kStages * 2 * kKV + 1024;
+  static constexpr uint32_t kCols = G * 4 * NR;            // per group S (2 x NR), then O1, O2
+  static constexpr uint32_t kTmem = kCols <= 64 ? 64 : (kCols <= 128 ? 128 : (kCols <= 256 ? 256 : 512));
+  static_assert(kSmem + (G == 1 ? 9728 : 12800) <= 227 * 1024, "shared memory with the static part");
+  static_assert(kCols <= 512 && 2 * NR <= 128 && NR % 16 == 0, "columns");
+};
+
+template <int D, int G, int NR>
+__global__ void __launch_bounds__(Cfg<D, G, NR>::kThreads, 1)
+    k_branch_attn_q8(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
+                     const __grid_constant__ Args a) {
+  using C = Cfg<D, G, NR>;
+  constexpr int NS = C::kStages, RT = C::kRows, NPB = C::kNPB;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t *const smem =
+      reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  __shared__ __align__(8) uint64_t kfull[NS], kempty[NS], vfull[NS], vempty[NS];
+  __shared__ __align__(8) uint64_t sfull[G][2], sfree[G][2], pfull[G][2], pvdone[G][2], qfull[2], qempty[2];
+  __shared__ uint32_t tmem_base;
+  __shared__ float meta_k[NS][kPages], meta_v[NS][kPages];  // block scales (v: -1 where the block is hidden)
+  __shared__ int meta_full[NS];                             // every key of the tile is a prefix key
+  __shared__ int par[2][kMaxNodes];
+  __shared__ uint32_t anc[2][kMaxNodes][kMaxNodes / 32];    // per query: the nodes that it sees
+  __shared__ float qs[2][RT];                               // row scales 2^e
+  __shared__ __align__(16) float4 rowc[G][NR / 2];          // two rows: 2^e, 2^e, 6 - m, 6 - m
+  __shared__ float s_m[G][NR], s_f[G][NR], red[G][4][NR];
+  __shared__ int s_nan[4];                                  // a tree node's v held NaN, by segment mod 4
+  __shared__ long long scan[32][2];
+  __shared__ Piece s_piece;
+  __shared__ volatile int s_abort;
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const float NEG_INF = -__int_as_float(0x7f800000);
+
+  if (tid == 0) {
+    for (int s = 0; s < NS; ++s) {
+      mbar_init(&kfull[s], 1);
+      mbar_init(&kempty[s], 1);
+      mbar_init(&vfull[s], 1);
+      mbar_init(&vempty[s], 1);
+    }
+    for (int u = 0; u < 2; ++u) {
+      for (int g = 0; g < G; ++g) {
+        mbar_init(&sfull[g][u], 1);
+        mbar_init(&sfree[g][u], 4);
+        mbar_init(&pfull[g][u], 4);
+        mbar_init(&pvdone[g][u], 1);
+      }
+      mbar_init(&qfull[u], 2);
+      mbar_init(&qempty[u], 1 + 4 * G);
+    }
+    fence_mbar_init();
+    s_abort = 0;
+    s_nan[0] = s_nan[1] = s_nan[2] = s_nan[3] = 0;
+    s_piece.left = 0;
+  }
+  if (warp == C::kMmaWarp) {
+    tmem_alloc(&tmem_base, C::kTmem);
+    tmem_relinquish();
+  }
+  // the line of units: every thread sums some sequences' tiles, then the sums are scanned
+  {
+    const int per = (a.B + C::kThreads - 1) / C::kThreads, b0 = tid * per, b1 = min(a.B, b0 + per);
+    long long mine = 0;
+    for (int b = b0; b < b1; ++b) mine += tiles_of(a, b);
+    long long inc = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long x = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += x;
+    }
+    if (lane == 31) scan[warp][0] = inc;
+    __syncthreads();
+    long long before = 0, total = 0;
+    for (int w = 0; w < C::kThreads / 32; ++w) {
+      if (w < warp) before += scan[w][0];
+      total += scan[w][0];
+    }
+    const long long T = total * a.per_b;
+    long long chunk = (T + gridDim.x - 1) / gridDim.x;
+    if (a.split && chunk < kMinChunk) chunk = kMinChunk;
+    const long long lo = chunk * blockIdx.x, hi = min(T, lo + chunk);
+    long long x = (before + inc - mine) * a.per_b;  // units before this thread's first sequence
+    if (lo < hi && lo >= x && lo < x + mine * a.per_b) {
+      int b = b0;
+      for (;; ++b) {
+        const long long n = static_cast<long long>(tiles_of(a, b)) * a.per_b;
+        if (lo < x + n) break;
+        x += n;
+      }
+      s_piece.b = b;
+      s_piece.off = lo - x;
+      s_piece.left = hi - lo;
+      s_piece.chunk = chunk;
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_base;
+  const Piece piece = s_piece;
+
+  // A segment's rows: q1, q2 and the row scales into buffer `buf`, the
+  // queries' tree masks; warp w of the n that share it (barrier `bar`).
+  auto prepare = [&](const Segments &sg, int buf, int w, int n, int bar) {
+    const int hk = sg.item / a.mtiles, mt = sg.item % a.mtiles;
+    const bool tree = sg.t1 * kKeys > sg.L;
+    if (tree)
+      for (int m = w * 32 + lane; m < a.N; m += n * 32) par[buf][m] = a.parent[static_cast<int64_t>(sg.b) * a.N + m];
+    if (w == 0 && lane == 0) {
+      const int L = a.prefix_len[sg.b];
+      if (L < 0 || static_cast<int64_t>(L) + a.N > static_cast<int64_t>(a.maxb) * kPage)
+        atomicOr(a.status, kFlagBadPrefix);
+    }
+    bar_sync(bar, n * 32);
+    if (tree) {
+      for (int i = w * 32 + lane; i < a.Nq; i += n * 32) {
+        uint32_t bits[kMaxNodes / 32] = {0, 0, 0, 0};
+        for (int m = a.N - a.Nq + i; m >= 0;) {
+#pragma unroll
+          for (int x = 0; x < kMaxNodes / 32; ++x)
+            if ((m >> 5) == x) bits[x] |= 1u << (m & 31);
+          const int up = par[buf][m];
+          if (up < -1 || up >= m) {
+            atomicOr(a.status, kFlagBadTree);
+            break;
+          }
+          m = up;
+        }
+#pragma unroll
+        for (int x = 0; x < kMaxNodes / 32; ++x) anc[buf][i][x] = bits[x];
+      }
+    }
+    uint8_t *const qb = smem + C::kQ + buf * C::kQBuf;
+    constexpr int E = D / 32;  // elements per lane
+    constexpr int U = 4;       // rows in flight
+    for (int r0 = w * U; r0 < RT; r0 += n * U) {
+      uint32_t x[U][E / 2];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int r = mt * RT + r0 + u;
+#pragma unroll
+        for (int e = 0; e < E / 2; ++e) x[u][e] = 0;
+        if (r0 + u < RT && r < a.nrows) {
+          const int qi = r / a.group, head = hk * a.group + r % a.group;
+          const uint16_t *src = a.q + ((static_cast<int64_t>(sg.b) * a.Nq + qi) * a.Hq + head) * D + lane * E;
+          if constexpr (E == 4) {
+            const uint2 v = __ldg(reinterpret_cast<const uint2 *>(src));
+            x[u][0] = v.x;
+            x[u][1] = v.y;
+          } else {
+            x[u][0] = __ldg(reinterpret_cast<const uint32_t *>(src));
+          }
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (r0 + u >= RT) break;
+        float f[E];
+        uint32_t m = 0;
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          const uint32_t bits = (e & 1) ? x[u][e / 2] & 0xFFFF0000u : x[u][e / 2] << 16;
+          f[e] = __uint_as_float(bits);
+          const uint32_t mag = bits & 0x7FFFFFFFu;
+          if (mag < 0x7F800000u) m = max(m, mag);
+          else f[e] = __int_as_float(0x7fc00000);  // an infinity too: e4m3 would clamp it
+        }
+#pragma unroll
+        for (int s = 16; s; s >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, s));
+        // 2^e brings the largest element into [2^7, 2^8); e in [-120, 120] (smaller rows: fewer bits)
+        const int e2 = m == 0 ? 0 : min(max(static_cast<int>(m >> 23) - 127 - 7, -120), 120);
+        const float inv = __uint_as_float(static_cast<uint32_t>(127 - e2) << 23);
+        uint32_t c1 = 0, c2 = 0;
+#pragma unroll
+        for (int e = 0; e < E; e += 2) {
+          const float u0 = f[e] * inv, u1 = f[e + 1] * inv;
+          const uint32_t h = e4m3_pair(u0, u1);
+          float b0, b1;
+          half2_to_float(e4m3_to_half2(static_cast<uint16_t>(h)), b0, b1);
+          c1 |= h << (8 * e);
+          c2 |= e4m3_pair(u0 - b0, u1 - b1) << (8 * e);
+        }
+        const int row = r0 + u, g = row / NR, j = row % NR;
+        uint8_t *const qg = qb + g * C::kQGroup;
+        if constexpr (D == 128) {
+          *reinterpret_cast<uint32_t *>(qg + sw128(j, lane * 4)) = c1;
+          *reinterpret_cast<uint32_t *>(qg + C::kQTile + sw128(j, lane * 4)) = c2;
+        } else {
+          *reinterpret_cast<uint16_t *>(qg + sw128(j, lane * 2)) = static_cast<uint16_t>(c1);
+          *reinterpret_cast<uint16_t *>(qg + sw128(j, 64 + lane * 2)) = static_cast<uint16_t>(c2);
+        }
+        if (lane == 0) qs[buf][row] = __uint_as_float(static_cast<uint32_t>(127 + e2) << 23);
+      }
+    }
+    fence_proxy_async();  // the operand tiles -> visible to the tensor cores
+    __syncwarp();
+  };
+
+  Segments sg;
+  if (warp == C::kTmaWarp) {
+    // ---------------- producer: one lane per page of K (0..7) and of V (8..15)
+    const int pg = lane & 7;
+    const bool isv = (lane & 8) != 0;
+    struct Tile {
+      int any, t, L, nkeys, hk, b, blk;
+      float sc;
+    };
+    bool more = sg.first(a, piece);
+    int t = more ? sg.t0 : 0;
+    auto fetch = [&](Tile &x) {  // the next tile's block ids
+      x.any = more;
+      x.blk = -1;
+      x.sc = 0.f;
+      if (!more) return;
+      x.t = t;
+      x.L = sg.L;
+      x.nkeys = sg.nkeys;
+      x.hk = sg.item / a.mtiles;
+      x.b = sg.b;
+      const int lp = t * kPages + pg;
+      if (lp < a.maxb && lp * static_cast<int64_t>(kPage) < sg.nkeys) {
+        x.blk = a.table[static_cast<int64_t>(sg.b) * a.maxb + lp];
+        if (x.blk < 0 || x.blk >= a.num_blocks) {
+          atomicOr(a.status, kFlagBadBlock);
+          x.blk = -1;
+        }
+      }
+      if (++t == sg.t1) {
+        more = sg.step(a);
+        t = 0;
+      }
+    };
+    auto scales = [&](Tile &x) {
+      if (x.blk >= 0) x.sc = __ldg((isv ? a.vs : a.ks) + static_cast<int64_t>(x.blk) * a.Hkv + x.hk);
+    };
+    Tile now, next;
+    fetch(now);
+    scales(now);
+    fetch(next);
+    int issued = 0;
+    for (int i = 0; now.any; ++i) {
+      const int st = i % NS;
+      scales(next);
+      Tile after;
+      fetch(after);
+      bool valid = now.blk >= 0;
+      const bool good = !valid || good_scale(now.sc);
+      if (!good) atomicOr(a.status, kFlagBadValue);
+      const bool other = __shfl_xor_sync(0xffffffffu, good, 8);  // the block's other scale
+      valid = valid && good && other;
+      const uint32_t mask = __ballot_sync(0xffffffffu, valid) & 0xFFu;
+      const uint32_t bytes = __popc(mask) * (kPage * D);
+      uint8_t *const ring = smem + C::kRing + st * 2 * C::kKV;
+      int ok = 1;
+      if (lane == 0) {
+        if (s_abort || (i >= NS && !mbar_wait_sleep(&kempty[st], ((i / NS) - 1) & 1))) ok = 0;
+        else mbar_arrive_expect_tx(&kfull[st], bytes);
+      }
+      ok = __shfl_sync(0xffffffffu, ok, 0);
+      if (!ok) {
+        s_abort = 1;
+        break;
+      }
+      if (lane < 8 && valid) tma_load_3d(ring + pg * (kPage * D), &kmap, 0, now.hk * kPage, now.blk, &kfull[st]);
+      if (lane == 0) ok = i < NS || mbar_wait_sleep(&vempty[st], ((i / NS) - 1) & 1);
+      ok = __shfl_sync(0xffffffffu, ok, 0);
+      issued = i + 1;
+      if (!ok) {
+        // the K copies are in flight; V's barrier is completed so that the drain below ends
+        if (lane == 0) mbar_arrive_expect_tx(&vfull[st], 0);
+        s_abort = 1;
+        break;
+      }
+      if (lane < 8) meta_k[st][pg] = valid ? now.sc : 0.f;
+      else if (lane < 16) meta_v[st][pg] = valid ? now.sc : -1.f;
+      if (lane == 0) meta_full[st] = mask == 0xFFu && (now.t + 1) * static_cast<int64_t>(kKeys) <= now.L;
+      __syncwarp();
+      if (lane == 0) mbar_arrive_expect_tx(&vfull[st], bytes);
+      __syncwarp();
+      if (isv && lane < 16 && valid)
+        tma_load_3d(ring + C::kKV + pg * (kPage * D), &vmap, 0, now.hk * kPage, now.blk, &vfull[st]);
+      now = next;
+      next = after;
+    }
+    if (s_abort && lane == 0) {  // copies in flight land before the shared memory is given back
+      for (int i = max(0, issued - NS); i < issued; ++i) {
+        (void)mbar_wait(&kfull[i % NS], (i / NS) & 1);
+        (void)mbar_wait(&vfull[i % NS], (i / NS) & 1);
+      }
+    }
+  } else if (warp == C::kMmaWarp) {
+    // ---------------- MMA issue (one thread): S(i), then O += P(i - 1) V(i - 1)
+    if (lane == 0) {
+      constexpr uint32_t idesc_s = idesc_f8(NR, 0), idesc_o = idesc_f8(2 * NR, 1);
+      const uint32_t base = smem_u32(smem);
+      bool ok = true;
+      auto issue_pv = [&](int i, bool fresh) {
+        const int st = i % NS;
+        if (!mbar_wait_sleep(&vfull[st], (i / NS) & 1)) {
+          ok = false;
+          return;
+        }
+        const uint32_t v = base + C::kRing + st * 2 * C::kKV + C::kKV;
+        for (int g = 0; g < G; ++g) {
+          if (!mbar_wait_sleep(&pfull[g][i & 1], (i >> 1) & 1)) {
+            ok = false;
+            return;
+          }
+          tc_fence_after();
+          const uint32_t p = base + C::kP + (g * NPB + i % NPB) * C::kPBuf;
+          const uint32_t o = tmem + g * 4 * NR + 2 * NR;
+#pragma unroll
+          for (int kk = 0; kk < kKeys / 32; ++kk) {
+            // 32 keys: four groups of 8 rows
+            const uint64_t vd = D == 128 ? smem_desc(v + kk * 4096, 16, 1024, kSw128)
+                                         : smem_desc(v + kk * 2048, 0, 512, kSw64);
+            umma_f8(o, vd, smem_desc(p + kk * 4096, 16, 1024, kSw128), idesc_o, (!fresh || kk > 0) ? 1u : 0u);
+          }
+          umma_commit(&pvdone[g][i & 1]);
+        }
+        umma_commit(&vempty[st]);
+      };
+      int i = 0, seg = 0;
+      bool fresh_prev = false;
+      for (bool more = sg.first(a, piece); more && ok; more = sg.step(a), ++seg) {
+        const int buf = seg & 1;
+        if (!mbar_wait_sleep(&qfull[buf], (seg >> 1) & 1)) ok = false;
+        for (int t = sg.t0; t < sg.t1 && ok; ++t, ++i) {
+          const int st = i % NS;
+          if (s_abort || !mbar_wait_sleep(&kfull[st], (i / NS) & 1)) {
+            ok = false;
+            break;
+          }
+          const uint32_t k = base + C::kRing + st * 2 * C::kKV;
+          for (int g = 0; g < G; ++g) {
+            if (i >= 2 && !mbar_wait_sleep(&sfree[g][i & 1], ((i - 2) >> 1) & 1)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            const uint32_t q = base + C::kQ + buf * C::kQBuf + g * C::kQGroup;
+            const uint32_t s = tmem + g * 4 * NR + (i & 1) * NR;
+#pragma unroll
+            for (int term = 0; term < 2; ++term)
+#pragma unroll
+              for (int kk = 0; kk < D / 32; ++kk) {
+                const uint64_t kd = D == 128 ? smem_desc(k + kk * 32, 16, 1024, kSw128)
+                                             : smem_desc(k + kk * 32, 16, 512, kSw64);
+                const uint32_t qa = q + (D == 128 ? term * C::kQTile : term * 64) + kk * 32;
+                umma_f8(s, kd, smem_desc(qa, 16, 1024, kSw128), idesc_s, (term > 0 || kk > 0) ? 1u : 0u);
+              }
+            umma_commit(&sfull[g][i & 1]);
+          }
+          if (!ok) break;
+          umma_commit(&kempty[st]);
+          if (t == sg.t1 - 1) umma_commit(&qempty[buf]);
+          if (i >= 1) issue_pv(i - 1, fresh_prev);
+          fresh_prev = t == sg.t0;
+        }
+      }
+      if (ok && i >= 1) issue_pv(i - 1, fresh_prev);
+      if (!ok) s_abort = 1;
+    }
+  } else if (warp >= C::kPrepWarp) {
+    // ---------------- the rows of the segments after the first
+    bool more = sg.first(a, piece);
+    if (more) {
+      prepare(sg, 0, C::kSoftWarps + warp - C::kPrepWarp, C::kSoftWarps + 2, 4);
+      bar_sync(4, (C::kSoftWarps + 2) * 32);
+      if (lane == 0) mbar_arrive1(&qfull[0]);
+      more = sg.step(a);
+    }
+    for (int seg = 1; more; more = sg.step(a), ++seg) {
+      const int buf = seg & 1;
+      const bool ok = seg < 2 || mbar_wait_sleep(&qempty[buf], ((seg >> 1) - 1) & 1);
+      if (bar_or(5, 64, !ok || s_abort)) {
+        s_abort = 1;
+        break;
+      }
+      prepare(sg, buf, warp - C::kPrepWarp, 2, 5);
+      if (lane == 0) mbar_arrive1(&qfull[buf]);
+    }
+  } else {
+    // ---------------- softmax: group g of four warps, one thread per key
+    const int g = warp / 4, wg = warp & 3, tg = tid & 127;
+    const uint32_t lane_off = static_cast<uint32_t>(wg * 32) << 16;
+    const uint32_t tS = tmem + g * 4 * NR + lane_off, tO = tS + 2 * NR;
+    const int bar = 1 + g;
+    int i = 0, seg = 0;
+    bool dead = false;
+    bool more = sg.first(a, piece);
+    if (more) {
+      prepare(sg, 0, warp, C::kSoftWarps + 2, 4);
+      bar_sync(4, (C::kSoftWarps + 2) * 32);
+    }
+    for (; more && !dead; more = sg.step(a), ++seg) {
+      const int buf = seg & 1;
+      const int hk = sg.item / a.mtiles, mt = sg.item % a.mtiles;
+      const int row0 = mt * RT + g * NR;  // the group's first row of (b, hk)
+      bool ok = __all_sync(0xffffffffu, mbar_wait_sleep(&qfull[buf], (seg >> 1) & 1));
+      if (tg < NR) {
+        s_m[g][tg] = NEG_INF;
+        float *const rc = reinterpret_cast<float *>(&rowc[g][tg >> 1]) + (tg & 1);
+        rc[0] = qs[buf][tg + g * NR];
+        rc[2] = 0.f;
+      }
+      if (g == 0 && tg == 0) s_nan[(seg + 2) & 3] = 0;
+      bar_sync(bar, 128);
+      uint64_t l2[NR / 2];
+#pragma unroll
+      for (int j = 0; j < NR / 2; ++j) l2[j] = 0;
+      for (int t = sg.t0; t < sg.t1; ++t, ++i) {
+        const int st = i % NS, u = i & 1;
+        const bool begin = t == sg.t0;
+        ok = __all_sync(0xffffffffu, ok && !s_abort && mbar_wait_sleep(&vfull[st], (i / NS) & 1) &&
+                                         mbar_wait_sleep(&sfull[g][u], (i >> 1) & 1));
+        tc_fence_after();
+        const float vsc = meta_v[st][tg / kPage];
+        const float c = meta_k[st][tg / kPage] * a.scale_log2;
+        const float lsv = log2f(fmaxf(vsc, kMinBlockScale));
+        const float wv = vsc < kMinBlockScale ? 0.f : vsc;
+        const bool full = meta_full[st] != 0;
+        // the rows that see this thread's key
+        uint64_t vis = ~0ull;
+        if (!full) {
+          const int pos = t * kKeys + tg;
+          if (vsc < 0.f || pos >= sg.nkeys) vis = 0;
+          else if (pos >= sg.L) {
+            const int n = pos - sg.L;
+            vis = 0;
+#pragma unroll
+            for (int j = 0; j < NR; ++j) {
+              const int qi = min(static_cast<int>(((row0 + j) * a.group_magic) >> 16), kMaxNodes - 1);
+              vis |= static_cast<uint64_t>((anc[buf][qi][n >> 5] >> (n & 31)) & 1u) << j;
+            }
+          }
+        }
+        const uint64_t c2 = pack2(c, c);
+        float y[NR];
+        // y = x - m + 6 (or x where rowc holds 0); hidden keys -inf
+        auto scores = [&]() {
+#pragma unroll
+          for (int j = 0; j < NR; j += 16) tmem_ld16_async(tS + u * NR + j, y + j);
+#pragma unroll
+          for (int j = 0; j < NR; j += 16) tmem_wait16(y + j);
+#pragma unroll
+          for (int j = 0; j < NR; j += 2) {
+            const float4 rc = rowc[g][j / 2];
+            unpack2(fma2(mul2(pack2(y[j], y[j + 1]), c2), pack2(rc.x, rc.y), pack2(rc.z, rc.w)), y[j], y[j + 1]);
+          }
+          if (!full) {
+#pragma unroll
+            for (int j = 0; j < NR; ++j) y[j] = ((vis >> j) & 1ull) ? y[j] : NEG_INF;
+          }
+        };
+        bool grow = begin;
+        if (!begin) {
+          scores();
+          float t4[4] = {y[0], y[1], y[2], y[3]};
+#pragma unroll
+          for (int j = 4; j < NR; ++j) t4[j & 3] = fmaxf(t4[j & 3], y[j]);
+          const float top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
+          grow = bar_or(bar, 128, top + lsv > kGrow || !ok);
+        }
+        if (grow) {
+          // the rows' largest x + log2 v_scale in this tile
+#pragma unroll
+          for (int j0 = 0; j0 < NR; j0 += 16) {
+            float z[16];
+            tmem_ld16_async(tS + u * NR + j0, z);
+            tmem_wait16(z);
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+              const float4 rc = rowc[g][(j0 + j) / 2];
+              z[j] = ((vis >> (j0 + j)) & 1ull) ? fmaf(z[j] * c, (j & 1) ? rc.y : rc.x, lsv) : NEG_INF;
+            }
+            const float top = warp_columns<false>(z, lane);
+            if (!(lane & 1)) red[g][wg][j0 + (lane >> 1)] = top;
+          }
+          if (!begin) {  // O is rescaled below: every P V before has to be in it
+            ok = __all_sync(0xffffffffu, mbar_wait(&pvdone[g][u ^ 1], ((i - 1) >> 1) & 1) && ok);
+            tc_fence_after();
+          }
+          if (bar_or(bar, 128, !ok)) {
+            dead = true;
+            break;
+          }
+          if (tg < NR) {
+            const float mx = fmaxf(fmaxf(red[g][0][tg], red[g][1][tg]), fmaxf(red[g][2][tg], red[g][3][tg]));
+            const float mo = s_m[g][tg], mn = fmaxf(mo, mx);
+            s_m[g][tg] = mn;
+            s_f[g][tg] = mo == NEG_INF ? (mn == NEG_INF ? 1.f : 0.f) : ex2(mo - mn);
+            reinterpret_cast<float *>(&rowc[g][tg >> 1])[2 + (tg & 1)] = mn == NEG_INF ? kUnset : kBias - mn;
+          }
+          bar_sync(bar, 128);
+          if (!begin) {
+#pragma unroll
+            for (int j = 0; j < NR / 2; ++j) l2[j] = mul2(l2[j], pack2(s_f[g][2 * j], s_f[g][2 * j + 1]));
+#pragma unroll
+            for (int j0 = 0; j0 < 2 * NR; j0 += 16) {
+              float o[16];
+              tmem_ld16(tO + j0, o);
+#pragma unroll
+              for (int j = 0; j < 16; ++j) o[j] *= s_f[g][(j0 + j) % NR];
+              tmem_st16(tO + j0, o);
+            }
+          }
+          scores();
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive1(&sfree[g][u]);
+        // the P buffer is free once P V of tile i - NPB is done
+        if (i >= NPB)
+          ok = __all_sync(0xffffffffu, mbar_wait_sleep(&pvdone[g][(i - NPB) & 1], ((i - NPB) >> 1) & 1) && ok);
+        uint8_t *const prow = smem + C::kP + (g * NPB + i % NPB) * C::kPBuf;
+        const uint64_t w2 = pack2(wv, wv);
+#pragma unroll
+        for (int j0 = 0; j0 < NR; j0 += 16) {
+          uint32_t p1[4], p2[4];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            uint16_t e1[2], e2[2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const int j = j0 + q * 4 + h * 2;
+              const uint64_t p = pack2(ex2(y[j]), ex2(y[j + 1]));
+              l2[j / 2] = add2(l2[j / 2], p);
+              float a0, a1;
+              unpack2(mul2(p, w2), a0, a1);
+              const uint32_t hp = half2_of(a0, a1);
+              e1[h] = e4m3_of_half2(hp);
+              // 32 (p - p1) in halves: exact (p is at most 2^8, the difference has at most 11 bits)
+              e2[h] = e4m3_of_half2(hfma2(e4m3_to_half2(e1[h]), 0xD000D000u, hmul2(hp, 0x50005000u)));
+            }
+            p1[q] = pack16(e1[0], e1[1]);
+            p2[q] = pack16(e2[0], e2[1]);
+          }
+          *reinterpret_cast<uint4 *>(prow + sw128(tg, j0)) = make_uint4(p1[0], p1[1], p1[2], p1[3]);
+          *reinterpret_cast<uint4 *>(prow + sw128(tg, NR + j0)) = make_uint4(p2[0], p2[1], p2[2], p2[3]);
+        }
+        if (!full && g == 0) {
+          // hidden keys take no part whatever their v holds (0 * NaN): their rows become 0; a tree node's NaN
+          // becomes 0 too, and reaches the rows that see it at the end
+          const int pos = t * kKeys + tg;
+          uint8_t *const vt = smem + C::kRing + st * 2 * C::kKV + C::kKV;
+          const bool hidden = vsc < 0.f || pos >= sg.nkeys;
+          if (hidden || pos >= sg.L) {
+#pragma unroll
+            for (int e = 0; e < D; e += 16) {
+              uint4 *const at = reinterpret_cast<uint4 *>(vt + (D == 128 ? sw128(tg, e) : sw64(tg, e)));
+              uint4 x = hidden ? make_uint4(0, 0, 0, 0) : *at;
+              if (!hidden) {
+                uint32_t *const wd = reinterpret_cast<uint32_t *>(&x);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                  const uint32_t nan = ((wd[q] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;  // bytes 0x7F, 0xFF
+                  if (nan) {
+                    wd[q] &= ~((nan >> 7) * 0xFFu);
+                    s_nan[seg & 3] = 1;
+                  }
+                }
+              }
+              *at = x;
+            }
+          }
+        }
+        fence_proxy_async();  // P and V (generic writes) -> visible to the tensor cores
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive1(&pfull[g][u]);
+      }
+      if (dead) break;
+      // ---------------- the segment's rows: l over the keys' threads, O from TMEM
+#pragma unroll
+      for (int j0 = 0; j0 < NR; j0 += 16) {
+        float z[16];
+#pragma unroll
+        for (int j = 0; j < 16; j += 2) unpack2(l2[(j0 + j) / 2], z[j], z[j + 1]);
+        const float sum = warp_columns<true>(z, lane);
+        if (!(lane & 1)) red[g][wg][j0 + (lane >> 1)] = sum;
+      }
+      ok = __all_sync(0xffffffffu, mbar_wait(&pvdone[g][(i - 1) & 1], ((i - 1) >> 1) & 1) && ok);
+      tc_fence_after();
+      if (bar_or(bar, 128, !ok)) {
+        dead = true;
+        break;
+      }
+      const bool whole = sg.t0 == 0 && sg.t1 == sg.nt;
+      const int slot = blockIdx.x * 2 + (sg.t0 > 0 ? 0 : 1);
+      if (tg < NR && row0 + tg < a.nrows) {
+        const float l = __fadd_rn(__fadd_rn(red[g][0][tg], red[g][1][tg]), __fadd_rn(red[g][2][tg], red[g][3][tg]));
+        const float m = s_m[g][tg];
+        if (whole) {
+          s_f[g][tg] = l == 0.f ? 0.f : 1.f / l;
+          const int r = row0 + tg, qi = r / a.group, head = hk * a.group + r % a.group;
+          if (a.lse)
+            a.lse[(static_cast<int64_t>(sg.b) * a.Nq + qi) * a.Hq + head] =
+                l == 0.f ? NEG_INF : (m - kBias + log2f(l)) * 0.69314718055994531f;
+        } else {
+          s_f[g][tg] = 1.f;
+          a.part_ml[slot * RT + g * NR + tg] = make_float2(m, l);
+        }
+      }
+      bar_sync(bar, 128);
+      const bool nan = s_nan[seg & 3] != 0;
+      if (D == 128 || wg < 2) {
+#pragma unroll
+        for (int j0 = 0; j0 < NR; j0 += 16) {
+          float o1[16], o2[16];
+          tmem_ld16_async(tO + j0, o1);
+          tmem_ld16_async(tO + NR + j0, o2);
+          tmem_wait16(o1);
+          tmem_wait16(o2);
+#pragma unroll
+          for (int j = 0; j < 16; ++j) o1[j] = fmaf(o2[j], 0.03125f, o1[j]) * s_f[g][j0 + j];
+          if (nan) {
+            // tree nodes of this segment whose v holds NaN at this thread's element
+            for (int n = max(0, sg.t0 * kKeys - sg.L); n < a.N && sg.L + n < min(sg.nkeys, sg.t1 * kKeys); ++n) {
+              const int pos = sg.L + n, blk = a.table[static_cast<int64_t>(sg.b) * a.maxb + pos / kPage];
+              if (blk < 0 || blk >= a.num_blocks) continue;
+              const int64_t unit = static_cast<int64_t>(blk) * a.Hkv + hk;
+              if (!good_scale(a.ks[unit]) || !good_scale(a.vs[unit])) continue;
+              if ((a.vc[(unit * kPage + pos % kPage) * D + tg] & 0x7F) != 0x7F) continue;
+#pragma unroll
+              for (int j = 0; j < 16; ++j) {
+                const int qi = min((row0 + j0 + j) / a.group, kMaxNodes - 1);
+                if ((anc[buf][qi][n >> 5] >> (n & 31)) & 1u) o1[j] = __int_as_float(0x7fc00000);
+              }
+            }
+          }
+          if (whole) {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+              const int r = row0 + j0 + j;
+              if (r >= a.nrows) break;
+              const int qi = static_cast<int>((r * a.group_magic) >> 16), head = hk * a.group + (r - qi * a.group);
+              uint32_t b2;
+              asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(b2) : "f"(0.f), "f"(o1[j]));
+              a.out[((static_cast<int64_t>(sg.b) * a.Nq + qi) * a.Hq + head) * D + tg] =
+                  static_cast<uint16_t>(b2 & 0xFFFFu);
+            }
+          } else {
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+              a.part_o[(static_cast<int64_t>(slot) * RT + g * NR + j0 + j) * D + tg] = o1[j];
+          }
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive1(&qempty[buf]);
+    }
+    if (dead) s_abort = 1;
+  }
+  if (tid == 0 && a.split) {  // what the piece's last item still needs
+    int4 need = make_int4(0, 0, 0, 0);
+    Segments x;
+    for (bool more = x.first(a, piece); more; more = x.step(a))
+      if (x.t0 == 0 && x.t1 < x.nt)
+        need = make_int4(1 + static_cast<int>((x.nt - x.t1 + piece.chunk - 1) / piece.chunk), x.b, x.item, 0);
+    a.info[blockIdx.x] = need;
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (s_abort && tid == 0) atomicOr(a.status, kFlagWaitTimeout);
+  if (warp == C::kMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc(tmem, C::kTmem);
+  }
+}
+
+// Joins the parts of the items that were cut: block (x, y) the item that CTA x
+// began and did not end, eight of its rows, a warp per row.
+template <int D, int RT>
+__global__ void __launch_bounds__(256) k_attn_q8_merge(const __grid_constant__ Args a) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the pieces are done
+  const int4 need = a.info[blockIdx.x];
+  const int lane = threadIdx.x & 31, j = blockIdx.y * 8 + (threadIdx.x >> 5);
+  const int hk = need.z / a.mtiles, mt = need.z % a.mtiles, row = mt * RT + j;
+  if (need.x == 0 || j >= RT || row >= a.nrows) return;
+  const float NEG_INF = -__int_as_float(0x7f800000);
+  // part 0 is the second slot of CTA x, the others the first slots of the CTAs behind it
+  auto slot = [&](int p) { return static_cast<int64_t>(blockIdx.x + p) * 2 + (p == 0 ? 1 : 0); };
+  float M = NEG_INF;
+  for (int p = lane; p < need.x; p += 32) M = fmaxf(M, a.part_ml[slot(p) * RT + j].x);
+  M = warp_max(M);
+  constexpr int E = D / 32;
+  float acc[E], l = 0.f;
+#pragma unroll
+  for (int e = 0; e < E; ++e) acc[e] = 0.f;
+#pragma unroll 4
+  for (int p = 0; p < need.x; ++p) {
+    const float2 ml = a.part_ml[slot(p) * RT + j];
+    if (ml.y == 0.f) continue;  // no key there
+    const float f = ex2(ml.x - M);
+    l = fmaf(ml.y, f, l);
+    const float *src = a.part_o + (slot(p) * RT + j) * D + lane * E;
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] = fmaf(src[e], f, acc[e]);
+  }
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  const int qi = row / a.group, head = hk * a.group + row % a.group;
+  const int64_t orow = (static_cast<int64_t>(need.y) * a.Nq + qi) * a.Hq + head;
+  uint32_t *dst = reinterpret_cast<uint32_t *>(a.out + orow * D) + lane * (E / 2);
+#pragma unroll
+  for (int e = 0; e < E; e += 2) {
+    uint32_t b2;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(b2) : "f"(acc[e + 1] * inv), "f"(acc[e] * inv));
+    dst[e / 2] = b2;
+  }
+  if (a.lse && lane == 0) a.lse[orow] = l == 0.f ? NEG_INF : (M - kBias + log2f(l)) * 0.69314718055994531f;
+}
+
+}  // namespace q8
+}  // namespace ssd
+
+using namespace ssd;
+
+namespace {
+
+using q8::Args;
+
+// [num_blocks][Hkv * 16 rows][d codes], boxes of one block's rows of a head
+bool make_code_map(CUtensorMap *m, const void *base, int64_t num_blocks, int Hkv, int d) {
+  EncodeTiledFn enc = encode_fn();
+  if (!enc) return false;
+  cuuint64_t dims[3] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(Hkv) * q8::kPage,
+                        static_cast<cuuint64_t>(num_blocks)};
+  cuuint64_t strides[2] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(d) * Hkv * q8::kPage};
+  cuuint32_t box[3] = {static_cast<cuuint32_t>(d), q8::kPage, 1};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void *>(base), dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, d == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Rows of a tile: up to 64 in one group of softmax warps, up to 128 in two; the
+// group's size is the next multiple of 16 (the MMA's step in N).
+struct Shape {
+  int nrows, mtiles, G, NR;
+};
+Shape shape_of(int Nq, int Hq, int Hkv) {
+  Shape s;
+  s.nrows = (Hq / Hkv) * Nq;
+  s.mtiles = (s.nrows + 127) / 128;
+  const int tile = (s.nrows + s.mtiles - 1) / s.mtiles;
+  s.G = tile > 64 ? 2 : 1;
+  s.NR = s.G == 1 ? (tile + 15) / 16 * 16 : (tile > 96 ? 64 : 48);
+  return s;
+}
+size_t align256(size_t x) { return (x + 255) / 256 * 256; }
+struct Workspace {
+  size_t o, ml, info, total;
+};
+Workspace workspace_of(const Shape &s, int d, int ctas) {
+  Workspace w;
+  const size_t rows = static_cast<size_t>(ctas) * 2 * s.G * s.NR;
+  w.o = 0;
+  w.ml = align256(rows * d * sizeof(float));
+  w.info = w.ml + align256(rows * sizeof(float2));
+  w.total = w.info + align256(static_cast<size_t>(ctas) * sizeof(int4));
+  return w;
+}
+
+template <int D, int G, int NR>
+cudaError_t launch(const CUtensorMap &kmap, const CUtensorMap &vmap, const Args &a, unsigned grid, cudaStream_t cs) {
+  using C = q8::Cfg<D, G, NR>;
+  cudaError_t e = cudaFuncSetAttribute(q8::k_branch_attn_q8<D, G, NR>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       C::kSmem);
+  if (e != cudaSuccess) return e;
+  q8::k_branch_attn_q8<D, G, NR><<<grid, C::kThreads, C::kSmem, cs>>>(kmap, vmap, a);
+  e = cudaGetLastError();
+  if (e != cudaSuccess || !a.split) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid, (min(C::kRows, a.nrows) + 7) / 8);
+  cfg.blockDim = dim3(256);
+  cfg.stream = cs;
+  cudaLaunchAttribute at;
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, q8::k_attn_q8_merge<D, C::kRows>, a);
 }
 
 template <int D>
-__global__ void __launch_bounds__(kKeys) k_branch_attn_q8(AttnArgs a) {
-  __shared__ float sq[D], sp[kKeys], sw[kKeys], red[kKeys / 32 + 1];
-  __shared__ int sblk[kKeys / kPage];
-  __shared__ uint32_t anc[kMaxNodes / 32];
-  const int tid = threadIdx.x;
-  const float NEG_INF = -__int_as_float(0x7f800000);
-  const int64_t row = blockIdx.x;  // (b, qi, h)
-  const int h = static_cast<int>(row % a.Hq);
-  const int64_t bq = row / a.Hq;
-  const int qi = static_cast<int>(bq % a.Nq), b = static_cast<int>(bq / a.Nq);
-  const int hk = h / a.group;
-  const int L_in = a.prefix_len[b], L = max(L_in, 0);
-  const int64_t nkeys64 = static_cast<int64_t>(L) + a.N;
-  const int64_t cap = static_cast<int64_t>(a.maxb) * kPage;
-  if (tid == 0) {
-    if (L_in < 0 || nkeys64 > cap) atomicOr(a.status, kFlagBadPrefix);
-    for (int w = 0; w < kMaxNodes / 32; ++w) anc[w] = 0;
-    for (int m = a.N - a.Nq + qi; m >= 0;) {
-      anc[m >> 5] |= 1u << (m & 31);
-      const int up = a.parent[static_cast<int64_t>(b) * a.N + m];
-      if (up < -1 || up >= m) {
-        atomicOr(a.status, kFlagBadTree);
-        break;
-      }
-      m = up;
-    }
+cudaError_t launch_shape(const Shape &s, const CUtensorMap &kmap, const CUtensorMap &vmap, const Args &a,
+                         unsigned grid, cudaStream_t cs) {
+  if (s.G == 2) return s.NR == 64 ? launch<D, 2, 64>(kmap, vmap, a, grid, cs) : launch<D, 2, 48>(kmap, vmap, a, grid, cs);
+  switch (s.NR) {
+    case 16: return launch<D, 1, 16>(kmap, vmap, a, grid, cs);
+    case 32: return launch<D, 1, 32>(kmap, vmap, a, grid, cs);
+    case 48: return launch<D, 1, 48>(kmap, vmap, a, grid, cs);
+    default: return launch<D, 1, 64>(kmap, vmap, a, grid, cs);
   }
-  bool bad_q = false;
-  for (int e = tid; e < D; e += kKeys) {
-    sq[e] = __uint_as_float(static_cast<uint32_t>(a.q[row * D + e]) << 16);
-    bad_q |= !(fabsf(sq[e]) <= 3.402823466e38f);
-  }
-  bad_q = __syncthreads_or(bad_q) != 0;
-  const int64_t nkeys = nkeys64 < cap ? nkeys64 : cap;
-  float m = NEG_INF, l = 0.f, o = 0.f;
-  for (int64_t t = 0; t < nkeys; t += kKeys) {
-    __syncthreads();
-    if (tid < kKeys / kPage) {
-      const int64_t p = t / kPage + tid;
-      int blk = -1;
-      if (p < a.maxb && p * kPage < nkeys) {
-        blk = a.table[static_cast<int64_t>(b) * a.maxb + p];
-        if (blk < 0 || blk >= a.num_blocks) {
-          atomicOr(a.status, kFlagBadBlock);
-          blk = -1;
-        } else if (!good_scale(a.ks[static_cast<int64_t>(blk) * a.Hkv + hk]) ||
-                   !good_scale(a.vs[static_cast<int64_t>(blk) * a.Hkv + hk])) {
-          atomicOr(a.status, kFlagBadValue);
-          blk = -1;
-        }
-      }
-      sblk[tid] = blk;
-    }
-    __syncthreads();
-    const int64_t key = t + tid;
-    const int blk = sblk[tid / kPage];
-    bool vis = blk >= 0 && key < nkeys;
-    if (vis && key >= L) {
-      const int n = static_cast<int>(key - L);
-      vis = (anc[n >> 5] >> (n & 31)) & 1u;
-    }
-    float x = NEG_INF;
-    sw[tid] = 0.f;
-    if (vis) {
-      const int64_t unit = static_cast<int64_t>(blk) * a.Hkv + hk;
-      const uint8_t *k = a.kc + (unit * kPage + key % kPage) * D;
-      float s = 0.f;
-      for (int e = 0; e < D; e += 4) {
-        float f[4];
-        e4m3_unpack4(*reinterpret_cast<const uint32_t *>(k + e), f);
-        for (int i = 0; i < 4; ++i) s = fmaf(sq[e + i], f[i], s);
-      }
-      x = s * (a.ks[unit] * a.scale_log2);
-      const float vsc = a.vs[unit];
-      sw[tid] = vsc < kMinBlockScale ? 0.f : vsc;
-    }
-    const float wmax = warp_max(x);  // fmaxf leaves NaN out
-    if ((tid & 31) == 0) red[tid >> 5] = wmax;
-    __syncthreads();
-    float top = red[0];
-    for (int w = 1; w < kKeys / 32; ++w) top = fmaxf(top, red[w]);
-    const float m_new = fmaxf(m, top);
-    const float f = m == NEG_INF ? 0.f : ex2(m - m_new);
-    const float p = vis ? ex2(x - (m_new == NEG_INF ? 0.f : m_new)) : 0.f;
-    sp[tid] = p;
-    __syncthreads();
-    const float wsum = warp_sum(p);
-    if ((tid & 31) == 0) red[tid >> 5] = wsum;
-    __syncthreads();
-    l = l * f + (red[0] + red[1] + red[2] + red[3]);
-    m = m_new;
-    if (tid < D) {
-      o *= f;
-      for (int j = 0; j < kKeys; ++j) {
-        if (sp[j] == 0.f) continue;  // hidden
-        const int64_t unit = static_cast<int64_t>(sblk[j / kPage]) * a.Hkv + hk;
-        o = fmaf(sp[j] * sw[j], code_value(a.vc[(unit * kPage + (t + j) % kPage) * D + tid]), o);
-      }
-    }
-  }
-  if (tid < D) {
-    const float y = bad_q ? __int_as_float(0x7fc00000) : (l > 0.f || l != l ? o / l : 0.f);
-    uint32_t r;
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(0.f), "f"(y));
-    a.out[row * D + tid] = static_cast<uint16_t>(r & 0xFFFFu);
-  }
-  if (tid == 0 && a.lse)
-    a.lse[row] = bad_q || l != l ? __int_as_float(0x7fc00000) : (l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : NEG_INF);
 }
 
 }  // namespace
@@ -159,8 +1060,10 @@ __global__ void __launch_bounds__(kKeys) k_branch_attn_q8(AttnArgs a) {
 extern "C" {
 
 size_t ssd_attention_q8_workspace_size(int B, int Nq, int Hq, int Hkv, int d) {
-  if (B <= 0 || Nq <= 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv || (d != 64 && d != 128)) return 0;
-  return 0;
+  if (B <= 0 || Nq <= 0 || Nq > q8::kMaxNodes || Hq <= 0 || Hkv <= 0 || Hq % Hkv || Hq / Hkv > 16 ||
+      (d != 64 && d != 128))
+    return 0;
+  return workspace_of(shape_of(Nq, Hq, Hkv), d, attn_num_sms()).total;
 }
 
 ssd_status_t ssd_branch_attention_q8(const void *q, const void *k_cache, const void *v_cache, const float *k_scale,
@@ -171,7 +1074,7 @@ ssd_status_t ssd_branch_attention_q8(const void *q, const void *k_cache, const v
   if (B < 0 || Hq <= 0 || Hkv <= 0 || !(scale > 0.f) || !std::isfinite(scale)) return SSD_ERR_INVALID_ARG;
   if (Hq % Hkv != 0) return SSD_ERR_INVALID_ARG;
   if (d != 64 && d != 128) return SSD_ERR_UNSUPPORTED;
-  if (Hq / Hkv > 16 || N < 1 || N > kMaxNodes || Nq < 1 || Nq > N) return SSD_ERR_UNSUPPORTED;
+  if (Hq / Hkv > 16 || N < 1 || N > q8::kMaxNodes || Nq < 1 || Nq > N) return SSD_ERR_UNSUPPORTED;
   if (B == 0) return SSD_OK;
   if (!q || !k_cache || !v_cache || !k_scale || !v_scale || !block_table || !prefix_len || !parent || !out ||
       !status || maxb < 1 || num_blocks < 1)
@@ -179,11 +1082,10 @@ ssd_status_t ssd_branch_attention_q8(const void *q, const void *k_cache, const v
   if ((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(k_cache) | reinterpret_cast<uintptr_t>(v_cache) |
        reinterpret_cast<uintptr_t>(out)) & 15u)
     return SSD_ERR_UNSUPPORTED;
-  const int64_t rows = static_cast<int64_t>(B) * Nq * Hq;
-  if (rows > 0x7fffffffLL) return SSD_ERR_UNSUPPORTED;
-  AttnArgs a{};
+  if (num_blocks > 0x7fffffffLL || static_cast<int64_t>(B) * Hkv > 0x7fffffffLL / 32) return SSD_ERR_UNSUPPORTED;
+  const Shape sh = shape_of(Nq, Hq, Hkv);
+  Args a{};
   a.q = static_cast<const uint16_t *>(q);
-  a.kc = static_cast<const uint8_t *>(k_cache);
   a.vc = static_cast<const uint8_t *>(v_cache);
   a.ks = k_scale;
   a.vs = v_scale;
@@ -192,23 +1094,41 @@ ssd_status_t ssd_branch_attention_q8(const void *q, const void *k_cache, const v
   a.num_blocks = num_blocks;
   a.prefix_len = prefix_len;
   a.parent = parent;
+  a.B = B;
   a.N = N;
   a.Nq = Nq;
   a.Hq = Hq;
   a.Hkv = Hkv;
   a.group = Hq / Hkv;
+  a.nrows = sh.nrows;
+  a.mtiles = sh.mtiles;
+  a.per_b = Hkv * sh.mtiles;
+  a.group_magic = (65536u + a.group - 1) / a.group;
   a.scale_log2 = scale * 1.4426950408889634f;
   a.out = static_cast<uint16_t *>(out);
   a.lse = lse;
   a.status = status;
-  (void)ws;
-  (void)ws_bytes;
+  // one CTA per SM, none without a tile of its own
+  const int sms = attn_num_sms();
+  const int64_t max_tiles = (static_cast<int64_t>(maxb) * q8::kPage + q8::kKeys - 1) / q8::kKeys;
+  const int64_t units = max_tiles * B * a.per_b;
+  const unsigned grid = static_cast<unsigned>(units < sms ? units : sms);
+  // items of up to kMinChunk tiles are not worth cutting; without room for the parts none is
+  const Workspace w = workspace_of(sh, d, sms);
+  a.split = max_tiles > q8::kMinChunk && ws && ws_bytes >= w.total && !(reinterpret_cast<uintptr_t>(ws) & 255u);
+  if (a.split) {
+    char *const p = static_cast<char *>(ws);
+    a.part_o = reinterpret_cast<float *>(p + w.o);
+    a.part_ml = reinterpret_cast<float2 *>(p + w.ml);
+    a.info = reinterpret_cast<int4 *>(p + w.info);
+  }
+  CUtensorMap kmap, vmap;
+  if (!make_code_map(&kmap, k_cache, num_blocks, Hkv, d) || !make_code_map(&vmap, v_cache, num_blocks, Hkv, d))
+    return SSD_ERR_CUDA;
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(s);
-  if (d == 64)
-    k_branch_attn_q8<64><<<static_cast<unsigned>(rows), kKeys, 0, cs>>>(a);
-  else
-    k_branch_attn_q8<128><<<static_cast<unsigned>(rows), kKeys, 0, cs>>>(a);
-  return cudaGetLastError() == cudaSuccess ? SSD_OK : SSD_ERR_CUDA;
+  const cudaError_t e = d == 64 ? launch_shape<64>(sh, kmap, vmap, a, grid, cs)
+                                : launch_shape<128>(sh, kmap, vmap, a, grid, cs);
+  return e == cudaSuccess ? SSD_OK : SSD_ERR_CUDA;
 }
 
 }  // extern "C"

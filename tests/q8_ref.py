@@ -189,15 +189,16 @@ def paths(parent, Nq):
 
 def attention(q, kc, vc, ks, vs, table, prefix, parent, scale, device="cpu"):
     """q [B, Nq, Hq, d] (any float), codes uint8, scales fp32.  Returns fp64
-    (out, lse, weight, xabs, share) and the flags: weight = softmax-weighted
-    |v| per element, xabs = the largest sum of |scale q k| of a row, share =
+    (out, lse, weight, (xabs, xcut), share) and the flags: weight =
+    softmax-weighted |v| per element, xabs = the largest sum of |scale q k| of a
+    row, xcut = scale max|q| times the largest sum of |k| of a key, share =
     max p v_scale * sum of |code| over the visible keys / sum of p, p = exp(x -
     max): what errors in p v_scale, relative to the row's largest, may move."""
     B, Nq, Hq, d = q.shape
     nb, Hkv = ks.shape
     maxb, N, G = table.shape[1], parent.shape[1], Hq // Hkv
     out = np.zeros((B, Nq, Hq, d))
-    lse, xabs = np.full((B, Nq, Hq), -np.inf), np.zeros((B, Nq, Hq))
+    lse, xabs, xcut = np.full((B, Nq, Hq), -np.inf), np.zeros((B, Nq, Hq)), np.zeros((B, Nq, Hq))
     weight, share = np.zeros((B, Nq, Hq, d)), np.zeros((B, Nq, Hq, d))
     flags = 0
     val = torch.tensor(VALUES, device=device)
@@ -252,4 +253,6 @@ def attention(q, kc, vc, ks, vs, table, prefix, parent, scale, device="cpu"):
             big = (p.nan_to_num(0) * sc).amax(-1, keepdim=True)
             share[b][:, hs] = (big * torch.einsum("ngt,td->ngd", sees, codes) / den).cpu().numpy()
             xabs[b][:, hs] = torch.where(mask[:, None], xa, torch.zeros_like(xa)).amax(-1).cpu().numpy()
-    return out, lse, weight, xabs, share, flags
+            ksum = torch.where(mask, kz.abs().nan_to_num(0).sum(-1), torch.zeros_like(kz[:, 0])).amax(-1)
+            xcut[b][:, hs] = (scale * qq.abs().amax(-1) * ksum[:, None]).cpu().numpy()
+    return out, lse, weight, (xabs, xcut), share, flags

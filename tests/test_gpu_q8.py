@@ -362,16 +362,18 @@ def gpu_attention(a, scale, use_ws=True, want_lse=True, stream=None):
 
 
 def check_attention(a, use_ws=True, scale=None, expect=0):
-    """Roundings counted: a probability is held as two e4m3 terms, half a step of the first taken up by the
-    second to half a step: 2^-4 * 2^-4 = 2^-8, and 2^-21 of the row's largest p v_scale where it underflows; a score is a fp32
-    sum (2^-20 of its terms' magnitudes: products and sums truncated below 2^-24 of the largest, d <= 128 of
-    them in 4 groups), which moves p by as much; the output rounds by 2^-8."""
+    """Roundings counted.  A probability is held as two e4m3 terms, half a step of the first taken up by the
+    second to half a step: 2^-4 * 2^-4 = 2^-8, and 2^-21 of the row's largest p v_scale where it underflows.  A
+    score is a fp32 sum (2^-20 of its terms' magnitudes: products and sums truncated below 2^-24 of the largest,
+    d <= 128 of them in 4 groups) of a query held as 2^e (q1 + q2) with max|q| in 2^e [2^7, 2^8): q1 leaves at
+    most 4 bits, which q2 holds but for those below its half step 2^-10, so q is off by at most 2^-10 2^e <=
+    2^-17 max|q| in each element; both move p by as much.  The output rounds by 2^-8."""
     scale = a["q"].shape[3] ** -0.5 if scale is None else scale
     out, lse, flags = gpu_attention(a, scale, use_ws)
-    o, l, weight, xabs, share, rf = ref.attention(a["q"], a["kc"], a["vc"], a["ks"], a["vs"], a["table"], a["prefix"],
+    o, l, weight, (xabs, xcut), share, rf = ref.attention(a["q"], a["kc"], a["vc"], a["ks"], a["vs"], a["table"], a["prefix"],
                                                   a["parent"], scale, device="cuda")
     assert flags == rf == expect
-    dx = 2.0 ** -20 * xabs + 2.0 ** -20
+    dx = 2.0 ** -20 * xabs + 2.0 ** -17 * xcut + 2.0 ** -20
     tol = 2.0 ** -8 * np.abs(o) + (2.0 ** -8 + 2 * dx[..., None]) * weight + 2.0 ** -21 * share + 1e-30
     nan = np.isnan(o)
     np.testing.assert_array_equal(np.isnan(out), nan)
