@@ -27,8 +27,11 @@
 // lengths are; a piece that covers part of an item leaves (O, m, l) in the
 // workspace and k_attn_q8_merge joins them.
 //
-// CTA: G groups of four softmax warps (NR rows each), a producer warp, an MMA
-// warp, two warps that prepare the next segment's rows (q1, q2, tree masks).
+// CTA: up to four groups of four softmax warps, 16 or 32 rows each, a producer
+// warp, an MMA warp, two warps that prepare the next segment's rows (q1, q2,
+// tree masks).  Several softmax warps per scheduler, each with few rows, hide
+// one another's latencies and share their instructions: one group with all 48
+// rows of the verification batch took 0.537 ms.
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <math.h>
@@ -239,49 +242,49 @@ struct Segments {
   }
 };
 
-template <int D, int G, int NR>
+template <int D, int RT, int CG>
 struct Cfg {
-  static constexpr int kRows = G * NR;                     // rows of a tile
-  static constexpr int kSoftWarps = 4 * G;
+  static constexpr int kGroups = RT / CG;                  // softmax groups of four warps, CG rows each
+  static constexpr int kSoftWarps = 4 * kGroups;
   static constexpr int kTmaWarp = kSoftWarps, kMmaWarp = kSoftWarps + 1, kPrepWarp = kSoftWarps + 2;
   static constexpr int kThreads = (kSoftWarps + 4) * 32;
-  static constexpr int kQTile = NR * 128;                  // q1 (or q2) of a group at D = 128; [q1 | q2] at D = 64
-  static constexpr int kQGroup = D == 128 ? 2 * kQTile : kQTile;
-  static constexpr int kQBuf = G * kQGroup;
-  static constexpr int kPBuf = kKeys * 128;                // a row per key: p1 [NR] then p2 [NR]
-  static constexpr int kNPB = G == 1 ? 2 : 1;              // P buffers of a group
+  static constexpr int kQTile = RT * 128;                  // q1 (or q2) at D = 128; [q1 | q2] at D = 64
+  static constexpr int kQBuf = D == 128 ? 2 * kQTile : kQTile;
+  static constexpr int kPBlock = kKeys * 128;              // 128 values of N: a 128-byte row per key
+  static constexpr int kPBuf = RT > 64 ? 2 * kPBlock : kPBlock;  // p1 [RT] then p2 [RT] along N
+  static constexpr int kNPB = RT > 64 ? 1 : 2;             // P buffers
   static constexpr int kKV = kKeys * D;                    // K or V of a tile
-  static constexpr int kFixed = 2 * kQBuf + G * kNPB * kPBuf;
+  static constexpr int kFixed = 2 * kQBuf + kNPB * kPBuf;
   static constexpr int kFit = (kSmemBudget - kFixed) / (2 * kKV);
   static constexpr int kStages = kFit > 8 ? 8 : kFit;
   static_assert(kStages >= 2, "two stages at least");
   static constexpr int kQ = 0, kP = 2 * kQBuf, kRing = kFixed;
   static constexpr int kSmem = kFixed + kStages * 2 * kKV + 1024;
-  static constexpr uint32_t kCols = G * 4 * NR;            // per group S (2 x NR), then O1, O2
+  static constexpr uint32_t kCols = 4 * RT;                // S (2 x RT), then O1, O2
   static constexpr uint32_t kTmem = kCols <= 64 ? 64 : (kCols <= 128 ? 128 : (kCols <= 256 ? 256 : 512));
-  static_assert(kSmem + (G == 1 ? 9728 : 12800) <= 227 * 1024, "shared memory with the static part");
-  static_assert(kCols <= 512 && 2 * NR <= 128 && NR % 16 == 0, "columns");
+  static_assert(kSmem + (RT <= 64 ? 9728 : 12800) <= 227 * 1024, "shared memory with the static part");
+  static_assert(kCols <= 512 && RT % CG == 0 && CG % 16 == 0 && CG <= 32 && kGroups <= 4, "rows");
 };
 
-template <int D, int G, int NR>
-__global__ void __launch_bounds__(Cfg<D, G, NR>::kThreads, 1)
+template <int D, int RT, int CG>
+__global__ void __launch_bounds__(Cfg<D, RT, CG>::kThreads, 1)
     k_branch_attn_q8(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                      const __grid_constant__ Args a) {
-  using C = Cfg<D, G, NR>;
-  constexpr int NS = C::kStages, RT = C::kRows, NPB = C::kNPB;
+  using C = Cfg<D, RT, CG>;
+  constexpr int NS = C::kStages, NPB = C::kNPB, G = C::kGroups;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t *const smem =
       reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   __shared__ __align__(8) uint64_t kfull[NS], kempty[NS], vfull[NS], vempty[NS];
-  __shared__ __align__(8) uint64_t sfull[G][2], sfree[G][2], pfull[G][2], pvdone[G][2], qfull[2], qempty[2];
+  __shared__ __align__(8) uint64_t sfull[2], sfree[2], pfull[2], pvdone[2], qfull[2], qempty[2];
   __shared__ uint32_t tmem_base;
   __shared__ float meta_k[NS][kPages], meta_v[NS][kPages];  // block scales (v: -1 where the block is hidden)
   __shared__ int meta_full[NS];                             // every key of the tile is a prefix key
   __shared__ int par[2][kMaxNodes];
   __shared__ uint32_t anc[2][kMaxNodes][kMaxNodes / 32];    // per query: the nodes that it sees
   __shared__ float qs[2][RT];                               // row scales 2^e
-  __shared__ __align__(16) float4 rowc[G][NR / 2];          // two rows: 2^e, 2^e, 6 - m, 6 - m
-  __shared__ float s_m[G][NR], s_f[G][NR], red[G][4][NR];
+  __shared__ __align__(16) float4 rowc[RT / 2];             // two rows: 2^e, 2^e, 6 - m, 6 - m
+  __shared__ float s_m[RT], s_f[RT], red[4][RT];
   __shared__ int s_nan[4];                                  // a tree node's v held NaN, by segment mod 4
   __shared__ long long scan[32][2];
   __shared__ Piece s_piece;
@@ -298,12 +301,10 @@ __global__ void __launch_bounds__(Cfg<D, G, NR>::kThreads, 1)
       mbar_init(&vempty[s], 1);
     }
     for (int u = 0; u < 2; ++u) {
-      for (int g = 0; g < G; ++g) {
-        mbar_init(&sfull[g][u], 1);
-        mbar_init(&sfree[g][u], 4);
-        mbar_init(&pfull[g][u], 4);
-        mbar_init(&pvdone[g][u], 1);
-      }
+      mbar_init(&sfull[u], 1);
+      mbar_init(&sfree[u], 4 * G);
+      mbar_init(&pfull[u], 4 * G);
+      mbar_init(&pvdone[u], 1);
       mbar_init(&qfull[u], 2);
       mbar_init(&qempty[u], 1 + 4 * G);
     }
@@ -439,14 +440,13 @@ __global__ void __launch_bounds__(Cfg<D, G, NR>::kThreads, 1)
           c1 |= h << (8 * e);
           c2 |= e4m3_pair(u0 - b0, u1 - b1) << (8 * e);
         }
-        const int row = r0 + u, g = row / NR, j = row % NR;
-        uint8_t *const qg = qb + g * C::kQGroup;
+        const int row = r0 + u;
         if constexpr (D == 128) {
-          *reinterpret_cast<uint32_t *>(qg + sw128(j, lane * 4)) = c1;
-          *reinterpret_cast<uint32_t *>(qg + C::kQTile + sw128(j, lane * 4)) = c2;
+          *reinterpret_cast<uint32_t *>(qb + sw128(row, lane * 4)) = c1;
+          *reinterpret_cast<uint32_t *>(qb + C::kQTile + sw128(row, lane * 4)) = c2;
         } else {
-          *reinterpret_cast<uint16_t *>(qg + sw128(j, lane * 2)) = static_cast<uint16_t>(c1);
-          *reinterpret_cast<uint16_t *>(qg + sw128(j, 64 + lane * 2)) = static_cast<uint16_t>(c2);
+          *reinterpret_cast<uint16_t *>(qb + sw128(row, lane * 2)) = static_cast<uint16_t>(c1);
+          *reinterpret_cast<uint16_t *>(qb + sw128(row, 64 + lane * 2)) = static_cast<uint16_t>(c2);
         }
         if (lane == 0) qs[buf][row] = __uint_as_float(static_cast<uint32_t>(127 + e2) << 23);
       }
@@ -550,33 +550,27 @@ __global__ void __launch_bounds__(Cfg<D, G, NR>::kThreads, 1)
   } else if (warp == C::kMmaWarp) {
     // ---------------- MMA issue (one thread): S(i), then O += P(i - 1) V(i - 1)
     if (lane == 0) {
-      constexpr uint32_t idesc_s = idesc_f8(NR, 0), idesc_o = idesc_f8(2 * NR, 1);
+      constexpr uint32_t idesc_s = idesc_f8(RT, 0), idesc_o = idesc_f8(2 * RT, 1);
       const uint32_t base = smem_u32(smem);
       bool ok = true;
       auto issue_pv = [&](int i, bool fresh) {
         const int st = i % NS;
-        if (!mbar_wait_sleep(&vfull[st], (i / NS) & 1)) {
+        if (!mbar_wait_sleep(&vfull[st], (i / NS) & 1) || !mbar_wait_sleep(&pfull[i & 1], (i >> 1) & 1)) {
           ok = false;
           return;
         }
+        tc_fence_after();
         const uint32_t v = base + C::kRing + st * 2 * C::kKV + C::kKV;
-        for (int g = 0; g < G; ++g) {
-          if (!mbar_wait_sleep(&pfull[g][i & 1], (i >> 1) & 1)) {
-            ok = false;
-            return;
-          }
-          tc_fence_after();
-          const uint32_t p = base + C::kP + (g * NPB + i % NPB) * C::kPBuf;
-          const uint32_t o = tmem + g * 4 * NR + 2 * NR;
+        const uint32_t p = base + C::kP + (i % NPB) * C::kPBuf;
 #pragma unroll
-          for (int kk = 0; kk < kKeys / 32; ++kk) {
-            // 32 keys: four groups of 8 rows
-            const uint64_t vd = D == 128 ? smem_desc(v + kk * 4096, 16, 1024, kSw128)
-                                         : smem_desc(v + kk * 2048, 0, 512, kSw64);
-            umma_f8(o, vd, smem_desc(p + kk * 4096, 16, 1024, kSw128), idesc_o, (!fresh || kk > 0) ? 1u : 0u);
-          }
-          umma_commit(&pvdone[g][i & 1]);
+        for (int kk = 0; kk < kKeys / 32; ++kk) {
+          // 32 keys: four groups of 8 rows
+          const uint64_t vd = D == 128 ? smem_desc(v + kk * 4096, 16, 1024, kSw128)
+                                       : smem_desc(v + kk * 2048, 0, 512, kSw64);
+          umma_f8(tmem + 2 * RT, vd, smem_desc(p + kk * 4096, C::kPBlock, 1024, kSw128), idesc_o,
+                  (!fresh || kk > 0) ? 1u : 0u);
         }
+        umma_commit(&pvdone[i & 1]);
         umma_commit(&vempty[st]);
       };
       int i = 0, seg = 0;
@@ -591,26 +585,23 @@ __global__ void __launch_bounds__(Cfg<D, G, NR>::kThreads, 1)
             break;
           }
           const uint32_t k = base + C::kRing + st * 2 * C::kKV;
-          for (int g = 0; g < G; ++g) {
-            if (i >= 2 && !mbar_wait_sleep(&sfree[g][i & 1], ((i - 2) >> 1) & 1)) {
-              ok = false;
-              break;
-            }
-            tc_fence_after();
-            const uint32_t q = base + C::kQ + buf * C::kQBuf + g * C::kQGroup;
-            const uint32_t s = tmem + g * 4 * NR + (i & 1) * NR;
-#pragma unroll
-            for (int term = 0; term < 2; ++term)
-#pragma unroll
-              for (int kk = 0; kk < D / 32; ++kk) {
-                const uint64_t kd = D == 128 ? smem_desc(k + kk * 32, 16, 1024, kSw128)
-                                             : smem_desc(k + kk * 32, 16, 512, kSw64);
-                const uint32_t qa = q + (D == 128 ? term * C::kQTile : term * 64) + kk * 32;
-                umma_f8(s, kd, smem_desc(qa, 16, 1024, kSw128), idesc_s, (term > 0 || kk > 0) ? 1u : 0u);
-              }
-            umma_commit(&sfull[g][i & 1]);
+          if (i >= 2 && !mbar_wait_sleep(&sfree[i & 1], ((i - 2) >> 1) & 1)) {
+            ok = false;
+            break;
           }
-          if (!ok) break;
+          tc_fence_after();
+          const uint32_t q = base + C::kQ + buf * C::kQBuf;
+#pragma unroll
+          for (int term = 0; term < 2; ++term)
+#pragma unroll
+            for (int kk = 0; kk < D / 32; ++kk) {
+              const uint64_t kd = D == 128 ? smem_desc(k + kk * 32, 16, 1024, kSw128)
+                                           : smem_desc(k + kk * 32, 16, 512, kSw64);
+              const uint32_t qa = q + (D == 128 ? term * C::kQTile : term * 64) + kk * 32;
+              umma_f8(tmem + (i & 1) * RT, kd, smem_desc(qa, 16, 1024, kSw128), idesc_s,
+                      (term > 0 || kk > 0) ? 1u : 0u);
+            }
+          umma_commit(&sfull[i & 1]);
           umma_commit(&kempty[st]);
           if (t == sg.t1 - 1) umma_commit(&qempty[buf]);
           if (i >= 1) issue_pv(i - 1, fresh_prev);
@@ -624,55 +615,55 @@ __global__ void __launch_bounds__(Cfg<D, G, NR>::kThreads, 1)
     // ---------------- the rows of the segments after the first
     bool more = sg.first(a, piece);
     if (more) {
-      prepare(sg, 0, C::kSoftWarps + warp - C::kPrepWarp, C::kSoftWarps + 2, 4);
-      bar_sync(4, (C::kSoftWarps + 2) * 32);
+      prepare(sg, 0, C::kSoftWarps + warp - C::kPrepWarp, C::kSoftWarps + 2, 6);
+      bar_sync(6, (C::kSoftWarps + 2) * 32);
       if (lane == 0) mbar_arrive1(&qfull[0]);
       more = sg.step(a);
     }
     for (int seg = 1; more; more = sg.step(a), ++seg) {
       const int buf = seg & 1;
       const bool ok = seg < 2 || mbar_wait_sleep(&qempty[buf], ((seg >> 1) - 1) & 1);
-      if (bar_or(5, 64, !ok || s_abort)) {
+      if (bar_or(7, 64, !ok || s_abort)) {
         s_abort = 1;
         break;
       }
-      prepare(sg, buf, warp - C::kPrepWarp, 2, 5);
+      prepare(sg, buf, warp - C::kPrepWarp, 2, 7);
       if (lane == 0) mbar_arrive1(&qfull[buf]);
     }
   } else {
-    // ---------------- softmax: group g of four warps, one thread per key
-    const int g = warp / 4, wg = warp & 3, tg = tid & 127;
+    // ---------------- softmax: group g of four warps and CG rows, one thread per key
+    const int g = warp / 4, wg = warp & 3, tg = tid & 127, col = g * CG;
     const uint32_t lane_off = static_cast<uint32_t>(wg * 32) << 16;
-    const uint32_t tS = tmem + g * 4 * NR + lane_off, tO = tS + 2 * NR;
+    const uint32_t tS = tmem + col + lane_off, tO1 = tmem + 2 * RT + col + lane_off, tO2 = tO1 + RT;
     const int bar = 1 + g;
     int i = 0, seg = 0;
     bool dead = false;
     bool more = sg.first(a, piece);
     if (more) {
-      prepare(sg, 0, warp, C::kSoftWarps + 2, 4);
-      bar_sync(4, (C::kSoftWarps + 2) * 32);
+      prepare(sg, 0, warp, C::kSoftWarps + 2, 6);
+      bar_sync(6, (C::kSoftWarps + 2) * 32);
     }
     for (; more && !dead; more = sg.step(a), ++seg) {
       const int buf = seg & 1;
       const int hk = sg.item / a.mtiles, mt = sg.item % a.mtiles;
-      const int row0 = mt * RT + g * NR;  // the group's first row of (b, hk)
+      const int row0 = mt * RT + col;  // the group's first row of (b, hk)
       bool ok = __all_sync(0xffffffffu, mbar_wait_sleep(&qfull[buf], (seg >> 1) & 1));
-      if (tg < NR) {
-        s_m[g][tg] = NEG_INF;
-        float *const rc = reinterpret_cast<float *>(&rowc[g][tg >> 1]) + (tg & 1);
-        rc[0] = qs[buf][tg + g * NR];
+      if (tg < CG) {
+        s_m[col + tg] = NEG_INF;
+        float *const rc = reinterpret_cast<float *>(&rowc[(col + tg) >> 1]) + (tg & 1);
+        rc[0] = qs[buf][col + tg];
         rc[2] = 0.f;
       }
       if (g == 0 && tg == 0) s_nan[(seg + 2) & 3] = 0;
       bar_sync(bar, 128);
-      uint64_t l2[NR / 2];
+      uint64_t l2[CG / 2];
 #pragma unroll
-      for (int j = 0; j < NR / 2; ++j) l2[j] = 0;
+      for (int j = 0; j < CG / 2; ++j) l2[j] = 0;
       for (int t = sg.t0; t < sg.t1; ++t, ++i) {
         const int st = i % NS, u = i & 1;
         const bool begin = t == sg.t0;
         ok = __all_sync(0xffffffffu, ok && !s_abort && mbar_wait_sleep(&vfull[st], (i / NS) & 1) &&
-                                         mbar_wait_sleep(&sfull[g][u], (i >> 1) & 1));
+                                         mbar_wait_sleep(&sfull[u], (i >> 1) & 1));
         tc_fence_after();
         const float vsc = meta_v[st][tg / kPage];
         const float c = meta_k[st][tg / kPage] * a.scale_log2;
@@ -680,36 +671,35 @@ __global__ void __launch_bounds__(Cfg<D, G, NR>::kThreads, 1)
         const float wv = vsc < kMinBlockScale ? 0.f : vsc;
         const bool full = meta_full[st] != 0;
         // the rows that see this thread's key
-        uint64_t vis = ~0ull;
+        uint32_t vis = ~0u;
         if (!full) {
           const int pos = t * kKeys + tg;
           if (vsc < 0.f || pos >= sg.nkeys) vis = 0;
           else if (pos >= sg.L) {
             const int n = pos - sg.L;
             vis = 0;
-#pragma unroll
-            for (int j = 0; j < NR; ++j) {
+            for (int j = 0; j < CG; ++j) {
               const int qi = min(static_cast<int>(((row0 + j) * a.group_magic) >> 16), kMaxNodes - 1);
-              vis |= static_cast<uint64_t>((anc[buf][qi][n >> 5] >> (n & 31)) & 1u) << j;
+              vis |= ((anc[buf][qi][n >> 5] >> (n & 31)) & 1u) << j;
             }
           }
         }
         const uint64_t c2 = pack2(c, c);
-        float y[NR];
+        float y[CG];
         // y = x - m + 6 (or x where rowc holds 0); hidden keys -inf
         auto scores = [&]() {
 #pragma unroll
-          for (int j = 0; j < NR; j += 16) tmem_ld16_async(tS + u * NR + j, y + j);
+          for (int j = 0; j < CG; j += 16) tmem_ld16_async(tS + u * RT + j, y + j);
 #pragma unroll
-          for (int j = 0; j < NR; j += 16) tmem_wait16(y + j);
+          for (int j = 0; j < CG; j += 16) tmem_wait16(y + j);
 #pragma unroll
-          for (int j = 0; j < NR; j += 2) {
-            const float4 rc = rowc[g][j / 2];
+          for (int j = 0; j < CG; j += 2) {
+            const float4 rc = rowc[(col + j) / 2];
             unpack2(fma2(mul2(pack2(y[j], y[j + 1]), c2), pack2(rc.x, rc.y), pack2(rc.z, rc.w)), y[j], y[j + 1]);
           }
           if (!full) {
 #pragma unroll
-            for (int j = 0; j < NR; ++j) y[j] = ((vis >> j) & 1ull) ? y[j] : NEG_INF;
+            for (int j = 0; j < CG; ++j) y[j] = ((vis >> j) & 1u) ? y[j] : NEG_INF;
           }
         };
         bool grow = begin;
@@ -717,65 +707,68 @@ __global__ void __launch_bounds__(Cfg<D, G, NR>::kThreads, 1)
           scores();
           float t4[4] = {y[0], y[1], y[2], y[3]};
 #pragma unroll
-          for (int j = 4; j < NR; ++j) t4[j & 3] = fmaxf(t4[j & 3], y[j]);
+          for (int j = 4; j < CG; ++j) t4[j & 3] = fmaxf(t4[j & 3], y[j]);
           const float top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
           grow = bar_or(bar, 128, top + lsv > kGrow || !ok);
         }
         if (grow) {
           // the rows' largest x + log2 v_scale in this tile
-#pragma unroll
-          for (int j0 = 0; j0 < NR; j0 += 16) {
+#pragma unroll 1
+          for (int j0 = 0; j0 < CG; j0 += 16) {
             float z[16];
-            tmem_ld16_async(tS + u * NR + j0, z);
+            tmem_ld16_async(tS + u * RT + j0, z);
             tmem_wait16(z);
 #pragma unroll
             for (int j = 0; j < 16; ++j) {
-              const float4 rc = rowc[g][(j0 + j) / 2];
-              z[j] = ((vis >> (j0 + j)) & 1ull) ? fmaf(z[j] * c, (j & 1) ? rc.y : rc.x, lsv) : NEG_INF;
+              const float4 rc = rowc[(col + j0 + j) / 2];
+              z[j] = ((vis >> (j0 + j)) & 1u) ? fmaf(z[j] * c, (j & 1) ? rc.y : rc.x, lsv) : NEG_INF;
             }
             const float top = warp_columns<false>(z, lane);
-            if (!(lane & 1)) red[g][wg][j0 + (lane >> 1)] = top;
+            if (!(lane & 1)) red[wg][col + j0 + (lane >> 1)] = top;
           }
           if (!begin) {  // O is rescaled below: every P V before has to be in it
-            ok = __all_sync(0xffffffffu, mbar_wait(&pvdone[g][u ^ 1], ((i - 1) >> 1) & 1) && ok);
+            ok = __all_sync(0xffffffffu, mbar_wait(&pvdone[u ^ 1], ((i - 1) >> 1) & 1) && ok);
             tc_fence_after();
           }
           if (bar_or(bar, 128, !ok)) {
             dead = true;
             break;
           }
-          if (tg < NR) {
-            const float mx = fmaxf(fmaxf(red[g][0][tg], red[g][1][tg]), fmaxf(red[g][2][tg], red[g][3][tg]));
-            const float mo = s_m[g][tg], mn = fmaxf(mo, mx);
-            s_m[g][tg] = mn;
-            s_f[g][tg] = mo == NEG_INF ? (mn == NEG_INF ? 1.f : 0.f) : ex2(mo - mn);
-            reinterpret_cast<float *>(&rowc[g][tg >> 1])[2 + (tg & 1)] = mn == NEG_INF ? kUnset : kBias - mn;
+          if (tg < CG) {
+            const int r = col + tg;
+            const float mx = fmaxf(fmaxf(red[0][r], red[1][r]), fmaxf(red[2][r], red[3][r]));
+            const float mo = s_m[r], mn = fmaxf(mo, mx);
+            s_m[r] = mn;
+            s_f[r] = mo == NEG_INF ? (mn == NEG_INF ? 1.f : 0.f) : ex2(mo - mn);
+            reinterpret_cast<float *>(&rowc[r >> 1])[2 + (tg & 1)] = mn == NEG_INF ? kUnset : kBias - mn;
           }
           bar_sync(bar, 128);
           if (!begin) {
 #pragma unroll
-            for (int j = 0; j < NR / 2; ++j) l2[j] = mul2(l2[j], pack2(s_f[g][2 * j], s_f[g][2 * j + 1]));
-#pragma unroll
-            for (int j0 = 0; j0 < 2 * NR; j0 += 16) {
+            for (int j = 0; j < CG / 2; ++j) l2[j] = mul2(l2[j], pack2(s_f[col + 2 * j], s_f[col + 2 * j + 1]));
+#pragma unroll 1
+            for (int j0 = 0; j0 < 2 * CG; j0 += 16) {
               float o[16];
-              tmem_ld16(tO + j0, o);
+              const int jc = j0 % CG;
+              const uint32_t at = (j0 < CG ? tO1 : tO2) + jc;
+              tmem_ld16(at, o);
 #pragma unroll
-              for (int j = 0; j < 16; ++j) o[j] *= s_f[g][(j0 + j) % NR];
-              tmem_st16(tO + j0, o);
+              for (int j = 0; j < 16; ++j) o[j] *= s_f[col + jc + j];
+              tmem_st16(at, o);
             }
           }
           scores();
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive1(&sfree[g][u]);
+        if (lane == 0) mbar_arrive1(&sfree[u]);
         // the P buffer is free once P V of tile i - NPB is done
         if (i >= NPB)
-          ok = __all_sync(0xffffffffu, mbar_wait_sleep(&pvdone[g][(i - NPB) & 1], ((i - NPB) >> 1) & 1) && ok);
-        uint8_t *const prow = smem + C::kP + (g * NPB + i % NPB) * C::kPBuf;
+          ok = __all_sync(0xffffffffu, mbar_wait_sleep(&pvdone[(i - NPB) & 1], ((i - NPB) >> 1) & 1) && ok);
+        uint8_t *const pb = smem + C::kP + (i % NPB) * C::kPBuf;
         const uint64_t w2 = pack2(wv, wv);
 #pragma unroll
-        for (int j0 = 0; j0 < NR; j0 += 16) {
+        for (int j0 = 0; j0 < CG; j0 += 16) {
           uint32_t p1[4], p2[4];
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
@@ -795,8 +788,11 @@ __global__ void __launch_bounds__(Cfg<D, G, NR>::kThreads, 1)
             p1[q] = pack16(e1[0], e1[1]);
             p2[q] = pack16(e2[0], e2[1]);
           }
-          *reinterpret_cast<uint4 *>(prow + sw128(tg, j0)) = make_uint4(p1[0], p1[1], p1[2], p1[3]);
-          *reinterpret_cast<uint4 *>(prow + sw128(tg, NR + j0)) = make_uint4(p2[0], p2[1], p2[2], p2[3]);
+          const int n1 = col + j0, n2 = RT + n1;  // places along N
+          *reinterpret_cast<uint4 *>(pb + (n1 >> 7) * C::kPBlock + sw128(tg, n1 & 127)) =
+              make_uint4(p1[0], p1[1], p1[2], p1[3]);
+          *reinterpret_cast<uint4 *>(pb + (n2 >> 7) * C::kPBlock + sw128(tg, n2 & 127)) =
+              make_uint4(p2[0], p2[1], p2[2], p2[3]);
         }
         if (!full && g == 0) {
           // hidden keys take no part whatever their v holds (0 * NaN): their rows become 0; a tree node's NaN
@@ -805,20 +801,19 @@ __global__ void __launch_bounds__(Cfg<D, G, NR>::kThreads, 1)
           uint8_t *const vt = smem + C::kRing + st * 2 * C::kKV + C::kKV;
           const bool hidden = vsc < 0.f || pos >= sg.nkeys;
           if (hidden || pos >= sg.L) {
-#pragma unroll
             for (int e = 0; e < D; e += 16) {
               uint4 *const at = reinterpret_cast<uint4 *>(vt + (D == 128 ? sw128(tg, e) : sw64(tg, e)));
-              uint4 x = hidden ? make_uint4(0, 0, 0, 0) : *at;
+              uint4 x = make_uint4(0, 0, 0, 0);
               if (!hidden) {
-                uint32_t *const wd = reinterpret_cast<uint32_t *>(&x);
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                  const uint32_t nan = ((wd[q] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;  // bytes 0x7F, 0xFF
-                  if (nan) {
-                    wd[q] &= ~((nan >> 7) * 0xFFu);
-                    s_nan[seg & 3] = 1;
-                  }
-                }
+                x = *at;
+                uint32_t any = 0;
+                auto clear = [&](uint32_t w) {
+                  const uint32_t nan = ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;  // bytes 0x7F, 0xFF
+                  any |= nan;
+                  return w & ~((nan >> 7) * 0xFFu);
+                };
+                x = make_uint4(clear(x.x), clear(x.y), clear(x.z), clear(x.w));
+                if (any) s_nan[seg & 3] = 1;
               }
               *at = x;
             }
@@ -827,19 +822,19 @@ __global__ void __launch_bounds__(Cfg<D, G, NR>::kThreads, 1)
         fence_proxy_async();  // P and V (generic writes) -> visible to the tensor cores
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive1(&pfull[g][u]);
+        if (lane == 0) mbar_arrive1(&pfull[u]);
       }
       if (dead) break;
       // ---------------- the segment's rows: l over the keys' threads, O from TMEM
 #pragma unroll
-      for (int j0 = 0; j0 < NR; j0 += 16) {
+      for (int j0 = 0; j0 < CG; j0 += 16) {
         float z[16];
 #pragma unroll
         for (int j = 0; j < 16; j += 2) unpack2(l2[(j0 + j) / 2], z[j], z[j + 1]);
         const float sum = warp_columns<true>(z, lane);
-        if (!(lane & 1)) red[g][wg][j0 + (lane >> 1)] = sum;
+        if (!(lane & 1)) red[wg][col + j0 + (lane >> 1)] = sum;
       }
-      ok = __all_sync(0xffffffffu, mbar_wait(&pvdone[g][(i - 1) & 1], ((i - 1) >> 1) & 1) && ok);
+      ok = __all_sync(0xffffffffu, mbar_wait(&pvdone[(i - 1) & 1], ((i - 1) >> 1) & 1) && ok);
       tc_fence_after();
       if (bar_or(bar, 128, !ok)) {
         dead = true;
@@ -847,32 +842,33 @@ __global__ void __launch_bounds__(Cfg<D, G, NR>::kThreads, 1)
       }
       const bool whole = sg.t0 == 0 && sg.t1 == sg.nt;
       const int slot = blockIdx.x * 2 + (sg.t0 > 0 ? 0 : 1);
-      if (tg < NR && row0 + tg < a.nrows) {
-        const float l = __fadd_rn(__fadd_rn(red[g][0][tg], red[g][1][tg]), __fadd_rn(red[g][2][tg], red[g][3][tg]));
-        const float m = s_m[g][tg];
+      if (tg < CG && row0 + tg < a.nrows) {
+        const int r = col + tg;
+        const float l = __fadd_rn(__fadd_rn(red[0][r], red[1][r]), __fadd_rn(red[2][r], red[3][r]));
+        const float m = s_m[r];
         if (whole) {
-          s_f[g][tg] = l == 0.f ? 0.f : 1.f / l;
-          const int r = row0 + tg, qi = r / a.group, head = hk * a.group + r % a.group;
+          s_f[r] = l == 0.f ? 0.f : 1.f / l;
+          const int row = row0 + tg, qi = row / a.group, head = hk * a.group + row % a.group;
           if (a.lse)
             a.lse[(static_cast<int64_t>(sg.b) * a.Nq + qi) * a.Hq + head] =
                 l == 0.f ? NEG_INF : (m - kBias + log2f(l)) * 0.69314718055994531f;
         } else {
-          s_f[g][tg] = 1.f;
-          a.part_ml[slot * RT + g * NR + tg] = make_float2(m, l);
+          s_f[r] = 1.f;
+          a.part_ml[slot * RT + r] = make_float2(m, l);
         }
       }
       bar_sync(bar, 128);
       const bool nan = s_nan[seg & 3] != 0;
       if (D == 128 || wg < 2) {
-#pragma unroll
-        for (int j0 = 0; j0 < NR; j0 += 16) {
+#pragma unroll 1
+        for (int j0 = 0; j0 < CG; j0 += 16) {
           float o1[16], o2[16];
-          tmem_ld16_async(tO + j0, o1);
-          tmem_ld16_async(tO + NR + j0, o2);
+          tmem_ld16_async(tO1 + j0, o1);
+          tmem_ld16_async(tO2 + j0, o2);
           tmem_wait16(o1);
           tmem_wait16(o2);
 #pragma unroll
-          for (int j = 0; j < 16; ++j) o1[j] = fmaf(o2[j], 0.03125f, o1[j]) * s_f[g][j0 + j];
+          for (int j = 0; j < 16; ++j) o1[j] = fmaf(o2[j], 0.03125f, o1[j]) * s_f[col + j0 + j];
           if (nan) {
             // tree nodes of this segment whose v holds NaN at this thread's element
             for (int n = max(0, sg.t0 * kKeys - sg.L); n < a.N && sg.L + n < min(sg.nkeys, sg.t1 * kKeys); ++n) {
@@ -901,8 +897,7 @@ __global__ void __launch_bounds__(Cfg<D, G, NR>::kThreads, 1)
             }
           } else {
 #pragma unroll
-            for (int j = 0; j < 16; ++j)
-              a.part_o[(static_cast<int64_t>(slot) * RT + g * NR + j0 + j) * D + tg] = o1[j];
+            for (int j = 0; j < 16; ++j) a.part_o[(static_cast<int64_t>(slot) * RT + col + j0 + j) * D + tg] = o1[j];
           }
         }
       }
@@ -994,18 +989,18 @@ bool make_code_map(CUtensorMap *m, const void *base, int64_t num_blocks, int Hkv
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Rows of a tile: up to 64 in one group of softmax warps, up to 128 in two; the
-// group's size is the next multiple of 16 (the MMA's step in N).
+// Rows of a tile: at most 128, the tiles of equal size, a multiple of the
+// softmax groups' 16 rows (32 above 64: four groups are all that 20 warps and
+// their registers allow).
 struct Shape {
-  int nrows, mtiles, G, NR;
+  int nrows, mtiles, RT;
 };
 Shape shape_of(int Nq, int Hq, int Hkv) {
   Shape s;
   s.nrows = (Hq / Hkv) * Nq;
   s.mtiles = (s.nrows + 127) / 128;
   const int tile = (s.nrows + s.mtiles - 1) / s.mtiles;
-  s.G = tile > 64 ? 2 : 1;
-  s.NR = s.G == 1 ? (tile + 15) / 16 * 16 : (tile > 96 ? 64 : 48);
+  s.RT = tile <= 64 ? (tile + 15) / 16 * 16 : (tile + 31) / 32 * 32;
   return s;
 }
 size_t align256(size_t x) { return (x + 255) / 256 * 256; }
@@ -1014,7 +1009,7 @@ struct Workspace {
 };
 Workspace workspace_of(const Shape &s, int d, int ctas) {
   Workspace w;
-  const size_t rows = static_cast<size_t>(ctas) * 2 * s.G * s.NR;
+  const size_t rows = static_cast<size_t>(ctas) * 2 * s.RT;
   w.o = 0;
   w.ml = align256(rows * d * sizeof(float));
   w.info = w.ml + align256(rows * sizeof(float2));
@@ -1022,17 +1017,17 @@ Workspace workspace_of(const Shape &s, int d, int ctas) {
   return w;
 }
 
-template <int D, int G, int NR>
+template <int D, int RT, int CG>
 cudaError_t launch(const CUtensorMap &kmap, const CUtensorMap &vmap, const Args &a, unsigned grid, cudaStream_t cs) {
-  using C = q8::Cfg<D, G, NR>;
-  cudaError_t e = cudaFuncSetAttribute(q8::k_branch_attn_q8<D, G, NR>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  using C = q8::Cfg<D, RT, CG>;
+  cudaError_t e = cudaFuncSetAttribute(q8::k_branch_attn_q8<D, RT, CG>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        C::kSmem);
   if (e != cudaSuccess) return e;
-  q8::k_branch_attn_q8<D, G, NR><<<grid, C::kThreads, C::kSmem, cs>>>(kmap, vmap, a);
+  q8::k_branch_attn_q8<D, RT, CG><<<grid, C::kThreads, C::kSmem, cs>>>(kmap, vmap, a);
   e = cudaGetLastError();
   if (e != cudaSuccess || !a.split) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid, (min(C::kRows, a.nrows) + 7) / 8);
+  cfg.gridDim = dim3(grid, (min(RT, a.nrows) + 7) / 8);
   cfg.blockDim = dim3(256);
   cfg.stream = cs;
   cudaLaunchAttribute at;
@@ -1040,18 +1035,19 @@ cudaError_t launch(const CUtensorMap &kmap, const CUtensorMap &vmap, const Args 
   at.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, q8::k_attn_q8_merge<D, C::kRows>, a);
+  return cudaLaunchKernelEx(&cfg, q8::k_attn_q8_merge<D, RT>, a);
 }
 
 template <int D>
 cudaError_t launch_shape(const Shape &s, const CUtensorMap &kmap, const CUtensorMap &vmap, const Args &a,
                          unsigned grid, cudaStream_t cs) {
-  if (s.G == 2) return s.NR == 64 ? launch<D, 2, 64>(kmap, vmap, a, grid, cs) : launch<D, 2, 48>(kmap, vmap, a, grid, cs);
-  switch (s.NR) {
-    case 16: return launch<D, 1, 16>(kmap, vmap, a, grid, cs);
-    case 32: return launch<D, 1, 32>(kmap, vmap, a, grid, cs);
-    case 48: return launch<D, 1, 48>(kmap, vmap, a, grid, cs);
-    default: return launch<D, 1, 64>(kmap, vmap, a, grid, cs);
+  switch (s.RT) {
+    case 16: return launch<D, 16, 16>(kmap, vmap, a, grid, cs);
+    case 32: return launch<D, 32, 16>(kmap, vmap, a, grid, cs);
+    case 48: return launch<D, 48, 16>(kmap, vmap, a, grid, cs);
+    case 64: return launch<D, 64, 16>(kmap, vmap, a, grid, cs);
+    case 96: return launch<D, 96, 32>(kmap, vmap, a, grid, cs);
+    default: return launch<D, 128, 32>(kmap, vmap, a, grid, cs);
   }
 }
 
