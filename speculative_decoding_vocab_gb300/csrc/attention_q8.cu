@@ -457,59 +457,82 @@ __global__ void __launch_bounds__(Cfg<D, RT, CG>::kThreads, 1)
 
   Segments sg;
   if (warp == C::kTmaWarp) {
-    // ---------------- producer: one lane per page of K (0..7) and of V (8..15)
-    const int pg = lane & 7;
-    const bool isv = (lane & 8) != 0;
-    struct Tile {
-      int any, t, L, nkeys, hk, b, blk;
-      float sc;
+    // ---------------- producer.  Block ids and scales are fetched for eight tiles at a time, one batch ahead
+    // (two dependent trips to memory for eight tiles, not for one): lane l holds blocks 2 (l % 4), + 1 of the
+    // batch's tile l / 4, and issues their copies.
+    struct Batch {
+      int t, L, hk;
+      bool any;
+      int blk[2];
+      float ks[2], vs[2];
     };
     bool more = sg.first(a, piece);
     int t = more ? sg.t0 : 0;
-    auto fetch = [&](Tile &x) {  // the next tile's block ids
+    auto advance = [&](int n) {  // this lane's place in the line of tiles
+      t += n;
+      while (more && t >= sg.t1) {
+        t -= sg.t1;
+        more = sg.step(a);
+      }
+    };
+    auto ids = [&](Batch &x) {
       x.any = more;
-      x.blk = -1;
-      x.sc = 0.f;
-      if (!more) return;
       x.t = t;
       x.L = sg.L;
-      x.nkeys = sg.nkeys;
-      x.hk = sg.item / a.mtiles;
-      x.b = sg.b;
-      const int lp = t * kPages + pg;
-      if (lp < a.maxb && lp * static_cast<int64_t>(kPage) < sg.nkeys) {
-        x.blk = a.table[static_cast<int64_t>(sg.b) * a.maxb + lp];
-        if (x.blk < 0 || x.blk >= a.num_blocks) {
+      x.hk = more ? sg.item / a.mtiles : 0;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int lp = t * kPages + (lane & 3) * 2 + e;
+        x.blk[e] = -1;
+        x.ks[e] = x.vs[e] = 0.f;
+        if (more && lp < a.maxb && lp * static_cast<int64_t>(kPage) < sg.nkeys)
+          x.blk[e] = a.table[static_cast<int64_t>(sg.b) * a.maxb + lp];
+        else
+          x.ks[e] = -1.f;  // no block there
+      }
+    };
+    auto scales = [&](Batch &x) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+        if (x.blk[e] >= 0 && x.blk[e] < a.num_blocks) {
+          const int64_t unit = static_cast<int64_t>(x.blk[e]) * a.Hkv + x.hk;
+          x.ks[e] = __ldg(a.ks + unit);
+          x.vs[e] = __ldg(a.vs + unit);
+        } else if (x.ks[e] >= 0.f) {
           atomicOr(a.status, kFlagBadBlock);
-          x.blk = -1;
+          x.ks[e] = -1.f;
+        }
+    };
+    Batch now, next;
+    advance(lane >> 2);
+    ids(now);
+    scales(now);
+    advance(8);
+    ids(next);
+    int issued = 0;
+    for (int i = 0;; ++i) {
+      const int st = i % NS, w = i & 7;
+      if (w == 0 && i > 0) {
+        now = next;
+        advance(8);
+        ids(next);
+      }
+      if (w == 4) scales(next);
+      if (!__shfl_sync(0xffffffffu, static_cast<int>(now.any), w * 4)) break;
+      const bool mine = (lane >> 2) == w;
+      bool valid[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        valid[e] = mine && now.blk[e] >= 0 && now.blk[e] < a.num_blocks;
+        if (valid[e] && !(good_scale(now.ks[e]) && good_scale(now.vs[e]))) {
+          atomicOr(a.status, kFlagBadValue);
+          valid[e] = false;
         }
       }
-      if (++t == sg.t1) {
-        more = sg.step(a);
-        t = 0;
-      }
-    };
-    auto scales = [&](Tile &x) {
-      if (x.blk >= 0) x.sc = __ldg((isv ? a.vs : a.ks) + static_cast<int64_t>(x.blk) * a.Hkv + x.hk);
-    };
-    Tile now, next;
-    fetch(now);
-    scales(now);
-    fetch(next);
-    int issued = 0;
-    for (int i = 0; now.any; ++i) {
-      const int st = i % NS;
-      scales(next);
-      Tile after;
-      fetch(after);
-      bool valid = now.blk >= 0;
-      const bool good = !valid || good_scale(now.sc);
-      if (!good) atomicOr(a.status, kFlagBadValue);
-      const bool other = __shfl_xor_sync(0xffffffffu, good, 8);  // the block's other scale
-      valid = valid && good && other;
-      const uint32_t mask = __ballot_sync(0xffffffffu, valid) & 0xFFu;
-      const uint32_t bytes = __popc(mask) * (kPage * D);
+      const int blocks = __popc(__ballot_sync(0xffffffffu, valid[0])) + __popc(__ballot_sync(0xffffffffu, valid[1]));
+      const uint32_t bytes = blocks * (kPage * D);
       uint8_t *const ring = smem + C::kRing + st * 2 * C::kKV;
+      const int p0 = (lane & 3) * 2;
       int ok = 1;
       if (lane == 0) {
         if (s_abort || (i >= NS && !mbar_wait_sleep(&kempty[st], ((i / NS) - 1) & 1))) ok = 0;
@@ -520,7 +543,10 @@ __global__ void __launch_bounds__(Cfg<D, RT, CG>::kThreads, 1)
         s_abort = 1;
         break;
       }
-      if (lane < 8 && valid) tma_load_3d(ring + pg * (kPage * D), &kmap, 0, now.hk * kPage, now.blk, &kfull[st]);
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+        if (valid[e])
+          tma_load_3d(ring + (p0 + e) * (kPage * D), &kmap, 0, now.hk * kPage, now.blk[e], &kfull[st]);
       if (lane == 0) ok = i < NS || mbar_wait_sleep(&vempty[st], ((i / NS) - 1) & 1);
       ok = __shfl_sync(0xffffffffu, ok, 0);
       issued = i + 1;
@@ -530,16 +556,21 @@ __global__ void __launch_bounds__(Cfg<D, RT, CG>::kThreads, 1)
         s_abort = 1;
         break;
       }
-      if (lane < 8) meta_k[st][pg] = valid ? now.sc : 0.f;
-      else if (lane < 16) meta_v[st][pg] = valid ? now.sc : -1.f;
-      if (lane == 0) meta_full[st] = mask == 0xFFu && (now.t + 1) * static_cast<int64_t>(kKeys) <= now.L;
+      if (mine) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          meta_k[st][p0 + e] = valid[e] ? now.ks[e] : 0.f;
+          meta_v[st][p0 + e] = valid[e] ? now.vs[e] : -1.f;
+        }
+        if (p0 == 0) meta_full[st] = blocks == kPages && (now.t + 1) * static_cast<int64_t>(kKeys) <= now.L;
+      }
       __syncwarp();
       if (lane == 0) mbar_arrive_expect_tx(&vfull[st], bytes);
       __syncwarp();
-      if (isv && lane < 16 && valid)
-        tma_load_3d(ring + C::kKV + pg * (kPage * D), &vmap, 0, now.hk * kPage, now.blk, &vfull[st]);
-      now = next;
-      next = after;
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+        if (valid[e])
+          tma_load_3d(ring + C::kKV + (p0 + e) * (kPage * D), &vmap, 0, now.hk * kPage, now.blk[e], &vfull[st]);
     }
     if (s_abort && lane == 0) {  // copies in flight land before the shared memory is given back
       for (int i = max(0, issued - NS); i < issued; ++i) {
