@@ -57,6 +57,9 @@ constexpr float kGrow = 8.f;               // ... and m moves before it exceeds 
 constexpr float kUnset = 1e30f;            // -m + 6 of a row without a visible key so far: any key moves it
 constexpr int kMinChunk = 4;               // tiles of the smallest piece: below, joining costs more than it gives
 constexpr int kSmemBudget = 222 * 1024;
+constexpr int kTmaWarps = 2;               // producer warps; each issues half of a tile's copies
+constexpr int kWarpPages = kPages / kTmaWarps;
+constexpr int kBatch = 32 / kWarpPages;    // tiles that a producer warp's lanes hold the blocks of
 
 SSD_DEV void umma_f8(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t accum) {
   asm volatile(
@@ -93,6 +96,14 @@ SSD_DEV void tma_load_3d(void *dst, const CUtensorMap *map, int x, int y, int z,
       "[%5];" ::"r"(smem_u32(dst)),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
       : "memory");
+}
+// One lane of the warp.  What it issues takes its operands from uniform
+// registers; under `if (lane == 0)` each operand is moved there first, and an
+// MMA cost about 100 clocks of the issuing warp.
+SSD_DEV bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
 }
 // 16 columns of this thread's lane, waited for by tmem_wait16
 SSD_DEV void tmem_ld16_async(uint32_t taddr, float *v) {
@@ -246,8 +257,8 @@ template <int D, int RT, int CG>
 struct Cfg {
   static constexpr int kGroups = RT / CG;                  // softmax groups of four warps, CG rows each
   static constexpr int kSoftWarps = 4 * kGroups;
-  static constexpr int kTmaWarp = kSoftWarps, kMmaWarp = kSoftWarps + 1, kPrepWarp = kSoftWarps + 2;
-  static constexpr int kThreads = (kSoftWarps + 4) * 32;
+  static constexpr int kTmaWarp = kSoftWarps, kMmaWarp = kTmaWarp + kTmaWarps, kPrepWarp = kMmaWarp + 1;
+  static constexpr int kThreads = (kPrepWarp + 2) * 32;
   static constexpr int kQTile = RT * 128;                  // q1 (or q2) at D = 128; [q1 | q2] at D = 64
   static constexpr int kQBuf = D == 128 ? 2 * kQTile : kQTile;
   static constexpr int kPBlock = kKeys * 128;              // 128 values of N: a 128-byte row per key
@@ -279,7 +290,7 @@ __global__ void __launch_bounds__(Cfg<D, RT, CG>::kThreads, 1)
   __shared__ __align__(8) uint64_t sfull[2], sfree[2], pfull[2], pvdone[2], qfull[2], qempty[2];
   __shared__ uint32_t tmem_base;
   __shared__ float meta_k[NS][kPages], meta_v[NS][kPages];  // block scales (v: -1 where the block is hidden)
-  __shared__ int meta_full[NS];                             // every key of the tile is a prefix key
+  __shared__ int meta_full[NS][kTmaWarps];                  // every key of these blocks is a prefix key
   __shared__ int par[2][kMaxNodes];
   __shared__ uint32_t anc[2][kMaxNodes][kMaxNodes / 32];    // per query: the nodes that it sees
   __shared__ float qs[2][RT];                               // row scales 2^e
@@ -290,14 +301,15 @@ __global__ void __launch_bounds__(Cfg<D, RT, CG>::kThreads, 1)
   __shared__ Piece s_piece;
   __shared__ volatile int s_abort;
 
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // known to be the same in all lanes
   const float NEG_INF = -__int_as_float(0x7f800000);
 
   if (tid == 0) {
     for (int s = 0; s < NS; ++s) {
-      mbar_init(&kfull[s], 1);
+      mbar_init(&kfull[s], kTmaWarps);
       mbar_init(&kempty[s], 1);
-      mbar_init(&vfull[s], 1);
+      mbar_init(&vfull[s], kTmaWarps);
       mbar_init(&vempty[s], 1);
     }
     for (int u = 0; u < 2; ++u) {
@@ -356,7 +368,7 @@ __global__ void __launch_bounds__(Cfg<D, RT, CG>::kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = tmem_base;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_base, 0);
   const Piece piece = s_piece;
 
   // A segment's rows: q1, q2 and the row scales into buffer `buf`, the
@@ -456,15 +468,17 @@ __global__ void __launch_bounds__(Cfg<D, RT, CG>::kThreads, 1)
   };
 
   Segments sg;
-  if (warp == C::kTmaWarp) {
-    // ---------------- producer.  Block ids and scales are fetched for eight tiles at a time, one batch ahead
-    // (two dependent trips to memory for eight tiles, not for one): lane l holds blocks 2 (l % 4), + 1 of the
-    // batch's tile l / 4, and issues their copies.
+  if (warp >= C::kTmaWarp && warp < C::kMmaWarp) {
+    // ---------------- producers.  A warp issues its lanes' copies one after the other (about 120 clocks each: one
+    // warp for a tile's 16 blocks of 2 KB would allow 16 bytes per clock), so the blocks of a tile are shared out
+    // among the producer warps.  Block ids and scales are fetched for kBatch tiles at a time, one batch ahead (two
+    // dependent trips to memory for a batch, not for a tile): lane l holds block l % kWarpPages of the warp's in
+    // tile l / kWarpPages of the batch.
+    const int page = (warp - C::kTmaWarp) * kWarpPages + lane % kWarpPages;  // of the tile
     struct Batch {
-      int t, L, hk;
+      int t, L, hk, blk;
       bool any;
-      int blk[2];
-      float ks[2], vs[2];
+      float ks, vs;
     };
     bool more = sg.first(a, piece);
     int t = more ? sg.t0 : 0;
@@ -480,59 +494,50 @@ __global__ void __launch_bounds__(Cfg<D, RT, CG>::kThreads, 1)
       x.t = t;
       x.L = sg.L;
       x.hk = more ? sg.item / a.mtiles : 0;
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int lp = t * kPages + (lane & 3) * 2 + e;
-        x.blk[e] = -1;
-        x.ks[e] = x.vs[e] = 0.f;
-        if (more && lp < a.maxb && lp * static_cast<int64_t>(kPage) < sg.nkeys)
-          x.blk[e] = a.table[static_cast<int64_t>(sg.b) * a.maxb + lp];
-        else
-          x.ks[e] = -1.f;  // no block there
+      x.blk = -1;
+      x.vs = 0.f;
+      x.ks = -1.f;  // no block there
+      const int64_t lp = static_cast<int64_t>(t) * kPages + page;
+      if (more && lp < a.maxb && lp * kPage < sg.nkeys) {
+        x.blk = a.table[static_cast<int64_t>(sg.b) * a.maxb + lp];
+        x.ks = 0.f;
       }
     };
     auto scales = [&](Batch &x) {
-#pragma unroll
-      for (int e = 0; e < 2; ++e)
-        if (x.blk[e] >= 0 && x.blk[e] < a.num_blocks) {
-          const int64_t unit = static_cast<int64_t>(x.blk[e]) * a.Hkv + x.hk;
-          x.ks[e] = __ldg(a.ks + unit);
-          x.vs[e] = __ldg(a.vs + unit);
-        } else if (x.ks[e] >= 0.f) {
-          atomicOr(a.status, kFlagBadBlock);
-          x.ks[e] = -1.f;
-        }
+      if (x.blk >= 0 && x.blk < a.num_blocks) {
+        const int64_t unit = static_cast<int64_t>(x.blk) * a.Hkv + x.hk;
+        x.ks = __ldg(a.ks + unit);
+        x.vs = __ldg(a.vs + unit);
+      } else if (x.ks >= 0.f) {
+        atomicOr(a.status, kFlagBadBlock);
+        x.blk = -1;
+      }
     };
     Batch now, next;
-    advance(lane >> 2);
+    advance(lane / kWarpPages);
     ids(now);
     scales(now);
-    advance(8);
+    advance(kBatch);
     ids(next);
     int issued = 0;
     for (int i = 0;; ++i) {
-      const int st = i % NS, w = i & 7;
+      const int st = i % NS, w = i % kBatch;
       if (w == 0 && i > 0) {
         now = next;
-        advance(8);
+        advance(kBatch);
         ids(next);
       }
-      if (w == 4) scales(next);
-      if (!__shfl_sync(0xffffffffu, static_cast<int>(now.any), w * 4)) break;
-      const bool mine = (lane >> 2) == w;
-      bool valid[2];
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        valid[e] = mine && now.blk[e] >= 0 && now.blk[e] < a.num_blocks;
-        if (valid[e] && !(good_scale(now.ks[e]) && good_scale(now.vs[e]))) {
-          atomicOr(a.status, kFlagBadValue);
-          valid[e] = false;
-        }
+      if (w == kBatch / 2) scales(next);
+      if (!__shfl_sync(0xffffffffu, static_cast<int>(now.any), w * kWarpPages)) break;
+      const bool mine = lane / kWarpPages == w;
+      bool valid = mine && now.blk >= 0;
+      if (valid && !(good_scale(now.ks) && good_scale(now.vs))) {
+        atomicOr(a.status, kFlagBadValue);
+        valid = false;
       }
-      const int blocks = __popc(__ballot_sync(0xffffffffu, valid[0])) + __popc(__ballot_sync(0xffffffffu, valid[1]));
+      const int blocks = __popc(__ballot_sync(0xffffffffu, valid));
       const uint32_t bytes = blocks * (kPage * D);
-      uint8_t *const ring = smem + C::kRing + st * 2 * C::kKV;
-      const int p0 = (lane & 3) * 2;
+      uint8_t *const ring = smem + C::kRing + st * 2 * C::kKV + (warp - C::kTmaWarp) * kWarpPages * (kPage * D);
       int ok = 1;
       if (lane == 0) {
         if (s_abort || (i >= NS && !mbar_wait_sleep(&kempty[st], ((i / NS) - 1) & 1))) ok = 0;
@@ -543,34 +548,34 @@ __global__ void __launch_bounds__(Cfg<D, RT, CG>::kThreads, 1)
         s_abort = 1;
         break;
       }
+      const uint32_t which = __ballot_sync(0xffffffffu, valid) >> (w * kWarpPages);
+      auto copy = [&](uint8_t *dst, const CUtensorMap *map, uint64_t *bar) {
 #pragma unroll
-      for (int e = 0; e < 2; ++e)
-        if (valid[e])
-          tma_load_3d(ring + (p0 + e) * (kPage * D), &kmap, 0, now.hk * kPage, now.blk[e], &kfull[st]);
+        for (int e = 0; e < kWarpPages; ++e) {
+          const int src = w * kWarpPages + e;
+          const int blk = __shfl_sync(0xffffffffu, now.blk, src), hk = __shfl_sync(0xffffffffu, now.hk, src);
+          if (((which >> e) & 1u) && elect_one()) tma_load_3d(dst + e * (kPage * D), map, 0, hk * kPage, blk, bar);
+        }
+      };
+      copy(ring, &kmap, &kfull[st]);
       if (lane == 0) ok = i < NS || mbar_wait_sleep(&vempty[st], ((i / NS) - 1) & 1);
       ok = __shfl_sync(0xffffffffu, ok, 0);
       issued = i + 1;
+      if (mine) {
+        meta_k[st][page] = valid ? now.ks : 0.f;
+        meta_v[st][page] = valid ? now.vs : -1.f;
+        if (lane % kWarpPages == 0)
+          meta_full[st][warp - C::kTmaWarp] =
+              blocks == kWarpPages && (now.t + 1) * static_cast<int64_t>(kKeys) <= now.L;
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive_expect_tx(&vfull[st], ok ? bytes : 0);
+      __syncwarp();
       if (!ok) {
-        // the K copies are in flight; V's barrier is completed so that the drain below ends
-        if (lane == 0) mbar_arrive_expect_tx(&vfull[st], 0);
         s_abort = 1;
         break;
       }
-      if (mine) {
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          meta_k[st][p0 + e] = valid[e] ? now.ks[e] : 0.f;
-          meta_v[st][p0 + e] = valid[e] ? now.vs[e] : -1.f;
-        }
-        if (p0 == 0) meta_full[st] = blocks == kPages && (now.t + 1) * static_cast<int64_t>(kKeys) <= now.L;
-      }
-      __syncwarp();
-      if (lane == 0) mbar_arrive_expect_tx(&vfull[st], bytes);
-      __syncwarp();
-#pragma unroll
-      for (int e = 0; e < 2; ++e)
-        if (valid[e])
-          tma_load_3d(ring + C::kKV + (p0 + e) * (kPage * D), &vmap, 0, now.hk * kPage, now.blk[e], &vfull[st]);
+      copy(ring + C::kKV, &vmap, &vfull[st]);
     }
     if (s_abort && lane == 0) {  // copies in flight land before the shared memory is given back
       for (int i = max(0, issued - NS); i < issued; ++i) {
@@ -579,20 +584,21 @@ __global__ void __launch_bounds__(Cfg<D, RT, CG>::kThreads, 1)
       }
     }
   } else if (warp == C::kMmaWarp) {
-    // ---------------- MMA issue (one thread): S(i), then O += P(i - 1) V(i - 1)
-    if (lane == 0) {
-      constexpr uint32_t idesc_s = idesc_f8(RT, 0), idesc_o = idesc_f8(2 * RT, 1);
-      const uint32_t base = smem_u32(smem);
-      bool ok = true;
-      auto issue_pv = [&](int i, bool fresh) {
-        const int st = i % NS;
-        if (!mbar_wait_sleep(&vfull[st], (i / NS) & 1) || !mbar_wait_sleep(&pfull[i & 1], (i >> 1) & 1)) {
-          ok = false;
-          return;
-        }
-        tc_fence_after();
-        const uint32_t v = base + C::kRing + st * 2 * C::kKV + C::kKV;
-        const uint32_t p = base + C::kP + (i % NPB) * C::kPBuf;
+    // ---------------- MMA issue (one elected lane): S(i), then O += P(i - 1) V(i - 1)
+    constexpr uint32_t idesc_s = idesc_f8(RT, 0), idesc_o = idesc_f8(2 * RT, 1);
+    const uint32_t base = smem_u32(smem);
+    bool ok = true;
+    auto wait = [&](uint64_t *bar, uint32_t parity) {
+      ok = __all_sync(0xffffffffu, ok && mbar_wait_sleep(bar, parity));
+      return ok;
+    };
+    auto issue_pv = [&](int i, bool fresh) {
+      const int st = i % NS;
+      if (!wait(&vfull[st], (i / NS) & 1) || !wait(&pfull[i & 1], (i >> 1) & 1)) return;
+      tc_fence_after();
+      const uint32_t v = base + C::kRing + st * 2 * C::kKV + C::kKV;
+      const uint32_t p = base + C::kP + (i % NPB) * C::kPBuf;
+      if (elect_one()) {
 #pragma unroll
         for (int kk = 0; kk < kKeys / 32; ++kk) {
           // 32 keys: four groups of 8 rows
@@ -603,25 +609,24 @@ __global__ void __launch_bounds__(Cfg<D, RT, CG>::kThreads, 1)
         }
         umma_commit(&pvdone[i & 1]);
         umma_commit(&vempty[st]);
-      };
-      int i = 0, seg = 0;
-      bool fresh_prev = false;
-      for (bool more = sg.first(a, piece); more && ok; more = sg.step(a), ++seg) {
-        const int buf = seg & 1;
-        if (!mbar_wait_sleep(&qfull[buf], (seg >> 1) & 1)) ok = false;
-        for (int t = sg.t0; t < sg.t1 && ok; ++t, ++i) {
-          const int st = i % NS;
-          if (s_abort || !mbar_wait_sleep(&kfull[st], (i / NS) & 1)) {
-            ok = false;
-            break;
-          }
-          const uint32_t k = base + C::kRing + st * 2 * C::kKV;
-          if (i >= 2 && !mbar_wait_sleep(&sfree[i & 1], ((i - 2) >> 1) & 1)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          const uint32_t q = base + C::kQ + buf * C::kQBuf;
+      }
+      __syncwarp();
+    };
+    int i = 0, seg = 0;
+    bool fresh_prev = false;
+    for (bool more = sg.first(a, piece); more && ok; more = sg.step(a), ++seg) {
+      const int buf = seg & 1;
+      wait(&qfull[buf], (seg >> 1) & 1);
+      for (int t = sg.t0; t < sg.t1 && ok; ++t, ++i) {
+        const int st = i % NS;
+        if (s_abort || !wait(&kfull[st], (i / NS) & 1) || (i >= 2 && !wait(&sfree[i & 1], ((i - 2) >> 1) & 1))) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t k = base + C::kRing + st * 2 * C::kKV;
+        const uint32_t q = base + C::kQ + buf * C::kQBuf;
+        if (elect_one()) {
 #pragma unroll
           for (int term = 0; term < 2; ++term)
 #pragma unroll
@@ -635,13 +640,14 @@ __global__ void __launch_bounds__(Cfg<D, RT, CG>::kThreads, 1)
           umma_commit(&sfull[i & 1]);
           umma_commit(&kempty[st]);
           if (t == sg.t1 - 1) umma_commit(&qempty[buf]);
-          if (i >= 1) issue_pv(i - 1, fresh_prev);
-          fresh_prev = t == sg.t0;
         }
+        __syncwarp();
+        if (i >= 1) issue_pv(i - 1, fresh_prev);
+        fresh_prev = t == sg.t0;
       }
-      if (ok && i >= 1) issue_pv(i - 1, fresh_prev);
-      if (!ok) s_abort = 1;
     }
+    if (ok && i >= 1) issue_pv(i - 1, fresh_prev);
+    if (!ok) s_abort = 1;
   } else if (warp >= C::kPrepWarp) {
     // ---------------- the rows of the segments after the first
     bool more = sg.first(a, piece);
@@ -700,7 +706,9 @@ __global__ void __launch_bounds__(Cfg<D, RT, CG>::kThreads, 1)
         const float c = meta_k[st][tg / kPage] * a.scale_log2;
         const float lsv = log2f(fmaxf(vsc, kMinBlockScale));
         const float wv = vsc < kMinBlockScale ? 0.f : vsc;
-        const bool full = meta_full[st] != 0;
+        bool full = true;
+#pragma unroll
+        for (int w = 0; w < kTmaWarps; ++w) full = full && meta_full[st][w] != 0;
         // the rows that see this thread's key
         uint32_t vis = ~0u;
         if (!full) {
