@@ -16,22 +16,27 @@
 //     2^-8 p, as a bf16 p would be, or 2^-15 where p2 underflows; p1 and p2
 //     lie side by side in N and fill two accumulators, O = O1 + O2 / 32.
 // A key's thread (its TMEM lane) knows its block's scales: x = s * k_scale *
-// scale * 2^e, P = 2^(x - m + 6), and P * v_scale is what is split into p1 and p2.
-// m is the row's largest x + log2(v_scale) when it was last moved: it moves
-// (and O, l are rescaled) when some P * v_scale exceeds 2^8, two binades above
-// where it started, so p has at least 13 binades above 2^-7, where p2 is cut.
-// l sums the fp32 P, unrounded.
+// scale * 2^e, P = 2^(x - m + 4), and P * v_scale is what is split into p1 and p2.
+// m starts as the largest x + log2(v_scale) of the row's first keys and moves
+// (O and l are rescaled) when some P * v_scale exceeds 2^8, so the row's
+// largest lies in [2^4, 2^8]: p2 underflows 2^-19 of it.  l sums the fp32 P.
 //
 // Work split: the key tiles of all (sequence, KV head, row tile) are one line
 // of units, cut into equal pieces, one per CTA (one CTA per SM), whatever the
 // lengths are; a piece that covers part of an item leaves (O, m, l) in the
 // workspace and k_attn_q8_merge joins them.
 //
-// CTA: up to four groups of four softmax warps, 16 or 32 rows each, a producer
-// warp, an MMA warp, two warps that prepare the next segment's rows (q1, q2,
-// tree masks).  Several softmax warps per scheduler, each with few rows, hide
-// one another's latencies and share their instructions: one group with all 48
-// rows of the verification batch took 0.537 ms.
+// CTA: two producer warps, an MMA warp, one warp that prepares the next
+// segment's rows (q1, q2, tree masks), and 12 or 16 softmax warps.  Up to 64
+// rows, the softmax warps form streams: stream s takes every NSTR-th tile with
+// all rows of it and has m, l, S, P and O of its own, joined when the segment
+// ends, so the warps of a scheduler are at different tiles and hide one
+// another's latencies, and a warp's fixed work per tile is paid once for all
+// rows.  Above 64 rows the registers and TMEM hold one stream, its rows shared
+// out among groups of 32.
+// K and V tiles come in the order in which the MMAs use them (S runs up to NB
+// tiles ahead of P V), through one ring of tile-sized slots, so that every slot that
+// is not being read is a copy in flight.
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <math.h>
@@ -52,11 +57,14 @@ constexpr int kPage = 16;
 constexpr int kMaxNodes = 128;
 constexpr int kKeys = 128;                 // keys per tile (MMA M of S^T, K of O^T)
 constexpr int kPages = kKeys / kPage;      // 8
-constexpr float kBias = 6.f;               // P is at most 2^6 where m was taken ...
-constexpr float kGrow = 8.f;               // ... and m moves before it exceeds 2^8 (e4m3 ends at 448)
-constexpr float kUnset = 1e30f;            // -m + 6 of a row without a visible key so far: any key moves it
+// P v_scale is at most 2^4 where m was taken (the first tile), and m moves
+// before it exceeds 2^8 (e4m3 ends at 448), to where it is 2^5: the first
+// tile's largest of 128 keys is a low guess of the largest of thousands, and
+// moving m costs about a tile's time.
+constexpr float kBias = 4.f, kMoved = 5.f, kGrow = 8.f;
 constexpr int kMinChunk = 4;               // tiles of the smallest piece: below, joining costs more than it gives
-constexpr int kSmemBudget = 222 * 1024;
+constexpr int kSmemBudget = 212 * 1024;
+constexpr int kMeta = 16;                  // tiles whose block scales are held
 constexpr int kTmaWarps = 2;               // producer warps; each issues half of a tile's copies
 constexpr int kWarpPages = kPages / kTmaWarps;
 constexpr int kBatch = 32 / kWarpPages;    // tiles that a producer warp's lanes hold the blocks of
@@ -104,6 +112,30 @@ SSD_DEV bool elect_one() {
   uint32_t p;
   asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
   return p != 0;
+}
+// Bounded wait of a whole warp for one phase.  All lanes wait: the warp is then
+// suspended until the phase completes (one poll, about 95 clocks from arrival
+// to wake-up); a wait by one lane in divergent code polls every 150 clocks,
+// wakes in 220 and, with a CTA of such warps, keeps the barrier unit busy.
+// Gives up after 2^20 polls of at most a few microseconds each; a role whose
+// wait gives up leaves, and with it, one bounded wait later, all others.
+SSD_DEV bool warp_wait(uint64_t *bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t.reg .u32 n;\n\t"
+      "mov.u32 n, 1048576;\n"
+      "POLL:\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "@p bra.uni DONE;\n\t"
+      "sub.u32 n, n, 1;\n\t"
+      "setp.ne.u32 q, n, 0;\n\t"
+      "@q bra.uni POLL;\n"
+      "DONE:\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return __any_sync(0xffffffffu, ok != 0);
 }
 // 16 columns of this thread's lane, waited for by tmem_wait16
 SSD_DEV void tmem_ld16_async(uint32_t taddr, float *v) {
@@ -214,6 +246,7 @@ struct Piece {
   int64_t off;      // units of that sequence before it
   int64_t left;     // units of the piece
   int64_t chunk;    // units of a full piece
+  int tiles;        // tiles that the CTA runs
 };
 
 // The segments of a piece: one item (or part of it) after the other.
@@ -253,51 +286,85 @@ struct Segments {
   }
 };
 
-template <int D, int RT, int CG>
+// The order of the MMAs, which is the order of the loads: S runs ahead of P V by
+// up to NB tiles, but not past the next segment (a third one's rows have no
+// buffer before the first one's are done).
+struct Order {
+  int begin, end, hold;  // of the segment that P V is in; the first tile that S may not reach
+  int n;
+  Segments sg;
+  bool more;
+  SSD_DEV void start(const Args &a, const Piece &p) {
+    n = p.tiles;
+    begin = 0;
+    more = sg.first(a, p);
+    end = more ? sg.t1 - sg.t0 : 0;
+    more = more && sg.step(a);
+    hold = more ? end + sg.t1 - sg.t0 : n;
+  }
+  SSD_DEV void done(const Args &a, int j) {  // P V has done j tiles
+    if (j < end || j >= n) return;
+    begin = end;
+    end = hold;
+    more = more && sg.step(a);
+    hold = more ? end + sg.t1 - sg.t0 : n;
+  }
+};
+
+template <int D, int RT>
 struct Cfg {
-  static constexpr int kGroups = RT / CG;                  // softmax groups of four warps, CG rows each
-  static constexpr int kSoftWarps = 4 * kGroups;
+  static constexpr int NSTR = RT <= 16 ? 3 : (RT <= 32 ? 2 : 1);  // streams
+  static constexpr int CG = RT <= 64 ? 16 : 32;            // rows of a softmax warp
+  static constexpr int kGroups = RT / CG;                  // groups of four warps in a stream
+  static constexpr int NB = NSTR > 1 ? NSTR : 2;           // S and P buffers; S runs NB tiles ahead
+  static constexpr int kSoftWarps = 4 * kGroups * NSTR;
   static constexpr int kTmaWarp = kSoftWarps, kMmaWarp = kTmaWarp + kTmaWarps, kPrepWarp = kMmaWarp + 1;
-  static constexpr int kThreads = (kPrepWarp + 2) * 32;
+  static constexpr int kWarps = kPrepWarp + 1;
+  static constexpr int kThreads = kWarps * 32;
+  static_assert(kWarps == 16 || kWarps == 20, "warps");    // 128 or 96 registers a thread
   static constexpr int kQTile = RT * 128;                  // q1 (or q2) at D = 128; [q1 | q2] at D = 64
   static constexpr int kQBuf = D == 128 ? 2 * kQTile : kQTile;
   static constexpr int kPBlock = kKeys * 128;              // 128 values of N: a 128-byte row per key
   static constexpr int kPBuf = RT > 64 ? 2 * kPBlock : kPBlock;  // p1 [RT] then p2 [RT] along N
-  static constexpr int kNPB = RT > 64 ? 1 : 2;             // P buffers
-  static constexpr int kKV = kKeys * D;                    // K or V of a tile
-  static constexpr int kFixed = 2 * kQBuf + kNPB * kPBuf;
-  static constexpr int kFit = (kSmemBudget - kFixed) / (2 * kKV);
-  static constexpr int kStages = kFit > 8 ? 8 : kFit;
-  static_assert(kStages >= 2, "two stages at least");
+  static constexpr int kSlot = kKeys * D;                  // K or V of a tile
+  static constexpr int kFixed = 2 * kQBuf + NB * kPBuf;
+  static constexpr int kFit = (kSmemBudget - kFixed) / kSlot;
+  static constexpr int kSlots = kFit > 16 ? 16 : kFit;
   static constexpr int kQ = 0, kP = 2 * kQBuf, kRing = kFixed;
-  static constexpr int kSmem = kFixed + kStages * 2 * kKV + 1024;
-  static constexpr uint32_t kCols = 4 * RT;                // S (2 x RT), then O1, O2
+  static constexpr int kSmem = kFixed + kSlots * kSlot + 1024;
+  static constexpr int kOCol = NB * RT;                    // TMEM: NB x S, then O1, O2 of each stream
+  static constexpr uint32_t kCols = kOCol + NSTR * 2 * RT;
   static constexpr uint32_t kTmem = kCols <= 64 ? 64 : (kCols <= 128 ? 128 : (kCols <= 256 ? 256 : 512));
-  static_assert(kSmem + (RT <= 64 ? 9728 : 12800) <= 227 * 1024, "shared memory with the static part");
-  static_assert(kCols <= 512 && RT % CG == 0 && CG % 16 == 0 && CG <= 32 && kGroups <= 4, "rows");
+  static_assert(kSmem + 13824 <= 227 * 1024, "shared memory with the static part");
+  static_assert(kSlots >= NB + 2, "S runs NB tiles ahead");
+  // the scales of tile i + kMeta are written when a slot used up to tile i + kMeta - NB - (kSlots + 1) / 2 is free
+  static_assert(kMeta >= NB + (kSlots + 1) / 2 + 1, "block scales");
+  static_assert(kCols <= 512 && RT % CG == 0 && CG % 16 == 0 && NSTR * kGroups <= 4, "rows");
 };
 
-template <int D, int RT, int CG>
-__global__ void __launch_bounds__(Cfg<D, RT, CG>::kThreads, 1)
+template <int D, int RT>
+__global__ void __launch_bounds__(Cfg<D, RT>::kThreads, 1)
     k_branch_attn_q8(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                      const __grid_constant__ Args a) {
-  using C = Cfg<D, RT, CG>;
-  constexpr int NS = C::kStages, NPB = C::kNPB, G = C::kGroups;
+  using C = Cfg<D, RT>;
+  constexpr int NSTR = C::NSTR, CG = C::CG, NB = C::NB, NSLOT = C::kSlots;
+  constexpr int kSoftThreads = C::kSoftWarps * 32;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t *const smem =
       reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  __shared__ __align__(8) uint64_t kfull[NS], kempty[NS], vfull[NS], vempty[NS];
-  __shared__ __align__(8) uint64_t sfull[2], sfree[2], pfull[2], pvdone[2], qfull[2], qempty[2];
+  __shared__ __align__(8) uint64_t full[NSLOT], empty[NSLOT];
+  __shared__ __align__(8) uint64_t sfull[NB], pfull[NB], pvdone[NB], qfull[2], qempty[2];
   __shared__ uint32_t tmem_base;
-  __shared__ float meta_k[NS][kPages], meta_v[NS][kPages];  // block scales (v: -1 where the block is hidden)
-  __shared__ int meta_full[NS][kTmaWarps];                  // every key of these blocks is a prefix key
+  // a block's k_scale * scale * log2 e, v_scale (-1: hidden), log2 v_scale
+  __shared__ __align__(16) float4 meta[kMeta][kPages];
   __shared__ int par[2][kMaxNodes];
   __shared__ uint32_t anc[2][kMaxNodes][kMaxNodes / 32];    // per query: the nodes that it sees
   __shared__ float qs[2][RT];                               // row scales 2^e
-  __shared__ __align__(16) float4 rowc[RT / 2];             // two rows: 2^e, 2^e, 6 - m, 6 - m
-  __shared__ float s_m[RT], s_f[RT], red[4][RT];
-  __shared__ int s_nan[4];                                  // a tree node's v held NaN, by segment mod 4
-  __shared__ long long scan[32][2];
+  __shared__ __align__(16) float4 rowc[NSTR][RT / 2];       // two rows: 2^e, 2^e, 4 - m, 4 - m
+  __shared__ float s_m[NSTR][RT], s_f[NSTR][RT], red[NSTR][4][RT];
+  __shared__ int s_over[NSTR][RT];                          // largest P v_scale above 2^8 (its log2's bits), or 0
+  __shared__ int s_nan[2];                                  // a tree node's v held NaN, by segment mod 2
+  __shared__ long long scan[32];
   __shared__ Piece s_piece;
   __shared__ volatile int s_abort;
 
@@ -306,25 +373,26 @@ __global__ void __launch_bounds__(Cfg<D, RT, CG>::kThreads, 1)
   const float NEG_INF = -__int_as_float(0x7f800000);
 
   if (tid == 0) {
-    for (int s = 0; s < NS; ++s) {
-      mbar_init(&kfull[s], kTmaWarps);
-      mbar_init(&kempty[s], 1);
-      mbar_init(&vfull[s], kTmaWarps);
-      mbar_init(&vempty[s], 1);
+    for (int s = 0; s < NSLOT; ++s) {
+      mbar_init(&full[s], kTmaWarps);
+      mbar_init(&empty[s], 1);
+    }
+    for (int u = 0; u < NB; ++u) {
+      mbar_init(&sfull[u], 1);
+      mbar_init(&pfull[u], 4 * C::kGroups);
+      mbar_init(&pvdone[u], 1);
     }
     for (int u = 0; u < 2; ++u) {
-      mbar_init(&sfull[u], 1);
-      mbar_init(&sfree[u], 4 * G);
-      mbar_init(&pfull[u], 4 * G);
-      mbar_init(&pvdone[u], 1);
-      mbar_init(&qfull[u], 2);
-      mbar_init(&qempty[u], 1 + 4 * G);
+      mbar_init(&qfull[u], 1);
+      mbar_init(&qempty[u], 1 + C::kSoftWarps);
     }
     fence_mbar_init();
     s_abort = 0;
-    s_nan[0] = s_nan[1] = s_nan[2] = s_nan[3] = 0;
+    s_nan[0] = s_nan[1] = 0;
     s_piece.left = 0;
+    s_piece.tiles = 0;
   }
+  for (int r = tid; r < NSTR * RT; r += C::kThreads) (&s_over[0][0])[r] = 0;
   if (warp == C::kMmaWarp) {
     tmem_alloc(&tmem_base, C::kTmem);
     tmem_relinquish();
@@ -340,12 +408,12 @@ __global__ void __launch_bounds__(Cfg<D, RT, CG>::kThreads, 1)
       const long long x = __shfl_up_sync(0xffffffffu, inc, o);
       if (lane >= o) inc += x;
     }
-    if (lane == 31) scan[warp][0] = inc;
+    if (lane == 31) scan[warp] = inc;
     __syncthreads();
     long long before = 0, total = 0;
     for (int w = 0; w < C::kThreads / 32; ++w) {
-      if (w < warp) before += scan[w][0];
-      total += scan[w][0];
+      if (w < warp) before += scan[w];
+      total += scan[w];
     }
     const long long T = total * a.per_b;
     long long chunk = (T + gridDim.x - 1) / gridDim.x;
@@ -359,10 +427,15 @@ __global__ void __launch_bounds__(Cfg<D, RT, CG>::kThreads, 1)
         if (lo < x + n) break;
         x += n;
       }
-      s_piece.b = b;
-      s_piece.off = lo - x;
-      s_piece.left = hi - lo;
-      s_piece.chunk = chunk;
+      Piece p;
+      p.b = b;
+      p.off = lo - x;
+      p.left = hi - lo;
+      p.chunk = chunk;
+      p.tiles = 0;
+      Segments sg;
+      for (bool more = sg.first(a, p); more; more = sg.step(a)) p.tiles += sg.t1 - sg.t0;
+      s_piece = p;
     }
   }
   tc_fence_before();
@@ -370,6 +443,7 @@ __global__ void __launch_bounds__(Cfg<D, RT, CG>::kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_base, 0);
   const Piece piece = s_piece;
+  const int ntiles = piece.tiles;
 
   // A segment's rows: q1, q2 and the row scales into buffer `buf`, the
   // queries' tree masks; warp w of the n that share it (barrier `bar`).
@@ -469,15 +543,12 @@ __global__ void __launch_bounds__(Cfg<D, RT, CG>::kThreads, 1)
 
   Segments sg;
   if (warp >= C::kTmaWarp && warp < C::kMmaWarp) {
-    // ---------------- producers.  A warp issues its lanes' copies one after the other (about 120 clocks each: one
-    // warp for a tile's 16 blocks of 2 KB would allow 16 bytes per clock), so the blocks of a tile are shared out
-    // among the producer warps.  Block ids and scales are fetched for kBatch tiles at a time, one batch ahead (two
-    // dependent trips to memory for a batch, not for a tile): lane l holds block l % kWarpPages of the warp's in
-    // tile l / kWarpPages of the batch.
-    const int page = (warp - C::kTmaWarp) * kWarpPages + lane % kWarpPages;  // of the tile
+    // ---------------- producers: each copies half of every tile's blocks.  Block ids and scales are fetched for
+    // kBatch tiles at a time, one batch ahead (two dependent trips to memory for a batch, not for a tile): lane l
+    // holds block l % kWarpPages of the warp's in tile l / kWarpPages of the batch.
+    const int page0 = (warp - C::kTmaWarp) * kWarpPages, page = page0 + lane % kWarpPages;  // of the tile
     struct Batch {
-      int t, L, hk, blk;
-      bool any;
+      int hk, blk;
       float ks, vs;
     };
     bool more = sg.first(a, piece);
@@ -490,9 +561,6 @@ __global__ void __launch_bounds__(Cfg<D, RT, CG>::kThreads, 1)
       }
     };
     auto ids = [&](Batch &x) {
-      x.any = more;
-      x.t = t;
-      x.L = sg.L;
       x.hk = more ? sg.item / a.mtiles : 0;
       x.blk = -1;
       x.vs = 0.f;
@@ -513,119 +581,106 @@ __global__ void __launch_bounds__(Cfg<D, RT, CG>::kThreads, 1)
         x.blk = -1;
       }
     };
-    Batch now, next;
+    auto check = [&](Batch &x) {  // bad scales hide their block
+      if (x.blk >= 0 && !(good_scale(x.ks) && good_scale(x.vs))) {
+        atomicOr(a.status, kFlagBadValue);
+        x.blk = -1;
+      }
+    };
+    Batch old, now, next;
     advance(lane / kWarpPages);
     ids(now);
     scales(now);
+    check(now);
     advance(kBatch);
     ids(next);
+    old = now;
+    int slot = 0;
+    uint32_t phase = 1;  // of empty[slot]; the first round's slots are free
     int issued = 0;
-    for (int i = 0;; ++i) {
-      const int st = i % NS, w = i % kBatch;
-      if (w == 0 && i > 0) {
-        now = next;
-        advance(kBatch);
-        ids(next);
-      }
-      if (w == kBatch / 2) scales(next);
-      if (!__shfl_sync(0xffffffffu, static_cast<int>(now.any), w * kWarpPages)) break;
-      const bool mine = lane / kWarpPages == w;
-      bool valid = mine && now.blk >= 0;
-      if (valid && !(good_scale(now.ks) && good_scale(now.vs))) {
-        atomicOr(a.status, kFlagBadValue);
-        valid = false;
-      }
-      const int blocks = __popc(__ballot_sync(0xffffffffu, valid));
-      const uint32_t bytes = blocks * (kPage * D);
-      uint8_t *const ring = smem + C::kRing + st * 2 * C::kKV + (warp - C::kTmaWarp) * kWarpPages * (kPage * D);
-      int ok = 1;
-      if (lane == 0) {
-        if (s_abort || (i >= NS && !mbar_wait_sleep(&kempty[st], ((i / NS) - 1) & 1))) ok = 0;
-        else mbar_arrive_expect_tx(&kfull[st], bytes);
-      }
-      ok = __shfl_sync(0xffffffffu, ok, 0);
-      if (!ok) {
-        s_abort = 1;
-        break;
-      }
-      const uint32_t which = __ballot_sync(0xffffffffu, valid) >> (w * kWarpPages);
-      auto copy = [&](uint8_t *dst, const CUtensorMap *map, uint64_t *bar) {
+    bool ok = true;
+    // one load: this warp's blocks of a tile into the next slot
+    auto load = [&](const Batch &x, int w, const CUtensorMap *map) {
+      const uint32_t which = __ballot_sync(0xffffffffu, x.blk >= 0) >> (w * kWarpPages) & ((1u << kWarpPages) - 1);
+      const int row = __shfl_sync(0xffffffffu, x.hk, w * kWarpPages) * kPage;
+      int blk[kWarpPages];
 #pragma unroll
-        for (int e = 0; e < kWarpPages; ++e) {
-          const int src = w * kWarpPages + e;
-          const int blk = __shfl_sync(0xffffffffu, now.blk, src), hk = __shfl_sync(0xffffffffu, now.hk, src);
-          if (((which >> e) & 1u) && elect_one()) tma_load_3d(dst + e * (kPage * D), map, 0, hk * kPage, blk, bar);
+      for (int e = 0; e < kWarpPages; ++e) blk[e] = __shfl_sync(0xffffffffu, x.blk, w * kWarpPages + e);
+      ok = issued < NSLOT || warp_wait(&empty[slot], phase);
+      if (!ok) return;
+      uint8_t *const dst = smem + C::kRing + slot * C::kSlot + page0 * (kPage * D);
+      if (elect_one()) {
+        mbar_arrive_expect_tx(&full[slot], __popc(which) * (kPage * D));
+#pragma unroll
+        for (int e = 0; e < kWarpPages; ++e)
+          if ((which >> e) & 1u) tma_load_3d(dst + e * (kPage * D), map, 0, row, blk[e], &full[slot]);
+      }
+      __syncwarp();
+      ++issued;
+      if (++slot == NSLOT) {
+        slot = 0;
+        phase ^= 1;
+      }
+    };
+    Order order;
+    order.start(a, piece);
+    for (int i = 0, j = 0; j < ntiles && ok;) {
+      if (i < ntiles && i - j < NB && i < order.hold) {  // K of tile i
+        const int w = i % kBatch;
+        if (w == 0 && i > 0) {
+          old = now;
+          now = next;
+          check(now);
+          advance(kBatch);
+          ids(next);
         }
-      };
-      copy(ring, &kmap, &kfull[st]);
-      if (lane == 0) ok = i < NS || mbar_wait_sleep(&vempty[st], ((i / NS) - 1) & 1);
-      ok = __shfl_sync(0xffffffffu, ok, 0);
-      issued = i + 1;
-      if (mine) {
-        meta_k[st][page] = valid ? now.ks : 0.f;
-        meta_v[st][page] = valid ? now.vs : -1.f;
-        if (lane % kWarpPages == 0)
-          meta_full[st][warp - C::kTmaWarp] =
-              blocks == kWarpPages && (now.t + 1) * static_cast<int64_t>(kKeys) <= now.L;
+        if (w == kBatch / 2) scales(next);
+        if (lane / kWarpPages == w) {
+          const float v = now.vs < kMinBlockScale ? 0.f : now.vs;
+          meta[i % kMeta][page] = now.blk >= 0
+                                      ? make_float4(now.ks * a.scale_log2, v, log2f(fmaxf(v, kMinBlockScale)), 0.f)
+                                      : make_float4(0.f, -1.f, 0.f, 0.f);
+        }
+        load(now, w, &kmap);
+        ++i;
+      } else {  // V of tile j
+        load(j / kBatch == (i - 1) / kBatch ? now : old, j % kBatch, &vmap);
+        order.done(a, ++j);
       }
-      __syncwarp();
-      if (lane == 0) mbar_arrive_expect_tx(&vfull[st], ok ? bytes : 0);
-      __syncwarp();
-      if (!ok) {
-        s_abort = 1;
-        break;
-      }
-      copy(ring + C::kKV, &vmap, &vfull[st]);
     }
-    if (s_abort && lane == 0) {  // copies in flight land before the shared memory is given back
-      for (int i = max(0, issued - NS); i < issued; ++i) {
-        (void)mbar_wait(&kfull[i % NS], (i / NS) & 1);
-        (void)mbar_wait(&vfull[i % NS], (i / NS) & 1);
-      }
+    if (!ok) {
+      s_abort = 1;
+      if (lane == 0)  // copies in flight land before the shared memory is given back
+        for (int i = max(0, issued - NSLOT); i < issued; ++i) (void)mbar_wait(&full[i % NSLOT], (i / NSLOT) & 1);
     }
   } else if (warp == C::kMmaWarp) {
-    // ---------------- MMA issue (one elected lane): S(i), then O += P(i - 1) V(i - 1)
+    // ---------------- MMA issue (one elected lane): O += P(i - NB) V(i - NB), then S(i)
     constexpr uint32_t idesc_s = idesc_f8(RT, 0), idesc_o = idesc_f8(2 * RT, 1);
     const uint32_t base = smem_u32(smem);
     bool ok = true;
-    auto wait = [&](uint64_t *bar, uint32_t parity) {
-      ok = __all_sync(0xffffffffu, ok && mbar_wait_sleep(bar, parity));
-      return ok;
-    };
-    auto issue_pv = [&](int i, bool fresh) {
-      const int st = i % NS;
-      if (!wait(&vfull[st], (i / NS) & 1) || !wait(&pfull[i & 1], (i >> 1) & 1)) return;
-      tc_fence_after();
-      const uint32_t v = base + C::kRing + st * 2 * C::kKV + C::kKV;
-      const uint32_t p = base + C::kP + (i % NPB) * C::kPBuf;
-      if (elect_one()) {
-#pragma unroll
-        for (int kk = 0; kk < kKeys / 32; ++kk) {
-          // 32 keys: four groups of 8 rows
-          const uint64_t vd = D == 128 ? smem_desc(v + kk * 4096, 16, 1024, kSw128)
-                                       : smem_desc(v + kk * 2048, 0, 512, kSw64);
-          umma_f8(tmem + 2 * RT, vd, smem_desc(p + kk * 4096, C::kPBlock, 1024, kSw128), idesc_o,
-                  (!fresh || kk > 0) ? 1u : 0u);
-        }
-        umma_commit(&pvdone[i & 1]);
-        umma_commit(&vempty[st]);
+    int slot = 0, seg = 0;
+    uint32_t phase = 0;  // of full[slot]
+    bool more = sg.first(a, piece);
+    int t = more ? sg.t0 : 0;
+    auto next_slot = [&] {
+      if (++slot == NSLOT) {
+        slot = 0;
+        phase ^= 1;
       }
-      __syncwarp();
     };
-    int i = 0, seg = 0;
-    bool fresh_prev = false;
-    for (bool more = sg.first(a, piece); more && ok; more = sg.step(a), ++seg) {
-      const int buf = seg & 1;
-      wait(&qfull[buf], (seg >> 1) & 1);
-      for (int t = sg.t0; t < sg.t1 && ok; ++t, ++i) {
-        const int st = i % NS;
-        if (s_abort || !wait(&kfull[st], (i / NS) & 1) || (i >= 2 && !wait(&sfree[i & 1], ((i - 2) >> 1) & 1))) {
-          ok = false;
-          break;
-        }
+    Order order;
+    order.start(a, piece);
+    for (int i = 0, j = 0; j < ntiles;) {
+      if (i < ntiles && i - j < NB && i < order.hold) {  // S of tile i
+        const int buf = seg & 1, u = i % NB;
+        if (t == sg.t0) ok = warp_wait(&qfull[buf], (seg >> 1) & 1);
+        // the S buffer is free: P of tile i - NB, made from it, has been waited for
+        ok = ok && warp_wait(&full[slot], phase);
+        if (!ok) break;
         tc_fence_after();
-        const uint32_t k = base + C::kRing + st * 2 * C::kKV;
+        const uint32_t k = base + C::kRing + slot * C::kSlot;
         const uint32_t q = base + C::kQ + buf * C::kQBuf;
+        const bool last = t == sg.t1 - 1;
         if (elect_one()) {
 #pragma unroll
           for (int term = 0; term < 2; ++term)
@@ -634,98 +689,120 @@ __global__ void __launch_bounds__(Cfg<D, RT, CG>::kThreads, 1)
               const uint64_t kd = D == 128 ? smem_desc(k + kk * 32, 16, 1024, kSw128)
                                            : smem_desc(k + kk * 32, 16, 512, kSw64);
               const uint32_t qa = q + (D == 128 ? term * C::kQTile : term * 64) + kk * 32;
-              umma_f8(tmem + (i & 1) * RT, kd, smem_desc(qa, 16, 1024, kSw128), idesc_s,
-                      (term > 0 || kk > 0) ? 1u : 0u);
+              umma_f8(tmem + u * RT, kd, smem_desc(qa, 16, 1024, kSw128), idesc_s, (term > 0 || kk > 0) ? 1u : 0u);
             }
-          umma_commit(&sfull[i & 1]);
-          umma_commit(&kempty[st]);
-          if (t == sg.t1 - 1) umma_commit(&qempty[buf]);
+          umma_commit(&sfull[u]);
+          umma_commit(&empty[slot]);
+          if (last) umma_commit(&qempty[buf]);
         }
         __syncwarp();
-        if (i >= 1) issue_pv(i - 1, fresh_prev);
-        fresh_prev = t == sg.t0;
+        next_slot();
+        ++i;
+        if (++t == sg.t1) {
+          more = sg.step(a);
+          t = sg.t0;
+          ++seg;
+        }
+      } else {  // P V of tile j
+        const int u = j % NB;
+        ok = warp_wait(&full[slot], phase) && warp_wait(&pfull[u], (j / NB) & 1);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t v = base + C::kRing + slot * C::kSlot;
+        const uint32_t p = base + C::kP + u * C::kPBuf;
+        const uint32_t o = tmem + C::kOCol + (j % NSTR) * (2 * RT);
+        const bool fresh = j - order.begin < NSTR;  // the stream's first tile of the segment
+        if (elect_one()) {
+#pragma unroll
+          for (int kk = 0; kk < kKeys / 32; ++kk) {
+            // 32 keys: four groups of 8 rows
+            const uint64_t vd = D == 128 ? smem_desc(v + kk * 4096, 16, 1024, kSw128)
+                                         : smem_desc(v + kk * 2048, 0, 512, kSw64);
+            umma_f8(o, vd, smem_desc(p + kk * 4096, C::kPBlock, 1024, kSw128), idesc_o, (!fresh || kk > 0) ? 1u : 0u);
+          }
+          umma_commit(&pvdone[u]);
+          umma_commit(&empty[slot]);
+        }
+        __syncwarp();
+        next_slot();
+        order.done(a, ++j);
       }
     }
-    if (ok && i >= 1) issue_pv(i - 1, fresh_prev);
     if (!ok) s_abort = 1;
-  } else if (warp >= C::kPrepWarp) {
+  } else if (warp == C::kPrepWarp) {
     // ---------------- the rows of the segments after the first
     bool more = sg.first(a, piece);
     if (more) {
-      prepare(sg, 0, C::kSoftWarps + warp - C::kPrepWarp, C::kSoftWarps + 2, 6);
-      bar_sync(6, (C::kSoftWarps + 2) * 32);
+      prepare(sg, 0, C::kSoftWarps, C::kSoftWarps + 1, 6);
+      bar_sync(6, (C::kSoftWarps + 1) * 32);
       if (lane == 0) mbar_arrive1(&qfull[0]);
       more = sg.step(a);
     }
     for (int seg = 1; more; more = sg.step(a), ++seg) {
       const int buf = seg & 1;
-      const bool ok = seg < 2 || mbar_wait_sleep(&qempty[buf], ((seg >> 1) - 1) & 1);
-      if (bar_or(7, 64, !ok || s_abort)) {
+      const bool ok = seg < 2 || warp_wait(&qempty[buf], ((seg >> 1) - 1) & 1);
+      if (!ok || __any_sync(0xffffffffu, s_abort != 0)) {
         s_abort = 1;
         break;
       }
-      prepare(sg, buf, warp - C::kPrepWarp, 2, 7);
+      prepare(sg, buf, 0, 1, 7);
       if (lane == 0) mbar_arrive1(&qfull[buf]);
     }
   } else {
-    // ---------------- softmax: group g of four warps and CG rows, one thread per key
-    const int g = warp / 4, wg = warp & 3, tg = tid & 127, col = g * CG;
+    // ---------------- softmax: stream s, group g of its rows, one thread per key
+    const int sgrp = warp / 4, s = sgrp / C::kGroups, g = sgrp % C::kGroups, wg = warp & 3, tg = tid & 127;
+    const int col = g * CG;
     const uint32_t lane_off = static_cast<uint32_t>(wg * 32) << 16;
-    const uint32_t tS = tmem + col + lane_off, tO1 = tmem + 2 * RT + col + lane_off, tO2 = tO1 + RT;
-    const int bar = 1 + g;
-    int i = 0, seg = 0;
+    const uint32_t tS = tmem + col + lane_off, tO = tmem + C::kOCol + s * (2 * RT) + col + lane_off;
+    const int bar = 1 + sgrp;
+    int i0 = 0, seg = 0;  // the segment's first tile in the CTA's count
+    uint32_t sphase = 0;  // parities of sfull
     bool dead = false;
     bool more = sg.first(a, piece);
     if (more) {
-      prepare(sg, 0, warp, C::kSoftWarps + 2, 6);
-      bar_sync(6, (C::kSoftWarps + 2) * 32);
+      prepare(sg, 0, warp, C::kSoftWarps + 1, 6);
+      bar_sync(6, (C::kSoftWarps + 1) * 32);
     }
-    for (; more && !dead; more = sg.step(a), ++seg) {
-      const int buf = seg & 1;
+    for (; more; more = sg.step(a), ++seg) {
+      const int buf = seg & 1, n = sg.t1 - sg.t0;
       const int hk = sg.item / a.mtiles, mt = sg.item % a.mtiles;
-      const int row0 = mt * RT + col;  // the group's first row of (b, hk)
-      bool ok = __all_sync(0xffffffffu, mbar_wait_sleep(&qfull[buf], (seg >> 1) & 1));
+      const int row0 = mt * RT + col;  // the warp's first row of (b, hk)
+      bool ok = warp_wait(&qfull[buf], (seg >> 1) & 1);
       if (tg < CG) {
-        s_m[col + tg] = NEG_INF;
-        float *const rc = reinterpret_cast<float *>(&rowc[(col + tg) >> 1]) + (tg & 1);
+        s_m[s][col + tg] = NEG_INF;
+        float *const rc = reinterpret_cast<float *>(&rowc[s][(col + tg) >> 1]) + (tg & 1);
         rc[0] = qs[buf][col + tg];
         rc[2] = 0.f;
       }
-      if (g == 0 && tg == 0) s_nan[(seg + 2) & 3] = 0;
       bar_sync(bar, 128);
       uint64_t l2[CG / 2];
 #pragma unroll
       for (int j = 0; j < CG / 2; ++j) l2[j] = 0;
-      for (int t = sg.t0; t < sg.t1; ++t, ++i) {
-        const int st = i % NS, u = i & 1;
-        const bool begin = t == sg.t0;
-        ok = __all_sync(0xffffffffu, ok && !s_abort && mbar_wait_sleep(&vfull[st], (i / NS) & 1) &&
-                                         mbar_wait_sleep(&sfull[u], (i >> 1) & 1));
+      bool begin = true, unset = true;  // before the stream's first tile; a row without a visible key so far
+      for (int x = (s + NSTR - i0 % NSTR) % NSTR; x < n; x += NSTR) {
+        const int i = i0 + x, t = sg.t0 + x;
+        const int u = NSTR > 1 ? s : i % NB;  // S and P buffer
+        ok = ok && warp_wait(&sfull[u], sphase >> u & 1);
+        sphase ^= 1u << u;  // the scales were there before K was
         tc_fence_after();
-        const float vsc = meta_v[st][tg / kPage];
-        const float c = meta_k[st][tg / kPage] * a.scale_log2;
-        const float lsv = log2f(fmaxf(vsc, kMinBlockScale));
-        const float wv = vsc < kMinBlockScale ? 0.f : vsc;
-        bool full = true;
-#pragma unroll
-        for (int w = 0; w < kTmaWarps; ++w) full = full && meta_full[st][w] != 0;
+        const float4 sc = meta[i % kMeta][tg / kPage];
+        const float c = sc.x, wv = fmaxf(sc.y, 0.f), lsv = sc.z;
         // the rows that see this thread's key
-        uint32_t vis = ~0u;
-        if (!full) {
-          const int pos = t * kKeys + tg;
-          if (vsc < 0.f || pos >= sg.nkeys) vis = 0;
-          else if (pos >= sg.L) {
-            const int n = pos - sg.L;
-            vis = 0;
-            for (int j = 0; j < CG; ++j) {
-              const int qi = min(static_cast<int>(((row0 + j) * a.group_magic) >> 16), kMaxNodes - 1);
-              vis |= ((anc[buf][qi][n >> 5] >> (n & 31)) & 1u) << j;
-            }
+        const int pos = t * kKeys + tg;
+        const bool hidden = sc.y < 0.f || pos >= sg.nkeys;
+        const bool part = __any_sync(0xffffffffu, hidden || pos >= sg.L);
+        uint64_t vis = hidden ? 0ull : ~0ull;
+        if (part && !hidden && pos >= sg.L) {
+          const int node = pos - sg.L;
+          vis = 0;
+          for (int j = 0; j < CG; ++j) {
+            const int qi = min(static_cast<int>(((row0 + j) * a.group_magic) >> 16), kMaxNodes - 1);
+            vis |= static_cast<uint64_t>((anc[buf][qi][node >> 5] >> (node & 31)) & 1u) << j;
           }
         }
         const uint64_t c2 = pack2(c, c);
         float y[CG];
-        // y = x - m + 6 (or x where rowc holds 0); hidden keys -inf
+        // y = x - m + 4 (x for a row without m); hidden keys -inf
         auto scores = [&]() {
 #pragma unroll
           for (int j = 0; j < CG; j += 16) tmem_ld16_async(tS + u * RT + j, y + j);
@@ -733,78 +810,99 @@ __global__ void __launch_bounds__(Cfg<D, RT, CG>::kThreads, 1)
           for (int j = 0; j < CG; j += 16) tmem_wait16(y + j);
 #pragma unroll
           for (int j = 0; j < CG; j += 2) {
-            const float4 rc = rowc[(col + j) / 2];
+            const float4 rc = rowc[s][(col + j) / 2];
             unpack2(fma2(mul2(pack2(y[j], y[j + 1]), c2), pack2(rc.x, rc.y), pack2(rc.z, rc.w)), y[j], y[j + 1]);
           }
-          if (!full) {
+          if (part) {
 #pragma unroll
-            for (int j = 0; j < CG; ++j) y[j] = ((vis >> j) & 1u) ? y[j] : NEG_INF;
+            for (int j = 0; j < CG; ++j) y[j] = ((vis >> j) & 1ull) ? y[j] : NEG_INF;
           }
         };
-        bool grow = begin;
-        if (!begin) {
+        // y, and whether a row's m has to move; then once more with the new m
+#pragma unroll 1
+        for (int pass = 0;; ++pass) {
           scores();
+          if (pass == 1) break;
           float t4[4] = {y[0], y[1], y[2], y[3]};
 #pragma unroll
           for (int j = 4; j < CG; ++j) t4[j & 3] = fmaxf(t4[j & 3], y[j]);
-          const float top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
-          grow = bar_or(bar, 128, top + lsv > kGrow || !ok);
-        }
-        if (grow) {
-          // the rows' largest x + log2 v_scale in this tile
+          const float top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3])) + lsv;
+          if (!bar_or(bar, 128, top > kGrow || unset || !ok)) break;
+          if (unset) {
+            // a row has seen no key yet (the segment's first tile): the tile's largest x + log2 v_scale of each row
 #pragma unroll 1
-          for (int j0 = 0; j0 < CG; j0 += 16) {
-            float z[16];
-            tmem_ld16_async(tS + u * RT + j0, z);
-            tmem_wait16(z);
+            for (int j0 = 0; j0 < CG; j0 += 16) {
+              float z[16];
+              tmem_ld16_async(tS + u * RT + j0, z);
+              tmem_wait16(z);
 #pragma unroll
-            for (int j = 0; j < 16; ++j) {
-              const float4 rc = rowc[(col + j0 + j) / 2];
-              z[j] = ((vis >> (j0 + j)) & 1u) ? fmaf(z[j] * c, (j & 1) ? rc.y : rc.x, lsv) : NEG_INF;
+              for (int j = 0; j < 16; ++j) {
+                const float4 rc = rowc[s][(col + j0 + j) / 2];
+                z[j] = ((vis >> (j0 + j)) & 1ull) ? fmaf(z[j] * c, (j & 1) ? rc.y : rc.x, lsv) : NEG_INF;
+              }
+              const float big = warp_columns<false>(z, lane);
+              if (!(lane & 1)) red[s][wg][col + j0 + (lane >> 1)] = big;
             }
-            const float top = warp_columns<false>(z, lane);
-            if (!(lane & 1)) red[wg][col + j0 + (lane >> 1)] = top;
+          } else if (top > kGrow) {
+#pragma unroll
+            for (int j = 0; j < CG; ++j)
+              if (y[j] + lsv > kGrow) atomicMax(&s_over[s][col + j], __float_as_int(y[j] + lsv));
           }
-          if (!begin) {  // O is rescaled below: every P V before has to be in it
-            ok = __all_sync(0xffffffffu, mbar_wait(&pvdone[u ^ 1], ((i - 1) >> 1) & 1) && ok);
+          // O is rescaled below: every P V before has to be in it (with several streams S of this tile came behind)
+          if (!begin && NSTR == 1) {
+            ok = warp_wait(&pvdone[(i - 1) % NB], ((i - 1) / NB) & 1) && ok;
             tc_fence_after();
           }
           if (bar_or(bar, 128, !ok)) {
             dead = true;
             break;
           }
+          bool none = false;
           if (tg < CG) {
             const int r = col + tg;
-            const float mx = fmaxf(fmaxf(red[0][r], red[1][r]), fmaxf(red[2][r], red[3][r]));
-            const float mo = s_m[r], mn = fmaxf(mo, mx);
-            s_m[r] = mn;
-            s_f[r] = mo == NEG_INF ? (mn == NEG_INF ? 1.f : 0.f) : ex2(mo - mn);
-            reinterpret_cast<float *>(&rowc[r >> 1])[2 + (tg & 1)] = mn == NEG_INF ? kUnset : kBias - mn;
+            const float mo = s_m[s][r];
+            float mn, f = 1.f;
+            if (unset) {
+              mn = fmaxf(mo, fmaxf(fmaxf(red[s][0][r], red[s][1][r]), fmaxf(red[s][2][r], red[s][3][r])));
+              if (mo != NEG_INF) f = ex2(mo - mn);
+              none = mn == NEG_INF;
+            } else {
+              const float over = __int_as_float(s_over[s][r]);
+              const float d = over > 0.f ? over - kMoved : 0.f;
+              mn = mo + d;
+              if (over > 0.f) f = ex2(-d);
+              s_over[s][r] = 0;
+            }
+            s_m[s][r] = mn;
+            s_f[s][r] = f;
+            reinterpret_cast<float *>(&rowc[s][r >> 1])[2 + (tg & 1)] = none ? 0.f : kBias - mn;
           }
-          bar_sync(bar, 128);
+          unset = bar_or(bar, 128, none);
           if (!begin) {
 #pragma unroll
-            for (int j = 0; j < CG / 2; ++j) l2[j] = mul2(l2[j], pack2(s_f[col + 2 * j], s_f[col + 2 * j + 1]));
-#pragma unroll 1
-            for (int j0 = 0; j0 < 2 * CG; j0 += 16) {
-              float o[16];
-              const int jc = j0 % CG;
-              const uint32_t at = (j0 < CG ? tO1 : tO2) + jc;
-              tmem_ld16(at, o);
+            for (int j0 = 0; j0 < CG; j0 += 16) {  // the 16 rows whose m moved
+              bool moved = false;
 #pragma unroll
-              for (int j = 0; j < 16; ++j) o[j] *= s_f[col + jc + j];
-              tmem_st16(at, o);
+              for (int j = 0; j < 16; ++j) moved = moved || s_f[s][col + j0 + j] != 1.f;
+              if (!moved) continue;
+#pragma unroll
+              for (int j = j0 / 2; j < j0 / 2 + 8; ++j)
+                l2[j] = mul2(l2[j], pack2(s_f[s][col + 2 * j], s_f[s][col + 2 * j + 1]));
+#pragma unroll 1
+              for (int term = 0; term < 2; ++term) {
+                float o[16];
+                tmem_ld16(tO + term * RT + j0, o);
+#pragma unroll
+                for (int j = 0; j < 16; ++j) o[j] *= s_f[s][col + j0 + j];
+                tmem_st16(tO + term * RT + j0, o);
+              }
             }
           }
-          scores();
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive1(&sfree[u]);
-        // the P buffer is free once P V of tile i - NPB is done
-        if (i >= NPB)
-          ok = __all_sync(0xffffffffu, mbar_wait_sleep(&pvdone[(i - NPB) & 1], ((i - NPB) >> 1) & 1) && ok);
-        uint8_t *const pb = smem + C::kP + (i % NPB) * C::kPBuf;
+        if (dead) break;
+        begin = false;
+        // the P buffer is free: S of this tile was issued behind P V of tile i - NB
+        uint8_t *const pb = smem + C::kP + u * C::kPBuf;
         const uint64_t w2 = pack2(wv, wv);
 #pragma unroll
         for (int j0 = 0; j0 < CG; j0 += 16) {
@@ -833,28 +931,30 @@ __global__ void __launch_bounds__(Cfg<D, RT, CG>::kThreads, 1)
           *reinterpret_cast<uint4 *>(pb + (n2 >> 7) * C::kPBlock + sw128(tg, n2 & 127)) =
               make_uint4(p2[0], p2[1], p2[2], p2[3]);
         }
-        if (!full && g == 0) {
+        if (part && g == 0) {
           // hidden keys take no part whatever their v holds (0 * NaN): their rows become 0; a tree node's NaN
           // becomes 0 too, and reaches the rows that see it at the end
-          const int pos = t * kKeys + tg;
-          uint8_t *const vt = smem + C::kRing + st * 2 * C::kKV + C::kKV;
-          const bool hidden = vsc < 0.f || pos >= sg.nkeys;
+          Segments after = sg;
+          const int hold = after.step(a) ? i0 + n + after.t1 - after.t0 : ntiles;
+          const int load = min(min(ntiles, i + NB), hold) + i;  // V's place in the order of loads
+          ok = warp_wait(&full[load % NSLOT], (load / NSLOT) & 1) && ok;
+          uint8_t *const vt = smem + C::kRing + (load % NSLOT) * C::kSlot;
           if (hidden || pos >= sg.L) {
             for (int e = 0; e < D; e += 16) {
               uint4 *const at = reinterpret_cast<uint4 *>(vt + (D == 128 ? sw128(tg, e) : sw64(tg, e)));
-              uint4 x = make_uint4(0, 0, 0, 0);
+              uint4 v = make_uint4(0, 0, 0, 0);
               if (!hidden) {
-                x = *at;
+                v = *at;
                 uint32_t any = 0;
                 auto clear = [&](uint32_t w) {
                   const uint32_t nan = ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;  // bytes 0x7F, 0xFF
                   any |= nan;
                   return w & ~((nan >> 7) * 0xFFu);
                 };
-                x = make_uint4(clear(x.x), clear(x.y), clear(x.z), clear(x.w));
-                if (any) s_nan[seg & 3] = 1;
+                v = make_uint4(clear(v.x), clear(v.y), clear(v.z), clear(v.w));
+                if (any) s_nan[seg & 1] = 1;
               }
-              *at = x;
+              *at = v;
             }
           }
         }
@@ -863,88 +963,112 @@ __global__ void __launch_bounds__(Cfg<D, RT, CG>::kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive1(&pfull[u]);
       }
-      if (dead) break;
-      // ---------------- the segment's rows: l over the keys' threads, O from TMEM
+      // ---------------- the segment's end: the streams' l and m joined, O from TMEM
+      if (dead) ok = false;
 #pragma unroll
       for (int j0 = 0; j0 < CG; j0 += 16) {
         float z[16];
 #pragma unroll
         for (int j = 0; j < 16; j += 2) unpack2(l2[(j0 + j) / 2], z[j], z[j + 1]);
         const float sum = warp_columns<true>(z, lane);
-        if (!(lane & 1)) red[wg][col + j0 + (lane >> 1)] = sum;
+        if (!(lane & 1)) red[s][wg][col + j0 + (lane >> 1)] = sum;
       }
-      ok = __all_sync(0xffffffffu, mbar_wait(&pvdone[(i - 1) & 1], ((i - 1) >> 1) & 1) && ok);
+      const int il = i0 + n - 1;
+      ok = ok && warp_wait(&pvdone[il % NB], (il / NB) & 1);
       tc_fence_after();
-      if (bar_or(bar, 128, !ok)) {
-        dead = true;
+      if (bar_or(5, kSoftThreads, !ok)) {
+        s_abort = 1;
         break;
       }
       const bool whole = sg.t0 == 0 && sg.t1 == sg.nt;
       const int slot = blockIdx.x * 2 + (sg.t0 > 0 ? 0 : 1);
-      if (tg < CG && row0 + tg < a.nrows) {
-        const int r = col + tg;
-        const float l = __fadd_rn(__fadd_rn(red[0][r], red[1][r]), __fadd_rn(red[2][r], red[3][r]));
-        const float m = s_m[r];
-        if (whole) {
-          s_f[r] = l == 0.f ? 0.f : 1.f / l;
-          const int row = row0 + tg, qi = row / a.group, head = hk * a.group + row % a.group;
-          if (a.lse)
+      // streams that had a tile: those at (i0 + k) % NSTR, k < n
+      auto took_part = [&](int k) { return NSTR == 1 || (k + NSTR - i0 % NSTR) % NSTR < n; };
+      if (tid == 0) s_nan[(seg + 1) & 1] = 0;
+      for (int r = tid; r < RT; r += kSoftThreads) {
+        float M = NEG_INF, L = 0.f, l[NSTR];
+#pragma unroll
+        for (int k = 0; k < NSTR; ++k) {
+          l[k] = __fadd_rn(__fadd_rn(red[k][0][r], red[k][1][r]), __fadd_rn(red[k][2][r], red[k][3][r]));
+          M = fmaxf(M, s_m[k][r]);
+        }
+#pragma unroll
+        for (int k = 0; k < NSTR; ++k) {
+          l[k] = l[k] == 0.f ? 0.f : l[k] * ex2(s_m[k][r] - M);
+          L = __fadd_rn(L, l[k]);
+        }
+        const float inv = !whole ? 1.f : (L == 0.f ? 0.f : 1.f / L);
+#pragma unroll
+        for (int k = 0; k < NSTR; ++k) s_f[k][r] = l[k] == 0.f ? 0.f : ex2(s_m[k][r] - M) * inv;
+        const int row = mt * RT + r;
+        if (row < a.nrows) {
+          if (!whole) a.part_ml[slot * RT + r] = make_float2(M, L);
+          else if (a.lse) {
+            const int qi = row / a.group, head = hk * a.group + row % a.group;
             a.lse[(static_cast<int64_t>(sg.b) * a.Nq + qi) * a.Hq + head] =
-                l == 0.f ? NEG_INF : (m - kBias + log2f(l)) * 0.69314718055994531f;
-        } else {
-          s_f[r] = 1.f;
-          a.part_ml[slot * RT + r] = make_float2(m, l);
+                L == 0.f ? NEG_INF : (M - kBias + log2f(L)) * 0.69314718055994531f;
+          }
         }
       }
-      bar_sync(bar, 128);
-      const bool nan = s_nan[seg & 3] != 0;
+      bar_sync(5, kSoftThreads);
+      const bool nan = s_nan[seg & 1] != 0;
       if (D == 128 || wg < 2) {
 #pragma unroll 1
-        for (int j0 = 0; j0 < CG; j0 += 16) {
-          float o1[16], o2[16];
-          tmem_ld16_async(tO1 + j0, o1);
-          tmem_ld16_async(tO2 + j0, o2);
-          tmem_wait16(o1);
-          tmem_wait16(o2);
+        for (int j0 = sgrp * 16; j0 < RT; j0 += NSTR * C::kGroups * 16) {
+          float o[16];
 #pragma unroll
-          for (int j = 0; j < 16; ++j) o1[j] = fmaf(o2[j], 0.03125f, o1[j]) * s_f[col + j0 + j];
+          for (int j = 0; j < 16; ++j) o[j] = 0.f;
+#pragma unroll 1
+          for (int k = 0; k < NSTR; ++k) {
+            if (!took_part(k)) continue;
+            float o1[16], o2[16];
+            const uint32_t at = tmem + C::kOCol + k * (2 * RT) + j0 + lane_off;
+            tmem_ld16_async(at, o1);
+            tmem_ld16_async(at + RT, o2);
+            tmem_wait16(o1);
+            tmem_wait16(o2);
+#pragma unroll
+            for (int j = 0; j < 16; ++j) o[j] = fmaf(fmaf(o2[j], 0.03125f, o1[j]), s_f[k][j0 + j], o[j]);
+          }
+          const int r0 = mt * RT + j0;
           if (nan) {
             // tree nodes of this segment whose v holds NaN at this thread's element
-            for (int n = max(0, sg.t0 * kKeys - sg.L); n < a.N && sg.L + n < min(sg.nkeys, sg.t1 * kKeys); ++n) {
-              const int pos = sg.L + n, blk = a.table[static_cast<int64_t>(sg.b) * a.maxb + pos / kPage];
+            for (int node = max(0, sg.t0 * kKeys - sg.L); node < a.N && sg.L + node < min(sg.nkeys, sg.t1 * kKeys);
+                 ++node) {
+              const int pos = sg.L + node, blk = a.table[static_cast<int64_t>(sg.b) * a.maxb + pos / kPage];
               if (blk < 0 || blk >= a.num_blocks) continue;
               const int64_t unit = static_cast<int64_t>(blk) * a.Hkv + hk;
               if (!good_scale(a.ks[unit]) || !good_scale(a.vs[unit])) continue;
               if ((a.vc[(unit * kPage + pos % kPage) * D + tg] & 0x7F) != 0x7F) continue;
 #pragma unroll
               for (int j = 0; j < 16; ++j) {
-                const int qi = min((row0 + j0 + j) / a.group, kMaxNodes - 1);
-                if ((anc[buf][qi][n >> 5] >> (n & 31)) & 1u) o1[j] = __int_as_float(0x7fc00000);
+                const int qi = min((r0 + j) / a.group, kMaxNodes - 1);
+                if ((anc[buf][qi][node >> 5] >> (node & 31)) & 1u) o[j] = __int_as_float(0x7fc00000);
               }
             }
           }
           if (whole) {
 #pragma unroll
             for (int j = 0; j < 16; ++j) {
-              const int r = row0 + j0 + j;
+              const int r = r0 + j;
               if (r >= a.nrows) break;
               const int qi = static_cast<int>((r * a.group_magic) >> 16), head = hk * a.group + (r - qi * a.group);
               uint32_t b2;
-              asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(b2) : "f"(0.f), "f"(o1[j]));
+              asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(b2) : "f"(0.f), "f"(o[j]));
               a.out[((static_cast<int64_t>(sg.b) * a.Nq + qi) * a.Hq + head) * D + tg] =
                   static_cast<uint16_t>(b2 & 0xFFFFu);
             }
           } else {
 #pragma unroll
-            for (int j = 0; j < 16; ++j) a.part_o[(static_cast<int64_t>(slot) * RT + col + j0 + j) * D + tg] = o1[j];
+            for (int j = 0; j < 16; ++j) a.part_o[(static_cast<int64_t>(slot) * RT + j0 + j) * D + tg] = o[j];
           }
         }
       }
       tc_fence_before();
-      __syncwarp();
+      bar_sync(5, kSoftThreads);  // O, the factors and the sums have been read
       if (lane == 0) mbar_arrive1(&qempty[buf]);
+      i0 += n;
     }
-    if (dead) s_abort = 1;
   }
   if (tid == 0 && a.split) {  // what the piece's last item still needs
     int4 need = make_int4(0, 0, 0, 0);
@@ -1028,9 +1152,8 @@ bool make_code_map(CUtensorMap *m, const void *base, int64_t num_blocks, int Hkv
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Rows of a tile: at most 128, the tiles of equal size, a multiple of the
-// softmax groups' 16 rows (32 above 64: four groups are all that 20 warps and
-// their registers allow).
+// Rows of a tile: at most 128, the tiles of equal size, a multiple of the MMA's
+// step of 16 (of the 32 rows of a softmax warp above 64).
 struct Shape {
   int nrows, mtiles, RT;
 };
@@ -1056,13 +1179,13 @@ Workspace workspace_of(const Shape &s, int d, int ctas) {
   return w;
 }
 
-template <int D, int RT, int CG>
+template <int D, int RT>
 cudaError_t launch(const CUtensorMap &kmap, const CUtensorMap &vmap, const Args &a, unsigned grid, cudaStream_t cs) {
-  using C = q8::Cfg<D, RT, CG>;
-  cudaError_t e = cudaFuncSetAttribute(q8::k_branch_attn_q8<D, RT, CG>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  using C = q8::Cfg<D, RT>;
+  cudaError_t e = cudaFuncSetAttribute(q8::k_branch_attn_q8<D, RT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        C::kSmem);
   if (e != cudaSuccess) return e;
-  q8::k_branch_attn_q8<D, RT, CG><<<grid, C::kThreads, C::kSmem, cs>>>(kmap, vmap, a);
+  q8::k_branch_attn_q8<D, RT><<<grid, C::kThreads, C::kSmem, cs>>>(kmap, vmap, a);
   e = cudaGetLastError();
   if (e != cudaSuccess || !a.split) return e;
   cudaLaunchConfig_t cfg = {};
@@ -1081,12 +1204,12 @@ template <int D>
 cudaError_t launch_shape(const Shape &s, const CUtensorMap &kmap, const CUtensorMap &vmap, const Args &a,
                          unsigned grid, cudaStream_t cs) {
   switch (s.RT) {
-    case 16: return launch<D, 16, 16>(kmap, vmap, a, grid, cs);
-    case 32: return launch<D, 32, 16>(kmap, vmap, a, grid, cs);
-    case 48: return launch<D, 48, 16>(kmap, vmap, a, grid, cs);
-    case 64: return launch<D, 64, 16>(kmap, vmap, a, grid, cs);
-    case 96: return launch<D, 96, 32>(kmap, vmap, a, grid, cs);
-    default: return launch<D, 128, 32>(kmap, vmap, a, grid, cs);
+    case 16: return launch<D, 16>(kmap, vmap, a, grid, cs);
+    case 32: return launch<D, 32>(kmap, vmap, a, grid, cs);
+    case 48: return launch<D, 48>(kmap, vmap, a, grid, cs);
+    case 64: return launch<D, 64>(kmap, vmap, a, grid, cs);
+    case 96: return launch<D, 96>(kmap, vmap, a, grid, cs);
+    default: return launch<D, 128>(kmap, vmap, a, grid, cs);
   }
 }
 
