@@ -226,7 +226,7 @@ struct Args {
   float *lse;
   float *part_o;   // [CTA][2][rows][d]: a piece's first item (begun elsewhere), then its last (ended elsewhere)
   float2 *part_ml;  // [CTA][2][rows] (m, l)
-  int4 *info;      // [CTA] what its last item still needs: {parts, sequence, item of the sequence, 0}
+  int4 *info;      // [CTA] what its last item still needs: {parts, sequence, KV head, row tile}
   uint32_t *status;
 };
 
@@ -242,25 +242,27 @@ SSD_DEV int tiles_of(const Args &a, int b) {
 
 // A CTA's piece of the line of units.
 struct Piece {
-  int b;            // sequence of the first unit
-  int64_t off;      // units of that sequence before it
-  int64_t left;     // units of the piece
-  int64_t chunk;    // units of a full piece
+  int b, item, t0;  // sequence, item of it and tile of the first unit
+  int left;         // units of the piece
+  int chunk;        // units of a full piece
   int tiles;        // tiles that the CTA runs
 };
 
 // The segments of a piece: one item (or part of it) after the other.
 struct Segments {
-  int b, item, nt, nkeys, L, t0, t1;
-  int64_t left;
+  int b, hk, mt, nt, nkeys, L, t0, t1, left;
+  SSD_DEV void sequence(const Args &a) {
+    nkeys = keys_of(a, b, L);
+    nt = (nkeys + kKeys - 1) / kKeys;
+  }
   SSD_DEV bool first(const Args &a, const Piece &p) {
     if (p.left <= 0) return false;
     b = p.b;
+    hk = p.item / a.mtiles;
+    mt = p.item - hk * a.mtiles;
+    t0 = p.t0;
     left = p.left;
-    nkeys = keys_of(a, b, L);
-    nt = (nkeys + kKeys - 1) / kKeys;
-    item = static_cast<int>(p.off / nt);
-    t0 = static_cast<int>(p.off % nt);
+    sequence(a);
     if (!a.split && t0 > 0) {  // begun in the piece before, which takes it whole
       left -= nt - t0;
       return step(a);
@@ -268,19 +270,20 @@ struct Segments {
     return take(a);
   }
   SSD_DEV bool take(const Args &a) {
-    t1 = (a.split && left < nt - t0) ? t0 + static_cast<int>(left) : nt;
+    t1 = (a.split && left < nt - t0) ? t0 + left : nt;
     left -= t1 - t0;
     return true;
   }
   SSD_DEV bool step(const Args &a) {
     if (left <= 0) return false;
     t0 = 0;
-    if (++item == a.per_b) {
-      item = 0;
-      ++b;
-      if (b >= a.B) return false;
-      nkeys = keys_of(a, b, L);
-      nt = (nkeys + kKeys - 1) / kKeys;
+    if (++mt == a.mtiles) {
+      mt = 0;
+      if (++hk == a.Hkv) {
+        hk = 0;
+        if (++b == a.B) return false;
+        sequence(a);
+      }
     }
     return take(a);
   }
@@ -339,8 +342,107 @@ struct Cfg {
   static_assert(kSlots >= NB + 2, "S runs NB tiles ahead");
   // the scales of tile i + kMeta are written when a slot used up to tile i + kMeta - NB - (kSlots + 1) / 2 is free
   static_assert(kMeta >= NB + (kSlots + 1) / 2 + 1, "block scales");
-  static_assert(kCols <= 512 && RT % CG == 0 && CG % 16 == 0 && NSTR * kGroups <= 4, "rows");
+  static_assert(kCols <= 512 && RT % CG == 0 && CG % 16 == 0 && NSTR * kGroups <= 8, "rows");
 };
+
+// A segment's rows: q1, q2 into the operand tiles at qb, the row scales, and
+// each query's tree mask, by warp w of the n that share it (barrier `bar`).
+template <int D, int RT>
+__device__ __noinline__ void prepare_rows(const Args &a, const Segments &sg, uint8_t *qb, int *par,
+                                          uint32_t (*anc)[kMaxNodes / 32], float *qs, int w, int n, int bar) {
+  using C = Cfg<D, RT>;
+  const int lane = threadIdx.x & 31;
+  const int hk = sg.hk, mt = sg.mt;
+  const bool tree = sg.t1 * kKeys > sg.L;
+  if (tree)
+    for (int m = w * 32 + lane; m < a.N; m += n * 32) par[m] = a.parent[static_cast<int64_t>(sg.b) * a.N + m];
+  if (w == 0 && lane == 0) {
+    const int L = a.prefix_len[sg.b];
+    if (L < 0 || static_cast<int64_t>(L) + a.N > static_cast<int64_t>(a.maxb) * kPage)
+      atomicOr(a.status, kFlagBadPrefix);
+  }
+  bar_sync(bar, n * 32);
+  if (tree) {
+    for (int i = w * 32 + lane; i < a.Nq; i += n * 32) {
+      uint32_t bits[kMaxNodes / 32] = {0, 0, 0, 0};
+      for (int m = a.N - a.Nq + i; m >= 0;) {
+#pragma unroll
+        for (int x = 0; x < kMaxNodes / 32; ++x)
+          if ((m >> 5) == x) bits[x] |= 1u << (m & 31);
+        const int up = par[m];
+        if (up < -1 || up >= m) {
+          atomicOr(a.status, kFlagBadTree);
+          break;
+        }
+        m = up;
+      }
+#pragma unroll
+      for (int x = 0; x < kMaxNodes / 32; ++x) anc[i][x] = bits[x];
+    }
+  }
+  constexpr int E = D / 32;  // elements per lane
+  constexpr int U = 4;       // rows in flight
+  for (int r0 = w * U; r0 < RT; r0 += n * U) {
+    uint32_t x[U][E / 2];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int r = mt * RT + r0 + u;
+#pragma unroll
+      for (int e = 0; e < E / 2; ++e) x[u][e] = 0;
+      if (r0 + u < RT && r < a.nrows) {
+        const int qi = static_cast<int>((r * a.group_magic) >> 16), head = hk * a.group + (r - qi * a.group);
+        const uint16_t *src = a.q + ((static_cast<int64_t>(sg.b) * a.Nq + qi) * a.Hq + head) * D + lane * E;
+        if constexpr (E == 4) {
+          const uint2 v = __ldg(reinterpret_cast<const uint2 *>(src));
+          x[u][0] = v.x;
+          x[u][1] = v.y;
+        } else {
+          x[u][0] = __ldg(reinterpret_cast<const uint32_t *>(src));
+        }
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (r0 + u >= RT) break;
+      float f[E];
+      uint32_t m = 0;
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        const uint32_t bits = (e & 1) ? x[u][e / 2] & 0xFFFF0000u : x[u][e / 2] << 16;
+        f[e] = __uint_as_float(bits);
+        const uint32_t mag = bits & 0x7FFFFFFFu;
+        if (mag < 0x7F800000u) m = max(m, mag);
+        else f[e] = __int_as_float(0x7fc00000);  // an infinity too: e4m3 would clamp it
+      }
+#pragma unroll
+      for (int s = 16; s; s >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, s));
+      // 2^e brings the largest element into [2^7, 2^8); e in [-120, 120] (smaller rows: fewer bits)
+      const int e2 = m == 0 ? 0 : min(max(static_cast<int>(m >> 23) - 127 - 7, -120), 120);
+      const float inv = __uint_as_float(static_cast<uint32_t>(127 - e2) << 23);
+      uint32_t c1 = 0, c2 = 0;
+#pragma unroll
+      for (int e = 0; e < E; e += 2) {
+        const float u0 = f[e] * inv, u1 = f[e + 1] * inv;
+        const uint32_t h = e4m3_pair(u0, u1);
+        float b0, b1;
+        half2_to_float(e4m3_to_half2(static_cast<uint16_t>(h)), b0, b1);
+        c1 |= h << (8 * e);
+        c2 |= e4m3_pair(u0 - b0, u1 - b1) << (8 * e);
+      }
+      const int row = r0 + u;
+      if constexpr (D == 128) {
+        *reinterpret_cast<uint32_t *>(qb + sw128(row, lane * 4)) = c1;
+        *reinterpret_cast<uint32_t *>(qb + C::kQTile + sw128(row, lane * 4)) = c2;
+      } else {
+        *reinterpret_cast<uint16_t *>(qb + sw128(row, lane * 2)) = static_cast<uint16_t>(c1);
+        *reinterpret_cast<uint16_t *>(qb + sw128(row, 64 + lane * 2)) = static_cast<uint16_t>(c2);
+      }
+      if (lane == 0) qs[row] = __uint_as_float(static_cast<uint32_t>(127 + e2) << 23);
+    }
+  }
+  fence_proxy_async();  // the operand tiles -> visible to the tensor cores
+  __syncwarp();
+}
 
 template <int D, int RT>
 __global__ void __launch_bounds__(Cfg<D, RT>::kThreads, 1)
@@ -429,9 +531,11 @@ __global__ void __launch_bounds__(Cfg<D, RT>::kThreads, 1)
       }
       Piece p;
       p.b = b;
-      p.off = lo - x;
-      p.left = hi - lo;
-      p.chunk = chunk;
+      const int nt = tiles_of(a, b);
+      p.item = static_cast<int>((lo - x) / nt);
+      p.t0 = static_cast<int>((lo - x) - static_cast<long long>(p.item) * nt);
+      p.left = static_cast<int>(hi - lo);
+      p.chunk = static_cast<int>(chunk);
       p.tiles = 0;
       Segments sg;
       for (bool more = sg.first(a, p); more; more = sg.step(a)) p.tiles += sg.t1 - sg.t0;
@@ -445,100 +549,9 @@ __global__ void __launch_bounds__(Cfg<D, RT>::kThreads, 1)
   const Piece piece = s_piece;
   const int ntiles = piece.tiles;
 
-  // A segment's rows: q1, q2 and the row scales into buffer `buf`, the
-  // queries' tree masks; warp w of the n that share it (barrier `bar`).
+  // the rows of segment `sg` into buffer `buf`, by warp w of the n that share it (barrier `bar`)
   auto prepare = [&](const Segments &sg, int buf, int w, int n, int bar) {
-    const int hk = sg.item / a.mtiles, mt = sg.item % a.mtiles;
-    const bool tree = sg.t1 * kKeys > sg.L;
-    if (tree)
-      for (int m = w * 32 + lane; m < a.N; m += n * 32) par[buf][m] = a.parent[static_cast<int64_t>(sg.b) * a.N + m];
-    if (w == 0 && lane == 0) {
-      const int L = a.prefix_len[sg.b];
-      if (L < 0 || static_cast<int64_t>(L) + a.N > static_cast<int64_t>(a.maxb) * kPage)
-        atomicOr(a.status, kFlagBadPrefix);
-    }
-    bar_sync(bar, n * 32);
-    if (tree) {
-      for (int i = w * 32 + lane; i < a.Nq; i += n * 32) {
-        uint32_t bits[kMaxNodes / 32] = {0, 0, 0, 0};
-        for (int m = a.N - a.Nq + i; m >= 0;) {
-#pragma unroll
-          for (int x = 0; x < kMaxNodes / 32; ++x)
-            if ((m >> 5) == x) bits[x] |= 1u << (m & 31);
-          const int up = par[buf][m];
-          if (up < -1 || up >= m) {
-            atomicOr(a.status, kFlagBadTree);
-            break;
-          }
-          m = up;
-        }
-#pragma unroll
-        for (int x = 0; x < kMaxNodes / 32; ++x) anc[buf][i][x] = bits[x];
-      }
-    }
-    uint8_t *const qb = smem + C::kQ + buf * C::kQBuf;
-    constexpr int E = D / 32;  // elements per lane
-    constexpr int U = 4;       // rows in flight
-    for (int r0 = w * U; r0 < RT; r0 += n * U) {
-      uint32_t x[U][E / 2];
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int r = mt * RT + r0 + u;
-#pragma unroll
-        for (int e = 0; e < E / 2; ++e) x[u][e] = 0;
-        if (r0 + u < RT && r < a.nrows) {
-          const int qi = r / a.group, head = hk * a.group + r % a.group;
-          const uint16_t *src = a.q + ((static_cast<int64_t>(sg.b) * a.Nq + qi) * a.Hq + head) * D + lane * E;
-          if constexpr (E == 4) {
-            const uint2 v = __ldg(reinterpret_cast<const uint2 *>(src));
-            x[u][0] = v.x;
-            x[u][1] = v.y;
-          } else {
-            x[u][0] = __ldg(reinterpret_cast<const uint32_t *>(src));
-          }
-        }
-      }
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        if (r0 + u >= RT) break;
-        float f[E];
-        uint32_t m = 0;
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-          const uint32_t bits = (e & 1) ? x[u][e / 2] & 0xFFFF0000u : x[u][e / 2] << 16;
-          f[e] = __uint_as_float(bits);
-          const uint32_t mag = bits & 0x7FFFFFFFu;
-          if (mag < 0x7F800000u) m = max(m, mag);
-          else f[e] = __int_as_float(0x7fc00000);  // an infinity too: e4m3 would clamp it
-        }
-#pragma unroll
-        for (int s = 16; s; s >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, s));
-        // 2^e brings the largest element into [2^7, 2^8); e in [-120, 120] (smaller rows: fewer bits)
-        const int e2 = m == 0 ? 0 : min(max(static_cast<int>(m >> 23) - 127 - 7, -120), 120);
-        const float inv = __uint_as_float(static_cast<uint32_t>(127 - e2) << 23);
-        uint32_t c1 = 0, c2 = 0;
-#pragma unroll
-        for (int e = 0; e < E; e += 2) {
-          const float u0 = f[e] * inv, u1 = f[e + 1] * inv;
-          const uint32_t h = e4m3_pair(u0, u1);
-          float b0, b1;
-          half2_to_float(e4m3_to_half2(static_cast<uint16_t>(h)), b0, b1);
-          c1 |= h << (8 * e);
-          c2 |= e4m3_pair(u0 - b0, u1 - b1) << (8 * e);
-        }
-        const int row = r0 + u;
-        if constexpr (D == 128) {
-          *reinterpret_cast<uint32_t *>(qb + sw128(row, lane * 4)) = c1;
-          *reinterpret_cast<uint32_t *>(qb + C::kQTile + sw128(row, lane * 4)) = c2;
-        } else {
-          *reinterpret_cast<uint16_t *>(qb + sw128(row, lane * 2)) = static_cast<uint16_t>(c1);
-          *reinterpret_cast<uint16_t *>(qb + sw128(row, 64 + lane * 2)) = static_cast<uint16_t>(c2);
-        }
-        if (lane == 0) qs[buf][row] = __uint_as_float(static_cast<uint32_t>(127 + e2) << 23);
-      }
-    }
-    fence_proxy_async();  // the operand tiles -> visible to the tensor cores
-    __syncwarp();
+    prepare_rows<D, RT>(a, sg, smem + C::kQ + buf * C::kQBuf, par[buf], anc[buf], qs[buf], w, n, bar);
   };
 
   Segments sg;
@@ -561,7 +574,7 @@ __global__ void __launch_bounds__(Cfg<D, RT>::kThreads, 1)
       }
     };
     auto ids = [&](Batch &x) {
-      x.hk = more ? sg.item / a.mtiles : 0;
+      x.hk = more ? sg.hk : 0;
       x.blk = -1;
       x.vs = 0.f;
       x.ks = -1.f;  // no block there
@@ -733,8 +746,8 @@ __global__ void __launch_bounds__(Cfg<D, RT>::kThreads, 1)
     // ---------------- the rows of the segments after the first
     bool more = sg.first(a, piece);
     if (more) {
-      prepare(sg, 0, C::kSoftWarps, C::kSoftWarps + 1, 6);
-      bar_sync(6, (C::kSoftWarps + 1) * 32);
+      prepare(sg, 0, C::kSoftWarps, C::kSoftWarps + 1, 10);
+      bar_sync(10, (C::kSoftWarps + 1) * 32);
       if (lane == 0) mbar_arrive1(&qfull[0]);
       more = sg.step(a);
     }
@@ -745,7 +758,7 @@ __global__ void __launch_bounds__(Cfg<D, RT>::kThreads, 1)
         s_abort = 1;
         break;
       }
-      prepare(sg, buf, 0, 1, 7);
+      prepare(sg, buf, 0, 1, 11);
       if (lane == 0) mbar_arrive1(&qfull[buf]);
     }
   } else {
@@ -760,12 +773,12 @@ __global__ void __launch_bounds__(Cfg<D, RT>::kThreads, 1)
     bool dead = false;
     bool more = sg.first(a, piece);
     if (more) {
-      prepare(sg, 0, warp, C::kSoftWarps + 1, 6);
-      bar_sync(6, (C::kSoftWarps + 1) * 32);
+      prepare(sg, 0, warp, C::kSoftWarps + 1, 10);
+      bar_sync(10, (C::kSoftWarps + 1) * 32);
     }
     for (; more; more = sg.step(a), ++seg) {
       const int buf = seg & 1, n = sg.t1 - sg.t0;
-      const int hk = sg.item / a.mtiles, mt = sg.item % a.mtiles;
+      const int hk = sg.hk, mt = sg.mt;
       const int row0 = mt * RT + col;  // the warp's first row of (b, hk)
       bool ok = warp_wait(&qfull[buf], (seg >> 1) & 1);
       if (tg < CG) {
@@ -976,7 +989,7 @@ __global__ void __launch_bounds__(Cfg<D, RT>::kThreads, 1)
       const int il = i0 + n - 1;
       ok = ok && warp_wait(&pvdone[il % NB], (il / NB) & 1);
       tc_fence_after();
-      if (bar_or(5, kSoftThreads, !ok)) {
+      if (bar_or(9, kSoftThreads, !ok)) {
         s_abort = 1;
         break;
       }
@@ -1004,13 +1017,13 @@ __global__ void __launch_bounds__(Cfg<D, RT>::kThreads, 1)
         if (row < a.nrows) {
           if (!whole) a.part_ml[slot * RT + r] = make_float2(M, L);
           else if (a.lse) {
-            const int qi = row / a.group, head = hk * a.group + row % a.group;
+            const int qi = static_cast<int>((row * a.group_magic) >> 16), head = hk * a.group + (row - qi * a.group);
             a.lse[(static_cast<int64_t>(sg.b) * a.Nq + qi) * a.Hq + head] =
                 L == 0.f ? NEG_INF : (M - kBias + log2f(L)) * 0.69314718055994531f;
           }
         }
       }
-      bar_sync(5, kSoftThreads);
+      bar_sync(9, kSoftThreads);
       const bool nan = s_nan[seg & 1] != 0;
       if (D == 128 || wg < 2) {
 #pragma unroll 1
@@ -1042,7 +1055,7 @@ __global__ void __launch_bounds__(Cfg<D, RT>::kThreads, 1)
               if ((a.vc[(unit * kPage + pos % kPage) * D + tg] & 0x7F) != 0x7F) continue;
 #pragma unroll
               for (int j = 0; j < 16; ++j) {
-                const int qi = min((r0 + j) / a.group, kMaxNodes - 1);
+                const int qi = min(static_cast<int>(((r0 + j) * a.group_magic) >> 16), kMaxNodes - 1);
                 if ((anc[buf][qi][node >> 5] >> (node & 31)) & 1u) o[j] = __int_as_float(0x7fc00000);
               }
             }
@@ -1065,7 +1078,7 @@ __global__ void __launch_bounds__(Cfg<D, RT>::kThreads, 1)
         }
       }
       tc_fence_before();
-      bar_sync(5, kSoftThreads);  // O, the factors and the sums have been read
+      bar_sync(9, kSoftThreads);  // O, the factors and the sums have been read
       if (lane == 0) mbar_arrive1(&qempty[buf]);
       i0 += n;
     }
@@ -1075,7 +1088,7 @@ __global__ void __launch_bounds__(Cfg<D, RT>::kThreads, 1)
     Segments x;
     for (bool more = x.first(a, piece); more; more = x.step(a))
       if (x.t0 == 0 && x.t1 < x.nt)
-        need = make_int4(1 + static_cast<int>((x.nt - x.t1 + piece.chunk - 1) / piece.chunk), x.b, x.item, 0);
+        need = make_int4(1 + (x.nt - x.t1 + piece.chunk - 1) / piece.chunk, x.b, x.hk, x.mt);
     a.info[blockIdx.x] = need;
   }
   tc_fence_before();
@@ -1094,7 +1107,7 @@ __global__ void __launch_bounds__(256) k_attn_q8_merge(const __grid_constant__ A
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the pieces are done
   const int4 need = a.info[blockIdx.x];
   const int lane = threadIdx.x & 31, j = blockIdx.y * 8 + (threadIdx.x >> 5);
-  const int hk = need.z / a.mtiles, mt = need.z % a.mtiles, row = mt * RT + j;
+  const int hk = need.z, mt = need.w, row = mt * RT + j;
   if (need.x == 0 || j >= RT || row >= a.nrows) return;
   const float NEG_INF = -__int_as_float(0x7f800000);
   // part 0 is the second slot of CTA x, the others the first slots of the CTAs behind it
@@ -1117,7 +1130,7 @@ __global__ void __launch_bounds__(256) k_attn_q8_merge(const __grid_constant__ A
     for (int e = 0; e < E; ++e) acc[e] = fmaf(src[e], f, acc[e]);
   }
   const float inv = l == 0.f ? 0.f : 1.f / l;
-  const int qi = row / a.group, head = hk * a.group + row % a.group;
+  const int qi = static_cast<int>((row * a.group_magic) >> 16), head = hk * a.group + (row - qi * a.group);
   const int64_t orow = (static_cast<int64_t>(need.y) * a.Nq + qi) * a.Hq + head;
   uint32_t *dst = reinterpret_cast<uint32_t *>(a.out + orow * D) + lane * (E / 2);
 #pragma unroll
