@@ -153,6 +153,16 @@ SSD_DEV void tmem_wait16(float *v) {  // orders the uses of v after the wait
                :
                : "memory");
 }
+// two groups of 4 columns
+SSD_DEV void tmem_ld4(uint32_t at0, float *v, uint32_t at1, float *w) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%8];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x4.b32 {%4, %5, %6, %7}, [%9];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(w[0]), "=f"(w[1]), "=f"(w[2]), "=f"(w[3])
+      : "r"(at0), "r"(at1)
+      : "memory");
+}
 SSD_DEV void bar_sync(int id, int n) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory"); }
 SSD_DEV bool bar_or(int id, int n, bool pred) {
   uint32_t r;
@@ -190,10 +200,9 @@ SSD_DEV uint32_t pack16(uint16_t lo, uint16_t hi) {
   return r;
 }
 
-// One value per 16 columns and lane -> the columns' maximum (or sum) over the
-// warp's lanes: five exchanges that halve the columns held (a fixed order).
-// Column (lane >> 1) & 15 ends in both lanes of a pair.
-template <bool SUM>
+// One value per 16 columns and lane -> the columns' sums over the warp's lanes:
+// five exchanges that halve the columns held (a fixed order).  Column
+// (lane >> 1) & 15 ends in both lanes of a pair.
 SSD_DEV float warp_columns(float *v, int lane) {
 #pragma unroll
   for (int s = 0; s < 4; ++s) {
@@ -202,12 +211,15 @@ SSD_DEV float warp_columns(float *v, int lane) {
 #pragma unroll
     for (int k = 0; k < n; ++k) {
       const float keep = up ? v[k + n] : v[k], send = up ? v[k] : v[k + n];
-      const float got = __shfl_xor_sync(0xffffffffu, send, o);
-      v[k] = SUM ? __fadd_rn(keep, got) : fmaxf(keep, got);
+      v[k] = __fadd_rn(keep, __shfl_xor_sync(0xffffffffu, send, o));
     }
   }
-  const float got = __shfl_xor_sync(0xffffffffu, v[0], 1);
-  return SUM ? __fadd_rn(v[0], got) : fmaxf(v[0], got);
+  return __fadd_rn(v[0], __shfl_xor_sync(0xffffffffu, v[0], 1));
+}
+SSD_DEV float warp_top(float v) {  // maximum over the warp, NaN left out
+  float r;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+  return r;
 }
 
 struct Args {
@@ -347,12 +359,29 @@ struct Cfg {
 
 // A segment's rows: q1, q2 into the operand tiles at qb, the row scales, and
 // each query's tree mask, by warp w of the n that share it (barrier `bar`).
+// Four lanes share a row, each with its quarter in registers (the next row's
+// is fetched meanwhile).
 template <int D, int RT>
-__device__ __noinline__ void prepare_rows(const Args &a, const Segments &sg, uint8_t *qb, int *par,
+__device__ __noinline__ void prepare_rows(const Args &a, const Segments sg, uint8_t *qb, int *par,
                                           uint32_t (*anc)[kMaxNodes / 32], float *qs, int w, int n, int bar) {
   using C = Cfg<D, RT>;
   const int lane = threadIdx.x & 31;
-  const int hk = sg.hk, mt = sg.mt;
+  constexpr int V = D / 32;  // 16-byte pieces of a quarter row
+  const int sub = lane & 3;
+  auto fetch = [&](int r, uint4 (&x)[V]) {
+    const int row = sg.mt * RT + r;
+#pragma unroll
+    for (int v = 0; v < V; ++v) x[v] = make_uint4(0, 0, 0, 0);
+    if (r < RT && row < a.nrows) {
+      const int qi = static_cast<int>((row * a.group_magic) >> 16), head = sg.hk * a.group + (row - qi * a.group);
+      const uint4 *src = reinterpret_cast<const uint4 *>(
+          a.q + ((static_cast<int64_t>(sg.b) * a.Nq + qi) * a.Hq + head) * D + sub * (D / 4));
+#pragma unroll
+      for (int v = 0; v < V; ++v) x[v] = __ldg(src + v);
+    }
+  };
+  uint4 x[V], next[V];
+  fetch(w * 8 + (lane >> 2), x);
   const bool tree = sg.t1 * kKeys > sg.L;
   if (tree)
     for (int m = w * 32 + lane; m < a.N; m += n * 32) par[m] = a.parent[static_cast<int64_t>(sg.b) * a.N + m];
@@ -364,11 +393,11 @@ __device__ __noinline__ void prepare_rows(const Args &a, const Segments &sg, uin
   bar_sync(bar, n * 32);
   if (tree) {
     for (int i = w * 32 + lane; i < a.Nq; i += n * 32) {
-      uint32_t bits[kMaxNodes / 32] = {0, 0, 0, 0};
-      for (int m = a.N - a.Nq + i; m >= 0;) {
+      uint32_t *const bits = anc[i];
 #pragma unroll
-        for (int x = 0; x < kMaxNodes / 32; ++x)
-          if ((m >> 5) == x) bits[x] |= 1u << (m & 31);
+      for (int k = 0; k < kMaxNodes / 32; ++k) bits[k] = 0;
+      for (int m = a.N - a.Nq + i; m >= 0;) {
+        bits[m >> 5] |= 1u << (m & 31);
         const int up = par[m];
         if (up < -1 || up >= m) {
           atomicOr(a.status, kFlagBadTree);
@@ -376,69 +405,55 @@ __device__ __noinline__ void prepare_rows(const Args &a, const Segments &sg, uin
         }
         m = up;
       }
-#pragma unroll
-      for (int x = 0; x < kMaxNodes / 32; ++x) anc[i][x] = bits[x];
     }
   }
-  constexpr int E = D / 32;  // elements per lane
-  constexpr int U = 4;       // rows in flight
-  for (int r0 = w * U; r0 < RT; r0 += n * U) {
-    uint32_t x[U][E / 2];
+#pragma unroll 1
+  for (int r0 = w * 8; r0 < RT; r0 += n * 8) {
+    const int r = r0 + (lane >> 2);
+    fetch(r + n * 8, next);
+    uint32_t m = 0;  // the row's largest finite magnitude
+    auto each = [&](auto &&f) {
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int r = mt * RT + r0 + u;
+      for (int v = 0; v < V; ++v) {
+        const uint32_t word[4] = {x[v].x, x[v].y, x[v].z, x[v].w};
 #pragma unroll
-      for (int e = 0; e < E / 2; ++e) x[u][e] = 0;
-      if (r0 + u < RT && r < a.nrows) {
-        const int qi = static_cast<int>((r * a.group_magic) >> 16), head = hk * a.group + (r - qi * a.group);
-        const uint16_t *src = a.q + ((static_cast<int64_t>(sg.b) * a.Nq + qi) * a.Hq + head) * D + lane * E;
-        if constexpr (E == 4) {
-          const uint2 v = __ldg(reinterpret_cast<const uint2 *>(src));
-          x[u][0] = v.x;
-          x[u][1] = v.y;
-        } else {
-          x[u][0] = __ldg(reinterpret_cast<const uint32_t *>(src));
-        }
+        for (int k = 0; k < 4; ++k) f(v, k, word[k]);
       }
+    };
+    each([&](int, int, uint32_t b) {
+      const uint32_t lo = (b << 16) & 0x7FFFFFFFu, hi = b & 0x7FFF0000u;
+      m = max(m, max(lo < 0x7F800000u ? lo : 0u, hi < 0x7F800000u ? hi : 0u));
+    });
+    m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+    m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+    // 2^e brings the largest element into [2^7, 2^8); e in [-120, 120] (smaller rows: fewer bits)
+    const int e2 = m == 0 ? 0 : min(max(static_cast<int>(m >> 23) - 127 - 7, -120), 120);
+    const float inv = __uint_as_float(static_cast<uint32_t>(127 - e2) << 23);
+    uint32_t c1[V * 2], c2[V * 2];
+#pragma unroll
+    for (int k = 0; k < V * 2; ++k) c1[k] = c2[k] = 0;
+    each([&](int v, int k, uint32_t b) {
+      float u0 = __uint_as_float(b << 16) * inv, u1 = __uint_as_float(b & 0xFFFF0000u) * inv;
+      if (!(fabsf(u0) <= 256.f)) u0 = __int_as_float(0x7fc00000);  // an infinity too: e4m3 would clamp it
+      if (!(fabsf(u1) <= 256.f)) u1 = __int_as_float(0x7fc00000);
+      const uint32_t h = e4m3_pair(u0, u1);
+      float b0, b1;
+      half2_to_float(e4m3_to_half2(static_cast<uint16_t>(h)), b0, b1);
+      c1[v * 2 + k / 2] |= h << (16 * (k & 1));
+      c2[v * 2 + k / 2] |= e4m3_pair(u0 - b0, u1 - b1) << (16 * (k & 1));
+    });
+    if (r < RT) {
+#pragma unroll
+      for (int v = 0; v < V; v += 2) {  // 16 codes
+        const int at = sub * (D / 4) + v * 8;
+        *reinterpret_cast<uint4 *>(qb + sw128(r, at)) = make_uint4(c1[v * 2], c1[v * 2 + 1], c1[v * 2 + 2], c1[v * 2 + 3]);
+        *reinterpret_cast<uint4 *>(qb + (D == 128 ? C::kQTile + sw128(r, at) : sw128(r, 64 + at))) =
+            make_uint4(c2[v * 2], c2[v * 2 + 1], c2[v * 2 + 2], c2[v * 2 + 3]);
+      }
+      if (sub == 0) qs[r] = __uint_as_float(static_cast<uint32_t>(127 + e2) << 23);
     }
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      if (r0 + u >= RT) break;
-      float f[E];
-      uint32_t m = 0;
-#pragma unroll
-      for (int e = 0; e < E; ++e) {
-        const uint32_t bits = (e & 1) ? x[u][e / 2] & 0xFFFF0000u : x[u][e / 2] << 16;
-        f[e] = __uint_as_float(bits);
-        const uint32_t mag = bits & 0x7FFFFFFFu;
-        if (mag < 0x7F800000u) m = max(m, mag);
-        else f[e] = __int_as_float(0x7fc00000);  // an infinity too: e4m3 would clamp it
-      }
-#pragma unroll
-      for (int s = 16; s; s >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, s));
-      // 2^e brings the largest element into [2^7, 2^8); e in [-120, 120] (smaller rows: fewer bits)
-      const int e2 = m == 0 ? 0 : min(max(static_cast<int>(m >> 23) - 127 - 7, -120), 120);
-      const float inv = __uint_as_float(static_cast<uint32_t>(127 - e2) << 23);
-      uint32_t c1 = 0, c2 = 0;
-#pragma unroll
-      for (int e = 0; e < E; e += 2) {
-        const float u0 = f[e] * inv, u1 = f[e + 1] * inv;
-        const uint32_t h = e4m3_pair(u0, u1);
-        float b0, b1;
-        half2_to_float(e4m3_to_half2(static_cast<uint16_t>(h)), b0, b1);
-        c1 |= h << (8 * e);
-        c2 |= e4m3_pair(u0 - b0, u1 - b1) << (8 * e);
-      }
-      const int row = r0 + u;
-      if constexpr (D == 128) {
-        *reinterpret_cast<uint32_t *>(qb + sw128(row, lane * 4)) = c1;
-        *reinterpret_cast<uint32_t *>(qb + C::kQTile + sw128(row, lane * 4)) = c2;
-      } else {
-        *reinterpret_cast<uint16_t *>(qb + sw128(row, lane * 2)) = static_cast<uint16_t>(c1);
-        *reinterpret_cast<uint16_t *>(qb + sw128(row, 64 + lane * 2)) = static_cast<uint16_t>(c2);
-      }
-      if (lane == 0) qs[row] = __uint_as_float(static_cast<uint32_t>(127 + e2) << 23);
-    }
+    for (int v = 0; v < V; ++v) x[v] = next[v];
   }
   fence_proxy_async();  // the operand tiles -> visible to the tensor cores
   __syncwarp();
@@ -464,7 +479,6 @@ __global__ void __launch_bounds__(Cfg<D, RT>::kThreads, 1)
   __shared__ float qs[2][RT];                               // row scales 2^e
   __shared__ __align__(16) float4 rowc[NSTR][RT / 2];       // two rows: 2^e, 2^e, 4 - m, 4 - m
   __shared__ float s_m[NSTR][RT], s_f[NSTR][RT], red[NSTR][4][RT];
-  __shared__ int s_over[NSTR][RT];                          // largest P v_scale above 2^8 (its log2's bits), or 0
   __shared__ int s_nan[2];                                  // a tree node's v held NaN, by segment mod 2
   __shared__ long long scan[32];
   __shared__ Piece s_piece;
@@ -494,7 +508,6 @@ __global__ void __launch_bounds__(Cfg<D, RT>::kThreads, 1)
     s_piece.left = 0;
     s_piece.tiles = 0;
   }
-  for (int r = tid; r < NSTR * RT; r += C::kThreads) (&s_over[0][0])[r] = 0;
   if (warp == C::kMmaWarp) {
     tmem_alloc(&tmem_base, C::kTmem);
     tmem_relinquish();
@@ -808,10 +821,12 @@ __global__ void __launch_bounds__(Cfg<D, RT>::kThreads, 1)
         if (part && !hidden && pos >= sg.L) {
           const int node = pos - sg.L;
           vis = 0;
-          for (int j = 0; j < CG; ++j) {
-            const int qi = min(static_cast<int>(((row0 + j) * a.group_magic) >> 16), kMaxNodes - 1);
-            vis |= static_cast<uint64_t>((anc[buf][qi][node >> 5] >> (node & 31)) & 1u) << j;
-          }
+          // row j is query (row0 + j) / group: the rows of one query are neighbours
+          int qi = static_cast<int>((row0 * a.group_magic) >> 16), j0 = 0;
+#pragma unroll 1
+          for (int j1 = (qi + 1) * a.group - row0; j0 < CG && qi < a.Nq; ++qi, j0 = j1, j1 += a.group)
+            if ((anc[buf][qi][node >> 5] >> (node & 31)) & 1u)
+              vis |= (j1 < 64 ? (1ull << j1) - 1ull : ~0ull) & (~0ull << j0);
         }
         const uint64_t c2 = pack2(c, c);
         float y[CG];
@@ -841,26 +856,14 @@ __global__ void __launch_bounds__(Cfg<D, RT>::kThreads, 1)
           for (int j = 4; j < CG; ++j) t4[j & 3] = fmaxf(t4[j & 3], y[j]);
           const float top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3])) + lsv;
           if (!bar_or(bar, 128, top > kGrow || unset || !ok)) break;
-          if (unset) {
-            // a row has seen no key yet (the segment's first tile): the tile's largest x + log2 v_scale of each row
-#pragma unroll 1
-            for (int j0 = 0; j0 < CG; j0 += 16) {
-              float z[16];
-              tmem_ld16_async(tS + u * RT + j0, z);
-              tmem_wait16(z);
+          // the rows' largest log2 of P v_scale (of a row without a key so far: x + log2 v_scale) in this tile
+          float big = NEG_INF;
 #pragma unroll
-              for (int j = 0; j < 16; ++j) {
-                const float4 rc = rowc[s][(col + j0 + j) / 2];
-                z[j] = ((vis >> (j0 + j)) & 1ull) ? fmaf(z[j] * c, (j & 1) ? rc.y : rc.x, lsv) : NEG_INF;
-              }
-              const float big = warp_columns<false>(z, lane);
-              if (!(lane & 1)) red[s][wg][col + j0 + (lane >> 1)] = big;
-            }
-          } else if (top > kGrow) {
-#pragma unroll
-            for (int j = 0; j < CG; ++j)
-              if (y[j] + lsv > kGrow) atomicMax(&s_over[s][col + j], __float_as_int(y[j] + lsv));
+          for (int j = 0; j < CG; ++j) {
+            const float z = warp_top(y[j] + lsv);
+            if (lane == j) big = z;
           }
+          if (lane < CG) red[s][wg][col + lane] = big;
           // O is rescaled below: every P V before has to be in it (with several streams S of this tile came behind)
           if (!begin && NSTR == 1) {
             ok = warp_wait(&pvdone[(i - 1) % NB], ((i - 1) / NB) & 1) && ok;
@@ -874,17 +877,14 @@ __global__ void __launch_bounds__(Cfg<D, RT>::kThreads, 1)
           if (tg < CG) {
             const int r = col + tg;
             const float mo = s_m[s][r];
-            float mn, f = 1.f;
-            if (unset) {
-              mn = fmaxf(mo, fmaxf(fmaxf(red[s][0][r], red[s][1][r]), fmaxf(red[s][2][r], red[s][3][r])));
-              if (mo != NEG_INF) f = ex2(mo - mn);
+            const float z = fmaxf(fmaxf(red[s][0][r], red[s][1][r]), fmaxf(red[s][2][r], red[s][3][r]));
+            float mn = mo, f = 1.f;
+            if (mo == NEG_INF) {
+              mn = z;
               none = mn == NEG_INF;
-            } else {
-              const float over = __int_as_float(s_over[s][r]);
-              const float d = over > 0.f ? over - kMoved : 0.f;
-              mn = mo + d;
-              if (over > 0.f) f = ex2(-d);
-              s_over[s][r] = 0;
+            } else if (z > kGrow) {
+              mn = mo + (z - kMoved);
+              f = ex2(kMoved - z);
             }
             s_m[s][r] = mn;
             s_f[s][r] = f;
@@ -983,7 +983,7 @@ __global__ void __launch_bounds__(Cfg<D, RT>::kThreads, 1)
         float z[16];
 #pragma unroll
         for (int j = 0; j < 16; j += 2) unpack2(l2[(j0 + j) / 2], z[j], z[j + 1]);
-        const float sum = warp_columns<true>(z, lane);
+        const float sum = warp_columns(z, lane);
         if (!(lane & 1)) red[s][wg][col + j0 + (lane >> 1)] = sum;
       }
       const int il = i0 + n - 1;
@@ -1027,23 +1027,19 @@ __global__ void __launch_bounds__(Cfg<D, RT>::kThreads, 1)
       const bool nan = s_nan[seg & 1] != 0;
       if (D == 128 || wg < 2) {
 #pragma unroll 1
-        for (int j0 = sgrp * 16; j0 < RT; j0 += NSTR * C::kGroups * 16) {
-          float o[16];
-#pragma unroll
-          for (int j = 0; j < 16; ++j) o[j] = 0.f;
+        for (int j0 = sgrp * 4; j0 < RT; j0 += NSTR * C::kGroups * 4) {
+          const int r0 = mt * RT + j0;
+          if (r0 >= a.nrows) break;
+          float o[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 1
           for (int k = 0; k < NSTR; ++k) {
             if (!took_part(k)) continue;
-            float o1[16], o2[16];
+            float o1[4], o2[4];
             const uint32_t at = tmem + C::kOCol + k * (2 * RT) + j0 + lane_off;
-            tmem_ld16_async(at, o1);
-            tmem_ld16_async(at + RT, o2);
-            tmem_wait16(o1);
-            tmem_wait16(o2);
+            tmem_ld4(at, o1, at + RT, o2);
 #pragma unroll
-            for (int j = 0; j < 16; ++j) o[j] = fmaf(fmaf(o2[j], 0.03125f, o1[j]), s_f[k][j0 + j], o[j]);
+            for (int j = 0; j < 4; ++j) o[j] = fmaf(fmaf(o2[j], 0.03125f, o1[j]), s_f[k][j0 + j], o[j]);
           }
-          const int r0 = mt * RT + j0;
           if (nan) {
             // tree nodes of this segment whose v holds NaN at this thread's element
             for (int node = max(0, sg.t0 * kKeys - sg.L); node < a.N && sg.L + node < min(sg.nkeys, sg.t1 * kKeys);
@@ -1054,7 +1050,7 @@ __global__ void __launch_bounds__(Cfg<D, RT>::kThreads, 1)
               if (!good_scale(a.ks[unit]) || !good_scale(a.vs[unit])) continue;
               if ((a.vc[(unit * kPage + pos % kPage) * D + tg] & 0x7F) != 0x7F) continue;
 #pragma unroll
-              for (int j = 0; j < 16; ++j) {
+              for (int j = 0; j < 4; ++j) {
                 const int qi = min(static_cast<int>(((r0 + j) * a.group_magic) >> 16), kMaxNodes - 1);
                 if ((anc[buf][qi][node >> 5] >> (node & 31)) & 1u) o[j] = __int_as_float(0x7fc00000);
               }
@@ -1062,7 +1058,7 @@ __global__ void __launch_bounds__(Cfg<D, RT>::kThreads, 1)
           }
           if (whole) {
 #pragma unroll
-            for (int j = 0; j < 16; ++j) {
+            for (int j = 0; j < 4; ++j) {
               const int r = r0 + j;
               if (r >= a.nrows) break;
               const int qi = static_cast<int>((r * a.group_magic) >> 16), head = hk * a.group + (r - qi * a.group);
@@ -1073,7 +1069,7 @@ __global__ void __launch_bounds__(Cfg<D, RT>::kThreads, 1)
             }
           } else {
 #pragma unroll
-            for (int j = 0; j < 16; ++j) a.part_o[(static_cast<int64_t>(slot) * RT + j0 + j) * D + tg] = o[j];
+            for (int j = 0; j < 4; ++j) a.part_o[(static_cast<int64_t>(slot) * RT + j0 + j) * D + tg] = o[j];
           }
         }
       }
