@@ -55,35 +55,39 @@ namespace q8 {
 
 constexpr int kPage = 16;
 constexpr int kMaxNodes = 128;
-constexpr int kKeys = 128;                 // keys per tile (MMA M of S^T, K of O^T)
-constexpr int kPages = kKeys / kPage;      // 8
+constexpr int kSub = 128;                  // keys of a sub-tile (MMA M of S^T, K of O^T)
+constexpr int kPages = kSub / kPage;       // 8
 // P v_scale is at most 2^4 where m was taken (the first tile), and m moves
 // before it exceeds 2^8 (e4m3 ends at 448), to where it is 2^5: the first
 // tile's largest of 128 keys is a low guess of the largest of thousands, and
 // moving m costs about a tile's time.
 constexpr float kBias = 4.f, kMoved = 5.f, kGrow = 8.f;
-constexpr int kMinChunk = 4;               // tiles of the smallest piece: below, joining costs more than it gives
+constexpr int kMinKeys = 512;              // keys of the smallest piece: below, joining costs more than it gives
 constexpr int kSmemBudget = 212 * 1024;
-constexpr int kMeta = 16;                  // tiles whose block scales are held
 constexpr int kTmaWarps = 2;               // producer warps; each issues half of a tile's copies
 constexpr int kWarpPages = kPages / kTmaWarps;
-constexpr int kBatch = 32 / kWarpPages;    // tiles that a producer warp's lanes hold the blocks of
+constexpr int kBatch = 32 / kWarpPages;    // sub-tiles that a producer warp's lanes hold the blocks of
 
-SSD_DEV void umma_f8(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t accum) {
+// D[tmem] (+)= A B of one 32-byte step of K; A and B by the low words of their
+// shared-memory descriptors (the high words are constants)
+SSD_DEV void umma_f8(uint32_t d_tmem, uint32_t alo, uint32_t ahi, uint32_t blo, uint32_t bhi, uint32_t idesc,
+                     uint32_t accum) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d_tmem),
-      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accum)
+      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
+      "mov.b64 a, {%1, %2};\n\t"
+      "mov.b64 b, {%3, %4};\n\t"
+      "setp.ne.b32 p, %6, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %5, p;\n\t}\n" ::"r"(d_tmem),
+      "r"(alo), "r"(ahi), "r"(blo), "r"(bhi), "r"(idesc), "r"(accum)
       : "memory");
 }
-// Shared-memory matrix descriptor, 128-byte (D = 128 rows) or 64-byte swizzle;
-// sbo: bytes between groups of 8 rows; lbo: between column blocks of an MN-major
-// operand (0: the second block repeats the first).
-SSD_DEV uint64_t smem_desc(uint32_t saddr, uint32_t lbo, uint32_t sbo, uint32_t swizzle) {
-  return static_cast<uint64_t>((saddr >> 4) & 0x3FFFu) | static_cast<uint64_t>((lbo >> 4) & 0x3FFFu) << 16 |
-         static_cast<uint64_t>((sbo >> 4) & 0x3FFFu) << 32 | static_cast<uint64_t>(1u) << 46 |
-         static_cast<uint64_t>(swizzle) << 61;
+// Shared-memory matrix descriptor, 128-byte or (D = 64 rows) 64-byte swizzle.
+// Low word: address / 16, and the bytes / 16 between column blocks of an
+// MN-major operand (0: the second block repeats the first); high word: bytes /
+// 16 between groups of 8 rows, version, swizzle.
+SSD_DEV constexpr uint32_t desc_lo(uint32_t saddr, uint32_t lbo) { return (saddr >> 4) | ((lbo >> 4) << 16); }
+__host__ __device__ constexpr uint32_t desc_hi(uint32_t sbo, uint32_t swizzle) {
+  return (sbo >> 4) | (1u << 14) | (swizzle << 29);
 }
 constexpr uint32_t kSw128 = 2, kSw64 = 4;
 // Instruction descriptor: fp32 sums, e4m3 A and B, both K-major (mn = 0) or MN-major (mn = 1), M = 128
@@ -233,6 +237,7 @@ struct Args {
   int B, N, Nq, Hq, Hkv, group, nrows, mtiles, per_b;  // per_b: items of a sequence
   uint32_t group_magic;                                // row / group = row * magic >> 16 (row < 4096)
   int split;                                           // pieces may cut items
+  int keys;                                            // keys of a tile
   float scale_log2;
   uint16_t *out;
   float *lse;
@@ -245,11 +250,11 @@ struct Args {
 SSD_DEV int keys_of(const Args &a, int b, int &L) {
   L = max(a.prefix_len[b], 0);
   const int64_t n = min(static_cast<int64_t>(L) + a.N, static_cast<int64_t>(a.maxb) * kPage);
-  return static_cast<int>(min(n, static_cast<int64_t>(0x7fffffff - kKeys)));
+  return static_cast<int>(min(n, static_cast<int64_t>(0x7fffffff - 2 * kSub)));
 }
 SSD_DEV int tiles_of(const Args &a, int b) {
   int L;
-  return (keys_of(a, b, L) + kKeys - 1) / kKeys;
+  return (keys_of(a, b, L) + a.keys - 1) / a.keys;
 }
 
 // A CTA's piece of the line of units.
@@ -265,7 +270,7 @@ struct Segments {
   int b, hk, mt, nt, nkeys, L, t0, t1, left;
   SSD_DEV void sequence(const Args &a) {
     nkeys = keys_of(a, b, L);
-    nt = (nkeys + kKeys - 1) / kKeys;
+    nt = (nkeys + a.keys - 1) / a.keys;
   }
   SSD_DEV bool first(const Args &a, const Piece &p) {
     if (p.left <= 0) return false;
@@ -328,7 +333,9 @@ struct Order {
 
 template <int D, int RT>
 struct Cfg {
-  static constexpr int NSTR = RT <= 16 ? 3 : (RT <= 32 ? 2 : 1);  // streams
+  static constexpr int KT = RT <= 64 ? 2 : 1;              // sub-tiles of a tile
+  static constexpr int kKeys = KT * kSub;                  // keys of a tile
+  static constexpr int NSTR = 1;                           // streams
   static constexpr int CG = RT <= 64 ? 16 : 32;            // rows of a softmax warp
   static constexpr int kGroups = RT / CG;                  // groups of four warps in a stream
   static constexpr int NB = NSTR > 1 ? NSTR : 2;           // S and P buffers; S runs NB tiles ahead
@@ -336,25 +343,25 @@ struct Cfg {
   static constexpr int kTmaWarp = kSoftWarps, kMmaWarp = kTmaWarp + kTmaWarps, kPrepWarp = kMmaWarp + 1;
   static constexpr int kWarps = kPrepWarp + 1;
   static constexpr int kThreads = kWarps * 32;
-  static_assert(kWarps == 16 || kWarps == 20, "warps");    // 128 or 96 registers a thread
   static constexpr int kQTile = RT * 128;                  // q1 (or q2) at D = 128; [q1 | q2] at D = 64
   static constexpr int kQBuf = D == 128 ? 2 * kQTile : kQTile;
-  static constexpr int kPBlock = kKeys * 128;              // 128 values of N: a 128-byte row per key
-  static constexpr int kPBuf = RT > 64 ? 2 * kPBlock : kPBlock;  // p1 [RT] then p2 [RT] along N
-  static constexpr int kSlot = kKeys * D;                  // K or V of a tile
-  static constexpr int kFixed = 2 * kQBuf + NB * kPBuf;
+  static constexpr int kPBlock = kSub * 128;               // 128 values of N: a 128-byte row per key
+  static constexpr int kPBuf = RT > 64 ? 2 * kPBlock : kPBlock;  // p1 [RT] then p2 [RT] along N, of a sub-tile
+  static constexpr int kSlot = kSub * D;                   // K or V of a sub-tile
+  static constexpr int kFixed = 2 * kQBuf + NB * KT * kPBuf;
   static constexpr int kFit = (kSmemBudget - kFixed) / kSlot;
   static constexpr int kSlots = kFit > 16 ? 16 : kFit;
   static constexpr int kQ = 0, kP = 2 * kQBuf, kRing = kFixed;
   static constexpr int kSmem = kFixed + kSlots * kSlot + 1024;
-  static constexpr int kOCol = NB * RT;                    // TMEM: NB x S, then O1, O2 of each stream
+  static constexpr int kOCol = NB * KT * RT;               // TMEM: NB x KT x S, then O1, O2 of each stream
   static constexpr uint32_t kCols = kOCol + NSTR * 2 * RT;
   static constexpr uint32_t kTmem = kCols <= 64 ? 64 : (kCols <= 128 ? 128 : (kCols <= 256 ? 256 : 512));
+  static constexpr int kMeta = 16 / KT;                    // tiles whose block scales are held
   static_assert(kSmem + 13824 <= 227 * 1024, "shared memory with the static part");
-  static_assert(kSlots >= NB + 2, "S runs NB tiles ahead");
-  // the scales of tile i + kMeta are written when a slot used up to tile i + kMeta - NB - (kSlots + 1) / 2 is free
-  static_assert(kMeta >= NB + (kSlots + 1) / 2 + 1, "block scales");
-  static_assert(kCols <= 512 && RT % CG == 0 && CG % 16 == 0 && NSTR * kGroups <= 8, "rows");
+  static_assert(kSlots >= (NB + 1) * KT, "S runs NB tiles ahead");
+  // the scales of tile i + kMeta are written when the slots used up to tile i + kMeta - NB - kSlots / (2 KT) are free
+  static_assert(kMeta >= NB + (kSlots + 2 * KT - 1) / (2 * KT) + 1, "block scales");
+  static_assert(kCols <= 512 && RT % CG == 0 && CG % 16 == 0 && CG <= 32 && NSTR * kGroups <= 8, "rows");
 };
 
 // A segment's rows: q1, q2 into the operand tiles at qb, the row scales, and
@@ -382,7 +389,7 @@ __device__ __noinline__ void prepare_rows(const Args &a, const Segments sg, uint
   };
   uint4 x[V], next[V];
   fetch(w * 8 + (lane >> 2), x);
-  const bool tree = sg.t1 * kKeys > sg.L;
+  const bool tree = static_cast<int64_t>(sg.t1) * C::kKeys > sg.L;
   if (tree)
     for (int m = w * 32 + lane; m < a.N; m += n * 32) par[m] = a.parent[static_cast<int64_t>(sg.b) * a.N + m];
   if (w == 0 && lane == 0) {
@@ -464,7 +471,7 @@ __global__ void __launch_bounds__(Cfg<D, RT>::kThreads, 1)
     k_branch_attn_q8(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                      const __grid_constant__ Args a) {
   using C = Cfg<D, RT>;
-  constexpr int NSTR = C::NSTR, CG = C::CG, NB = C::NB, NSLOT = C::kSlots;
+  constexpr int NSTR = C::NSTR, CG = C::CG, NB = C::NB, NSLOT = C::kSlots, KT = C::KT, kMeta = C::kMeta;
   constexpr int kSoftThreads = C::kSoftWarps * 32;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t *const smem =
@@ -473,7 +480,7 @@ __global__ void __launch_bounds__(Cfg<D, RT>::kThreads, 1)
   __shared__ __align__(8) uint64_t sfull[NB], pfull[NB], pvdone[NB], qfull[2], qempty[2];
   __shared__ uint32_t tmem_base;
   // a block's k_scale * scale * log2 e, v_scale (-1: hidden), log2 v_scale
-  __shared__ __align__(16) float4 meta[kMeta][kPages];
+  __shared__ __align__(16) float4 meta[kMeta][KT * kPages];
   __shared__ int par[2][kMaxNodes];
   __shared__ uint32_t anc[2][kMaxNodes][kMaxNodes / 32];    // per query: the nodes that it sees
   __shared__ float qs[2][RT];                               // row scales 2^e
@@ -532,7 +539,7 @@ __global__ void __launch_bounds__(Cfg<D, RT>::kThreads, 1)
     }
     const long long T = total * a.per_b;
     long long chunk = (T + gridDim.x - 1) / gridDim.x;
-    if (a.split && chunk < kMinChunk) chunk = kMinChunk;
+    if (a.split) chunk = max(chunk, static_cast<long long>(kMinKeys / C::kKeys));
     const long long lo = chunk * blockIdx.x, hi = min(T, lo + chunk);
     long long x = (before + inc - mine) * a.per_b;  // units before this thread's first sequence
     if (lo < hi && lo >= x && lo < x + mine * a.per_b) {
@@ -578,11 +585,11 @@ __global__ void __launch_bounds__(Cfg<D, RT>::kThreads, 1)
       float ks, vs;
     };
     bool more = sg.first(a, piece);
-    int t = more ? sg.t0 : 0;
-    auto advance = [&](int n) {  // this lane's place in the line of tiles
+    int t = more ? sg.t0 * KT : 0;
+    auto advance = [&](int n) {  // this lane's place in the line of sub-tiles
       t += n;
-      while (more && t >= sg.t1) {
-        t -= sg.t1;
+      while (more && t >= sg.t1 * KT) {
+        t -= sg.t1 * KT;
         more = sg.step(a);
       }
     };
@@ -652,25 +659,30 @@ __global__ void __launch_bounds__(Cfg<D, RT>::kThreads, 1)
     order.start(a, piece);
     for (int i = 0, j = 0; j < ntiles && ok;) {
       if (i < ntiles && i - j < NB && i < order.hold) {  // K of tile i
-        const int w = i % kBatch;
-        if (w == 0 && i > 0) {
-          old = now;
-          now = next;
-          check(now);
-          advance(kBatch);
-          ids(next);
+        for (int h = 0; h < KT && ok; ++h) {
+          const int x = i * KT + h, w = x % kBatch;
+          if (w == 0 && x > 0) {
+            old = now;
+            now = next;
+            check(now);
+            advance(kBatch);
+            ids(next);
+          }
+          if (w == kBatch / 2) scales(next);
+          if (lane / kWarpPages == w) {
+            const float v = now.vs < kMinBlockScale ? 0.f : now.vs;
+            meta[i % kMeta][h * kPages + page] =
+                now.blk >= 0 ? make_float4(now.ks * a.scale_log2, v, log2f(fmaxf(v, kMinBlockScale)), 0.f)
+                             : make_float4(0.f, -1.f, 0.f, 0.f);
+          }
+          load(now, w, &kmap);
         }
-        if (w == kBatch / 2) scales(next);
-        if (lane / kWarpPages == w) {
-          const float v = now.vs < kMinBlockScale ? 0.f : now.vs;
-          meta[i % kMeta][page] = now.blk >= 0
-                                      ? make_float4(now.ks * a.scale_log2, v, log2f(fmaxf(v, kMinBlockScale)), 0.f)
-                                      : make_float4(0.f, -1.f, 0.f, 0.f);
-        }
-        load(now, w, &kmap);
         ++i;
       } else {  // V of tile j
-        load(j / kBatch == (i - 1) / kBatch ? now : old, j % kBatch, &vmap);
+        for (int h = 0; h < KT && ok; ++h) {
+          const int x = j * KT + h;
+          load(x / kBatch == (i * KT - 1) / kBatch ? now : old, x % kBatch, &vmap);
+        }
         order.done(a, ++j);
       }
     }
@@ -680,9 +692,13 @@ __global__ void __launch_bounds__(Cfg<D, RT>::kThreads, 1)
         for (int i = max(0, issued - NSLOT); i < issued; ++i) (void)mbar_wait(&full[i % NSLOT], (i / NSLOT) & 1);
     }
   } else if (warp == C::kMmaWarp) {
-    // ---------------- MMA issue (one elected lane): O += P(i - NB) V(i - NB), then S(i)
+    // ---------------- MMA issue (one elected lane): S of up to NB tiles ahead, then P V and S in turn.  This loop
+    // is one warp's chain of scalar work per tile, so what can be is kept in running words.
     constexpr uint32_t idesc_s = idesc_f8(RT, 0), idesc_o = idesc_f8(2 * RT, 1);
+    constexpr uint32_t hi128 = desc_hi(1024, kSw128), hi64 = desc_hi(512, kSw64), hi_kv = D == 128 ? hi128 : hi64;
     const uint32_t base = smem_u32(smem);
+    const uint32_t ring_k = desc_lo(base + C::kRing, 16), ring_v = desc_lo(base + C::kRing, D == 128 ? 16 : 0);
+    const uint32_t p_lo = desc_lo(base + C::kP, C::kPBlock);
     bool ok = true;
     int slot = 0, seg = 0;
     uint32_t phase = 0;  // of full[slot]
@@ -694,63 +710,69 @@ __global__ void __launch_bounds__(Cfg<D, RT>::kThreads, 1)
         phase ^= 1;
       }
     };
-    Order order;
-    order.start(a, piece);
-    for (int i = 0, j = 0; j < ntiles;) {
-      if (i < ntiles && i - j < NB && i < order.hold) {  // S of tile i
-        const int buf = seg & 1, u = i % NB;
-        if (t == sg.t0) ok = warp_wait(&qfull[buf], (seg >> 1) & 1);
+    auto umma_s = [&](uint32_t d, uint32_t k, uint32_t q) {
+#pragma unroll
+      for (int term = 0; term < 2; ++term)
+#pragma unroll
+        for (int kk = 0; kk < D / 32; ++kk)
+          umma_f8(d, k + kk * 2, hi_kv, q + (term * (D == 128 ? C::kQTile : 64) >> 4) + kk * 2, hi128, idesc_s,
+                  (term > 0 || kk > 0) ? 1u : 0u);
+    };
+    auto issue_s = [&](int i) {
+      const int buf = seg & 1, u = i % NB;
+      if (t == sg.t0) ok = warp_wait(&qfull[buf], (seg >> 1) & 1);
+      const uint32_t q = desc_lo(base + C::kQ, 16) + buf * (C::kQBuf >> 4);
+      const bool last = ++t == sg.t1;
+#pragma unroll
+      for (int h = 0; h < KT; ++h) {
         // the S buffer is free: P of tile i - NB, made from it, has been waited for
         ok = ok && warp_wait(&full[slot], phase);
-        if (!ok) break;
         tc_fence_after();
-        const uint32_t k = base + C::kRing + slot * C::kSlot;
-        const uint32_t q = base + C::kQ + buf * C::kQBuf;
-        const bool last = t == sg.t1 - 1;
+        if (!ok) return;
         if (elect_one()) {
-#pragma unroll
-          for (int term = 0; term < 2; ++term)
-#pragma unroll
-            for (int kk = 0; kk < D / 32; ++kk) {
-              const uint64_t kd = D == 128 ? smem_desc(k + kk * 32, 16, 1024, kSw128)
-                                           : smem_desc(k + kk * 32, 16, 512, kSw64);
-              const uint32_t qa = q + (D == 128 ? term * C::kQTile : term * 64) + kk * 32;
-              umma_f8(tmem + u * RT, kd, smem_desc(qa, 16, 1024, kSw128), idesc_s, (term > 0 || kk > 0) ? 1u : 0u);
-            }
-          umma_commit(&sfull[u]);
+          umma_s(tmem + (u * KT + h) * RT, ring_k + slot * (C::kSlot >> 4), q);
           umma_commit(&empty[slot]);
-          if (last) umma_commit(&qempty[buf]);
+          if (h == KT - 1) {
+            umma_commit(&sfull[u]);
+            if (last) umma_commit(&qempty[buf]);
+          }
         }
         __syncwarp();
         next_slot();
-        ++i;
-        if (++t == sg.t1) {
-          more = sg.step(a);
-          t = sg.t0;
-          ++seg;
-        }
+      }
+      if (last) {
+        more = sg.step(a);
+        t = sg.t0;
+        ++seg;
+      }
+    };
+    Order order;
+    order.start(a, piece);
+    for (int i = 0, j = 0; j < ntiles && ok;) {
+      if (i < ntiles && i - j < NB && i < order.hold) {
+        issue_s(i++);
       } else {  // P V of tile j
         const int u = j % NB;
-        ok = warp_wait(&full[slot], phase) && warp_wait(&pfull[u], (j / NB) & 1);
-        if (!ok) break;
-        tc_fence_after();
-        const uint32_t v = base + C::kRing + slot * C::kSlot;
-        const uint32_t p = base + C::kP + u * C::kPBuf;
-        const uint32_t o = tmem + C::kOCol + (j % NSTR) * (2 * RT);
-        const bool fresh = j - order.begin < NSTR;  // the stream's first tile of the segment
-        if (elect_one()) {
+        const uint32_t o = tmem + C::kOCol + (NSTR == 1 ? 0 : (j % NSTR) * (2 * RT));
+        const uint32_t later = j - order.begin >= NSTR;  // not the stream's first tile of the segment
+        ok = warp_wait(&pfull[u], (j / NB) & 1);
 #pragma unroll
-          for (int kk = 0; kk < kKeys / 32; ++kk) {
-            // 32 keys: four groups of 8 rows
-            const uint64_t vd = D == 128 ? smem_desc(v + kk * 4096, 16, 1024, kSw128)
-                                         : smem_desc(v + kk * 2048, 0, 512, kSw64);
-            umma_f8(o, vd, smem_desc(p + kk * 4096, C::kPBlock, 1024, kSw128), idesc_o, (!fresh || kk > 0) ? 1u : 0u);
+        for (int h = 0; h < KT; ++h) {
+          ok = ok && warp_wait(&full[slot], phase);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t v = ring_v + slot * (C::kSlot >> 4), p = p_lo + (u * KT + h) * (C::kPBuf >> 4);
+          if (elect_one()) {
+#pragma unroll
+            for (int kk = 0; kk < kSub / 32; ++kk)  // 32 keys: four groups of 8 rows
+              umma_f8(o, v + kk * ((32 * D) >> 4), hi_kv, p + kk * (4096 >> 4), hi128, idesc_o,
+                      (h > 0 || kk > 0) ? 1u : later);
+            umma_commit(&empty[slot]);
+            if (h == KT - 1) umma_commit(&pvdone[u]);
           }
-          umma_commit(&pvdone[u]);
-          umma_commit(&empty[slot]);
+          __syncwarp();
+          next_slot();
         }
-        __syncwarp();
-        next_slot();
         order.done(a, ++j);
       }
     }
@@ -811,39 +833,62 @@ __global__ void __launch_bounds__(Cfg<D, RT>::kThreads, 1)
         ok = ok && warp_wait(&sfull[u], sphase >> u & 1);
         sphase ^= 1u << u;  // the scales were there before K was
         tc_fence_after();
-        const float4 sc = meta[i % kMeta][tg / kPage];
-        const float c = sc.x, wv = fmaxf(sc.y, 0.f), lsv = sc.z;
-        // the rows that see this thread's key
-        const int pos = t * kKeys + tg;
-        const bool hidden = sc.y < 0.f || pos >= sg.nkeys;
-        const bool part = __any_sync(0xffffffffu, hidden || pos >= sg.L);
-        uint64_t vis = hidden ? 0ull : ~0ull;
-        if (part && !hidden && pos >= sg.L) {
-          const int node = pos - sg.L;
-          vis = 0;
-          // row j is query (row0 + j) / group: the rows of one query are neighbours
-          int qi = static_cast<int>((row0 * a.group_magic) >> 16), j0 = 0;
-#pragma unroll 1
-          for (int j1 = (qi + 1) * a.group - row0; j0 < CG && qi < a.Nq; ++qi, j0 = j1, j1 += a.group)
-            if ((anc[buf][qi][node >> 5] >> (node & 31)) & 1u)
-              vis |= (j1 < 64 ? (1ull << j1) - 1ull : ~0ull) & (~0ull << j0);
+        // this thread's keys: their scales, and the rows that see them
+        float c[KT], wv[KT], lsv[KT];
+        uint32_t vis[KT];
+        bool hidden[KT], part = false;
+#pragma unroll
+        for (int h = 0; h < KT; ++h) {
+          const float4 sc = meta[i % kMeta][h * kPages + tg / kPage];
+          c[h] = sc.x;
+          wv[h] = fmaxf(sc.y, 0.f);
+          lsv[h] = sc.z;
+          const int pos = t * C::kKeys + h * kSub + tg;
+          hidden[h] = sc.y < 0.f || pos >= sg.nkeys;
+          part = part || hidden[h] || pos >= sg.L;
         }
-        const uint64_t c2 = pack2(c, c);
-        float y[CG];
+        part = __any_sync(0xffffffffu, part);
+        if (part) {
+#pragma unroll
+          for (int h = 0; h < KT; ++h) {
+            const int node = t * C::kKeys + h * kSub + tg - sg.L;
+            vis[h] = hidden[h] ? 0u : ~0u;
+            if (!hidden[h] && node >= 0) {
+              // row j is query (row0 + j) / group: the rows of one query are neighbours
+              uint32_t see = 0;
+              int qi = static_cast<int>((row0 * a.group_magic) >> 16), j0 = 0;
+#pragma unroll 1
+              for (int j1 = (qi + 1) * a.group - row0; j0 < CG && qi < a.Nq; ++qi, j0 = j1, j1 += a.group)
+                if ((anc[buf][qi][node >> 5] >> (node & 31)) & 1u)
+                  see |= (j1 < 32 ? (1u << j1) - 1u : ~0u) & (~0u << j0);
+              vis[h] = see;
+            }
+          }
+        }
+        float y[KT][CG];
         // y = x - m + 4 (x for a row without m); hidden keys -inf
         auto scores = [&]() {
 #pragma unroll
-          for (int j = 0; j < CG; j += 16) tmem_ld16_async(tS + u * RT + j, y + j);
+          for (int h = 0; h < KT; ++h)
 #pragma unroll
-          for (int j = 0; j < CG; j += 16) tmem_wait16(y + j);
+            for (int j = 0; j < CG; j += 16) tmem_ld16_async(tS + (u * KT + h) * RT + j, y[h] + j);
+#pragma unroll
+          for (int h = 0; h < KT; ++h)
+#pragma unroll
+            for (int j = 0; j < CG; j += 16) tmem_wait16(y[h] + j);
 #pragma unroll
           for (int j = 0; j < CG; j += 2) {
             const float4 rc = rowc[s][(col + j) / 2];
-            unpack2(fma2(mul2(pack2(y[j], y[j + 1]), c2), pack2(rc.x, rc.y), pack2(rc.z, rc.w)), y[j], y[j + 1]);
+#pragma unroll
+            for (int h = 0; h < KT; ++h)
+              unpack2(fma2(mul2(pack2(y[h][j], y[h][j + 1]), pack2(c[h], c[h])), pack2(rc.x, rc.y), pack2(rc.z, rc.w)),
+                      y[h][j], y[h][j + 1]);
           }
           if (part) {
 #pragma unroll
-            for (int j = 0; j < CG; ++j) y[j] = ((vis >> j) & 1ull) ? y[j] : NEG_INF;
+            for (int h = 0; h < KT; ++h)
+#pragma unroll
+              for (int j = 0; j < CG; ++j) y[h][j] = ((vis[h] >> j) & 1u) ? y[h][j] : NEG_INF;
           }
         };
         // y, and whether a row's m has to move; then once more with the new m
@@ -851,16 +896,22 @@ __global__ void __launch_bounds__(Cfg<D, RT>::kThreads, 1)
         for (int pass = 0;; ++pass) {
           scores();
           if (pass == 1) break;
-          float t4[4] = {y[0], y[1], y[2], y[3]};
+          float top = NEG_INF;
 #pragma unroll
-          for (int j = 4; j < CG; ++j) t4[j & 3] = fmaxf(t4[j & 3], y[j]);
-          const float top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3])) + lsv;
+          for (int h = 0; h < KT; ++h) {
+            float t4[4] = {y[h][0], y[h][1], y[h][2], y[h][3]};
+#pragma unroll
+            for (int j = 4; j < CG; ++j) t4[j & 3] = fmaxf(t4[j & 3], y[h][j]);
+            top = fmaxf(top, fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3])) + lsv[h]);
+          }
           if (!bar_or(bar, 128, top > kGrow || unset || !ok)) break;
           // the rows' largest log2 of P v_scale (of a row without a key so far: x + log2 v_scale) in this tile
           float big = NEG_INF;
 #pragma unroll
           for (int j = 0; j < CG; ++j) {
-            const float z = warp_top(y[j] + lsv);
+            float z = y[0][j] + lsv[0];
+            if (KT == 2) z = fmaxf(z, y[KT - 1][j] + lsv[KT - 1]);
+            z = warp_top(z);
             if (lane == j) big = z;
           }
           if (lane < CG) red[s][wg][col + lane] = big;
@@ -915,48 +966,56 @@ __global__ void __launch_bounds__(Cfg<D, RT>::kThreads, 1)
         if (dead) break;
         begin = false;
         // the P buffer is free: S of this tile was issued behind P V of tile i - NB
-        uint8_t *const pb = smem + C::kP + u * C::kPBuf;
-        const uint64_t w2 = pack2(wv, wv);
 #pragma unroll
-        for (int j0 = 0; j0 < CG; j0 += 16) {
-          uint32_t p1[4], p2[4];
+        for (int h = 0; h < KT; ++h) {
+          uint8_t *const pb = smem + C::kP + (u * KT + h) * C::kPBuf;
+          const uint64_t w2 = pack2(wv[h], wv[h]);
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            uint16_t e1[2], e2[2];
+          for (int j0 = 0; j0 < CG; j0 += 16) {
+            uint32_t p1[4], p2[4];
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const int j = j0 + q * 4 + h * 2;
-              const uint64_t p = pack2(ex2(y[j]), ex2(y[j + 1]));
-              l2[j / 2] = add2(l2[j / 2], p);
-              float a0, a1;
-              unpack2(mul2(p, w2), a0, a1);
-              const uint32_t hp = half2_of(a0, a1);
-              e1[h] = e4m3_of_half2(hp);
-              // 32 (p - p1) in halves: exact (p is at most 2^8, the difference has at most 11 bits)
-              e2[h] = e4m3_of_half2(hfma2(e4m3_to_half2(e1[h]), 0xD000D000u, hmul2(hp, 0x50005000u)));
+            for (int q = 0; q < 4; ++q) {
+              uint16_t e1[2], e2[2];
+#pragma unroll
+              for (int x = 0; x < 2; ++x) {
+                const int j = j0 + q * 4 + x * 2;
+                const uint64_t p = pack2(ex2(y[h][j]), ex2(y[h][j + 1]));
+                l2[j / 2] = add2(l2[j / 2], p);
+                float a0, a1;
+                unpack2(mul2(p, w2), a0, a1);
+                const uint32_t hp = half2_of(a0, a1);
+                e1[x] = e4m3_of_half2(hp);
+                // 32 (p - p1) in halves: exact (p is at most 2^8, the difference has at most 11 bits)
+                e2[x] = e4m3_of_half2(hfma2(e4m3_to_half2(e1[x]), 0xD000D000u, hmul2(hp, 0x50005000u)));
+              }
+              p1[q] = pack16(e1[0], e1[1]);
+              p2[q] = pack16(e2[0], e2[1]);
             }
-            p1[q] = pack16(e1[0], e1[1]);
-            p2[q] = pack16(e2[0], e2[1]);
+            const int n1 = col + j0, n2 = RT + n1;  // places along N
+            *reinterpret_cast<uint4 *>(pb + (n1 >> 7) * C::kPBlock + sw128(tg, n1 & 127)) =
+                make_uint4(p1[0], p1[1], p1[2], p1[3]);
+            *reinterpret_cast<uint4 *>(pb + (n2 >> 7) * C::kPBlock + sw128(tg, n2 & 127)) =
+                make_uint4(p2[0], p2[1], p2[2], p2[3]);
           }
-          const int n1 = col + j0, n2 = RT + n1;  // places along N
-          *reinterpret_cast<uint4 *>(pb + (n1 >> 7) * C::kPBlock + sw128(tg, n1 & 127)) =
-              make_uint4(p1[0], p1[1], p1[2], p1[3]);
-          *reinterpret_cast<uint4 *>(pb + (n2 >> 7) * C::kPBlock + sw128(tg, n2 & 127)) =
-              make_uint4(p2[0], p2[1], p2[2], p2[3]);
         }
         if (part && g == 0) {
           // hidden keys take no part whatever their v holds (0 * NaN): their rows become 0; a tree node's NaN
           // becomes 0 too, and reaches the rows that see it at the end
           Segments after = sg;
           const int hold = after.step(a) ? i0 + n + after.t1 - after.t0 : ntiles;
-          const int load = min(min(ntiles, i + NB), hold) + i;  // V's place in the order of loads
-          ok = warp_wait(&full[load % NSLOT], (load / NSLOT) & 1) && ok;
-          uint8_t *const vt = smem + C::kRing + (load % NSLOT) * C::kSlot;
-          if (hidden || pos >= sg.L) {
+          const int load0 = (min(min(ntiles, i + NB), hold) + i) * KT;  // V's place in the order of loads
+#pragma unroll 1
+          for (int h = 0; h < KT; ++h) {
+            const int load = load0 + h;
+            const bool gone = KT == 2 && h ? hidden[KT - 1] : hidden[0];
+            ok = warp_wait(&full[load % NSLOT], (load / NSLOT) & 1) && ok;
+            uint8_t *const vt = smem + C::kRing + (load % NSLOT) * C::kSlot;
+            if (!gone && t * C::kKeys + h * kSub + tg < sg.L) continue;
+#pragma unroll 1
             for (int e = 0; e < D; e += 16) {
               uint4 *const at = reinterpret_cast<uint4 *>(vt + (D == 128 ? sw128(tg, e) : sw64(tg, e)));
               uint4 v = make_uint4(0, 0, 0, 0);
-              if (!hidden) {
+              if (!gone) {
                 v = *at;
                 uint32_t any = 0;
                 auto clear = [&](uint32_t w) {
@@ -1042,8 +1101,8 @@ __global__ void __launch_bounds__(Cfg<D, RT>::kThreads, 1)
           }
           if (nan) {
             // tree nodes of this segment whose v holds NaN at this thread's element
-            for (int node = max(0, sg.t0 * kKeys - sg.L); node < a.N && sg.L + node < min(sg.nkeys, sg.t1 * kKeys);
-                 ++node) {
+            const int from = sg.t0 * C::kKeys - sg.L, to = min(sg.nkeys, sg.t1 * C::kKeys) - sg.L;
+            for (int node = max(0, from); node < to; ++node) {
               const int pos = sg.L + node, blk = a.table[static_cast<int64_t>(sg.b) * a.maxb + pos / kPage];
               if (blk < 0 || blk >= a.num_blocks) continue;
               const int64_t unit = static_cast<int64_t>(blk) * a.Hkv + hk;
@@ -1191,6 +1250,7 @@ Workspace workspace_of(const Shape &s, int d, int ctas) {
 template <int D, int RT>
 cudaError_t launch(const CUtensorMap &kmap, const CUtensorMap &vmap, const Args &a, unsigned grid, cudaStream_t cs) {
   using C = q8::Cfg<D, RT>;
+  if (a.keys != C::kKeys) return cudaErrorInvalidValue;
   cudaError_t e = cudaFuncSetAttribute(q8::k_branch_attn_q8<D, RT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        C::kSmem);
   if (e != cudaSuccess) return e;
@@ -1277,12 +1337,14 @@ ssd_status_t ssd_branch_attention_q8(const void *q, const void *k_cache, const v
   a.status = status;
   // one CTA per SM, none without a tile of its own
   const int sms = attn_num_sms();
-  const int64_t max_tiles = (static_cast<int64_t>(maxb) * q8::kPage + q8::kKeys - 1) / q8::kKeys;
+  a.keys = sh.RT <= 64 ? 2 * q8::kSub : q8::kSub;
+  const int64_t max_keys = static_cast<int64_t>(maxb) * q8::kPage;
+  const int64_t max_tiles = (max_keys + a.keys - 1) / a.keys;
   const int64_t units = max_tiles * B * a.per_b;
   const unsigned grid = static_cast<unsigned>(units < sms ? units : sms);
-  // items of up to kMinChunk tiles are not worth cutting; without room for the parts none is
+  // items of up to kMinKeys keys are not worth cutting; without room for the parts none is
   const Workspace w = workspace_of(sh, d, sms);
-  a.split = max_tiles > q8::kMinChunk && ws && ws_bytes >= w.total && !(reinterpret_cast<uintptr_t>(ws) & 255u);
+  a.split = max_keys > q8::kMinKeys && ws && ws_bytes >= w.total && !(reinterpret_cast<uintptr_t>(ws) & 255u);
   if (a.split) {
     char *const p = static_cast<char *>(ws);
     a.part_o = reinterpret_cast<float *>(p + w.o);
