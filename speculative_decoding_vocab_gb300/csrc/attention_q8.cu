@@ -64,9 +64,8 @@ constexpr int kPages = kSub / kPage;       // 8
 constexpr float kBias = 4.f, kMoved = 5.f, kGrow = 8.f;
 constexpr int kMinKeys = 512;              // keys of the smallest piece: below, joining costs more than it gives
 constexpr int kSmemBudget = 212 * 1024;
-constexpr int kTmaWarps = 2;               // producer warps; each issues half of a tile's copies
-constexpr int kWarpPages = kPages / kTmaWarps;
-constexpr int kBatch = 32 / kWarpPages;    // sub-tiles that a producer warp's lanes hold the blocks of
+constexpr int kTmaWarps = 2;               // producer warps: warp p loads every sub-tile whose number is p modulo this
+constexpr int kBatch = 32 / kPages;        // sub-tiles that a producer warp's lanes hold the blocks of
 
 // D[tmem] (+)= A B of one 32-byte step of K; A and B by the low words of their
 // shared-memory descriptors (the high words are constants)
@@ -359,8 +358,11 @@ struct Cfg {
   static constexpr int kMeta = 16 / KT;                    // tiles whose block scales are held
   static_assert(kSmem + 13824 <= 227 * 1024, "shared memory with the static part");
   static_assert(kSlots >= (NB + 1) * KT, "S runs NB tiles ahead");
-  // the scales of tile i + kMeta are written when the slots used up to tile i + kMeta - NB - kSlots / (2 KT) are free
-  static_assert(kMeta >= NB + (kSlots + 2 * KT - 1) / (2 * KT) + 1, "block scales");
+  // A warp writes the scales of tile i before the wait of its load; its load before that lies at most kTmaWarps + 1
+  // loads back (KT = 1: K, V, and the other warps' pairs: 2 kTmaWarps - 1) and waited for the use of its slot, kSlots
+  // loads further back.  P V of tile i - NB is the last of a tile before the K loads of tile i.
+  static constexpr int kBack = kSlots + 2 * kTmaWarps + KT - 1;
+  static_assert(kMeta >= NB + (kBack + 2 * KT - 1) / (2 * KT), "block scales");
   static_assert(kCols <= 512 && RT % CG == 0 && CG % 16 == 0 && CG <= 32 && NSTR * kGroups <= 8, "rows");
 };
 
@@ -497,7 +499,7 @@ __global__ void __launch_bounds__(Cfg<D, RT>::kThreads, 1)
 
   if (tid == 0) {
     for (int s = 0; s < NSLOT; ++s) {
-      mbar_init(&full[s], kTmaWarps);
+      mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
     }
     for (int u = 0; u < NB; ++u) {
@@ -576,10 +578,11 @@ __global__ void __launch_bounds__(Cfg<D, RT>::kThreads, 1)
 
   Segments sg;
   if (warp >= C::kTmaWarp && warp < C::kMmaWarp) {
-    // ---------------- producers: each copies half of every tile's blocks.  Block ids and scales are fetched for
-    // kBatch tiles at a time, one batch ahead (two dependent trips to memory for a batch, not for a tile): lane l
-    // holds block l % kWarpPages of the warp's in tile l / kWarpPages of the batch.
-    const int page0 = (warp - C::kTmaWarp) * kWarpPages, page = page0 + lane % kWarpPages;  // of the tile
+    // ---------------- producers.  A load's fixed work costs its warp about 500 clocks and a copy 65 (the TMA unit's
+    // own pace for 2 KB), so a warp issues all eight copies of every second sub-tile.  Block ids and scales are
+    // fetched for kBatch of its sub-tiles at a time, one batch ahead (two dependent trips to memory for a batch):
+    // lane l holds block l % 8 of the batch's sub-tile l / 8.
+    const int pw = warp - C::kTmaWarp, page = lane % kPages;
     struct Batch {
       int hk, blk;
       float ks, vs;
@@ -603,6 +606,7 @@ __global__ void __launch_bounds__(Cfg<D, RT>::kThreads, 1)
         x.blk = a.table[static_cast<int64_t>(sg.b) * a.maxb + lp];
         x.ks = 0.f;
       }
+      advance(kBatch * kTmaWarps);
     };
     auto scales = [&](Batch &x) {
       if (x.blk >= 0 && x.blk < a.num_blocks) {
@@ -614,82 +618,94 @@ __global__ void __launch_bounds__(Cfg<D, RT>::kThreads, 1)
         x.blk = -1;
       }
     };
-    auto check = [&](Batch &x) {  // bad scales hide their block
-      if (x.blk >= 0 && !(good_scale(x.ks) && good_scale(x.vs))) {
-        atomicOr(a.status, kFlagBadValue);
-        x.blk = -1;
-      }
-    };
     Batch old, now, next;
-    advance(lane / kWarpPages);
-    ids(now);
-    scales(now);
-    check(now);
-    advance(kBatch);
+    advance(lane / kPages * kTmaWarps + pw);
     ids(next);
-    old = now;
-    int slot = 0;
-    uint32_t phase = 1;  // of empty[slot]; the first round's slots are free
-    int issued = 0;
+    scales(next);
+    now = old = next;
+    int slot = 0, mine = 0;  // `mine`: K sub-tiles that this warp has loaded
+    uint32_t phase = 1;      // of empty[slot]; the first round's slots are free
+    int issued = 0;          // loads so far, all warps'
+    uint32_t own = 0;        // bit k: the load k before the last was this warp's
     bool ok = true;
-    // one load: this warp's blocks of a tile into the next slot
-    auto load = [&](const Batch &x, int w, const CUtensorMap *map) {
-      const uint32_t which = __ballot_sync(0xffffffffu, x.blk >= 0) >> (w * kWarpPages) & ((1u << kWarpPages) - 1);
-      const int row = __shfl_sync(0xffffffffu, x.hk, w * kWarpPages) * kPage;
-      int blk[kWarpPages];
-#pragma unroll
-      for (int e = 0; e < kWarpPages; ++e) blk[e] = __shfl_sync(0xffffffffu, x.blk, w * kWarpPages + e);
-      ok = issued < NSLOT || warp_wait(&empty[slot], phase);
-      if (!ok) return;
-      uint8_t *const dst = smem + C::kRing + slot * C::kSlot + page0 * (kPage * D);
-      if (elect_one()) {
-        mbar_arrive_expect_tx(&full[slot], __popc(which) * (kPage * D));
-#pragma unroll
-        for (int e = 0; e < kWarpPages; ++e)
-          if ((which >> e) & 1u) tma_load_3d(dst + e * (kPage * D), map, 0, row, blk[e], &full[slot]);
-      }
-      __syncwarp();
+    auto next_slot = [&](bool mine) {
       ++issued;
+      own = own << 1 | static_cast<uint32_t>(mine);
       if (++slot == NSLOT) {
         slot = 0;
         phase ^= 1;
       }
+    };
+    // one load: sub-tile w of batch x into the next slot
+    auto load = [&](const Batch &x, int w, const CUtensorMap *map) {
+      const uint32_t which = __ballot_sync(0xffffffffu, x.blk >= 0) >> (w * kPages) & 0xFFu;
+      const int row = __shfl_sync(0xffffffffu, x.hk, w * kPages) * kPage;
+      int blk[kPages];
+#pragma unroll
+      for (int e = 0; e < kPages; ++e) blk[e] = __shfl_sync(0xffffffffu, x.blk, w * kPages + e);
+      ok = issued < NSLOT || warp_wait(&empty[slot], phase);
+      if (!ok) return;
+      uint8_t *const dst = smem + C::kRing + slot * C::kSlot;
+      if (elect_one()) {
+        mbar_arrive_expect_tx(&full[slot], __popc(which) * (kPage * D));
+        if (which == 0xFFu) {
+#pragma unroll
+          for (int e = 0; e < kPages; ++e) tma_load_3d(dst + e * (kPage * D), map, 0, row, blk[e], &full[slot]);
+        } else {
+#pragma unroll
+          for (int e = 0; e < kPages; ++e)
+            if ((which >> e) & 1u) tma_load_3d(dst + e * (kPage * D), map, 0, row, blk[e], &full[slot]);
+        }
+      }
+      __syncwarp();
     };
     Order order;
     order.start(a, piece);
     for (int i = 0, j = 0; j < ntiles && ok;) {
       if (i < ntiles && i - j < NB && i < order.hold) {  // K of tile i
         for (int h = 0; h < KT && ok; ++h) {
-          const int x = i * KT + h, w = x % kBatch;
-          if (w == 0 && x > 0) {
-            old = now;
-            now = next;
-            check(now);
-            advance(kBatch);
-            ids(next);
+          const bool m = (i * KT + h) % kTmaWarps == pw;
+          if (m) {
+            const int w = mine++ % kBatch;
+            if (w == 0) {
+              old = now;
+              now = next;
+              if (now.blk >= 0 && !(good_scale(now.ks) && good_scale(now.vs))) {  // bad scales hide their block
+                atomicOr(a.status, kFlagBadValue);
+                now.blk = -1;
+              }
+              ids(next);
+            }
+            if (w == kBatch / 2) scales(next);
+            if (lane / kPages == w) {
+              const float v = now.vs < kMinBlockScale ? 0.f : now.vs;
+              meta[i % kMeta][h * kPages + page] =
+                  now.blk >= 0 ? make_float4(now.ks * a.scale_log2, v, __log2f(fmaxf(v, kMinBlockScale)), 0.f)
+                               : make_float4(0.f, -1.f, 0.f, 0.f);
+            }
+            load(now, w, &kmap);
           }
-          if (w == kBatch / 2) scales(next);
-          if (lane / kWarpPages == w) {
-            const float v = now.vs < kMinBlockScale ? 0.f : now.vs;
-            meta[i % kMeta][h * kPages + page] =
-                now.blk >= 0 ? make_float4(now.ks * a.scale_log2, v, log2f(fmaxf(v, kMinBlockScale)), 0.f)
-                             : make_float4(0.f, -1.f, 0.f, 0.f);
-          }
-          load(now, w, &kmap);
+          next_slot(m && ok);
         }
         ++i;
       } else {  // V of tile j
         for (int h = 0; h < KT && ok; ++h) {
           const int x = j * KT + h;
-          load(x / kBatch == (i * KT - 1) / kBatch ? now : old, x % kBatch, &vmap);
+          const bool m = x % kTmaWarps == pw;
+          if (m) {
+            const int k = x / kTmaWarps;  // its number among this warp's
+            load(k / kBatch == (mine - 1) / kBatch ? now : old, k % kBatch, &vmap);
+          }
+          next_slot(m && ok);
         }
         order.done(a, ++j);
       }
     }
     if (!ok) {
       s_abort = 1;
-      if (lane == 0)  // copies in flight land before the shared memory is given back
-        for (int i = max(0, issued - NSLOT); i < issued; ++i) (void)mbar_wait(&full[i % NSLOT], (i / NSLOT) & 1);
+      // this warp's copies in flight land before the shared memory is given back
+      for (int k = 0, i = issued; k < NSLOT && --i >= 0; ++k)
+        if ((own >> k) & 1u) (void)warp_wait(&full[i % NSLOT], (i / NSLOT) & 1);
     }
   } else if (warp == C::kMmaWarp) {
     // ---------------- MMA issue (one elected lane): S of up to NB tiles ahead, then P V and S in turn.  This loop
