@@ -465,52 +465,53 @@ def ssd_tree_verify(target, draft, V, T, parent, tokens, u_acc, u_bonus, accept_
 # ---------------------------------------------------------------------------
 # the 8-bit cache of the branch decode
 # ---------------------------------------------------------------------------
-def _dense(x, dtype, shape, what):
-    """Address of a dense tensor of the given dtype and shape (None passes through)."""
+# These calls are made per layer and decode step, where the kernels take a few
+# microseconds: one pass of checks per tensor, messages built only for a refusal.
+def _refuse(x, dtype, shape, dev, what, how="contiguous"):
+    if x.get_device() != dev:
+        raise ValueError(f"all tensors of a call must live on one device, got {what} on {x.device}")
+    raise ValueError(f"{what} must be a {how} {dtype} tensor of shape {shape}, got {x.dtype} {tuple(x.shape)}")
+
+
+def _dense(x, dtype, shape, dev, what):
+    """Address of a dense tensor of the given dtype, shape and device (None passes through)."""
     if x is None:
         return None
-    if x.dtype != dtype or tuple(x.shape) != shape or not x.is_contiguous():
-        raise ValueError(f"{what} must be a contiguous {dtype} tensor of shape {shape}, got {x.dtype} {tuple(x.shape)}")
+    if x.dtype is not dtype or x.shape != shape or x.get_device() != dev or not x.is_contiguous():
+        _refuse(x, dtype, shape, dev, what)
     return x.data_ptr()
 
 
-def _codes(x, shape, what):
-    if x.dtype not in (torch.float8_e4m3fn, torch.uint8):
-        raise ValueError(f"{what} must hold e4m3 codes (float8_e4m3fn or uint8), got {x.dtype}")
-    return _dense(x, x.dtype, shape, what)
+def _codes(x, shape, dev, what):
+    dtype = x.dtype
+    if dtype is not torch.float8_e4m3fn and dtype is not torch.uint8:
+        raise ValueError(f"{what} must hold e4m3 codes (float8_e4m3fn or uint8), got {dtype}")
+    return _dense(x, dtype, shape, dev, what)
 
 
-def _rows(x, dtype, shape, what):
+def _rows(x, dtype, shape, dev, what):
     """Address and (sequence, token) strides of [B, S, H, d] rows whose heads are dense."""
-    if x.dtype != dtype or tuple(x.shape) != shape:
-        raise ValueError(f"{what} must be a {dtype} tensor of shape {shape}, got {x.dtype} {tuple(x.shape)}")
+    if x.dtype is not dtype or x.shape != shape or x.get_device() != dev:
+        _refuse(x, dtype, shape, dev, what, "strided")
     ss, ts, hs, es = x.stride()
     if (es != 1 and shape[3] > 1) or (hs != shape[3] and shape[2] > 1):
         raise ValueError(f"{what}: the heads of a token must be contiguous")
     return x.data_ptr(), ss if shape[0] > 1 else 0, ts if shape[1] > 1 else 0
 
 
-def _launch(call, fn, device, stream, *args):
-    """Call ``fn(*args, stream)`` with ``device`` (the tensors') current."""
-    if device.type != "cuda":
+def _launch(call, dev, stream, *args):
+    """``call(*args, stream)`` of the library with device ``dev`` (the tensors') current."""
+    if dev < 0:
         raise ValueError("tensors passed to the library must live on a CUDA device")
-    if stream is not None:
-        s = stream.cuda_stream
-    else:
-        s = torch._C._cuda_getCurrentRawStream(device.index)
-    if device.index == torch._C._cuda_getDevice():
+    fn = getattr(load(), call)
+    s = torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+    if dev == torch._C._cuda_getDevice():
         code = fn(*args, s)
     else:
-        with torch.cuda.device(device):
+        with torch.cuda.device(dev):
             code = fn(*args, s)
     if code != SSD_OK:
         _check(call, code)
-
-
-def _same_device(device, *tensors):
-    for x in tensors:
-        if x is not None and x.device != device:
-            raise ValueError(f"all tensors of a call must live on one device, got {device} and {x.device}")
 
 
 def ssd_block_table_update(length, reserve, block_table, pages, ring, pool, slots=None, status=None, stream=None):
@@ -522,12 +523,12 @@ def ssd_block_table_update(length, reserve, block_table, pages, ring, pool, slot
     n = ring.shape[0]
     S = 0 if slots is None else slots.shape[1]
     i32 = torch.int32
-    _same_device(block_table.device, length, pages, ring, pool, slots, status)
-    _launch("ssd_block_table_update", load().ssd_block_table_update, block_table.device, stream,
-            _dense(length, i32, (B,), "length"), int(reserve), B, _dense(block_table, i32, (B, maxb), "block_table"),
-            maxb, _dense(pages, i32, (B,), "pages"), _dense(ring, i32, (n,), "ring"), n,
-            _dense(pool, i32, (4,), "pool"), _dense(slots, i32, (B, S), "slots"), S,
-            _dense(status, i32, (1,), "status"))
+    dev = block_table.get_device()
+    _launch("ssd_block_table_update", dev, stream,
+            _dense(length, i32, (B,), dev, "length"), int(reserve), B, _dense(block_table, i32, (B, maxb), dev, "block_table"),
+            maxb, _dense(pages, i32, (B,), dev, "pages"), _dense(ring, i32, (n,), dev, "ring"), n,
+            _dense(pool, i32, (4,), dev, "pool"), _dense(slots, i32, (B, S), dev, "slots"), S,
+            _dense(status, i32, (1,), dev, "status"))
 
 
 def ssd_rope_frequencies(rot, base=10000.0, factor=1.0, original_len=0.0, fast=32.0, slow=1.0):
@@ -556,15 +557,15 @@ def ssd_tree_rope(q, k, turns, rot, prefix_len, q_out, k_out, parent=None, node0
     Hkv = 0 if k is None else k.shape[2]
     none = (None, 0, 0)
     N = 0 if parent is None else parent.shape[1]
-    _same_device(x.device, q, k, q_out, k_out, turns, prefix_len, parent, status)
-    _launch("ssd_tree_rope", load().ssd_tree_rope, x.device, stream,
-            *(none if q is None else _rows(q, x.dtype, (B, S, Hq, d), "q")),
-            *(none if q is None else _rows(q_out, x.dtype, (B, S, Hq, d), "q_out")),
-            *(none if k is None else _rows(k, x.dtype, (B, S, Hkv, d), "k")),
-            *(none if k is None else _rows(k_out, x.dtype, (B, S, Hkv, d), "k_out")), dt,
-            _dense(turns, torch.int64, (int(rot) // 2,), "turns"), int(rot), int(bool(interleaved)), float(mscale),
-            _dense(prefix_len, torch.int32, (B,), "prefix_len"), _dense(parent, torch.int32, (B, N), "parent"), N,
-            int(node0), B, S, Hq, Hkv, d, _dense(status, torch.int32, (1,), "status"))
+    dev = x.get_device()
+    _launch("ssd_tree_rope", dev, stream,
+            *(none if q is None else _rows(q, x.dtype, (B, S, Hq, d), dev, "q")),
+            *(none if q is None else _rows(q_out, x.dtype, (B, S, Hq, d), dev, "q_out")),
+            *(none if k is None else _rows(k, x.dtype, (B, S, Hkv, d), dev, "k")),
+            *(none if k is None else _rows(k_out, x.dtype, (B, S, Hkv, d), dev, "k_out")), dt,
+            _dense(turns, torch.int64, (int(rot) // 2,), dev, "turns"), int(rot), int(bool(interleaved)), float(mscale),
+            _dense(prefix_len, torch.int32, (B,), dev, "prefix_len"), _dense(parent, torch.int32, (B, N), dev, "parent"), N,
+            int(node0), B, S, Hq, Hkv, d, _dense(status, torch.int32, (1,), dev, "status"))
 
 
 def ssd_kv_append_q8(k_new, v_new, k_cache, v_cache, k_scale, v_scale, block_table, prefix_len, node0, count=None,
@@ -576,14 +577,14 @@ def ssd_kv_append_q8(k_new, v_new, k_cache, v_cache, k_scale, v_scale, block_tab
     nb = k_cache.shape[0]
     maxb = block_table.shape[1]
     i32, f32 = torch.int32, torch.float32
-    _same_device(k_cache.device, k_new, v_new, v_cache, k_scale, v_scale, block_table, prefix_len, count, status)
-    _launch("ssd_kv_append_q8", load().ssd_kv_append_q8, k_cache.device, stream,
-            *_rows(k_new, torch.bfloat16, (B, S, Hkv, d), "k_new"),
-            *_rows(v_new, torch.bfloat16, (B, S, Hkv, d), "v_new"),
-            _codes(k_cache, (nb, Hkv, 16, d), "k_cache"), _codes(v_cache, (nb, Hkv, 16, d), "v_cache"),
-            _dense(k_scale, f32, (nb, Hkv), "k_scale"), _dense(v_scale, f32, (nb, Hkv), "v_scale"),
-            _dense(block_table, i32, (B, maxb), "block_table"), maxb, nb, _dense(prefix_len, i32, (B,), "prefix_len"),
-            _dense(count, i32, (B,), "count"), int(node0), B, S, Hkv, d, _dense(status, i32, (1,), "status"))
+    dev = k_cache.get_device()
+    _launch("ssd_kv_append_q8", dev, stream,
+            *_rows(k_new, torch.bfloat16, (B, S, Hkv, d), dev, "k_new"),
+            *_rows(v_new, torch.bfloat16, (B, S, Hkv, d), dev, "v_new"),
+            _codes(k_cache, (nb, Hkv, 16, d), dev, "k_cache"), _codes(v_cache, (nb, Hkv, 16, d), dev, "v_cache"),
+            _dense(k_scale, f32, (nb, Hkv), dev, "k_scale"), _dense(v_scale, f32, (nb, Hkv), dev, "v_scale"),
+            _dense(block_table, i32, (B, maxb), dev, "block_table"), maxb, nb, _dense(prefix_len, i32, (B,), dev, "prefix_len"),
+            _dense(count, i32, (B,), dev, "count"), int(node0), B, S, Hkv, d, _dense(status, i32, (1,), dev, "status"))
 
 
 def ssd_attention_q8_workspace_size(B, Nq, Hq, Hkv, d) -> int:
@@ -601,14 +602,12 @@ def ssd_branch_attention_q8(q, k_cache, v_cache, k_scale, v_scale, block_table, 
     i32, f32, bf16 = torch.int32, torch.float32, torch.bfloat16
     if scale is None:
         scale = d ** -0.5
-    if ws is not None and (ws.dtype != torch.uint8 or not ws.is_contiguous()):
-        raise ValueError("ws must be a contiguous uint8 tensor")
-    _same_device(q.device, k_cache, v_cache, k_scale, v_scale, block_table, prefix_len, parent, out, lse, status, ws)
-    _launch("ssd_branch_attention_q8", load().ssd_branch_attention_q8, q.device, stream,
-            _dense(q, bf16, (B, Nq, Hq, d), "q"), _codes(k_cache, (nb, Hkv, 16, d), "k_cache"),
-            _codes(v_cache, (nb, Hkv, 16, d), "v_cache"), _dense(k_scale, f32, (nb, Hkv), "k_scale"),
-            _dense(v_scale, f32, (nb, Hkv), "v_scale"), _dense(block_table, i32, (B, maxb), "block_table"), maxb, nb,
-            _dense(prefix_len, i32, (B,), "prefix_len"), _dense(parent, i32, (B, N), "parent"), B, N, Nq, Hq, Hkv, d,
-            float(scale), _dense(out, bf16, (B, Nq, Hq, d), "out"), _dense(lse, f32, (B, Nq, Hq), "lse"),
-            _dense(status, i32, (1,), "status"), None if ws is None else ws.data_ptr(),
-            0 if ws is None else ws.numel())
+    dev = q.get_device()
+    ws_bytes = 0 if ws is None else ws.numel()
+    _launch("ssd_branch_attention_q8", dev, stream,
+            _dense(q, bf16, (B, Nq, Hq, d), dev, "q"), _codes(k_cache, (nb, Hkv, 16, d), dev, "k_cache"),
+            _codes(v_cache, (nb, Hkv, 16, d), dev, "v_cache"), _dense(k_scale, f32, (nb, Hkv), dev, "k_scale"),
+            _dense(v_scale, f32, (nb, Hkv), dev, "v_scale"), _dense(block_table, i32, (B, maxb), dev, "block_table"), maxb, nb,
+            _dense(prefix_len, i32, (B,), dev, "prefix_len"), _dense(parent, i32, (B, N), dev, "parent"), B, N, Nq, Hq, Hkv, d,
+            float(scale), _dense(out, bf16, (B, Nq, Hq, d), dev, "out"), _dense(lse, f32, (B, Nq, Hq), dev, "lse"),
+            _dense(status, i32, (1,), dev, "status"), _dense(ws, torch.uint8, (ws_bytes,), dev, "ws"), ws_bytes)
