@@ -6,11 +6,15 @@
 // (an fp32 product is off by 0.06 rad at a million positions).  The angle
 // then enters sincospi as half-turns in [-1, 1).
 //
-//   k_tree_rope   one CTA per token.  It walks the token's ancestors in shared
-//                 memory (position = prefix + depth), computes the rot/2
-//                 rotations once, and applies them to all Hq + Hkv heads in
-//                 16-byte pieces.
-// Bound by HBM: every element is read and written once.
+//   k_tree_rope   one CTA per token.  Its threads first ask for their pieces of
+//                 the heads; meanwhile they walk the token's ancestors in
+//                 shared memory (position = prefix + depth) and compute the
+//                 rot/2 rotations once for all Hq + Hkv heads.
+// Bound by HBM: every element is read and written once.  64 + 8 heads of 128
+// with 64 rotated, 16396 tokens (604 MB): 101 us, 6.0 TB/s (128 us
+// when the pieces were asked for after the rotations); 2 or 4 pieces per thread
+// at a time 107 and 110 us (fewer threads fit).  A decode step of 256 tokens:
+// 2.8 us, two dependent reads and a launch.
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
@@ -24,7 +28,7 @@ namespace {
 
 using namespace ssd;
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 192;  // at most; 128, 256, 384 and 640 threads: 99, 103, 108, 125 us for the prompts below
 constexpr int kMaxNodes = 128;
 constexpr int kMaxD = 512;
 
@@ -41,59 +45,56 @@ struct RopeArgs {
   uint32_t *status;
 };
 
-template <class E, int VEC>
-struct Piece;  // VEC elements moved in one access
-template <>
-struct Piece<EF32, 4> {
-  SSD_DEV static void load(const void *p, int64_t i, float *f) {
-    EF32::unpack(*reinterpret_cast<const uint4 *>(static_cast<const float *>(p) + i), f);
-  }
-  SSD_DEV static void store(void *p, int64_t i, const float *f) {
-    *reinterpret_cast<float4 *>(static_cast<float *>(p) + i) = make_float4(f[0], f[1], f[2], f[3]);
-  }
-};
-template <>
-struct Piece<EF32, 1> {
-  SSD_DEV static void load(const void *p, int64_t i, float *f) { f[0] = static_cast<const float *>(p)[i]; }
-  SSD_DEV static void store(void *p, int64_t i, const float *f) { static_cast<float *>(p)[i] = f[0]; }
-};
 SSD_DEV uint32_t bf16_pair(float lo, float hi) {  // round to nearest even: the output's only rounding
   uint32_t r;
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
+template <class E, int VEC>
+struct Piece;  // VEC elements moved in one access
+template <>
+struct Piece<EF32, 4> {
+  using Elem = float;
+  using Raw = uint4;
+  SSD_DEV static void unpack(const Raw &w, float *f) { EF32::unpack(w, f); }
+  SSD_DEV static Raw pack(const float *f) {
+    return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+  }
+};
+template <>
+struct Piece<EF32, 1> {
+  using Elem = float;
+  using Raw = uint32_t;
+  SSD_DEV static void unpack(const Raw &w, float *f) { f[0] = __uint_as_float(w); }
+  SSD_DEV static Raw pack(const float *f) { return __float_as_uint(f[0]); }
+};
 template <>
 struct Piece<EBF16, 8> {
-  SSD_DEV static void load(const void *p, int64_t i, float *f) {
-    EBF16::unpack(*reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p) + i), f);
-  }
-  SSD_DEV static void store(void *p, int64_t i, const float *f) {
-    *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p) + i) =
-        make_uint4(bf16_pair(f[0], f[1]), bf16_pair(f[2], f[3]), bf16_pair(f[4], f[5]), bf16_pair(f[6], f[7]));
+  using Elem = uint16_t;
+  using Raw = uint4;
+  SSD_DEV static void unpack(const Raw &w, float *f) { EBF16::unpack(w, f); }
+  SSD_DEV static Raw pack(const float *f) {
+    return make_uint4(bf16_pair(f[0], f[1]), bf16_pair(f[2], f[3]), bf16_pair(f[4], f[5]), bf16_pair(f[6], f[7]));
   }
 };
 template <>
 struct Piece<EBF16, 4> {
-  SSD_DEV static void load(const void *p, int64_t i, float *f) {
-    const uint2 w = *reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(p) + i);
+  using Elem = uint16_t;
+  using Raw = uint2;
+  SSD_DEV static void unpack(const Raw &w, float *f) {
     f[0] = __uint_as_float(w.x << 16);
     f[1] = __uint_as_float(w.x & 0xFFFF0000u);
     f[2] = __uint_as_float(w.y << 16);
     f[3] = __uint_as_float(w.y & 0xFFFF0000u);
   }
-  SSD_DEV static void store(void *p, int64_t i, const float *f) {
-    *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p) + i) =
-        make_uint2(bf16_pair(f[0], f[1]), bf16_pair(f[2], f[3]));
-  }
+  SSD_DEV static Raw pack(const float *f) { return make_uint2(bf16_pair(f[0], f[1]), bf16_pair(f[2], f[3])); }
 };
 template <>
 struct Piece<EBF16, 1> {
-  SSD_DEV static void load(const void *p, int64_t i, float *f) {
-    f[0] = __uint_as_float(static_cast<uint32_t>(static_cast<const uint16_t *>(p)[i]) << 16);
-  }
-  SSD_DEV static void store(void *p, int64_t i, const float *f) {
-    static_cast<uint16_t *>(p)[i] = static_cast<uint16_t>(bf16_pair(f[0], 0.f) & 0xFFFFu);
-  }
+  using Elem = uint16_t;
+  using Raw = uint16_t;
+  SSD_DEV static void unpack(const Raw &w, float *f) { f[0] = __uint_as_float(static_cast<uint32_t>(w) << 16); }
+  SSD_DEV static Raw pack(const float *f) { return static_cast<uint16_t>(bf16_pair(f[0], 0.f) & 0xFFFFu); }
 };
 
 SSD_DEV void rotate(float2 w, float &a, float &b) {
@@ -106,15 +107,60 @@ SSD_DEV void rotate(float2 w, float &a, float &b) {
 template <class E, int VEC, bool INTER>
 __global__ void __launch_bounds__(kThreads) k_tree_rope(RopeArgs a) {
   using P = Piece<E, VEC>;
-  __shared__ float2 turn[kMaxD / 2];  // mscale (cos, sin) of each pair
+  using Raw = typename P::Raw;
+  constexpr bool kOne = INTER && VEC > 1;  // a unit is one piece with whole pairs, else the two halves of VEC pairs
+  __shared__ float2 turn[kMaxD / 2];       // mscale (cos, sin) of each pair
   __shared__ int par[kMaxNodes];
-  const int tid = threadIdx.x;
+  const int tid = threadIdx.x, nt = blockDim.x;
   const int b = blockIdx.x / a.S, i = blockIdx.x % a.S;
+  const int half = a.rot / 2, total = a.H * a.units;
+  struct Unit {
+    Raw x, y;
+    Raw *dst;
+    int pair, second;  // first pair (-1: a copied piece), elements from x to y
+  };
+  auto load = [&](int w, Unit &t) {
+    const int h = w / a.units, u = w - h * a.units;
+    const bool isq = h < a.Hq;
+    const int64_t hoff = static_cast<int64_t>(isq ? h : h - a.Hq) * a.d;
+    const int64_t si = b * (isq ? a.q_ss : a.k_ss) + i * (isq ? a.q_ts : a.k_ts) + hoff;
+    const int64_t di = b * (isq ? a.qo_ss : a.ko_ss) + i * (isq ? a.qo_ts : a.ko_ts) + hoff;
+    const bool copy = u >= a.pair_units;
+    const int e = copy ? a.rot + (u - a.pair_units) * VEC : (INTER && VEC == 1 ? 2 * u : u * VEC);
+    t.pair = copy ? -1 : (kOne ? e / 2 : u * VEC);
+    t.second = INTER ? 1 : half;
+    const typename P::Elem *const src = static_cast<const typename P::Elem *>(isq ? a.q : a.k) + si + e;
+    t.dst = reinterpret_cast<Raw *>(static_cast<typename P::Elem *>(isq ? a.qo : a.ko) + di + e);
+    t.x = *reinterpret_cast<const Raw *>(src);
+    if (!kOne && !copy) t.y = *reinterpret_cast<const Raw *>(src + t.second);
+  };
+  auto turned = [&](const Unit &t) {
+    if (t.pair < 0) {
+      *t.dst = t.x;
+      return;
+    }
+    float x[VEC], y[VEC];
+    P::unpack(t.x, x);
+    if (kOne) {
+#pragma unroll
+      for (int v = 0; v < VEC; v += 2) rotate(turn[t.pair + v / 2], x[v], x[v + 1 < VEC ? v + 1 : v]);
+      *t.dst = P::pack(x);
+    } else {
+      P::unpack(t.y, y);
+#pragma unroll
+      for (int v = 0; v < VEC; ++v) rotate(turn[t.pair + v], x[v], y[v]);
+      *t.dst = P::pack(x);
+      *reinterpret_cast<Raw *>(reinterpret_cast<typename P::Elem *>(t.dst) + t.second) = P::pack(y);
+    }
+  };
+  // the first unit is on its way while the position and the angles are found
+  Unit unit;
+  if (tid < total) load(tid, unit);
   const int L = a.prefix_len[b];
   int64_t pos = static_cast<int64_t>(max(L, 0));
   if (L < 0 && tid == 0) atomicOr(a.status, kFlagBadPrefix);
   if (a.parent) {
-    for (int m = tid; m < a.N; m += kThreads) par[m] = a.parent[static_cast<int64_t>(b) * a.N + m];
+    for (int m = tid; m < a.N; m += nt) par[m] = a.parent[static_cast<int64_t>(b) * a.N + m];
     __syncthreads();
     for (int m = a.node0 + i;; ++pos) {
       const int up = par[m];
@@ -128,53 +174,28 @@ __global__ void __launch_bounds__(kThreads) k_tree_rope(RopeArgs a) {
   } else {
     pos += a.node0 + i;
   }
-  const int half = a.rot / 2;
-  for (int j = tid; j < half; j += kThreads) {
+  for (int j = tid; j < half; j += nt) {
     const uint64_t t = static_cast<uint64_t>(pos) * a.turns[j];
     float s, c;
     sincospif(static_cast<float>(static_cast<int32_t>(t >> 32)) * 0x1p-31f, &s, &c);
     turn[j] = make_float2(c * a.mscale, s * a.mscale);
   }
   __syncthreads();
-  const int total = a.H * a.units;
-  for (int w = tid; w < total; w += kThreads) {
-    const int h = w / a.units, u = w % a.units;
-    const bool isq = h < a.Hq;
-    const void *src = isq ? a.q : a.k;
-    void *dst = isq ? a.qo : a.ko;
-    const int64_t hoff = static_cast<int64_t>(isq ? h : h - a.Hq) * a.d;
-    const int64_t si = b * (isq ? a.q_ss : a.k_ss) + i * (isq ? a.q_ts : a.k_ts) + hoff;
-    const int64_t di = b * (isq ? a.qo_ss : a.ko_ss) + i * (isq ? a.qo_ts : a.ko_ts) + hoff;
-    float x[VEC], y[VEC];
-    if (u >= a.pair_units) {
-      const int e = a.rot + (u - a.pair_units) * VEC;
-      P::load(src, si + e, x);
-      P::store(dst, di + e, x);
-    } else if (INTER && VEC > 1) {
-      const int e = u * VEC;
-      P::load(src, si + e, x);
-#pragma unroll
-      for (int v = 0; v < VEC; v += 2) rotate(turn[(e + v) / 2], x[v], x[v + 1 < VEC ? v + 1 : v]);
-      P::store(dst, di + e, x);
-    } else {
-      const int j = u * VEC;  // the first pair
-      const int e0 = INTER ? 2 * j : j, e1 = INTER ? 2 * j + 1 : j + half;
-      P::load(src, si + e0, x);
-      P::load(src, si + e1, y);
-#pragma unroll
-      for (int v = 0; v < VEC; ++v) rotate(turn[j + v], x[v], y[v]);
-      P::store(dst, di + e0, x);
-      P::store(dst, di + e1, y);
-    }
+  for (int w = tid; w < total; w += nt) {
+    if (w != tid) load(w, unit);
+    turned(unit);
   }
 }
 
 template <class E, int VEC>
 void launch(const RopeArgs &a, bool inter, unsigned grid, cudaStream_t cs) {
+  // every thread has the same number of units, but for the last warps'
+  const int units = a.H * a.units, rounds = (units + kThreads - 1) / kThreads;
+  const int threads = ((units + rounds - 1) / rounds + 31) / 32 * 32;
   if (inter)
-    k_tree_rope<E, VEC, true><<<grid, kThreads, 0, cs>>>(a);
+    k_tree_rope<E, VEC, true><<<grid, threads, 0, cs>>>(a);
   else
-    k_tree_rope<E, VEC, false><<<grid, kThreads, 0, cs>>>(a);
+    k_tree_rope<E, VEC, false><<<grid, threads, 0, cs>>>(a);
 }
 
 }  // namespace
