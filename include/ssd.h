@@ -527,8 +527,8 @@ ssd_status_t ssd_fallback_plan(const float *p_hit, const float *e_hit, int B, do
  * (NO_BLOCKS).  A length beyond 16 maxb - reserve, a pages entry outside [0,
  * maxb] (clamped) and a pool outside its range (taken as empty) set
  * BAD_PREFIX; such a length leaves the sequence as it is.
- * num_blocks <= 2^27 (slots are 32 bits), B <= 65536.  One launch; calls that share
- * a pool must not overlap on the GPU.
+ * num_blocks <= 2^27 (slots are 32 bits), B <= 65536, S <= 2^24.  One launch;
+ * calls that share a pool must not overlap on the GPU.
  */
 ssd_status_t ssd_block_table_update(const int32_t *len, int reserve, int B, int32_t *block_table,
                                     int maxb, int32_t *pages, int32_t *ring, int64_t num_blocks,
