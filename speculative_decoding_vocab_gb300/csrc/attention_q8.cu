@@ -63,6 +63,9 @@ constexpr int kPages = kSub / kPage;       // 8
 // moving m costs about a tile's time.
 constexpr float kBias = 4.f, kMoved = 5.f, kGrow = 8.f;
 constexpr int kMinKeys = 512;              // keys of the smallest piece: below, joining costs more than it gives
+// An item's end costs its CTA about two tiles' time and, where items are short, the rows of the next one six
+// (one warp prepares them).  Ragged batch of 1 to 16384 keys: 0: 129 us, 2: 112, 4: 107, 6: 95, 8: 97, 12: 104.
+constexpr int kEnd = 6;
 constexpr int kSmemBudget = 212 * 1024;
 constexpr int kTmaWarps = 2;               // producer warps: warp p loads every sub-tile whose number is p modulo this
 constexpr int kBatch = 32 / kPages;        // sub-tiles that a producer warp's lanes hold the blocks of
@@ -192,6 +195,11 @@ SSD_DEV uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c) {
   asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
   return r;
 }
+SSD_DEV uint32_t max_u16x2(uint32_t x, uint32_t y) {
+  uint32_t r;
+  asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(y));
+  return r;
+}
 SSD_DEV uint32_t hmul2(uint32_t a, uint32_t b) {
   uint32_t r;
   asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
@@ -251,20 +259,26 @@ SSD_DEV int keys_of(const Args &a, int b, int &L) {
   const int64_t n = min(static_cast<int64_t>(L) + a.N, static_cast<int64_t>(a.maxb) * kPage);
   return static_cast<int>(min(n, static_cast<int64_t>(0x7fffffff - 2 * kSub)));
 }
-SSD_DEV int tiles_of(const Args &a, int b) {
+SSD_DEV int units_of(const Args &a, int b) {  // of an item
   int L;
-  return (keys_of(a, b, L) + a.keys - 1) / a.keys;
+  return (keys_of(a, b, L) + a.keys - 1) / a.keys + kEnd;
+}
+
+SSD_DEV long long quotient(long long x, int y) {  // x >= 0, y > 0; a 64-bit division takes ten times a 32-bit one's time
+  return x >> 32 ? x / y : static_cast<long long>(static_cast<uint32_t>(x) / static_cast<uint32_t>(y));
 }
 
 // A CTA's piece of the line of units.
 struct Piece {
-  int b, item, t0;  // sequence, item of it and tile of the first unit
+  int b, item, t0;  // sequence, item of it and the first unit's number in it
   int left;         // units of the piece
   int chunk;        // units of a full piece
   int tiles;        // tiles that the CTA runs
 };
 
-// The segments of a piece: one item (or part of it) after the other.
+// The segments of a piece: one item (or part of it) after the other.  An item
+// has kEnd units behind its tiles, for the time that its end takes (O leaves
+// TMEM, the next rows come in), or a CTA of many short items would be the last.
 struct Segments {
   int b, hk, mt, nt, nkeys, L, t0, t1, left;
   SSD_DEV void sequence(const Args &a) {
@@ -279,15 +293,15 @@ struct Segments {
     t0 = p.t0;
     left = p.left;
     sequence(a);
-    if (!a.split && t0 > 0) {  // begun in the piece before, which takes it whole
-      left -= nt - t0;
+    if (t0 >= nt || (!a.split && t0 > 0)) {  // the item's end, or begun in the piece before, which takes it whole
+      left -= nt + kEnd - t0;
       return step(a);
     }
     return take(a);
   }
   SSD_DEV bool take(const Args &a) {
     t1 = (a.split && left < nt - t0) ? t0 + left : nt;
-    left -= t1 - t0;
+    left -= t1 < nt ? t1 - t0 : nt + kEnd - t0;
     return true;
   }
   SSD_DEV bool step(const Args &a) {
@@ -420,36 +434,53 @@ __device__ __noinline__ void prepare_rows(const Args &a, const Segments sg, uint
   for (int r0 = w * 8; r0 < RT; r0 += n * 8) {
     const int r = r0 + (lane >> 2);
     fetch(r + n * 8, next);
-    uint32_t m = 0;  // the row's largest finite magnitude
     auto each = [&](auto &&f) {
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        const uint32_t word[4] = {x[v].x, x[v].y, x[v].z, x[v].w};
-#pragma unroll
-        for (int k = 0; k < 4; ++k) f(v, k, word[k]);
+        f(v * 2, 0, x[v].x);
+        f(v * 2, 16, x[v].y);
+        f(v * 2 + 1, 0, x[v].z);
+        f(v * 2 + 1, 16, x[v].w);
       }
     };
-    each([&](int, int, uint32_t b) {
-      const uint32_t lo = (b << 16) & 0x7FFFFFFFu, hi = b & 0x7FFF0000u;
-      m = max(m, max(lo < 0x7F800000u ? lo : 0u, hi < 0x7F800000u ? hi : 0u));
-    });
+    uint32_t m2 = 0;  // the row's largest magnitude: bf16 magnitudes order like integers
+    each([&](int, int, uint32_t b) { m2 = max_u16x2(m2, b & 0x7FFF7FFFu); });
+    uint32_t m = max(m2 & 0xFFFFu, m2 >> 16);
+    if (__any_sync(0xffffffffu, m >= 0x7F80u)) {  // infinities (which e4m3 would clamp) and NaN: NaN, and not the largest
+      m = 0;
+#pragma unroll 1
+      for (int v = 0; v < V; ++v) {
+        uint4 w = x[0];
+#pragma unroll
+        for (int k = 1; k < V; ++k) w = v == k ? x[k] : w;
+        auto clean = [&](uint32_t b) {
+          uint32_t lo = b & 0xFFFFu, hi = b >> 16;
+          if ((lo & 0x7FFFu) < 0x7F80u) m = max(m, lo & 0x7FFFu);
+          else lo = 0x7FC0u;
+          if ((hi & 0x7FFFu) < 0x7F80u) m = max(m, hi & 0x7FFFu);
+          else hi = 0x7FC0u;
+          return lo | hi << 16;
+        };
+        w = make_uint4(clean(w.x), clean(w.y), clean(w.z), clean(w.w));
+#pragma unroll
+        for (int k = 0; k < V; ++k) x[k] = v == k ? w : x[k];
+      }
+    }
     m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
     m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
     // 2^e brings the largest element into [2^7, 2^8); e in [-120, 120] (smaller rows: fewer bits)
-    const int e2 = m == 0 ? 0 : min(max(static_cast<int>(m >> 23) - 127 - 7, -120), 120);
+    const int e2 = m == 0 ? 0 : min(max(static_cast<int>(m >> 7) - 127 - 7, -120), 120);
     const float inv = __uint_as_float(static_cast<uint32_t>(127 - e2) << 23);
     uint32_t c1[V * 2], c2[V * 2];
 #pragma unroll
     for (int k = 0; k < V * 2; ++k) c1[k] = c2[k] = 0;
-    each([&](int v, int k, uint32_t b) {
-      float u0 = __uint_as_float(b << 16) * inv, u1 = __uint_as_float(b & 0xFFFF0000u) * inv;
-      if (!(fabsf(u0) <= 256.f)) u0 = __int_as_float(0x7fc00000);  // an infinity too: e4m3 would clamp it
-      if (!(fabsf(u1) <= 256.f)) u1 = __int_as_float(0x7fc00000);
-      const uint32_t h = e4m3_pair(u0, u1);
-      float b0, b1;
-      half2_to_float(e4m3_to_half2(static_cast<uint16_t>(h)), b0, b1);
-      c1[v * 2 + k / 2] |= h << (16 * (k & 1));
-      c2[v * 2 + k / 2] |= e4m3_pair(u0 - b0, u1 - b1) << (16 * (k & 1));
+    // in halves: a value has 8 bits and both terms lie above their last place, 2^-24 (what is smaller e4m3 cuts)
+    each([&](int word, int shift, uint32_t b) {
+      const uint32_t h = half2_of(__uint_as_float(b << 16) * inv, __uint_as_float(b & 0xFFFF0000u) * inv);
+      const uint32_t t1 = e4m3_of_half2(h);
+      const uint32_t t2 = e4m3_of_half2(hfma2(e4m3_to_half2(static_cast<uint16_t>(t1)), 0xBC00BC00u, h));
+      c1[word] |= t1 << shift;
+      c2[word] |= t2 << shift;
     });
     if (r < RT) {
 #pragma unroll
@@ -521,11 +552,11 @@ __global__ void __launch_bounds__(Cfg<D, RT>::kThreads, 1)
     tmem_alloc(&tmem_base, C::kTmem);
     tmem_relinquish();
   }
-  // the line of units: every thread sums some sequences' tiles, then the sums are scanned
+  // the line of units: every thread sums some sequences' units, then the sums are scanned
   {
     const int per = (a.B + C::kThreads - 1) / C::kThreads, b0 = tid * per, b1 = min(a.B, b0 + per);
     long long mine = 0;
-    for (int b = b0; b < b1; ++b) mine += tiles_of(a, b);
+    for (int b = b0; b < b1; ++b) mine += units_of(a, b);
     long long inc = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -534,28 +565,31 @@ __global__ void __launch_bounds__(Cfg<D, RT>::kThreads, 1)
     }
     if (lane == 31) scan[warp] = inc;
     __syncthreads();
-    long long before = 0, total = 0;
-    for (int w = 0; w < C::kThreads / 32; ++w) {
-      if (w < warp) before += scan[w];
-      total += scan[w];
+    long long upto = lane < C::kWarps ? scan[lane] : 0;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long x = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += x;
     }
+    const long long total = __shfl_sync(0xffffffffu, upto, 31);
+    const long long before = __shfl_sync(0xffffffffu, upto, max(warp - 1, 0)) * (warp > 0);
     const long long T = total * a.per_b;
-    long long chunk = (T + gridDim.x - 1) / gridDim.x;
+    long long chunk = quotient(T + gridDim.x - 1, gridDim.x);
     if (a.split) chunk = max(chunk, static_cast<long long>(kMinKeys / C::kKeys));
     const long long lo = chunk * blockIdx.x, hi = min(T, lo + chunk);
     long long x = (before + inc - mine) * a.per_b;  // units before this thread's first sequence
     if (lo < hi && lo >= x && lo < x + mine * a.per_b) {
       int b = b0;
       for (;; ++b) {
-        const long long n = static_cast<long long>(tiles_of(a, b)) * a.per_b;
+        const long long n = static_cast<long long>(units_of(a, b)) * a.per_b;
         if (lo < x + n) break;
         x += n;
       }
       Piece p;
       p.b = b;
-      const int nt = tiles_of(a, b);
-      p.item = static_cast<int>((lo - x) / nt);
-      p.t0 = static_cast<int>((lo - x) - static_cast<long long>(p.item) * nt);
+      const int n = units_of(a, b);
+      p.item = static_cast<int>(quotient(lo - x, n));
+      p.t0 = static_cast<int>((lo - x) - static_cast<long long>(p.item) * n);
       p.left = static_cast<int>(hi - lo);
       p.chunk = static_cast<int>(chunk);
       p.tiles = 0;
