@@ -348,11 +348,10 @@ template <int D, int RT>
 struct Cfg {
   static constexpr int KT = RT <= 64 ? 2 : 1;              // sub-tiles of a tile
   static constexpr int kKeys = KT * kSub;                  // keys of a tile
-  static constexpr int NSTR = 1;                           // streams
   static constexpr int CG = RT <= 64 ? 16 : 32;            // rows of a softmax warp
-  static constexpr int kGroups = RT / CG;                  // groups of four warps in a stream
-  static constexpr int NB = NSTR > 1 ? NSTR : 2;           // S and P buffers; S runs NB tiles ahead
-  static constexpr int kSoftWarps = 4 * kGroups * NSTR;
+  static constexpr int kGroups = RT / CG;                  // groups of four warps
+  static constexpr int NB = 2;                             // S and P buffers; S runs NB tiles ahead
+  static constexpr int kSoftWarps = 4 * kGroups;
   static constexpr int kTmaWarp = kSoftWarps, kMmaWarp = kTmaWarp + kTmaWarps, kPrepWarp = kMmaWarp + 1;
   static constexpr int kWarps = kPrepWarp + 1;
   static constexpr int kThreads = kWarps * 32;
@@ -366,8 +365,8 @@ struct Cfg {
   static constexpr int kSlots = kFit > 16 ? 16 : kFit;
   static constexpr int kQ = 0, kP = 2 * kQBuf, kRing = kFixed;
   static constexpr int kSmem = kFixed + kSlots * kSlot + 1024;
-  static constexpr int kOCol = NB * KT * RT;               // TMEM: NB x KT x S, then O1, O2 of each stream
-  static constexpr uint32_t kCols = kOCol + NSTR * 2 * RT;
+  static constexpr int kOCol = NB * KT * RT;               // TMEM: NB x KT x S, then O1, O2
+  static constexpr uint32_t kCols = kOCol + 2 * RT;
   static constexpr uint32_t kTmem = kCols <= 64 ? 64 : (kCols <= 128 ? 128 : (kCols <= 256 ? 256 : 512));
   static constexpr int kMeta = 16 / KT;                    // tiles whose block scales are held
   static_assert(kSmem + 13824 <= 227 * 1024, "shared memory with the static part");
@@ -377,7 +376,7 @@ struct Cfg {
   // loads further back.  P V of tile i - NB is the last of a tile before the K loads of tile i.
   static constexpr int kBack = kSlots + 2 * kTmaWarps + KT - 1;
   static_assert(kMeta >= NB + (kBack + 2 * KT - 1) / (2 * KT), "block scales");
-  static_assert(kCols <= 512 && RT % CG == 0 && CG % 16 == 0 && CG <= 32 && NSTR * kGroups <= 8, "rows");
+  static_assert(kCols <= 512 && RT % CG == 0 && CG % 16 == 0 && CG <= 32 && kGroups <= 8, "rows");
 };
 
 // A segment's rows: q1, q2 into the operand tiles at qb, the row scales, and
@@ -504,7 +503,7 @@ __global__ void __launch_bounds__(Cfg<D, RT>::kThreads, 1)
     k_branch_attn_q8(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                      const __grid_constant__ Args a) {
   using C = Cfg<D, RT>;
-  constexpr int NSTR = C::NSTR, CG = C::CG, NB = C::NB, NSLOT = C::kSlots, KT = C::KT, kMeta = C::kMeta;
+  constexpr int CG = C::CG, NB = C::NB, NSLOT = C::kSlots, KT = C::KT, kMeta = C::kMeta;
   constexpr int kSoftThreads = C::kSoftWarps * 32;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t *const smem =
@@ -517,8 +516,8 @@ __global__ void __launch_bounds__(Cfg<D, RT>::kThreads, 1)
   __shared__ int par[2][kMaxNodes];
   __shared__ uint32_t anc[2][kMaxNodes][kMaxNodes / 32];    // per query: the nodes that it sees
   __shared__ float qs[2][RT];                               // row scales 2^e
-  __shared__ __align__(16) float4 rowc[NSTR][RT / 2];       // two rows: 2^e, 2^e, 4 - m, 4 - m
-  __shared__ float s_m[NSTR][RT], s_f[NSTR][RT], red[NSTR][4][RT];
+  __shared__ __align__(16) float4 rowc[RT / 2];             // two rows: 2^e, 2^e, 4 - m, 4 - m
+  __shared__ float s_m[RT], s_f[RT], red[4][RT];
   __shared__ int s_nan[2];                                  // a tree node's v held NaN, by segment mod 2
   __shared__ long long scan[32];
   __shared__ Piece s_piece;
@@ -803,8 +802,8 @@ __global__ void __launch_bounds__(Cfg<D, RT>::kThreads, 1)
         issue_s(i++);
       } else {  // P V of tile j
         const int u = j % NB;
-        const uint32_t o = tmem + C::kOCol + (NSTR == 1 ? 0 : (j % NSTR) * (2 * RT));
-        const uint32_t later = j - order.begin >= NSTR;  // not the stream's first tile of the segment
+        const uint32_t o = tmem + C::kOCol;
+        const uint32_t later = j > order.begin;  // not the segment's first tile
         ok = warp_wait(&pfull[u], (j / NB) & 1);
 #pragma unroll
         for (int h = 0; h < KT; ++h) {
@@ -847,12 +846,12 @@ __global__ void __launch_bounds__(Cfg<D, RT>::kThreads, 1)
       if (lane == 0) mbar_arrive1(&qfull[buf]);
     }
   } else {
-    // ---------------- softmax: stream s, group g of its rows, one thread per key
-    const int sgrp = warp / 4, s = sgrp / C::kGroups, g = sgrp % C::kGroups, wg = warp & 3, tg = tid & 127;
+    // ---------------- softmax: group g of the rows, one thread per key
+    const int g = warp / 4, wg = warp & 3, tg = tid & 127;
     const int col = g * CG;
     const uint32_t lane_off = static_cast<uint32_t>(wg * 32) << 16;
-    const uint32_t tS = tmem + col + lane_off, tO = tmem + C::kOCol + s * (2 * RT) + col + lane_off;
-    const int bar = 1 + sgrp;
+    const uint32_t tS = tmem + col + lane_off, tO = tmem + C::kOCol + col + lane_off;
+    const int bar = 1 + g;
     int i0 = 0, seg = 0;  // the segment's first tile in the CTA's count
     uint32_t sphase = 0;  // parities of sfull
     bool dead = false;
@@ -867,8 +866,8 @@ __global__ void __launch_bounds__(Cfg<D, RT>::kThreads, 1)
       const int row0 = mt * RT + col;  // the warp's first row of (b, hk)
       bool ok = warp_wait(&qfull[buf], (seg >> 1) & 1);
       if (tg < CG) {
-        s_m[s][col + tg] = NEG_INF;
-        float *const rc = reinterpret_cast<float *>(&rowc[s][(col + tg) >> 1]) + (tg & 1);
+        s_m[col + tg] = NEG_INF;
+        float *const rc = reinterpret_cast<float *>(&rowc[(col + tg) >> 1]) + (tg & 1);
         rc[0] = qs[buf][col + tg];
         rc[2] = 0.f;
       }
@@ -876,10 +875,9 @@ __global__ void __launch_bounds__(Cfg<D, RT>::kThreads, 1)
       uint64_t l2[CG / 2];
 #pragma unroll
       for (int j = 0; j < CG / 2; ++j) l2[j] = 0;
-      bool begin = true, unset = true;  // before the stream's first tile; a row without a visible key so far
-      for (int x = (s + NSTR - i0 % NSTR) % NSTR; x < n; x += NSTR) {
-        const int i = i0 + x, t = sg.t0 + x;
-        const int u = NSTR > 1 ? s : i % NB;  // S and P buffer
+      bool begin = true, unset = true;  // before the segment's first tile; a row without a visible key so far
+      for (int x = 0; x < n; ++x) {
+        const int i = i0 + x, t = sg.t0 + x, u = i % NB;  // u: S and P buffer
         ok = ok && warp_wait(&sfull[u], sphase >> u & 1);
         sphase ^= 1u << u;  // the scales were there before K was
         tc_fence_after();
@@ -928,7 +926,7 @@ __global__ void __launch_bounds__(Cfg<D, RT>::kThreads, 1)
             for (int j = 0; j < CG; j += 16) tmem_wait16(y[h] + j);
 #pragma unroll
           for (int j = 0; j < CG; j += 2) {
-            const float4 rc = rowc[s][(col + j) / 2];
+            const float4 rc = rowc[(col + j) / 2];
 #pragma unroll
             for (int h = 0; h < KT; ++h)
               unpack2(fma2(mul2(pack2(y[h][j], y[h][j + 1]), pack2(c[h], c[h])), pack2(rc.x, rc.y), pack2(rc.z, rc.w)),
@@ -964,9 +962,9 @@ __global__ void __launch_bounds__(Cfg<D, RT>::kThreads, 1)
             z = warp_top(z);
             if (lane == j) big = z;
           }
-          if (lane < CG) red[s][wg][col + lane] = big;
-          // O is rescaled below: every P V before has to be in it (with several streams S of this tile came behind)
-          if (!begin && NSTR == 1) {
+          if (lane < CG) red[wg][col + lane] = big;
+          // O is rescaled below: every P V before has to be in it
+          if (!begin) {
             ok = warp_wait(&pvdone[(i - 1) % NB], ((i - 1) / NB) & 1) && ok;
             tc_fence_after();
           }
@@ -977,8 +975,8 @@ __global__ void __launch_bounds__(Cfg<D, RT>::kThreads, 1)
           bool none = false;
           if (tg < CG) {
             const int r = col + tg;
-            const float mo = s_m[s][r];
-            const float z = fmaxf(fmaxf(red[s][0][r], red[s][1][r]), fmaxf(red[s][2][r], red[s][3][r]));
+            const float mo = s_m[r];
+            const float z = fmaxf(fmaxf(red[0][r], red[1][r]), fmaxf(red[2][r], red[3][r]));
             float mn = mo, f = 1.f;
             if (mo == NEG_INF) {
               mn = z;
@@ -987,9 +985,9 @@ __global__ void __launch_bounds__(Cfg<D, RT>::kThreads, 1)
               mn = mo + (z - kMoved);
               f = ex2(kMoved - z);
             }
-            s_m[s][r] = mn;
-            s_f[s][r] = f;
-            reinterpret_cast<float *>(&rowc[s][r >> 1])[2 + (tg & 1)] = none ? 0.f : kBias - mn;
+            s_m[r] = mn;
+            s_f[r] = f;
+            reinterpret_cast<float *>(&rowc[r >> 1])[2 + (tg & 1)] = none ? 0.f : kBias - mn;
           }
           unset = bar_or(bar, 128, none);
           if (!begin) {
@@ -997,17 +995,17 @@ __global__ void __launch_bounds__(Cfg<D, RT>::kThreads, 1)
             for (int j0 = 0; j0 < CG; j0 += 16) {  // the 16 rows whose m moved
               bool moved = false;
 #pragma unroll
-              for (int j = 0; j < 16; ++j) moved = moved || s_f[s][col + j0 + j] != 1.f;
+              for (int j = 0; j < 16; ++j) moved = moved || s_f[col + j0 + j] != 1.f;
               if (!moved) continue;
 #pragma unroll
               for (int j = j0 / 2; j < j0 / 2 + 8; ++j)
-                l2[j] = mul2(l2[j], pack2(s_f[s][col + 2 * j], s_f[s][col + 2 * j + 1]));
+                l2[j] = mul2(l2[j], pack2(s_f[col + 2 * j], s_f[col + 2 * j + 1]));
 #pragma unroll 1
               for (int term = 0; term < 2; ++term) {
                 float o[16];
                 tmem_ld16(tO + term * RT + j0, o);
 #pragma unroll
-                for (int j = 0; j < 16; ++j) o[j] *= s_f[s][col + j0 + j];
+                for (int j = 0; j < 16; ++j) o[j] *= s_f[col + j0 + j];
                 tmem_st16(tO + term * RT + j0, o);
               }
             }
@@ -1085,7 +1083,7 @@ __global__ void __launch_bounds__(Cfg<D, RT>::kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive1(&pfull[u]);
       }
-      // ---------------- the segment's end: the streams' l and m joined, O from TMEM
+      // ---------------- the segment's end: l, then O from TMEM
       if (dead) ok = false;
 #pragma unroll
       for (int j0 = 0; j0 < CG; j0 += 16) {
@@ -1093,7 +1091,7 @@ __global__ void __launch_bounds__(Cfg<D, RT>::kThreads, 1)
 #pragma unroll
         for (int j = 0; j < 16; j += 2) unpack2(l2[(j0 + j) / 2], z[j], z[j + 1]);
         const float sum = warp_columns(z, lane);
-        if (!(lane & 1)) red[s][wg][col + j0 + (lane >> 1)] = sum;
+        if (!(lane & 1)) red[wg][col + j0 + (lane >> 1)] = sum;
       }
       const int il = i0 + n - 1;
       ok = ok && warp_wait(&pvdone[il % NB], (il / NB) & 1);
@@ -1104,24 +1102,10 @@ __global__ void __launch_bounds__(Cfg<D, RT>::kThreads, 1)
       }
       const bool whole = sg.t0 == 0 && sg.t1 == sg.nt;
       const int slot = blockIdx.x * 2 + (sg.t0 > 0 ? 0 : 1);
-      // streams that had a tile: those at (i0 + k) % NSTR, k < n
-      auto took_part = [&](int k) { return NSTR == 1 || (k + NSTR - i0 % NSTR) % NSTR < n; };
       if (tid == 0) s_nan[(seg + 1) & 1] = 0;
       for (int r = tid; r < RT; r += kSoftThreads) {
-        float M = NEG_INF, L = 0.f, l[NSTR];
-#pragma unroll
-        for (int k = 0; k < NSTR; ++k) {
-          l[k] = __fadd_rn(__fadd_rn(red[k][0][r], red[k][1][r]), __fadd_rn(red[k][2][r], red[k][3][r]));
-          M = fmaxf(M, s_m[k][r]);
-        }
-#pragma unroll
-        for (int k = 0; k < NSTR; ++k) {
-          l[k] = l[k] == 0.f ? 0.f : l[k] * ex2(s_m[k][r] - M);
-          L = __fadd_rn(L, l[k]);
-        }
-        const float inv = !whole ? 1.f : (L == 0.f ? 0.f : 1.f / L);
-#pragma unroll
-        for (int k = 0; k < NSTR; ++k) s_f[k][r] = l[k] == 0.f ? 0.f : ex2(s_m[k][r] - M) * inv;
+        const float M = s_m[r], L = __fadd_rn(__fadd_rn(red[0][r], red[1][r]), __fadd_rn(red[2][r], red[3][r]));
+        s_f[r] = L == 0.f ? 0.f : (whole ? 1.f / L : 1.f);
         const int row = mt * RT + r;
         if (row < a.nrows) {
           if (!whole) a.part_ml[slot * RT + r] = make_float2(M, L);
@@ -1134,52 +1118,48 @@ __global__ void __launch_bounds__(Cfg<D, RT>::kThreads, 1)
       }
       bar_sync(9, kSoftThreads);
       const bool nan = s_nan[seg & 1] != 0;
-      if (D == 128 || wg < 2) {
+      // four rows at a time; at d = 64 the upper 64 lanes of O repeat the lower ones and take half of the rows
+      constexpr int kShares = C::kGroups * (128 / D);
+      const int share = D == 128 ? g : g * 2 + (wg >> 1), el = tg & (D - 1);
 #pragma unroll 1
-        for (int j0 = sgrp * 4; j0 < RT; j0 += NSTR * C::kGroups * 4) {
-          const int r0 = mt * RT + j0;
-          if (r0 >= a.nrows) break;
-          float o[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 1
-          for (int k = 0; k < NSTR; ++k) {
-            if (!took_part(k)) continue;
-            float o1[4], o2[4];
-            const uint32_t at = tmem + C::kOCol + k * (2 * RT) + j0 + lane_off;
-            tmem_ld4(at, o1, at + RT, o2);
+      for (int j0 = share * 4; j0 < RT; j0 += kShares * 4) {
+        const int r0 = mt * RT + j0;
+        if (r0 >= a.nrows) break;
+        float o[4], o2[4];
+        const uint32_t at = tmem + C::kOCol + j0 + lane_off;
+        tmem_ld4(at, o, at + RT, o2);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) o[j] = fmaf(fmaf(o2[j], 0.03125f, o1[j]), s_f[k][j0 + j], o[j]);
-          }
-          if (nan) {
-            // tree nodes of this segment whose v holds NaN at this thread's element
-            const int from = sg.t0 * C::kKeys - sg.L, to = min(sg.nkeys, sg.t1 * C::kKeys) - sg.L;
-            for (int node = max(0, from); node < to; ++node) {
-              const int pos = sg.L + node, blk = a.table[static_cast<int64_t>(sg.b) * a.maxb + pos / kPage];
-              if (blk < 0 || blk >= a.num_blocks) continue;
-              const int64_t unit = static_cast<int64_t>(blk) * a.Hkv + hk;
-              if (!good_scale(a.ks[unit]) || !good_scale(a.vs[unit])) continue;
-              if ((a.vc[(unit * kPage + pos % kPage) * D + tg] & 0x7F) != 0x7F) continue;
-#pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                const int qi = min(static_cast<int>(((r0 + j) * a.group_magic) >> 16), kMaxNodes - 1);
-                if ((anc[buf][qi][node >> 5] >> (node & 31)) & 1u) o[j] = __int_as_float(0x7fc00000);
-              }
-            }
-          }
-          if (whole) {
+        for (int j = 0; j < 4; ++j) o[j] = fmaf(o2[j], 0.03125f, o[j]) * s_f[j0 + j];
+        if (nan) {
+          // tree nodes of this segment whose v holds NaN at this thread's element
+          const int from = sg.t0 * C::kKeys - sg.L, to = min(sg.nkeys, sg.t1 * C::kKeys) - sg.L;
+          for (int node = max(0, from); node < to; ++node) {
+            const int pos = sg.L + node, blk = a.table[static_cast<int64_t>(sg.b) * a.maxb + pos / kPage];
+            if (blk < 0 || blk >= a.num_blocks) continue;
+            const int64_t unit = static_cast<int64_t>(blk) * a.Hkv + hk;
+            if (!good_scale(a.ks[unit]) || !good_scale(a.vs[unit])) continue;
+            if ((a.vc[(unit * kPage + pos % kPage) * D + el] & 0x7F) != 0x7F) continue;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-              const int r = r0 + j;
-              if (r >= a.nrows) break;
-              const int qi = static_cast<int>((r * a.group_magic) >> 16), head = hk * a.group + (r - qi * a.group);
-              uint32_t b2;
-              asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(b2) : "f"(0.f), "f"(o[j]));
-              a.out[((static_cast<int64_t>(sg.b) * a.Nq + qi) * a.Hq + head) * D + tg] =
-                  static_cast<uint16_t>(b2 & 0xFFFFu);
+              const int qi = min(static_cast<int>(((r0 + j) * a.group_magic) >> 16), kMaxNodes - 1);
+              if ((anc[buf][qi][node >> 5] >> (node & 31)) & 1u) o[j] = __int_as_float(0x7fc00000);
             }
-          } else {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) a.part_o[(static_cast<int64_t>(slot) * RT + j0 + j) * D + tg] = o[j];
           }
+        }
+        if (whole) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int r = r0 + j;
+            if (r >= a.nrows) break;
+            const int qi = static_cast<int>((r * a.group_magic) >> 16), head = hk * a.group + (r - qi * a.group);
+            uint32_t b2;
+            asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(b2) : "f"(0.f), "f"(o[j]));
+            a.out[((static_cast<int64_t>(sg.b) * a.Nq + qi) * a.Hq + head) * D + el] =
+                static_cast<uint16_t>(b2 & 0xFFFFu);
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) a.part_o[(static_cast<int64_t>(slot) * RT + j0 + j) * D + el] = o[j];
         }
       }
       tc_fence_before();
