@@ -21,22 +21,34 @@
 // (O and l are rescaled) when some P * v_scale exceeds 2^8, so the row's
 // largest lies in [2^4, 2^8]: p2 underflows 2^-19 of it.  l sums the fp32 P.
 //
-// Work split: the key tiles of all (sequence, KV head, row tile) are one line
-// of units, cut into equal pieces, one per CTA (one CTA per SM), whatever the
-// lengths are; a piece that covers part of an item leaves (O, m, l) in the
-// workspace and k_attn_q8_merge joins them.
+// Work split: the key tiles of all (sequence, KV head, row tile), and kEnd more
+// for each one's end, are one line of units, cut into equal pieces, one per CTA
+// (one CTA per SM), whatever the lengths are; a piece that covers part of an
+// item leaves (O, m, l) in the workspace and k_attn_q8_merge joins them.
 //
-// CTA: two producer warps, an MMA warp, one warp that prepares the next
-// segment's rows (q1, q2, tree masks), and 12 or 16 softmax warps.  Up to 64
-// rows, the softmax warps form streams: stream s takes every NSTR-th tile with
-// all rows of it and has m, l, S, P and O of its own, joined when the segment
-// ends, so the warps of a scheduler are at different tiles and hide one
-// another's latencies, and a warp's fixed work per tile is paid once for all
-// rows.  Above 64 rows the registers and TMEM hold one stream, its rows shared
-// out among groups of 32.
-// K and V tiles come in the order in which the MMAs use them (S runs up to NB
-// tiles ahead of P V), through one ring of tile-sized slots, so that every slot that
-// is not being read is a copy in flight.
+// CTA: softmax warps (groups of four; a group has 16 rows of the tile up to 64
+// rows, 32 above), two producer warps, an MMA warp, and one warp that prepares
+// the next segment's rows (q1, q2, tree masks).  A tile is 256 keys up to 64
+// rows and 128 above (S twice, P twice and O fill the 512 columns of TMEM):
+// what a warp does once per tile costs it as much as the arithmetic, so tiles
+// are as large as fits.  K and V sub-tiles come in the order in which the MMAs
+// use them (S runs up to NB tiles ahead of P V), through one ring, so that every
+// slot that is not being read is a copy in flight; a producer warp issues all
+// eight 2 KB copies of every second sub-tile.
+//
+// Bound: HBM where the rows are few; else the softmax warps' latencies (4 per
+// scheduler, 51% of issue slots used).  64 sequences of 8192 keys, 8 KV heads of
+// 128 with 6 queries of 8 heads each (1.08 GB): 201 us, 5.4 TB/s; without
+// softmax and MMAs 181, without copies too 93.  Ragged batch of 48 sequences up
+// to 16384 keys, 64 rows (411 MB): 96 us, 4.3 TB/s (137 without the ends'
+// units).  One sequence, 100003 keys, one query (205 MB): 46 us, of which the
+// set-up, the first tile and the merge take 12.  16 sequences of 2048 keys with
+// 256 rows (d 64): 84 us, 19 instructions per score.
+//   tried: all softmax in streams of whole tiles (instruction fetch), four
+//   producer warps (verify 214), two prep warps (registers: 110 for the draft),
+//   setmaxnreg (spills), m voted per tile but moved always (every tile pays),
+//   next rows prepared by the softmax warps behind short items (4% of the ragged
+//   batch), row tiles of 64 instead of 128 (83 against 84).
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <math.h>
@@ -1372,6 +1384,7 @@ ssd_status_t ssd_branch_attention_q8(const void *q, const void *k_cache, const v
   const int64_t max_tiles = (max_keys + a.keys - 1) / a.keys;
   const int64_t units = max_tiles * B * a.per_b;
   const unsigned grid = static_cast<unsigned>(units < sms ? units : sms);
+  if ((max_tiles + q8::kEnd) * B * a.per_b / grid > 0x3fffffff) return SSD_ERR_UNSUPPORTED;  // a piece counts in 32 bits
   // items of up to kMinKeys keys are not worth cutting; without room for the parts none is
   const Workspace w = workspace_of(sh, d, sms);
   a.split = max_keys > q8::kMinKeys && ws && ws_bytes >= w.total && !(reinterpret_cast<uintptr_t>(ws) & 255u);

@@ -91,6 +91,18 @@ def test_attention_refusals(lib):
     assert size(0, 1, 8, 2, 64) == 0 and size(2, 1, 7, 2, 64) == 0 and size(2, 1, 8, 2, 96) == 0
 
 
+def test_sizes_beyond_the_counters(lib):
+    """Calls whose counts would leave 32 bits are refused before anything is launched."""
+    good = dict(q=P, kc=P, vc=P, ks=P, vs=P, table=P, maxb=1 << 30, n=100, prefix=P, parent=P, B=1 << 20, N=4, Nq=4,
+                Hq=256, Hkv=32, d=64, scale=0.1, out=P, lse=None, status=P, ws=None, wsb=0, s=None)
+    call(lib.ssd_branch_attention_q8, good, UNS)
+    call(lib.ssd_branch_attention_q8, good, UNS, B=1 << 26)
+    call(lib.ssd_branch_attention_q8, good, UNS, n=1 << 31)
+    good = dict(length=P, reserve=0, B=2, table=P, maxb=4, pages=P, ring=P, n=8, pool=P, slots=P, S=3, status=P, s=None)
+    for k, v in (("S", (1 << 24) + 1), ("B", 65537), ("n", (1 << 27) + 1), ("maxb", (1 << 27) + 1)):
+        call(lib.ssd_block_table_update, good, UNS, **{k: v})
+
+
 @pytest.mark.parametrize("rot,base,factor,original,fast,slow", [
     (64, 10000.0, 1.0, 0.0, 32.0, 1.0), (128, 500000.0, 8.0, 0.0, 32.0, 1.0), (128, 10000.0, 16.0, 4096.0, 32.0, 1.0),
     (2, 10000.0, 2.0, 2048.0, 32.0, 1.0), (24, 1000.0, 40.0, 4096.0, 16.0, 2.0)])

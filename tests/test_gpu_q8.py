@@ -409,6 +409,19 @@ def test_attention(use_ws, d, Hq, Hkv, lengths, parent, Nq):
                     use_ws=use_ws)
 
 
+@pytest.mark.parametrize("use_ws", [True, False], ids=["split", "unsplit"])
+@pytest.mark.parametrize("d,Hq,Hkv,Nq", [(64, 2, 2, 1), (128, 16, 1, 8), (128, 4, 1, 9)])
+@pytest.mark.parametrize("B,long", [(151, ()), (153, (0,)), (700, (13, 350, 699)), (320, (100, 101, 102))])
+def test_attention_many_short_sequences(use_ws, d, Hq, Hkv, Nq, B, long):
+    """Hundreds of sequences of one tile and a few of many: pieces begin and end at any place of an item, its end
+    included, and a CTA runs many items."""
+    rng = np.random.default_rng(B + d)
+    lengths = [int(x) for x in rng.integers(0, 40, B)]
+    for b in long:
+        lengths[b] = 2500 + b
+    check_attention(attention_inputs(B, Hq, Hkv, d, lengths, CHAIN(Nq), Nq, seed=B), use_ws=use_ws)
+
+
 @pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("group", [1, 2, 5, 16])
 def test_attention_largest_trees(d, group):
