@@ -74,7 +74,9 @@ constexpr int kPages = kSub / kPage;       // 8
 // tile's largest of 128 keys is a low guess of the largest of thousands, and
 // moving m costs about a tile's time.
 constexpr float kBias = 4.f, kMoved = 5.f, kGrow = 8.f;
-constexpr int kMinKeys = 512;              // keys of the smallest piece: below, joining costs more than it gives
+// Keys of the smallest piece, and the longest table whose items are not cut: joining costs 3 us.  One query, 8 heads:
+// 2000 keys 14.2 us in pieces of 512, 15.9 of 1024, 17.2 whole; 1000 keys 13.3 in pieces of 512, 12.5 whole.
+constexpr int kMinKeys = 512, kWholeKeys = 1024;
 // An item's end costs its CTA about two tiles' time and, where items are short, the rows of the next one six
 // (one warp prepares them).  Ragged batch of 1 to 16384 keys: 0: 129 us, 2: 112, 4: 107, 6: 95, 8: 97, 12: 104.
 constexpr int kEnd = 6;
@@ -1385,9 +1387,9 @@ ssd_status_t ssd_branch_attention_q8(const void *q, const void *k_cache, const v
   const int64_t units = max_tiles * B * a.per_b;
   const unsigned grid = static_cast<unsigned>(units < sms ? units : sms);
   if ((max_tiles + q8::kEnd) * B * a.per_b / grid > 0x3fffffff) return SSD_ERR_UNSUPPORTED;  // a piece counts in 32 bits
-  // items of up to kMinKeys keys are not worth cutting; without room for the parts none is
+  // short items are not worth cutting; without room for the parts none is cut
   const Workspace w = workspace_of(sh, d, sms);
-  a.split = max_keys > q8::kMinKeys && ws && ws_bytes >= w.total && !(reinterpret_cast<uintptr_t>(ws) & 255u);
+  a.split = max_keys > q8::kWholeKeys && ws && ws_bytes >= w.total && !(reinterpret_cast<uintptr_t>(ws) & 255u);
   if (a.split) {
     char *const p = static_cast<char *>(ws);
     a.part_o = reinterpret_cast<float *>(p + w.o);
