@@ -110,6 +110,10 @@ constexpr uint32_t kSw128 = 2, kSw64 = 4;
 __host__ __device__ constexpr uint32_t idesc_f8(int N, uint32_t mn) {
   return (1u << 4) | (mn << 15) | (mn << 16) | (static_cast<uint32_t>(N >> 3) << 17) | (8u << 24);
 }
+// the same with A K-major and B MN-major
+__host__ __device__ constexpr uint32_t idesc_f8_kn(int N) {
+  return (1u << 4) | (1u << 16) | (static_cast<uint32_t>(N >> 3) << 17) | (8u << 24);
+}
 // byte offset of (row r, byte c) in a block of 128-byte rows, 128-byte swizzled
 SSD_DEV uint32_t sw128(int r, int c) {
   return (r >> 3) * 1024 + (r & 7) * 128 + ((((c >> 4) ^ (r & 7)) << 4) | (c & 15));
@@ -360,6 +364,7 @@ struct Order {
 
 template <int D, int RT>
 struct Cfg {
+  static constexpr bool kRowLanes = RT > 64;               // rows, not keys, on the MMA's 128-wide side
   static constexpr int KT = RT <= 64 ? 2 : 1;              // sub-tiles of a tile
   static constexpr int kKeys = KT * kSub;                  // keys of a tile
   static constexpr int CG = RT <= 64 ? 16 : 32;            // rows of a softmax warp
@@ -380,7 +385,7 @@ struct Cfg {
   static constexpr int kQ = 0, kP = 2 * kQBuf, kRing = kFixed;
   static constexpr int kSmem = kFixed + kSlots * kSlot + 1024;
   static constexpr int kOCol = NB * KT * RT;               // TMEM: NB x KT x S, then O1, O2
-  static constexpr uint32_t kCols = kOCol + 2 * RT;
+  static constexpr uint32_t kCols = kOCol + 2 * (kRowLanes ? D : RT);
   static constexpr uint32_t kTmem = kCols <= 64 ? 64 : (kCols <= 128 ? 128 : (kCols <= 256 ? 256 : 512));
   static constexpr int kMeta = 16 / KT;                    // tiles whose block scales are held
   static_assert(kSmem + 13824 <= 227 * 1024, "shared memory with the static part");
@@ -390,6 +395,7 @@ struct Cfg {
   // loads further back.  P V of tile i - NB is the last of a tile before the K loads of tile i.
   static constexpr int kBack = kSlots + 2 * kTmaWarps + KT - 1;
   static_assert(kMeta >= NB + (kBack + 2 * KT - 1) / (2 * KT), "block scales");
+  static_assert(!kRowLanes || (RT == 128 && kGroups == 4), "a lane per row, a quarter of the keys per group");
   static_assert(kCols <= 512 && RT % CG == 0 && CG % 16 == 0 && CG <= 32 && kGroups <= 8, "rows");
 };
 
@@ -623,6 +629,37 @@ __global__ void __launch_bounds__(Cfg<D, RT>::kThreads, 1)
     prepare_rows<D, RT>(a, sg, smem + C::kQ + buf * C::kQBuf, par[buf], anc[buf], qs[buf], w, n, bar);
   };
 
+  // V of tile i, sub-tile h (of segment x: tiles i0 .. i0 + n - 1), this thread's key: hidden keys take no part whatever
+  // their v holds (0 * NaN): their rows become 0; a tree node's NaN becomes 0 too, and reaches the rows that see it at
+  // the segment's end; a prefix key stays.  False when the wait for V gave up.
+  auto void_rows = [&](const Segments &x, int seg, int i, int i0, int n, bool gone, bool prefix, int h) -> bool {
+    Segments after = x;
+    const int hold = after.step(a) ? i0 + n + after.t1 - after.t0 : ntiles;
+    const int load = (min(min(ntiles, i + NB), hold) + i) * KT + h;  // V's place in the order of loads
+    const bool ok = warp_wait(&full[load % NSLOT], (load / NSLOT) & 1);
+    if (prefix) return ok;
+    const int key = tid & 127;
+    uint8_t *const vt = smem + C::kRing + (load % NSLOT) * C::kSlot;
+#pragma unroll 1
+    for (int e = 0; e < D; e += 16) {
+      uint4 *const at = reinterpret_cast<uint4 *>(vt + (D == 128 ? sw128(key, e) : sw64(key, e)));
+      uint4 v = make_uint4(0, 0, 0, 0);
+      if (!gone) {
+        v = *at;
+        uint32_t any = 0;
+        auto clear = [&](uint32_t w) {
+          const uint32_t nan = ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;  // bytes 0x7F, 0xFF
+          any |= nan;
+          return w & ~((nan >> 7) * 0xFFu);
+        };
+        v = make_uint4(clear(v.x), clear(v.y), clear(v.z), clear(v.w));
+        if (any) s_nan[seg & 1] = 1;
+      }
+      *at = v;
+    }
+    return ok;
+  };
+
   Segments sg;
   if (warp >= C::kTmaWarp && warp < C::kMmaWarp) {
     // ---------------- producers.  A load's fixed work costs its warp about 500 clocks and a copy 65 (the TMA unit's
@@ -757,11 +794,12 @@ __global__ void __launch_bounds__(Cfg<D, RT>::kThreads, 1)
   } else if (warp == C::kMmaWarp) {
     // ---------------- MMA issue (one elected lane): S of up to NB tiles ahead, then P V and S in turn.  This loop
     // is one warp's chain of scalar work per tile, so what can be is kept in running words.
-    constexpr uint32_t idesc_s = idesc_f8(RT, 0), idesc_o = idesc_f8(2 * RT, 1);
+    constexpr uint32_t idesc_s = idesc_f8(C::kRowLanes ? kSub : RT, 0);
+    constexpr uint32_t idesc_o = C::kRowLanes ? idesc_f8_kn(D) : idesc_f8(2 * RT, 1);
     constexpr uint32_t hi128 = desc_hi(1024, kSw128), hi64 = desc_hi(512, kSw64), hi_kv = D == 128 ? hi128 : hi64;
     const uint32_t base = smem_u32(smem);
     const uint32_t ring_k = desc_lo(base + C::kRing, 16), ring_v = desc_lo(base + C::kRing, D == 128 ? 16 : 0);
-    const uint32_t p_lo = desc_lo(base + C::kP, C::kPBlock);
+    const uint32_t p_lo = desc_lo(base + C::kP, C::kRowLanes ? 16 : C::kPBlock);
     bool ok = true;
     int slot = 0, seg = 0;
     uint32_t phase = 0;  // of full[slot]
@@ -777,9 +815,13 @@ __global__ void __launch_bounds__(Cfg<D, RT>::kThreads, 1)
 #pragma unroll
       for (int term = 0; term < 2; ++term)
 #pragma unroll
-        for (int kk = 0; kk < D / 32; ++kk)
-          umma_f8(d, k + kk * 2, hi_kv, q + (term * (D == 128 ? C::kQTile : 64) >> 4) + kk * 2, hi128, idesc_s,
-                  (term > 0 || kk > 0) ? 1u : 0u);
+        for (int kk = 0; kk < D / 32; ++kk) {
+          const uint32_t qk = q + (term * (D == 128 ? C::kQTile : 64) >> 4) + kk * 2, more = (term > 0 || kk > 0) ? 1u : 0u;
+          if (C::kRowLanes)
+            umma_f8(d, qk, hi128, k + kk * 2, hi_kv, idesc_s, more);
+          else
+            umma_f8(d, k + kk * 2, hi_kv, qk, hi128, idesc_s, more);
+        }
     };
     auto issue_s = [&](int i) {
       const int buf = seg & 1, u = i % NB;
@@ -827,9 +869,15 @@ __global__ void __launch_bounds__(Cfg<D, RT>::kThreads, 1)
           const uint32_t v = ring_v + slot * (C::kSlot >> 4), p = p_lo + (u * KT + h) * (C::kPBuf >> 4);
           if (elect_one()) {
 #pragma unroll
-            for (int kk = 0; kk < kSub / 32; ++kk)  // 32 keys: four groups of 8 rows
-              umma_f8(o, v + kk * ((32 * D) >> 4), hi_kv, p + kk * (4096 >> 4), hi128, idesc_o,
-                      (h > 0 || kk > 0) ? 1u : later);
+            for (int kk = 0; kk < kSub / 32; ++kk) {  // 32 keys: four groups of 8 rows
+              const uint32_t vk = v + kk * ((32 * D) >> 4), more = (h > 0 || kk > 0) ? 1u : later;
+              if (C::kRowLanes) {
+                umma_f8(o, p + kk * 2, hi128, vk, hi_kv, idesc_o, more);
+                umma_f8(o + D, p + (C::kPBlock >> 4) + kk * 2, hi128, vk, hi_kv, idesc_o, more);
+              } else {
+                umma_f8(o, vk, hi_kv, p + kk * (4096 >> 4), hi128, idesc_o, more);
+              }
+            }
             umma_commit(&empty[slot]);
             if (h == KT - 1) umma_commit(&pvdone[u]);
           }
@@ -858,6 +906,246 @@ __global__ void __launch_bounds__(Cfg<D, RT>::kThreads, 1)
       }
       prepare(sg, buf, 0, 1, 11);
       if (lane == 0) mbar_arrive1(&qfull[buf]);
+    }
+  } else if constexpr (C::kRowLanes) {
+    // ---------------- softmax, a lane per row: group g has the keys g * 32 .. + 31 of every tile
+    const int g = warp / 4, wg = warp & 3, r = tid & 127;
+    const uint32_t lane_off = static_cast<uint32_t>(wg * 32) << 16;
+    const uint32_t tS = tmem + g * 32 + lane_off, tO = tmem + C::kOCol + g * (D / 4) + lane_off;
+    const int bar = 1 + wg;  // the four warps that share 32 rows
+    int i0 = 0, seg = 0;     // the segment's first tile in the CTA's count
+    uint32_t sphase = 0;     // parities of sfull
+    bool dead = false;
+    bool more = sg.first(a, piece);
+    if (more) {
+      prepare(sg, 0, warp, C::kSoftWarps + 1, 10);
+      bar_sync(10, (C::kSoftWarps + 1) * 32);
+    }
+    for (; more; more = sg.step(a), ++seg) {
+      const int buf = seg & 1, n = sg.t1 - sg.t0, row = sg.mt * RT + r;
+      const bool live = row < a.nrows, some = sg.mt * RT + wg * 32 < a.nrows;  // this row; some row of the warp
+      const int qi = min(static_cast<int>((row * a.group_magic) >> 16), kMaxNodes - 1);
+      bool ok = warp_wait(&qfull[buf], (seg >> 1) & 1);
+      const float qscale = live ? qs[buf][r] : 0.f;
+      // the row's m (all four groups keep it), and what is added to its scores; a row behind the last gets p = 0
+      float m = NEG_INF, add = live ? 0.f : -1e30f;
+      uint64_t l2[2] = {0, 0};
+      bool begin = true, unset = live;  // before the segment's first tile; no visible key so far
+      for (int x = 0; x < n; ++x) {
+        const int i = i0 + x, t = sg.t0 + x, u = i % NB;  // u: S and P buffer
+        ok = ok && warp_wait(&sfull[u], sphase >> u & 1);
+        sphase ^= 1u << u;  // the scales were there before K was
+        tc_fence_after();
+        bool part = (t + 1) * kSub > min(sg.L, sg.nkeys);
+        part = __any_sync(0xffffffffu, part || (lane < kPages && meta[i % kMeta][lane].y < 0.f));
+        if (some) {
+          float cq[2], wv[2], lsv[2];
+          uint32_t vis = ~0u;
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float4 sc = meta[i % kMeta][g * 2 + e];
+            cq[e] = fminf(sc.x * qscale, 3e38f);
+            wv[e] = fmaxf(sc.y, 0.f);
+            lsv[e] = sc.z;
+            if (sc.y < 0.f) vis &= e ? 0x0000FFFFu : 0xFFFF0000u;
+          }
+          if (part) {
+            const int k0 = t * kSub + g * 32, left = sg.nkeys - k0, node = k0 - sg.L;  // of bit 0
+            if (left < 32) vis &= left <= 0 ? 0u : (1u << left) - 1u;
+            if (node > -32) {
+              const uint32_t *const bits = anc[buf][qi];
+              const int word = node >> 5;
+              const uint32_t lo = node < 0 ? ~0u : (word < kMaxNodes / 32 ? bits[word] : 0u);
+              const uint32_t hi = word + 1 < kMaxNodes / 32 ? bits[word + 1] : 0u;
+              vis &= __funnelshift_r(lo, hi, node & 31);
+            }
+          }
+          float y[32];
+          // y = x - m + 4 (x for a row without m); hidden keys -inf
+          auto scores = [&]() {
+            tmem_ld16_async(tS + u * kSub, y);
+            tmem_ld16_async(tS + u * kSub + 16, y + 16);
+            tmem_wait16(y);
+            tmem_wait16(y + 16);
+            const uint64_t add2 = pack2(add, add);
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const uint64_t c2 = pack2(cq[e], cq[e]);
+#pragma unroll
+              for (int j = e * 16; j < e * 16 + 16; j += 2)
+                unpack2(fma2(pack2(y[j], y[j + 1]), c2, add2), y[j], y[j + 1]);
+            }
+            if (part) {
+#pragma unroll
+              for (int j = 0; j < 32; ++j) y[j] = ((vis >> j) & 1u) ? y[j] : NEG_INF;
+            }
+          };
+          // y, and whether a row's m has to move; then once more with the new m
+#pragma unroll 1
+          for (int pass = 0;; ++pass) {
+            scores();
+            if (pass == 1) break;
+            float top = NEG_INF;
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              float t4[4] = {y[e * 16], y[e * 16 + 1], y[e * 16 + 2], y[e * 16 + 3]};
+#pragma unroll
+              for (int j = 4; j < 16; ++j) t4[j & 3] = fmaxf(t4[j & 3], y[e * 16 + j]);
+              top = fmaxf(top, fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3])) + lsv[e]);
+            }
+            if (!bar_or(bar, 128, top > kGrow || unset || !ok)) break;
+            red[g][r] = top;
+            // O is rescaled below: every P V before has to be in it
+            if (!begin) {
+              ok = warp_wait(&pvdone[(i - 1) % NB], ((i - 1) / NB) & 1) && ok;
+              tc_fence_after();
+            }
+            if (bar_or(bar, 128, !ok)) {
+              dead = true;
+              break;
+            }
+            const float z = fmaxf(fmaxf(red[0][r], red[1][r]), fmaxf(red[2][r], red[3][r]));
+            bar_sync(bar, 128);  // read, before the next is written
+            float f = 1.f;
+            if (live) {
+              if (m == NEG_INF) {
+                m = z;
+                unset = m == NEG_INF;
+              } else if (z > kGrow) {
+                m += z - kMoved;
+                f = ex2(kMoved - z);
+              }
+              add = unset ? 0.f : kBias - m;
+            }
+            if (!begin && __any_sync(0xffffffffu, f != 1.f)) {
+              const uint64_t f2 = pack2(f, f);
+              l2[0] = mul2(l2[0], f2);
+              l2[1] = mul2(l2[1], f2);
+#pragma unroll 1
+              for (int k = 0; k < 2 * (D / 64); ++k) {  // this group's quarter of both accumulators
+                const uint32_t at = tO + (k & 1) * D + (k >> 1) * 16;
+                float o[16];
+                tmem_ld16(at, o);
+#pragma unroll
+                for (int j = 0; j < 16; ++j) o[j] *= f;
+                tmem_st16(at, o);
+              }
+            }
+          }
+          if (dead) break;
+          begin = false;
+          // the P buffer is free: S of this tile was issued behind P V of tile i - NB
+          uint8_t *const pb = smem + C::kP + u * C::kPBuf;
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const uint64_t w2 = pack2(wv[e], wv[e]);
+            uint32_t p1[4], p2[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              uint16_t e1[2], e2[2];
+#pragma unroll
+              for (int k = 0; k < 2; ++k) {
+                const int j = e * 16 + q * 4 + k * 2;
+                const uint64_t p = pack2(ex2(y[j]), ex2(y[j + 1]));
+                l2[k] = ssd::add2(l2[k], p);
+                float a0, a1;
+                unpack2(mul2(p, w2), a0, a1);
+                const uint32_t hp = half2_of(a0, a1);
+                e1[k] = e4m3_of_half2(hp);
+                // 32 (p - p1) in halves: exact (p is at most 2^8, the difference has at most 11 bits)
+                e2[k] = e4m3_of_half2(hfma2(e4m3_to_half2(e1[k]), 0xD000D000u, hmul2(hp, 0x50005000u)));
+              }
+              p1[q] = pack16(e1[0], e1[1]);
+              p2[q] = pack16(e2[0], e2[1]);
+            }
+            const uint32_t at = sw128(r, g * 32 + e * 16);
+            *reinterpret_cast<uint4 *>(pb + at) = make_uint4(p1[0], p1[1], p1[2], p1[3]);
+            *reinterpret_cast<uint4 *>(pb + C::kPBlock + at) = make_uint4(p2[0], p2[1], p2[2], p2[3]);
+          }
+        }
+        if (part && g == 0) {
+          const int pos = t * kSub + r;  // here a lane has a key
+          const bool gone = meta[i % kMeta][r / kPage].y < 0.f || pos >= sg.nkeys;
+          ok = void_rows(sg, seg, i, i0, n, gone, !gone && pos < sg.L, 0) && ok;
+        }
+        fence_proxy_async();  // P and V (generic writes) -> visible to the tensor cores
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive1(&pfull[u]);
+      }
+      // ---------------- the segment's end: l, then O from TMEM, a quarter of the row's elements each
+      if (dead) ok = false;
+      {
+        float l0, l1, l3, l4;
+        unpack2(l2[0], l0, l1);
+        unpack2(l2[1], l3, l4);
+        red[g][r] = __fadd_rn(__fadd_rn(l0, l1), __fadd_rn(l3, l4));
+      }
+      const int il = i0 + n - 1;
+      ok = ok && warp_wait(&pvdone[il % NB], (il / NB) & 1);
+      tc_fence_after();
+      if (bar_or(9, kSoftThreads, !ok)) {
+        s_abort = 1;
+        break;
+      }
+      const bool whole = sg.t0 == 0 && sg.t1 == sg.nt, nan = s_nan[seg & 1] != 0;
+      if (tid == 0) s_nan[(seg + 1) & 1] = 0;
+      if (some) {
+        const int slot = blockIdx.x * 2 + (sg.t0 > 0 ? 0 : 1);
+        const float L = __fadd_rn(__fadd_rn(red[0][r], red[1][r]), __fadd_rn(red[2][r], red[3][r]));
+        const float factor = L == 0.f ? 0.f : (whole ? 1.f / L : 1.f);
+        const int64_t orow = (static_cast<int64_t>(sg.b) * a.Nq + qi) * a.Hq + sg.hk * a.group + (row - qi * a.group);
+        if (live && g == 0) {
+          if (!whole)
+            a.part_ml[slot * RT + r] = make_float2(m, L);
+          else if (a.lse)
+            a.lse[orow] = L == 0.f ? NEG_INF : (m - kBias + log2f(L)) * 0.69314718055994531f;
+        }
+#pragma unroll 1
+        for (int j0 = 0; j0 < D / 4; j0 += 16) {
+          float o[16], o2[16];
+          tmem_ld16_async(tO + j0, o);
+          tmem_ld16_async(tO + D + j0, o2);
+          tmem_wait16(o);
+          tmem_wait16(o2);
+#pragma unroll
+          for (int j = 0; j < 16; ++j) o[j] = fmaf(o2[j], 0.03125f, o[j]) * factor;
+          if (!live) continue;
+          const int e0 = g * (D / 4) + j0;
+          if (nan) {
+            // tree nodes of this segment that this row sees and whose v holds NaN
+            const int from = sg.t0 * C::kKeys - sg.L, to = min(sg.nkeys, sg.t1 * C::kKeys) - sg.L;
+            for (int node = max(0, from); node < to; ++node) {
+              if (!((anc[buf][qi][node >> 5] >> (node & 31)) & 1u)) continue;
+              const int pos = sg.L + node, blk = a.table[static_cast<int64_t>(sg.b) * a.maxb + pos / kPage];
+              if (blk < 0 || blk >= a.num_blocks) continue;
+              const int64_t unit = static_cast<int64_t>(blk) * a.Hkv + sg.hk;
+              if (!good_scale(a.ks[unit]) || !good_scale(a.vs[unit])) continue;
+              const uint8_t *const code = a.vc + (unit * kPage + pos % kPage) * D + e0;
+#pragma unroll
+              for (int j = 0; j < 16; ++j)
+                if ((code[j] & 0x7F) == 0x7F) o[j] = __int_as_float(0x7fc00000);
+            }
+          }
+          if (whole) {
+            uint32_t h[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(h[j]) : "f"(o[2 * j + 1]), "f"(o[2 * j]));
+            uint4 *const to = reinterpret_cast<uint4 *>(a.out + orow * D + e0);
+            to[0] = make_uint4(h[0], h[1], h[2], h[3]);
+            to[1] = make_uint4(h[4], h[5], h[6], h[7]);
+          } else {
+            float4 *const to = reinterpret_cast<float4 *>(a.part_o + (static_cast<int64_t>(slot) * RT + r) * D + e0);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) to[j] = make_float4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+          }
+        }
+      }
+      tc_fence_before();
+      bar_sync(9, kSoftThreads);  // O and the sums have been read
+      if (lane == 0) mbar_arrive1(&qempty[buf]);
+      i0 += n;
     }
   } else {
     // ---------------- softmax: group g of the rows, one thread per key
@@ -1061,35 +1349,10 @@ __global__ void __launch_bounds__(Cfg<D, RT>::kThreads, 1)
           }
         }
         if (part && g == 0) {
-          // hidden keys take no part whatever their v holds (0 * NaN): their rows become 0; a tree node's NaN
-          // becomes 0 too, and reaches the rows that see it at the end
-          Segments after = sg;
-          const int hold = after.step(a) ? i0 + n + after.t1 - after.t0 : ntiles;
-          const int load0 = (min(min(ntiles, i + NB), hold) + i) * KT;  // V's place in the order of loads
 #pragma unroll 1
           for (int h = 0; h < KT; ++h) {
-            const int load = load0 + h;
             const bool gone = KT == 2 && h ? hidden[KT - 1] : hidden[0];
-            ok = warp_wait(&full[load % NSLOT], (load / NSLOT) & 1) && ok;
-            uint8_t *const vt = smem + C::kRing + (load % NSLOT) * C::kSlot;
-            if (!gone && t * C::kKeys + h * kSub + tg < sg.L) continue;
-#pragma unroll 1
-            for (int e = 0; e < D; e += 16) {
-              uint4 *const at = reinterpret_cast<uint4 *>(vt + (D == 128 ? sw128(tg, e) : sw64(tg, e)));
-              uint4 v = make_uint4(0, 0, 0, 0);
-              if (!gone) {
-                v = *at;
-                uint32_t any = 0;
-                auto clear = [&](uint32_t w) {
-                  const uint32_t nan = ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;  // bytes 0x7F, 0xFF
-                  any |= nan;
-                  return w & ~((nan >> 7) * 0xFFu);
-                };
-                v = make_uint4(clear(v.x), clear(v.y), clear(v.z), clear(v.w));
-                if (any) s_nan[seg & 1] = 1;
-              }
-              *at = v;
-            }
+            ok = void_rows(sg, seg, i, i0, n, gone, !gone && t * C::kKeys + h * kSub + tg < sg.L, h) && ok;
           }
         }
         fence_proxy_async();  // P and V (generic writes) -> visible to the tensor cores
@@ -1264,8 +1527,7 @@ bool make_code_map(CUtensorMap *m, const void *base, int64_t num_blocks, int Hkv
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Rows of a tile: at most 128, the tiles of equal size, a multiple of the MMA's
-// step of 16 (of the 32 rows of a softmax warp above 64).
+// Rows of a tile: up to 64, the tiles of equal size, a multiple of the MMA's step of 16; above, 128 (the MMA's M).
 struct Shape {
   int nrows, mtiles, RT;
 };
@@ -1274,7 +1536,7 @@ Shape shape_of(int Nq, int Hq, int Hkv) {
   s.nrows = (Hq / Hkv) * Nq;
   s.mtiles = (s.nrows + 127) / 128;
   const int tile = (s.nrows + s.mtiles - 1) / s.mtiles;
-  s.RT = tile <= 64 ? (tile + 15) / 16 * 16 : (tile + 31) / 32 * 32;
+  s.RT = tile <= 64 ? (tile + 15) / 16 * 16 : 128;
   return s;
 }
 size_t align256(size_t x) { return (x + 255) / 256 * 256; }
@@ -1321,7 +1583,6 @@ cudaError_t launch_shape(const Shape &s, const CUtensorMap &kmap, const CUtensor
     case 32: return launch<D, 32>(kmap, vmap, a, grid, cs);
     case 48: return launch<D, 48>(kmap, vmap, a, grid, cs);
     case 64: return launch<D, 64>(kmap, vmap, a, grid, cs);
-    case 96: return launch<D, 96>(kmap, vmap, a, grid, cs);
     default: return launch<D, 128>(kmap, vmap, a, grid, cs);
   }
 }
