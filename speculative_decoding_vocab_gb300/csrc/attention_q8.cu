@@ -2,10 +2,12 @@
 // in 8 bits (e4m3 codes, one scale per block of 16 positions and KV head), on
 // the sm_103a tensor cores.
 //
-// The codes go to the tensor cores as they are (kind::f8f6f4, fp32 sums); a
-// decode step has few query rows and many keys, so the keys take the MMA's
-// 128-wide side and the rows its N:
-//     S^T [128 keys x rows] = K8 Q^T,      O^T [d x rows] += V8^T P^T.
+// The codes go to the tensor cores as they are (kind::f8f6f4, fp32 sums).  A
+// decode step has few query rows and many keys, so up to 64 rows per KV head
+// the keys take the MMA's 128-wide side and the rows its N:
+//     S^T [128 keys x rows] = K8 Q^T,      O^T [d x rows] += V8^T P^T;
+// above, the rows fill that side themselves:
+//     S [128 rows x 128 keys] = Q K8^T,    O [128 rows x d] += P V8.
 // What 8 bits would lose of the bf16 queries and of the probabilities is kept
 // in a second term:
 //   q = 2^e (q1 + q2): e4m3 holds 4 significant bits, so q1 = e4m3(q) leaves a
@@ -15,40 +17,42 @@
 //   p = p1 + p2 / 32 with p1 = e4m3(p), p2 = e4m3(32 (p - p1)): off by at most
 //     2^-8 p, as a bf16 p would be, or 2^-15 where p2 underflows; p1 and p2
 //     lie side by side in N and fill two accumulators, O = O1 + O2 / 32.
-// A key's thread (its TMEM lane) knows its block's scales: x = s * k_scale *
-// scale * 2^e, P = 2^(x - m + 4), and P * v_scale is what is split into p1 and p2.
-// m starts as the largest x + log2(v_scale) of the row's first keys and moves
-// (O and l are rescaled) when some P * v_scale exceeds 2^8, so the row's
-// largest lies in [2^4, 2^8]: p2 underflows 2^-19 of it.  l sums the fp32 P.
+// Block scales enter in fp32: x = s * k_scale * scale * 2^e, P = 2^(x - m + 4),
+// and P * v_scale is what is split into p1 and p2 (a lane has one key of 16 rows,
+// or one row of 32 keys).  m starts as the largest x + log2(v_scale) of the
+// row's first keys and moves (O and l are rescaled) when some P * v_scale exceeds
+// 2^8, so the row's largest lies in [2^4, 2^8]: p2 underflows 2^-19 of it.  l sums
+// the fp32 P.
 //
 // Work split: the key tiles of all (sequence, KV head, row tile), and kEnd more
 // for each one's end, are one line of units, cut into equal pieces, one per CTA
 // (one CTA per SM), whatever the lengths are; a piece that covers part of an
 // item leaves (O, m, l) in the workspace and k_attn_q8_merge joins them.
 //
-// CTA: softmax warps (groups of four; a group has 16 rows of the tile up to 64
-// rows, 32 above), two producer warps, an MMA warp, and one warp that prepares
-// the next segment's rows (q1, q2, tree masks).  A tile is 256 keys up to 64
-// rows and 128 above (S twice, P twice and O fill the 512 columns of TMEM):
-// what a warp does once per tile costs it as much as the arithmetic, so tiles
-// are as large as fits.  K and V sub-tiles come in the order in which the MMAs
+// CTA: softmax warps (groups of four: 16 rows of the tile each, or with a lane
+// per row a quarter of its keys), two producer warps, an MMA warp, and one warp
+// that prepares the next segment's rows (q1, q2, tree masks).  A tile is 256
+// keys up to 64 rows and 128 above (S twice, P twice and O fill TMEM's 512
+// columns): what a warp does once per tile costs it as much as the arithmetic, so
+// tiles are as large as fits.  K and V sub-tiles come in the order in which the MMAs
 // use them (S runs up to NB tiles ahead of P V), through one ring, so that every
 // slot that is not being read is a copy in flight; a producer warp issues all
 // eight 2 KB copies of every second sub-tile.
 //
 // Bound: HBM where the rows are few; else the softmax warps' latencies (4 per
-// scheduler, 51% of issue slots used).  64 sequences of 8192 keys, 8 KV heads of
+// scheduler, half of the issue slots used).  64 sequences of 8192 keys, 8 KV heads of
 // 128 with 6 queries of 8 heads each (1.08 GB): 201 us, 5.4 TB/s; without
 // softmax and MMAs 181, without copies too 93.  Ragged batch of 48 sequences up
 // to 16384 keys, 64 rows (411 MB): 96 us, 4.3 TB/s (137 without the ends'
 // units).  One sequence, 100003 keys, one query (205 MB): 46 us, of which the
 // set-up, the first tile and the merge take 12.  16 sequences of 2048 keys with
-// 256 rows (d 64): 84 us, 19 instructions per score.
+// 256 rows (d 64): 66 us, 15 instructions per score (84 us and 19 with the keys
+// on the 128-wide side: masks, maxima and row constants are a lane's own here).
 //   tried: all softmax in streams of whole tiles (instruction fetch), four
 //   producer warps (verify 214), two prep warps (registers: 110 for the draft),
 //   setmaxnreg (spills), m voted per tile but moved always (every tile pays),
 //   next rows prepared by the softmax warps behind short items (4% of the ragged
-//   batch), row tiles of 64 instead of 128 (83 against 84).
+//   batch), three S and P buffers for the draft (67).
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <math.h>
@@ -367,7 +371,7 @@ struct Cfg {
   static constexpr bool kRowLanes = RT > 64;               // rows, not keys, on the MMA's 128-wide side
   static constexpr int KT = RT <= 64 ? 2 : 1;              // sub-tiles of a tile
   static constexpr int kKeys = KT * kSub;                  // keys of a tile
-  static constexpr int CG = RT <= 64 ? 16 : 32;            // rows of a softmax warp
+  static constexpr int CG = RT <= 64 ? 16 : 32;            // rows of a softmax warp (keys, with a lane per row)
   static constexpr int kGroups = RT / CG;                  // groups of four warps
   static constexpr int NB = 2;                             // S and P buffers; S runs NB tiles ahead
   static constexpr int kSoftWarps = 4 * kGroups;
