@@ -1531,7 +1531,9 @@ bool make_code_map(CUtensorMap *m, const void *base, int64_t num_blocks, int Hkv
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Rows of a tile: up to 64, the tiles of equal size, a multiple of the MMA's step of 16; above, 128 (the MMA's M).
+// Rows of a tile: up to 64, the tiles of equal size, a multiple of the MMA's step of 16; above, 128 (the MMA's M, a
+// lane per row).  With a lane per row 64 rows take 142 us instead of 94 (ragged batch), 48 rows 336 instead of 198
+// (verify): half of the lanes have none.
 struct Shape {
   int nrows, mtiles, RT;
 };
