@@ -466,11 +466,24 @@ def ssd_tree_verify(target, draft, V, T, parent, tokens, u_acc, u_bonus, accept_
 # the 8-bit cache of the branch decode
 # ---------------------------------------------------------------------------
 # These calls are made per layer and decode step, where the kernels take a few
-# microseconds: one pass of checks per tensor, messages built only for a refusal.
-def _refuse(x, dtype, shape, dev, what, how="contiguous"):
-    if x.get_device() != dev:
-        raise ValueError(f"all tensors of a call must live on one device, got {what} on {x.device}")
-    raise ValueError(f"{what} must be a {how} {dtype} tensor of shape {shape}, got {x.dtype} {tuple(x.shape)}")
+# microseconds: each call tests its tensors in one expression, and only a
+# refusal looks for the one to name.
+def _refuse(dev, *tensors):
+    """Raise for the first of (tensor, dtype, shape, name) that is not a dense tensor of these on device ``dev``."""
+    for x, dtype, shape, what in tensors:
+        if x is None:
+            continue
+        if x.get_device() != dev:
+            raise ValueError(f"all tensors of a call must live on one device, got {what} on {x.device}")
+        if dtype is None and x.dtype not in _CODES:
+            raise ValueError(f"{what} must hold e4m3 codes (float8_e4m3fn or uint8), got {x.dtype}")
+        if (dtype is not None and x.dtype != dtype) or x.shape != shape or not x.is_contiguous():
+            raise ValueError(f"{what} must be a contiguous {dtype or 'e4m3'} tensor of shape {tuple(shape)}, "
+                             f"got {x.dtype} {tuple(x.shape)}")
+    raise ValueError("tensors of a call must be dense and live on one device")
+
+
+_CODES = (torch.float8_e4m3fn, torch.uint8)
 
 
 def _dense(x, dtype, shape, dev, what):
@@ -478,21 +491,14 @@ def _dense(x, dtype, shape, dev, what):
     if x is None:
         return None
     if x.dtype is not dtype or x.shape != shape or x.get_device() != dev or not x.is_contiguous():
-        _refuse(x, dtype, shape, dev, what)
+        _refuse(dev, (x, dtype, shape, what))
     return x.data_ptr()
-
-
-def _codes(x, shape, dev, what):
-    dtype = x.dtype
-    if dtype is not torch.float8_e4m3fn and dtype is not torch.uint8:
-        raise ValueError(f"{what} must hold e4m3 codes (float8_e4m3fn or uint8), got {dtype}")
-    return _dense(x, dtype, shape, dev, what)
 
 
 def _rows(x, dtype, shape, dev, what):
     """Address and (sequence, token) strides of [B, S, H, d] rows whose heads are dense."""
     if x.dtype is not dtype or x.shape != shape or x.get_device() != dev:
-        _refuse(x, dtype, shape, dev, what, "strided")
+        _refuse(dev, (x, dtype, shape, what))
     ss, ts, hs, es = x.stride()
     if (es != 1 and shape[3] > 1) or (hs != shape[3] and shape[2] > 1):
         raise ValueError(f"{what}: the heads of a token must be contiguous")
@@ -525,8 +531,9 @@ def ssd_block_table_update(length, reserve, block_table, pages, ring, pool, slot
     i32 = torch.int32
     dev = block_table.get_device()
     _launch("ssd_block_table_update", dev, stream,
-            _dense(length, i32, (B,), dev, "length"), int(reserve), B, _dense(block_table, i32, (B, maxb), dev, "block_table"),
-            maxb, _dense(pages, i32, (B,), dev, "pages"), _dense(ring, i32, (n,), dev, "ring"), n,
+            _dense(length, i32, (B,), dev, "length"), int(reserve), B,
+            _dense(block_table, i32, (B, maxb), dev, "block_table"), maxb,
+            _dense(pages, i32, (B,), dev, "pages"), _dense(ring, i32, (n,), dev, "ring"), n,
             _dense(pool, i32, (4,), dev, "pool"), _dense(slots, i32, (B, S), dev, "slots"), S,
             _dense(status, i32, (1,), dev, "status"))
 
@@ -564,8 +571,8 @@ def ssd_tree_rope(q, k, turns, rot, prefix_len, q_out, k_out, parent=None, node0
             *(none if k is None else _rows(k, x.dtype, (B, S, Hkv, d), dev, "k")),
             *(none if k is None else _rows(k_out, x.dtype, (B, S, Hkv, d), dev, "k_out")), dt,
             _dense(turns, torch.int64, (int(rot) // 2,), dev, "turns"), int(rot), int(bool(interleaved)), float(mscale),
-            _dense(prefix_len, torch.int32, (B,), dev, "prefix_len"), _dense(parent, torch.int32, (B, N), dev, "parent"), N,
-            int(node0), B, S, Hq, Hkv, d, _dense(status, torch.int32, (1,), dev, "status"))
+            _dense(prefix_len, torch.int32, (B,), dev, "prefix_len"),
+            _dense(parent, torch.int32, (B, N), dev, "parent"), N, int(node0), B, S, Hq, Hkv, d, _dense(status, torch.int32, (1,), dev, "status"))
 
 
 def ssd_kv_append_q8(k_new, v_new, k_cache, v_cache, k_scale, v_scale, block_table, prefix_len, node0, count=None,
@@ -573,18 +580,38 @@ def ssd_kv_append_q8(k_new, v_new, k_cache, v_cache, k_scale, v_scale, block_tab
     """Quantise the rows ``k_new``/``v_new`` [B, S, Hkv, d] (bf16, heads
     contiguous) into the 8-bit caches at tree nodes node0.. of every sequence
     (rows i >= count[b] are left out)."""
-    B, S, Hkv, d = k_new.shape
+    rows = k_new.shape
+    B, S, Hkv, d = rows
     nb = k_cache.shape[0]
     maxb = block_table.shape[1]
-    i32, f32 = torch.int32, torch.float32
     dev = k_cache.get_device()
+    i32, f32, bf16 = torch.int32, torch.float32, torch.bfloat16
+    kss, kts, khs, kes = k_new.stride()
+    vss, vts, vhs, ves = v_new.stride()
+    # heads of a token contiguous
+    if (kes != 1 and d > 1) or (khs != d and Hkv > 1) or (ves != 1 and d > 1) or (vhs != d and Hkv > 1):
+        raise ValueError("k_new and v_new: the heads of a token must be contiguous")
+    codes, scales = (nb, Hkv, 16, d), (nb, Hkv)
+    if (k_new.dtype is not bf16 or v_new.dtype is not bf16 or v_new.shape != rows
+            or k_cache.dtype not in _CODES or k_cache.shape != codes or not k_cache.is_contiguous()
+            or v_cache.dtype not in _CODES or v_cache.shape != codes or not v_cache.is_contiguous()
+            or k_scale.dtype is not f32 or k_scale.shape != scales or not k_scale.is_contiguous()
+            or v_scale.dtype is not f32 or v_scale.shape != scales or not v_scale.is_contiguous()
+            or block_table.dtype is not i32 or block_table.shape[0] != B or not block_table.is_contiguous()
+            or prefix_len.dtype is not i32 or prefix_len.shape != (B,) or not prefix_len.is_contiguous()
+            or not (dev == k_new.get_device() == v_new.get_device() == v_cache.get_device() == k_scale.get_device()
+                    == v_scale.get_device() == block_table.get_device() == prefix_len.get_device())):
+        if k_new.dtype != bf16 or v_new.dtype != bf16 or v_new.shape != rows:
+            raise ValueError(f"k_new and v_new must be {bf16} tensors of one shape")
+        _refuse(dev, (k_cache, None, codes, "k_cache"), (v_cache, None, codes, "v_cache"),
+                (k_scale, f32, scales, "k_scale"), (v_scale, f32, scales, "v_scale"),
+                (block_table, i32, (B, maxb), "block_table"), (prefix_len, i32, (B,), "prefix_len"))
     _launch("ssd_kv_append_q8", dev, stream,
-            *_rows(k_new, torch.bfloat16, (B, S, Hkv, d), dev, "k_new"),
-            *_rows(v_new, torch.bfloat16, (B, S, Hkv, d), dev, "v_new"),
-            _codes(k_cache, (nb, Hkv, 16, d), dev, "k_cache"), _codes(v_cache, (nb, Hkv, 16, d), dev, "v_cache"),
-            _dense(k_scale, f32, (nb, Hkv), dev, "k_scale"), _dense(v_scale, f32, (nb, Hkv), dev, "v_scale"),
-            _dense(block_table, i32, (B, maxb), dev, "block_table"), maxb, nb, _dense(prefix_len, i32, (B,), dev, "prefix_len"),
-            _dense(count, i32, (B,), dev, "count"), int(node0), B, S, Hkv, d, _dense(status, i32, (1,), dev, "status"))
+            k_new.data_ptr(), kss if B > 1 else 0, kts if S > 1 else 0,
+            v_new.data_ptr(), vss if B > 1 else 0, vts if S > 1 else 0,
+            k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+            block_table.data_ptr(), maxb, nb, prefix_len.data_ptr(), _dense(count, i32, (B,), dev, "count"), int(node0),
+            B, S, Hkv, d, _dense(status, i32, (1,), dev, "status"))
 
 
 def ssd_attention_q8_workspace_size(B, Nq, Hq, Hkv, d) -> int:
@@ -595,8 +622,9 @@ def ssd_branch_attention_q8(q, k_cache, v_cache, k_scale, v_scale, block_table, 
                             scale=None, status=None, ws=None, stream=None):
     """ssd_branch_attention over the 8-bit caches [num_blocks, Hkv, 16, d] with
     block scales [num_blocks, Hkv]."""
-    B, Nq, Hq, d = q.shape
-    nb, Hkv = k_scale.shape
+    rows, scales = q.shape, k_scale.shape
+    B, Nq, Hq, d = rows
+    nb, Hkv = scales
     N = parent.shape[1]
     maxb = block_table.shape[1]
     i32, f32, bf16 = torch.int32, torch.float32, torch.bfloat16
@@ -604,10 +632,25 @@ def ssd_branch_attention_q8(q, k_cache, v_cache, k_scale, v_scale, block_table, 
         scale = d ** -0.5
     dev = q.get_device()
     ws_bytes = 0 if ws is None else ws.numel()
-    _launch("ssd_branch_attention_q8", dev, stream,
-            _dense(q, bf16, (B, Nq, Hq, d), dev, "q"), _codes(k_cache, (nb, Hkv, 16, d), dev, "k_cache"),
-            _codes(v_cache, (nb, Hkv, 16, d), dev, "v_cache"), _dense(k_scale, f32, (nb, Hkv), dev, "k_scale"),
-            _dense(v_scale, f32, (nb, Hkv), dev, "v_scale"), _dense(block_table, i32, (B, maxb), dev, "block_table"), maxb, nb,
-            _dense(prefix_len, i32, (B,), dev, "prefix_len"), _dense(parent, i32, (B, N), dev, "parent"), B, N, Nq, Hq, Hkv, d,
-            float(scale), _dense(out, bf16, (B, Nq, Hq, d), dev, "out"), _dense(lse, f32, (B, Nq, Hq), dev, "lse"),
-            _dense(status, i32, (1,), dev, "status"), _dense(ws, torch.uint8, (ws_bytes,), dev, "ws"), ws_bytes)
+    codes = (nb, Hkv, 16, d)
+    if (q.dtype is not bf16 or not q.is_contiguous()
+            or out.dtype is not bf16 or out.shape != rows or not out.is_contiguous()
+            or k_cache.dtype not in _CODES or k_cache.shape != codes or not k_cache.is_contiguous()
+            or v_cache.dtype not in _CODES or v_cache.shape != codes or not v_cache.is_contiguous()
+            or k_scale.dtype is not f32 or not k_scale.is_contiguous()
+            or v_scale.dtype is not f32 or v_scale.shape != scales or not v_scale.is_contiguous()
+            or block_table.dtype is not i32 or block_table.shape[0] != B or not block_table.is_contiguous()
+            or prefix_len.dtype is not i32 or prefix_len.shape != (B,) or not prefix_len.is_contiguous()
+            or parent.dtype is not i32 or parent.shape[0] != B or not parent.is_contiguous()
+            or not (dev == out.get_device() == k_cache.get_device() == v_cache.get_device() == k_scale.get_device()
+                    == v_scale.get_device() == block_table.get_device() == prefix_len.get_device()
+                    == parent.get_device())):
+        _refuse(dev, (q, bf16, rows, "q"), (out, bf16, rows, "out"), (k_cache, None, codes, "k_cache"),
+                (v_cache, None, codes, "v_cache"), (k_scale, f32, scales, "k_scale"), (v_scale, f32, scales, "v_scale"),
+                (block_table, i32, (B, maxb), "block_table"), (prefix_len, i32, (B,), "prefix_len"),
+                (parent, i32, (B, N), "parent"))
+    _launch("ssd_branch_attention_q8", dev, stream, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+            k_scale.data_ptr(), v_scale.data_ptr(), block_table.data_ptr(), maxb, nb, prefix_len.data_ptr(),
+            parent.data_ptr(), B, N, Nq, Hq, Hkv, d, float(scale), out.data_ptr(),
+            _dense(lse, f32, (B, Nq, Hq), dev, "lse"), _dense(status, i32, (1,), dev, "status"),
+            None if ws is None else _dense(ws, torch.uint8, (ws_bytes,), dev, "ws"), ws_bytes)

@@ -156,3 +156,46 @@ def test_binding_refuses_wrong_tensors(lib):
     with pytest.raises(ValueError, match="CUDA device"):
         ssd.ssd_block_table_update(i32, 0, table, i32, torch.zeros(8, dtype=torch.int32),
                                    torch.zeros(4, dtype=torch.int32), status=torch.zeros(1, dtype=torch.int32))
+
+
+def _bad(x):
+    """The same tensor with a wrong dtype, a wrong shape, and strides that are not dense."""
+    yield x.to(torch.float64)
+    yield x.reshape(-1)[:-1] if x.numel() > 1 else x.expand(2)
+    if x.dim() > 1 and x.shape[-2] > 1 and x.shape[-1] > 1:
+        yield x.transpose(-1, -2).contiguous().transpose(-1, -2)
+
+
+def test_every_tensor_is_checked():
+    """A tensor that is not as the call wants it is refused by its name, whichever it is."""
+    B, S, Hq, Hkv, d, nb, maxb = 2, 3, 4, 2, 64, 5, 3
+    z = torch.zeros
+    i32, bf = torch.int32, torch.bfloat16
+    cache = {k: z(nb, Hkv, 16, d, dtype=torch.uint8) for k in ("k_cache", "v_cache")}
+    cache.update({k: z(nb, Hkv) for k in ("k_scale", "v_scale")})
+    table = dict(block_table=z(B, maxb, dtype=i32), prefix_len=z(B, dtype=i32))
+    calls = [
+        (ssd.ssd_branch_attention_q8, dict(q=z(B, S, Hq, d, dtype=bf), **cache, **table, parent=z(B, S, dtype=i32),
+                                           out=z(B, S, Hq, d, dtype=bf), lse=z(B, S, Hq), status=z(1, dtype=i32),
+                                           ws=z(512, dtype=torch.uint8))),
+        (ssd.ssd_kv_append_q8, dict(k_new=z(B, S, Hkv, d, dtype=bf), v_new=z(B, S, Hkv, d, dtype=bf), **cache, **table,
+                                    node0=0, count=z(B, dtype=i32), status=z(1, dtype=i32))),
+        (ssd.ssd_tree_rope, dict(q=z(B, S, Hq, d, dtype=bf), k=z(B, S, Hkv, d, dtype=bf), turns=z(d // 2, dtype=torch.int64),
+                                 rot=d, prefix_len=z(B, dtype=i32), q_out=z(B, S, Hq, d, dtype=bf),
+                                 k_out=z(B, S, Hkv, d, dtype=bf), parent=z(B, S, dtype=i32), status=z(1, dtype=i32))),
+        (ssd.ssd_block_table_update, dict(length=z(B, dtype=i32), reserve=0, block_table=z(B, maxb, dtype=i32),
+                                          pages=z(B, dtype=i32), ring=z(nb, dtype=i32), pool=z(4, dtype=i32),
+                                          slots=z(B, 2, dtype=i32), status=z(1, dtype=i32))),
+    ]
+    for fn, good in calls:
+        with pytest.raises(ValueError, match="CUDA device"):
+            fn(**good)
+        for name, x in good.items():
+            if not torch.is_tensor(x):
+                continue
+            for k, bad in enumerate(_bad(x)):
+                if name == "ws" and k == 1 or name == "ring" and k == 1:  # any length will do
+                    continue
+                with pytest.raises((ValueError, IndexError)) as e:
+                    fn(**{**good, name: bad})
+                assert "CUDA device" not in str(e.value), (fn.__name__, name, k)
