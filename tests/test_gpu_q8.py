@@ -501,6 +501,74 @@ def test_attention_nan(d):
         assert np.isnan(o[0, 3, 1]).all() and np.isnan(l[0, 3, 1]) and not np.isnan(o[0, 3, 0, :3]).any()
 
 
+# The same edges with more than 64 rows per KV head (a lane per row): 16 heads per KV head, 5 to 9 queries.
+@pytest.mark.parametrize("d", [64, 128])
+def test_attention_many_rows_after_spine(d):
+    parent = CHAIN(60) + [3, 3, 60, 61, 0]
+    check_attention(attention_inputs(17, 16, 1, d, [47 + i for i in range(17)], parent, 5, seed=60 + d))
+    check_attention(attention_inputs(9, 3, 1, d, [120 + i for i in range(9)], parent, 65, seed=61 + d))
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_attention_many_rows_sharp_and_flat(d):
+    a = attention_inputs(3, 16, 1, d, [700, 3000, 700], CHAIN(9), 9, seed=62, spread=0)
+    check_attention(a, scale=1.0)
+    a["q"][1] = 0
+    one = a["kc"][a["table"][2, 0], 0, 0].copy()
+    a["kc"][a["table"][2, 0], 0, 0] = ref.e4m3_round(np.sign(a["q"][2, 0, 0]) * 20.0)
+    check_attention(a)
+    a["kc"][a["table"][2, 0], 0, 0] = one
+    a["kc"][a["table"][2, 40], 0, 7] = ref.e4m3_round(np.sign(a["q"][2, 0, 0]) * 60.0)
+    check_attention(a)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_attention_many_rows_scales(d):
+    a = attention_inputs(4, 32, 2, d, [300, 300, 300, 40], CHAIN(5), 5, seed=63)
+    t = a["table"]
+    a["vs"][t[0, :19]] = 0.0                      # no value anywhere but in the last block
+    a["vs"][t[1, ::2][t[1, ::2] >= 0]] *= 2.0 ** -30
+    a["vs"][t[2][t[2] >= 0]] *= 0.3
+    a["ks"][t[2][t[2] >= 0]] *= 0.7
+    a["ks"][t[3][t[3] >= 0]] = 0.0                # all scores equal
+    check_attention(a)
+    a["vs"][t[3][t[3] >= 0]] = 2.0 ** -90
+    a["vs"][t[1][t[1] >= 0]] *= 2.0 ** 90
+    check_attention(a)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_attention_many_rows_bad_blocks(d):
+    a = attention_inputs(4, 32, 2, d, [200, 60, 14, 40], CHAIN(5), 5, seed=64)
+    a["table"][0, 3] = 10 ** 6
+    a["table"][1, :] = -1                         # nothing left: 0 and -inf
+    out, lse = check_attention(a, expect=ssd.FLAG_BAD_BLOCK)
+    assert (out[1] == 0).all() and (lse[1] == -math.inf).all()
+    a["ks"][a["table"][0, 5], 1], a["vs"][a["table"][2, 0], 0] = -1.0, math.inf
+    check_attention(a, expect=ssd.FLAG_BAD_BLOCK | ssd.FLAG_BAD_VALUE)
+    a["prefix"][2], a["prefix"][3] = 16 * a["table"].shape[1] - 1, -7
+    a["parent"][0, 1] = 1
+    check_attention(a, expect=ssd.FLAG_BAD_BLOCK | ssd.FLAG_BAD_VALUE | ssd.FLAG_BAD_PREFIX | ssd.FLAG_BAD_TREE)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_attention_many_rows_nan(d):
+    parent = [-1, 0, 0, 1, 2]                     # 1 and 2 are siblings
+    for length in (5, 126, 300, 1500):
+        a = attention_inputs(2, 32, 2, d, [length, 40], parent, 5, seed=65 + length)
+
+        def at(b, pos, h):
+            return a["table"][b, pos // 16], h, pos % 16
+        a["vc"][at(0, length + 1, 0)][3] = 0xFF   # a tree node: seen by itself and node 3, 16 heads each
+        a["kc"][at(0, length + 2, 1)][5] = 0x7F   # a tree node: seen by itself and node 4
+        a["vc"][at(1, 7, 1)][d - 1] = 0x7F        # the prefix: seen by all
+        out, _ = check_attention(a)
+        assert np.isnan(out).sum() == 2 * 16 + 2 * 16 * d + 5 * 16
+        a["q"][0, 3, 1, 0] = math.inf
+        o, l, st = gpu_attention(a, 0.1)
+        assert np.isnan(o[0, 3, 1]).all() and np.isnan(l[0, 3, 1]) and not np.isnan(o[0, 3, 0, :3]).any()
+
+
 def test_attention_two_streams_and_graph():
     """Two calls at once with workspaces of their own, and a captured call replayed on new inputs."""
     sets = [attention_inputs(3, 8, 2, 128, [4000, 50, 900], CHAIN(4), 4, seed=50 + i) for i in range(3)]
