@@ -81,8 +81,9 @@ constexpr float kBias = 4.f, kMoved = 5.f, kGrow = 8.f;
 // Keys of the smallest piece, and the longest table whose items are not cut: joining costs 3 us.  One query, 8 heads:
 // 2000 keys 14.2 us in pieces of 512, 15.9 of 1024, 17.2 whole; 1000 keys 13.3 in pieces of 512, 12.5 whole.
 constexpr int kMinKeys = 512, kWholeKeys = 1024;
-// An item's end costs its CTA about two tiles' time and, where items are short, the rows of the next one six
-// (one warp prepares them).  Ragged batch of 1 to 16384 keys: 0: 129 us, 2: 112, 4: 107, 6: 95, 8: 97, 12: 104.
+// An item's end costs its CTA a few tiles' time: O leaves TMEM, the next rows come in, the pipeline drains.  Ragged
+// batch of 1 to 16384 keys: 3: 99 us, 4: 95, 6: 92, 8: 95 (without ends in the split 131); 64 sequences of 100 to
+// 600 keys (draft): 97, 90, 88, 86; equal lengths: within 2%.
 constexpr int kEnd = 6;
 constexpr int kSmemBudget = 212 * 1024;
 constexpr int kTmaWarps = 2;               // producer warps: warp p loads every sub-tile whose number is p modulo this
@@ -342,27 +343,22 @@ struct Segments {
 };
 
 // The order of the MMAs, which is the order of the loads: S runs ahead of P V by
-// up to NB tiles, but not past the next segment (a third one's rows have no
-// buffer before the first one's are done).
+// up to NB tiles, but not into the next segment, whose rows may not be ready: its
+// first S comes behind the last P V, while the softmax warps write O out.
 struct Order {
-  int begin, end, hold;  // of the segment that P V is in; the first tile that S may not reach
-  int n;
+  int begin, end;  // of the segment that P V is in
   Segments sg;
   bool more;
   SSD_DEV void start(const Args &a, const Piece &p) {
-    n = p.tiles;
     begin = 0;
     more = sg.first(a, p);
     end = more ? sg.t1 - sg.t0 : 0;
-    more = more && sg.step(a);
-    hold = more ? end + sg.t1 - sg.t0 : n;
   }
   SSD_DEV void done(const Args &a, int j) {  // P V has done j tiles
-    if (j < end || j >= n) return;
+    if (j < end) return;
     begin = end;
-    end = hold;
     more = more && sg.step(a);
-    hold = more ? end + sg.t1 - sg.t0 : n;
+    if (more) end += sg.t1 - sg.t0;
   }
 };
 
@@ -633,13 +629,11 @@ __global__ void __launch_bounds__(Cfg<D, RT>::kThreads, 1)
     prepare_rows<D, RT>(a, sg, smem + C::kQ + buf * C::kQBuf, par[buf], anc[buf], qs[buf], w, n, bar);
   };
 
-  // V of tile i, sub-tile h (of segment x: tiles i0 .. i0 + n - 1), this thread's key: hidden keys take no part whatever
+  // V of tile i, sub-tile h (of segment seg, whose tiles end before `end`), this thread's key: hidden keys take no part whatever
   // their v holds (0 * NaN): their rows become 0; a tree node's NaN becomes 0 too, and reaches the rows that see it at
   // the segment's end; a prefix key stays.  False when the wait for V gave up.
-  auto void_rows = [&](const Segments &x, int seg, int i, int i0, int n, bool gone, bool prefix, int h) -> bool {
-    Segments after = x;
-    const int hold = after.step(a) ? i0 + n + after.t1 - after.t0 : ntiles;
-    const int load = (min(min(ntiles, i + NB), hold) + i) * KT + h;  // V's place in the order of loads
+  auto void_rows = [&](int seg, int i, int end, bool gone, bool prefix, int h) -> bool {
+    const int load = (min(i + NB, end) + i) * KT + h;  // V's place in the order of loads
     const bool ok = warp_wait(&full[load % NSLOT], (load / NSLOT) & 1);
     if (prefix) return ok;
     const int key = tid & 127;
@@ -750,7 +744,7 @@ __global__ void __launch_bounds__(Cfg<D, RT>::kThreads, 1)
     Order order;
     order.start(a, piece);
     for (int i = 0, j = 0; j < ntiles && ok;) {
-      if (i < ntiles && i - j < NB && i < order.hold) {  // K of tile i
+      if (i - j < NB && i < order.end) {  // K of tile i
         for (int h = 0; h < KT && ok; ++h) {
           const bool m = (i * KT + h) % kTmaWarps == pw;
           if (m) {
@@ -858,7 +852,7 @@ __global__ void __launch_bounds__(Cfg<D, RT>::kThreads, 1)
     Order order;
     order.start(a, piece);
     for (int i = 0, j = 0; j < ntiles && ok;) {
-      if (i < ntiles && i - j < NB && i < order.hold) {
+      if (i - j < NB && i < order.end) {
         issue_s(i++);
       } else {  // P V of tile j
         const int u = j % NB;
@@ -1070,7 +1064,7 @@ __global__ void __launch_bounds__(Cfg<D, RT>::kThreads, 1)
         if (part && g == 0) {
           const int pos = t * kSub + r;  // here a lane has a key
           const bool gone = meta[i % kMeta][r / kPage].y < 0.f || pos >= sg.nkeys;
-          ok = void_rows(sg, seg, i, i0, n, gone, !gone && pos < sg.L, 0) && ok;
+          ok = void_rows(seg, i, i0 + n, gone, !gone && pos < sg.L, 0) && ok;
         }
         fence_proxy_async();  // P and V (generic writes) -> visible to the tensor cores
         tc_fence_before();
@@ -1356,7 +1350,7 @@ __global__ void __launch_bounds__(Cfg<D, RT>::kThreads, 1)
 #pragma unroll 1
           for (int h = 0; h < KT; ++h) {
             const bool gone = KT == 2 && h ? hidden[KT - 1] : hidden[0];
-            ok = void_rows(sg, seg, i, i0, n, gone, !gone && t * C::kKeys + h * kSub + tg < sg.L, h) && ok;
+            ok = void_rows(seg, i, i0 + n, gone, !gone && t * C::kKeys + h * kSub + tg < sg.L, h) && ok;
           }
         }
         fence_proxy_async();  // P and V (generic writes) -> visible to the tensor cores
