@@ -477,9 +477,12 @@ def _refuse(dev, *tensors):
             raise ValueError(f"all tensors of a call must live on one device, got {what} on {x.device}")
         if dtype is None and x.dtype not in _CODES:
             raise ValueError(f"{what} must hold e4m3 codes (float8_e4m3fn or uint8), got {x.dtype}")
-        if (dtype is not None and x.dtype != dtype) or x.shape != shape or not x.is_contiguous():
+        if (dtype is not None and x.dtype != dtype) or x.shape != shape:
             raise ValueError(f"{what} must be a contiguous {dtype or 'e4m3'} tensor of shape {tuple(shape)}, "
                              f"got {x.dtype} {tuple(x.shape)}")
+    for x, dtype, shape, what in tensors:
+        if x is not None and not x.is_contiguous():
+            raise ValueError(f"{what} must be contiguous, got strides {x.stride()}")
     raise ValueError("tensors of a call must be dense and live on one device")
 
 
@@ -495,14 +498,23 @@ def _dense(x, dtype, shape, dev, what):
     return x.data_ptr()
 
 
-def _rows(x, dtype, shape, dev, what):
-    """Address and (sequence, token) strides of [B, S, H, d] rows whose heads are dense."""
-    if x.dtype is not dtype or x.shape != shape or x.get_device() != dev:
-        _refuse(dev, (x, dtype, shape, what))
-    ss, ts, hs, es = x.stride()
-    if (es != 1 and shape[3] > 1) or (hs != shape[3] and shape[2] > 1):
-        raise ValueError(f"{what}: the heads of a token must be contiguous")
-    return x.data_ptr(), ss if shape[0] > 1 else 0, ts if shape[1] > 1 else 0
+def _rows(x, y, dtype, lead, dev, what):
+    """Addresses and (sequence, token) strides of [B, S, H, d] rows x and their output y, whose heads are dense."""
+    shape = x.shape
+    B, S, H, d = shape
+    a, b, h, e = x.stride()
+    ya, yb, yh, ye = y.stride()
+    if ((B, S, d) != lead or x.dtype is not dtype or y.dtype is not dtype or y.shape != shape
+            or x.get_device() != dev or y.get_device() != dev):
+        shape = (*lead[:2], H, lead[2])
+        _refuse(dev, (x, dtype, shape, what), (y, dtype, shape, what + "_out"))
+    if ((e != 1 or ye != 1) and d > 1) or ((h != d or yh != d) and H > 1):
+        raise ValueError(f"{what} and {what}_out: the heads of a token must be contiguous")
+    if B == 1:
+        a = ya = 0
+    if S == 1:
+        b = yb = 0
+    return x.data_ptr(), a, b, y.data_ptr(), ya, yb
 
 
 def _launch(call, dev, stream, *args):
@@ -562,17 +574,16 @@ def ssd_tree_rope(q, k, turns, rot, prefix_len, q_out, k_out, parent=None, node0
         raise ValueError(f"q and k must be float32 or bfloat16, got {x.dtype}")
     Hq = 0 if q is None else q.shape[2]
     Hkv = 0 if k is None else k.shape[2]
-    none = (None, 0, 0)
+    none = (None, 0, 0, None, 0, 0)
     N = 0 if parent is None else parent.shape[1]
     dev = x.get_device()
+    i32, lead = torch.int32, (B, S, d)
     _launch("ssd_tree_rope", dev, stream,
-            *(none if q is None else _rows(q, x.dtype, (B, S, Hq, d), dev, "q")),
-            *(none if q is None else _rows(q_out, x.dtype, (B, S, Hq, d), dev, "q_out")),
-            *(none if k is None else _rows(k, x.dtype, (B, S, Hkv, d), dev, "k")),
-            *(none if k is None else _rows(k_out, x.dtype, (B, S, Hkv, d), dev, "k_out")), dt,
+            *(none if q is None else _rows(q, q_out, x.dtype, lead, dev, "q")),
+            *(none if k is None else _rows(k, k_out, x.dtype, lead, dev, "k")), dt,
             _dense(turns, torch.int64, (int(rot) // 2,), dev, "turns"), int(rot), int(bool(interleaved)), float(mscale),
-            _dense(prefix_len, torch.int32, (B,), dev, "prefix_len"),
-            _dense(parent, torch.int32, (B, N), dev, "parent"), N, int(node0), B, S, Hq, Hkv, d, _dense(status, torch.int32, (1,), dev, "status"))
+            _dense(prefix_len, i32, (B,), dev, "prefix_len"), _dense(parent, i32, (B, N), dev, "parent"), N, int(node0),
+            B, S, Hq, Hkv, d, _dense(status, i32, (1,), dev, "status"))
 
 
 def ssd_kv_append_q8(k_new, v_new, k_cache, v_cache, k_scale, v_scale, block_table, prefix_len, node0, count=None,
