@@ -41,18 +41,19 @@
 //
 // Bound: HBM where the rows are few; else the softmax warps' latencies (4 per
 // scheduler, half of the issue slots used).  64 sequences of 8192 keys, 8 KV heads of
-// 128 with 6 queries of 8 heads each (1.08 GB): 201 us, 5.4 TB/s; without
+// 128 with 6 queries of 8 heads each (1.08 GB): 198 us, 5.5 TB/s; without
 // softmax and MMAs 181, without copies too 93.  Ragged batch of 48 sequences up
-// to 16384 keys, 64 rows (411 MB): 96 us, 4.3 TB/s (137 without the ends'
+// to 16384 keys, 64 rows (411 MB): 95 us, 4.3 TB/s (137 without the ends'
 // units).  One sequence, 100003 keys, one query (205 MB): 46 us, of which the
 // set-up, the first tile and the merge take 12.  16 sequences of 2048 keys with
 // 256 rows (d 64): 66 us, 15 instructions per score (84 us and 19 with the keys
 // on the 128-wide side: masks, maxima and row constants are a lane's own here).
-//   tried: all softmax in streams of whole tiles (instruction fetch), four
+//   tried: softmax warps in streams of whole tiles (instruction fetch), four
 //   producer warps (verify 214), two prep warps (registers: 110 for the draft),
-//   setmaxnreg (spills), m voted per tile but moved always (every tile pays),
-//   next rows prepared by the softmax warps behind short items (4% of the ragged
-//   batch), three S and P buffers for the draft (67).
+//   setmaxnreg (spills), m moved in every tile (each pays a tile's time), next
+//   rows prepared by the softmax warps behind short items (no gain), S of the next
+//   item before the last P V (verify 198 replayed instead of 195), three S and P
+//   buffers for the draft (67 instead of 66).
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <math.h>

@@ -11,10 +11,10 @@
 //                 shared memory (position = prefix + depth) and compute the
 //                 rot/2 rotations once for all Hq + Hkv heads.
 // Bound by HBM: every element is read and written once.  64 + 8 heads of 128
-// with 64 rotated, 16396 tokens (604 MB): 101 us, 6.0 TB/s (128 us
+// with 64 rotated, 16396 tokens (604 MB): 104 us, 5.8 TB/s (128 us
 // when the pieces were asked for after the rotations); 2 or 4 pieces per thread
 // at a time 107 and 110 us (fewer threads fit).  A decode step of 256 tokens:
-// 2.8 us, two dependent reads and a launch.
+// 3 us, two dependent reads and a launch.
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
