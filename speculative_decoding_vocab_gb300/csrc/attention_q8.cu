@@ -377,7 +377,7 @@ struct Cfg {
   static constexpr int kThreads = kWarps * 32;
   static constexpr int kQTile = RT * 128;                  // q1 (or q2) at D = 128; [q1 | q2] at D = 64
   static constexpr int kQBuf = D == 128 ? 2 * kQTile : kQTile;
-  static constexpr int kPBlock = kSub * 128;               // 128 values of N: a 128-byte row per key
+  static constexpr int kPBlock = kSub * 128;               // 128-byte rows: 128 of N per key, or a row's 128 keys
   static constexpr int kPBuf = RT > 64 ? 2 * kPBlock : kPBlock;  // p1 [RT] then p2 [RT] along N, of a sub-tile
   static constexpr int kSlot = kSub * D;                   // K or V of a sub-tile
   static constexpr int kFixed = 2 * kQBuf + NB * KT * kPBuf;
@@ -1397,6 +1397,7 @@ __global__ void __launch_bounds__(Cfg<D, RT>::kThreads, 1)
       // four rows at a time; at d = 64 the upper 64 lanes of O repeat the lower ones and take half of the rows
       constexpr int kShares = C::kGroups * (128 / D);
       const int share = D == 128 ? g : g * 2 + (wg >> 1), el = tg & (D - 1);
+      uint16_t *const to = a.out + (static_cast<int64_t>(sg.b) * a.Nq * a.Hq + hk * a.group) * D + el;
 #pragma unroll 1
       for (int j0 = share * 4; j0 < RT; j0 += kShares * 4) {
         const int r0 = mt * RT + j0;
@@ -1427,11 +1428,10 @@ __global__ void __launch_bounds__(Cfg<D, RT>::kThreads, 1)
           for (int j = 0; j < 4; ++j) {
             const int r = r0 + j;
             if (r >= a.nrows) break;
-            const int qi = static_cast<int>((r * a.group_magic) >> 16), head = hk * a.group + (r - qi * a.group);
+            const int qi = static_cast<int>((r * a.group_magic) >> 16), at = qi * a.Hq + (r - qi * a.group);
             uint32_t b2;
             asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(b2) : "f"(0.f), "f"(o[j]));
-            a.out[((static_cast<int64_t>(sg.b) * a.Nq + qi) * a.Hq + head) * D + el] =
-                static_cast<uint16_t>(b2 & 0xFFFFu);
+            to[static_cast<int64_t>(at) * D] = static_cast<uint16_t>(b2 & 0xFFFFu);
           }
         } else {
 #pragma unroll
