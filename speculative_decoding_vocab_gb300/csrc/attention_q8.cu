@@ -219,11 +219,6 @@ SSD_DEV uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c) {
   asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
   return r;
 }
-SSD_DEV uint32_t max_u16x2(uint32_t x, uint32_t y) {
-  uint32_t r;
-  asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(y));
-  return r;
-}
 SSD_DEV uint32_t hmul2(uint32_t a, uint32_t b) {
   uint32_t r;
   asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
@@ -368,7 +363,7 @@ struct Cfg {
   static constexpr bool kRowLanes = RT > 64;               // rows, not keys, on the MMA's 128-wide side
   static constexpr int KT = RT <= 64 ? 2 : 1;              // sub-tiles of a tile
   static constexpr int kKeys = KT * kSub;                  // keys of a tile
-  static constexpr int CG = RT <= 64 ? 16 : 32;            // rows of a softmax warp (keys, with a lane per row)
+  static constexpr int CG = kRowLanes ? 32 : 16;           // rows of a softmax warp (keys, with a lane per row)
   static constexpr int kGroups = RT / CG;                  // groups of four warps
   static constexpr int NB = 2;                             // S and P buffers; S runs NB tiles ahead
   static constexpr int kSoftWarps = 4 * kGroups;
@@ -397,7 +392,8 @@ struct Cfg {
   static constexpr int kBack = kSlots + 2 * kTmaWarps + KT - 1;
   static_assert(kMeta >= NB + (kBack + 2 * KT - 1) / (2 * KT), "block scales");
   static_assert(!kRowLanes || (RT == 128 && kGroups == 4), "a lane per row, a quarter of the keys per group");
-  static_assert(kCols <= 512 && RT % CG == 0 && CG % 16 == 0 && CG <= 32 && kGroups <= 8, "rows");
+  static_assert(kRowLanes || (KT == 2 && CG == 16 && 2 * RT <= 128), "tiles of two sub-tiles, P in rows of 128 bytes");
+  static_assert(kCols <= 512 && RT % CG == 0 && kGroups <= 4, "rows");
 };
 
 // A segment's rows: q1, q2 into the operand tiles at qb, the row scales, and
@@ -1209,7 +1205,7 @@ __global__ void __launch_bounds__(Cfg<D, RT>::kThreads, 1)
 #pragma unroll 1
               for (int j1 = (qi + 1) * a.group - row0; j0 < CG && qi < a.Nq; ++qi, j0 = j1, j1 += a.group)
                 if ((anc[buf][qi][node >> 5] >> (node & 31)) & 1u)
-                  see |= (j1 < 32 ? (1u << j1) - 1u : ~0u) & (~0u << j0);
+                  see |= (j1 < CG ? (1u << j1) - 1u : ~0u) & (~0u << j0);
               vis[h] = see;
             }
           }
@@ -1218,13 +1214,9 @@ __global__ void __launch_bounds__(Cfg<D, RT>::kThreads, 1)
         // y = x - m + 4 (x for a row without m); hidden keys -inf
         auto scores = [&]() {
 #pragma unroll
-          for (int h = 0; h < KT; ++h)
+          for (int h = 0; h < KT; ++h) tmem_ld16_async(tS + (u * KT + h) * RT, y[h]);
 #pragma unroll
-            for (int j = 0; j < CG; j += 16) tmem_ld16_async(tS + (u * KT + h) * RT + j, y[h] + j);
-#pragma unroll
-          for (int h = 0; h < KT; ++h)
-#pragma unroll
-            for (int j = 0; j < CG; j += 16) tmem_wait16(y[h] + j);
+          for (int h = 0; h < KT; ++h) tmem_wait16(y[h]);
 #pragma unroll
           for (int j = 0; j < CG; j += 2) {
             const float4 rc = rowc[(col + j) / 2];
@@ -1258,9 +1250,7 @@ __global__ void __launch_bounds__(Cfg<D, RT>::kThreads, 1)
           float big = NEG_INF;
 #pragma unroll
           for (int j = 0; j < CG; ++j) {
-            float z = y[0][j] + lsv[0];
-            if (KT == 2) z = fmaxf(z, y[KT - 1][j] + lsv[KT - 1]);
-            z = warp_top(z);
+            const float z = warp_top(fmaxf(y[0][j] + lsv[0], y[1][j] + lsv[1]));
             if (lane == j) big = z;
           }
           if (lane < CG) red[wg][col + lane] = big;
@@ -1292,22 +1282,19 @@ __global__ void __launch_bounds__(Cfg<D, RT>::kThreads, 1)
           }
           unset = bar_or(bar, 128, none);
           if (!begin) {
+            bool moved = false;
 #pragma unroll
-            for (int j0 = 0; j0 < CG; j0 += 16) {  // the 16 rows whose m moved
-              bool moved = false;
+            for (int j = 0; j < CG; ++j) moved = moved || s_f[col + j] != 1.f;
+            if (moved) {
 #pragma unroll
-              for (int j = 0; j < 16; ++j) moved = moved || s_f[col + j0 + j] != 1.f;
-              if (!moved) continue;
-#pragma unroll
-              for (int j = j0 / 2; j < j0 / 2 + 8; ++j)
-                l2[j] = mul2(l2[j], pack2(s_f[col + 2 * j], s_f[col + 2 * j + 1]));
+              for (int j = 0; j < CG / 2; ++j) l2[j] = mul2(l2[j], pack2(s_f[col + 2 * j], s_f[col + 2 * j + 1]));
 #pragma unroll 1
               for (int term = 0; term < 2; ++term) {
-                float o[16];
-                tmem_ld16(tO + term * RT + j0, o);
+                float o[CG];
+                tmem_ld16(tO + term * RT, o);
 #pragma unroll
-                for (int j = 0; j < 16; ++j) o[j] *= s_f[col + j0 + j];
-                tmem_st16(tO + term * RT + j0, o);
+                for (int j = 0; j < CG; ++j) o[j] *= s_f[col + j];
+                tmem_st16(tO + term * RT, o);
               }
             }
           }
@@ -1319,38 +1306,33 @@ __global__ void __launch_bounds__(Cfg<D, RT>::kThreads, 1)
         for (int h = 0; h < KT; ++h) {
           uint8_t *const pb = smem + C::kP + (u * KT + h) * C::kPBuf;
           const uint64_t w2 = pack2(wv[h], wv[h]);
+          uint32_t p1[4], p2[4];
 #pragma unroll
-          for (int j0 = 0; j0 < CG; j0 += 16) {
-            uint32_t p1[4], p2[4];
+          for (int q = 0; q < 4; ++q) {
+            uint16_t e1[2], e2[2];
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              uint16_t e1[2], e2[2];
-#pragma unroll
-              for (int x = 0; x < 2; ++x) {
-                const int j = j0 + q * 4 + x * 2;
-                const uint64_t p = pack2(ex2(y[h][j]), ex2(y[h][j + 1]));
-                l2[j / 2] = add2(l2[j / 2], p);
-                float a0, a1;
-                unpack2(mul2(p, w2), a0, a1);
-                const uint32_t hp = half2_of(a0, a1);
-                e1[x] = e4m3_of_half2(hp);
-                // 32 (p - p1) in halves: exact (p is at most 2^8, the difference has at most 11 bits)
-                e2[x] = e4m3_of_half2(hfma2(e4m3_to_half2(e1[x]), 0xD000D000u, hmul2(hp, 0x50005000u)));
-              }
-              p1[q] = pack16(e1[0], e1[1]);
-              p2[q] = pack16(e2[0], e2[1]);
+            for (int x = 0; x < 2; ++x) {
+              const int j = q * 4 + x * 2;
+              const uint64_t p = pack2(ex2(y[h][j]), ex2(y[h][j + 1]));
+              l2[j / 2] = add2(l2[j / 2], p);
+              float a0, a1;
+              unpack2(mul2(p, w2), a0, a1);
+              const uint32_t hp = half2_of(a0, a1);
+              e1[x] = e4m3_of_half2(hp);
+              // 32 (p - p1) in halves: exact (p is at most 2^8, the difference has at most 11 bits)
+              e2[x] = e4m3_of_half2(hfma2(e4m3_to_half2(e1[x]), 0xD000D000u, hmul2(hp, 0x50005000u)));
             }
-            const int n1 = col + j0, n2 = RT + n1;  // places along N
-            *reinterpret_cast<uint4 *>(pb + (n1 >> 7) * C::kPBlock + sw128(tg, n1 & 127)) =
-                make_uint4(p1[0], p1[1], p1[2], p1[3]);
-            *reinterpret_cast<uint4 *>(pb + (n2 >> 7) * C::kPBlock + sw128(tg, n2 & 127)) =
-                make_uint4(p2[0], p2[1], p2[2], p2[3]);
+            p1[q] = pack16(e1[0], e1[1]);
+            p2[q] = pack16(e2[0], e2[1]);
           }
+          // places along N: p1 of the group's rows, then p2
+          *reinterpret_cast<uint4 *>(pb + sw128(tg, col)) = make_uint4(p1[0], p1[1], p1[2], p1[3]);
+          *reinterpret_cast<uint4 *>(pb + sw128(tg, RT + col)) = make_uint4(p2[0], p2[1], p2[2], p2[3]);
         }
         if (part && g == 0) {
 #pragma unroll 1
           for (int h = 0; h < KT; ++h) {
-            const bool gone = KT == 2 && h ? hidden[KT - 1] : hidden[0];
+            const bool gone = h ? hidden[1] : hidden[0];
             ok = void_rows(seg, i, i0 + n, gone, !gone && t * C::kKeys + h * kSub + tg < sg.L, h) && ok;
           }
         }
@@ -1361,13 +1343,12 @@ __global__ void __launch_bounds__(Cfg<D, RT>::kThreads, 1)
       }
       // ---------------- the segment's end: l, then O from TMEM
       if (dead) ok = false;
+      {
+        float z[CG];
 #pragma unroll
-      for (int j0 = 0; j0 < CG; j0 += 16) {
-        float z[16];
-#pragma unroll
-        for (int j = 0; j < 16; j += 2) unpack2(l2[(j0 + j) / 2], z[j], z[j + 1]);
+        for (int j = 0; j < CG; j += 2) unpack2(l2[j / 2], z[j], z[j + 1]);
         const float sum = warp_columns(z, lane);
-        if (!(lane & 1)) red[wg][col + j0 + (lane >> 1)] = sum;
+        if (!(lane & 1)) red[wg][col + (lane >> 1)] = sum;
       }
       const int il = i0 + n - 1;
       ok = ok && warp_wait(&pvdone[il % NB], (il / NB) & 1);

@@ -47,12 +47,6 @@ struct AppendArgs {
   uint32_t *status;
 };
 
-SSD_DEV uint32_t max_u16x2(uint32_t x, uint32_t y) {
-  uint32_t r;
-  asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(y));
-  return r;
-}
-
 // the smallest power of two s >= 2^-100 with amax <= 448 s (448 = 1.75 * 2^8)
 SSD_DEV float pow2_scale(float amax) {
   const uint32_t b = __float_as_uint(amax);
