@@ -605,9 +605,13 @@ ssd_status_t ssd_kv_append_q8(const void *k_new, int64_t k_seq_stride, int64_t k
  * not finite hides its block (BAD_VALUE); v scales below 2^-100 count as 0.
  * A NaN code of a key reaches the rows that see the key, in v only its
  * element; what hidden positions hold does not matter.  A query row with a
- * value that is not finite gives NaN.  Workspace:
- * ssd_attention_q8_workspace_size() bytes, 256-byte aligned, for splitting
- * long key ranges; NULL or short: not split, same result, slower.
+ * value that is not finite gives NaN.  Accuracy: the elements of q count down
+ * to 2^-17 of their row's largest; with P = exp(score - max) * v_scale, a key's
+ * P is rounded by up to 2^-11 of itself, or by 2^-36 of the row's largest P
+ * where that is more (so n keys lose at most n * 2^-36 of it); sums are fp32.
+ * Workspace: ssd_attention_q8_workspace_size() bytes, 256-byte aligned, for
+ * splitting long key ranges; NULL or short: not split, the same result but for
+ * these roundings, slower.
  */
 size_t ssd_attention_q8_workspace_size(int B, int Nq, int Hq, int Hkv, int d);
 ssd_status_t ssd_branch_attention_q8(const void *q, const void *k_cache, const void *v_cache,

@@ -2,26 +2,32 @@
 // in 8 bits (e4m3 codes, one scale per block of 16 positions and KV head), on
 // the sm_103a tensor cores.
 //
-// The codes go to the tensor cores as they are (kind::f8f6f4, fp32 sums).  A
-// decode step has few query rows and many keys, so up to 64 rows per KV head
+// A decode step has few query rows and many keys, so up to 64 rows per KV head
 // the keys take the MMA's 128-wide side and the rows its N:
-//     S^T [128 keys x rows] = K8 Q^T,      O^T [d x rows] += V8^T P^T;
+//     S^T [128 keys x rows] = K8 Q^T,      O^T [d x rows] += V^T P^T;
 // above, the rows fill that side themselves:
-//     S [128 rows x 128 keys] = Q K8^T,    O [128 rows x d] += P V8.
-// What 8 bits would lose of the bf16 queries and of the probabilities is kept
-// in a second term:
+//     S [128 rows x 128 keys] = Q K8^T,    O [128 rows x d] += P V.
+// S: the keys' codes go to the tensor cores as they are (kind::f8f6f4, fp32
+// sums), and what 8 bits would lose of the bf16 queries is kept in a second term:
 //   q = 2^e (q1 + q2): e4m3 holds 4 significant bits, so q1 = e4m3(q) leaves a
 //     remainder of at most 4 bits, and q2 = e4m3(q - q1) is exact (bf16 has 8;
 //     below 2^-17 of the row's largest element the remainder is cut): two MMAs
 //     into the same S.
-//   p = p1 + p2 / 32 with p1 = e4m3(p), p2 = e4m3(32 (p - p1)): off by at most
-//     2^-8 p, as a bf16 p would be, or 2^-15 where p2 underflows; p1 and p2
-//     lie side by side in N and fill two accumulators, O = O1 + O2 / 32.
-// Block scales enter in fp32: x = s * k_scale * scale * 2^e, P = 2^(x - m + 4),
-// and P * v_scale is what is split into p1 and p2 (a lane has one key of 16 rows,
-// or one row of 32 keys).  m starts as the largest x + log2(v_scale) of the
-// row's first keys and moves (O and l are rescaled) when some P * v_scale exceeds
-// 2^8, so the row's largest lies in [2^4, 2^8]: p2 underflows 2^-19 of it.  l sums
+// P V: in halves (kind::f16, fp32 sums).  A half holds every code of V exactly,
+// and a probability to 11 bits, off by at most 2^-11 of itself, or by 2^-25 where it
+// is subnormal, 2^-36 of the row's largest or less: a key that takes most of a row (an
+// attention sink) does not cost the row the thousands of others.  Two e4m3 terms
+// did: they end 2^-19 below the largest, and with 0.99 of a row on one of 8192
+// keys, its value 0, the output was off by 0.6 of itself.
+// The product takes its A from TMEM, so that is where V^T (or P) goes in halves:
+// byte columns of a V sub-tile by ldmatrix, two codes per conversion, stored in the
+// lanes' fragment order.  With a lane per row P is there and V, as the B, in
+// shared memory.
+// Block scales enter in fp32: x = s * k_scale * scale * 2^e, P = 2^(x - m + 11),
+// and P * v_scale is what is rounded (a lane has one key of 16 rows, or one row of
+// 32 keys).  m starts as the largest x + log2(v_scale) of the row's first keys
+// and moves (O and l are rescaled) when some P * v_scale exceeds 2^15, so the
+// row's largest lies in [2^11, 2^15] and halves end 2^36 to 2^40 below it.  l sums
 // the fp32 P.
 //
 // Work split: the key tiles of all (sequence, KV head, row tile), and kEnd more
@@ -30,30 +36,33 @@
 // item leaves (O, m, l) in the workspace and k_attn_q8_merge joins them.
 //
 // CTA: softmax warps (groups of four: 16 rows of the tile each, or with a lane
-// per row a quarter of its keys), two producer warps, an MMA warp, and one warp
-// that prepares the next segment's rows (q1, q2, tree masks).  A tile is 256
-// keys up to 64 rows and 128 above (S twice, P twice and O fill TMEM's 512
-// columns): what a warp does once per tile costs it as much as the arithmetic, so
-// tiles are as large as fits.  K and V sub-tiles come in the order in which the MMAs
-// use them (S runs up to NB tiles ahead of P V), through one ring, so that every
-// slot that is not being read is a copy in flight; a producer warp issues all
-// eight 2 KB copies of every second sub-tile.
+// per row a quarter of its keys), four helper warps that turn V into halves and
+// prepare the next segment's rows (q1, q2, tree masks), one or two producer warps
+// and an MMA warp.  A tile is 256 keys up to 64 rows and 128 above (S twice, P or
+// V in halves twice and O fill TMEM's 512 columns): what a warp does once per tile costs
+// it as much as the arithmetic, so tiles are as large as fits.  K and V sub-tiles come
+// in the order in which they are used (S runs up to NB tiles ahead of P V),
+// through one ring, so that every slot that is not being read is a copy in flight; V's
+// slot goes back when its codes have been read.
 //
 // Bound: HBM where the rows are few; else the softmax warps' latencies (4 per
-// scheduler, half of the issue slots used).  64 sequences of 8192 keys, 8 KV heads of
-// 128 with 6 queries of 8 heads each (1.08 GB): 198 us, 5.5 TB/s; without
-// softmax and MMAs 181, without copies too 93.  Ragged batch of 48 sequences up
-// to 16384 keys, 64 rows (411 MB): 95 us, 4.3 TB/s (137 without the ends'
-// units).  One sequence, 100003 keys, one query (205 MB): 46 us, of which the
-// set-up, the first tile and the merge take 12.  16 sequences of 2048 keys with
-// 256 rows (d 64): 66 us, 15 instructions per score (84 us and 19 with the keys
-// on the 128-wide side: masks, maxima and row constants are a lane's own here).
+// scheduler, half of the issue slots used).  All roles' loops run at once, and what they
+// take together does not fit the SM's instruction cache: smaller code is
+// faster code here (loops that are not the softmax warps' are rolled).
+// 64 sequences of 8192 keys, 8 KV heads of 128 with 6 queries of 8 heads each
+// (1.08 GB): 194 us, 5.6 TB/s.  Ragged batch of 48 sequences up to 16384 keys, 64 rows
+// (411 MB): 98 us, 4.2 TB/s.  One sequence, 100003 keys, one query (205 MB): 44 us,
+// of which the set-up, the first tile and the merge take 12.  16 sequences of
+// 2048 keys with 256 rows (d 64): 60 us (66 with P in two e4m3 terms, which
+// two conversions and three packed operations a pair took).
+//   tried for V in halves: by the softmax warps (verify 227, ragged 114), P V issued by a
+//   warp of its own (verify 205, ragged 109), V's buffers by sub-tiles in a ring of
+//   three at 64 rows (ragged 98 instead of 97).
 //   tried: softmax warps in streams of whole tiles (instruction fetch), four
-//   producer warps (verify 214), two prep warps (registers: 110 for the draft),
-//   setmaxnreg (spills), m moved in every tile (each pays a tile's time), next
-//   rows prepared by the softmax warps behind short items (no gain), S of the next
-//   item before the last P V (verify 198 replayed instead of 195), three S and P
-//   buffers for the draft (67 instead of 66).
+//   producer warps (verify 214), setmaxnreg (spills), m moved in every tile (each
+//   pays a tile's time), next rows prepared by the softmax warps behind short items
+//   (no gain), S of the next item before the last P V (verify 198 replayed instead of
+//   195), three S and P buffers for the draft (67 instead of 66).
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <math.h>
@@ -74,11 +83,12 @@ constexpr int kPage = 16;
 constexpr int kMaxNodes = 128;
 constexpr int kSub = 128;                  // keys of a sub-tile (MMA M of S^T, K of O^T)
 constexpr int kPages = kSub / kPage;       // 8
-// P v_scale is at most 2^4 where m was taken (the first tile), and m moves
-// before it exceeds 2^8 (e4m3 ends at 448), to where it is 2^5: the first
-// tile's largest of 128 keys is a low guess of the largest of thousands, and
-// moving m costs about a tile's time.
-constexpr float kBias = 4.f, kMoved = 5.f, kGrow = 8.f;
+// P v_scale goes to halves: at most 2^11 where m was taken (the first tile), and
+// m moves before it exceeds 2^15 (halves end just below 2^16), to where it is
+// 2^12: the first tile's largest of 128 keys is a low guess of the largest of
+// thousands, and moving m costs about a tile's time.  l sums P / 2^7: with
+// v_scale down to 2^-100, P itself reaches 2^115, and thousands of those pass fp32.
+constexpr float kBias = 11.f, kMoved = 12.f, kGrow = 15.f, kSumUnit = 0x1p-7f, kSumBias = kBias - 7.f;
 // Keys of the smallest piece, and the longest table whose items are not cut: joining costs 3 us.  One query, 8 heads:
 // 2000 keys 14.2 us in pieces of 512, 15.9 of 1024, 17.2 whole; 1000 keys 13.3 in pieces of 512, 12.5 whole.
 constexpr int kMinKeys = 512, kWholeKeys = 1024;
@@ -87,8 +97,8 @@ constexpr int kMinKeys = 512, kWholeKeys = 1024;
 // 600 keys (draft): 97, 90, 88, 86; equal lengths: within 2%.
 constexpr int kEnd = 6;
 constexpr int kSmemBudget = 212 * 1024;
-constexpr int kTmaWarps = 2;               // producer warps: warp p loads every sub-tile whose number is p modulo this
-constexpr int kBatch = 32 / kPages;        // sub-tiles that a producer warp's lanes hold the blocks of
+constexpr int kBatch = 32 / kPages;        // tiles that a producer warp's lanes hold the blocks of
+constexpr int kIds = 4 * kBatch;           // tiles whose block ids are held in shared memory (K runs two tiles ahead of V)
 
 // D[tmem] (+)= A B of one 32-byte step of K; A and B by the low words of their
 // shared-memory descriptors (the high words are constants)
@@ -103,21 +113,29 @@ SSD_DEV void umma_f8(uint32_t d_tmem, uint32_t alo, uint32_t ahi, uint32_t blo, 
       "r"(alo), "r"(ahi), "r"(blo), "r"(bhi), "r"(idesc), "r"(accum)
       : "memory");
 }
+// D[tmem] (+)= A B of one step of 16 halves of K; A in TMEM (lane = row, two of K per column), B as above
+SSD_DEV void umma_f16(uint32_t d_tmem, uint32_t a_tmem, uint32_t blo, uint32_t bhi, uint32_t idesc, uint32_t accum) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\t"
+      "mov.b64 b, {%2, %3};\n\t"
+      "setp.ne.b32 p, %5, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n\t}\n" ::"r"(d_tmem),
+      "r"(a_tmem), "r"(blo), "r"(bhi), "r"(idesc), "r"(accum)
+      : "memory");
+}
 // Shared-memory matrix descriptor, 128-byte or (D = 64 rows) 64-byte swizzle.
 // Low word: address / 16, and the bytes / 16 between column blocks of an
-// MN-major operand (0: the second block repeats the first); high word: bytes /
-// 16 between groups of 8 rows, version, swizzle.
+// MN-major operand; high word: bytes / 16 between groups of 8 rows, version, swizzle.
 SSD_DEV constexpr uint32_t desc_lo(uint32_t saddr, uint32_t lbo) { return (saddr >> 4) | ((lbo >> 4) << 16); }
 __host__ __device__ constexpr uint32_t desc_hi(uint32_t sbo, uint32_t swizzle) {
   return (sbo >> 4) | (1u << 14) | (swizzle << 29);
 }
 constexpr uint32_t kSw128 = 2, kSw64 = 4;
-// Instruction descriptor: fp32 sums, e4m3 A and B, both K-major (mn = 0) or MN-major (mn = 1), M = 128
-__host__ __device__ constexpr uint32_t idesc_f8(int N, uint32_t mn) {
-  return (1u << 4) | (mn << 15) | (mn << 16) | (static_cast<uint32_t>(N >> 3) << 17) | (8u << 24);
+// Instruction descriptors, fp32 sums, M = 128: e4m3 A and B, both K-major; fp16 A K-major, B MN-major
+__host__ __device__ constexpr uint32_t idesc_f8(int N) {
+  return (1u << 4) | (static_cast<uint32_t>(N >> 3) << 17) | (8u << 24);
 }
-// the same with A K-major and B MN-major
-__host__ __device__ constexpr uint32_t idesc_f8_kn(int N) {
+__host__ __device__ constexpr uint32_t idesc_f16(int N) {
   return (1u << 4) | (1u << 16) | (static_cast<uint32_t>(N >> 3) << 17) | (8u << 24);
 }
 // byte offset of (row r, byte c) in a block of 128-byte rows, 128-byte swizzled
@@ -183,15 +201,38 @@ SSD_DEV void tmem_wait16(float *v) {  // orders the uses of v after the wait
                :
                : "memory");
 }
-// two groups of 4 columns
-SSD_DEV void tmem_ld4(uint32_t at0, float *v, uint32_t at1, float *w) {
+SSD_DEV void tmem_ld4(uint32_t at, float *v) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%8];\n\t"
-      "tcgen05.ld.sync.aligned.32x32b.x4.b32 {%4, %5, %6, %7}, [%9];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];\n\t"
       "tcgen05.wait::ld.sync.aligned;"
-      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(w[0]), "=f"(w[1]), "=f"(w[2]), "=f"(w[3])
-      : "r"(at0), "r"(at1)
+      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3])
+      : "r"(at)
       : "memory");
+}
+// 16 columns of this thread's lane; the stores are waited for by tmem_wait_st
+SSD_DEV void tmem_st16_async(uint32_t at, const uint32_t *v) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(at),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+      "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+      : "memory");
+}
+// 16 TMEM lanes x 16 columns: of columns 8 w .. + 7, lane l holds columns 2 (l % 4) and the next of TMEM lane l / 4 (v[4 w],
+// v[4 w + 1]) and of TMEM lane 8 + l / 4 (v[4 w + 2], v[4 w + 3])
+SSD_DEV void tmem_st_16x16(uint32_t at, const uint32_t *v) {
+  asm volatile("tcgen05.st.sync.aligned.16x256b.x2.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(at), "r"(v[0]),
+               "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
+SSD_DEV void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+// Two 16 x 16 byte blocks, transposed: lane l gives the address of row l % 16 of block l / 16 and gets bytes 4 (l % 4) .. + 3
+// of columns l / 4 (c[2 b]) and 8 + l / 4 (c[2 b + 1]) of block b: four rows' bytes of one column
+SSD_DEV void load_columns(uint32_t saddr, uint32_t *c) {
+  asm volatile("ldmatrix.sync.aligned.m16n16.x2.trans.shared.b8 {%0, %1, %2, %3}, [%4];"
+               : "=r"(c[0]), "=r"(c[1]), "=r"(c[2]), "=r"(c[3])
+               : "r"(saddr)
+               : "memory");
 }
 SSD_DEV void bar_sync(int id, int n) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory"); }
 SSD_DEV bool bar_or(int id, int n, bool pred) {
@@ -219,15 +260,16 @@ SSD_DEV uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c) {
   asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
   return r;
 }
-SSD_DEV uint32_t hmul2(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
+// four codes -> four halves (exact)
+SSD_DEV void halves_of(uint32_t codes, uint32_t &h0, uint32_t &h1) {
+  h0 = e4m3_to_half2(static_cast<uint16_t>(codes & 0xFFFFu));
+  h1 = e4m3_to_half2(static_cast<uint16_t>(codes >> 16));
 }
-SSD_DEV uint32_t pack16(uint16_t lo, uint16_t hi) {
-  uint32_t r;
-  asm("mov.b32 %0, {%1, %2};" : "=r"(r) : "h"(lo), "h"(hi));
-  return r;
+// four codes with NaN ones made 0; `any` collects whether there were some
+SSD_DEV uint32_t without_nan(uint32_t codes, uint32_t among, uint32_t &any) {
+  const uint32_t nan = ((codes & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u & among;  // bytes 0x7F, 0xFF
+  any |= nan;
+  return codes & ~((nan >> 7) * 0xFFu);
 }
 
 // One value per 16 columns and lane -> the columns' sums over the warp's lanes:
@@ -363,37 +405,42 @@ struct Cfg {
   static constexpr bool kRowLanes = RT > 64;               // rows, not keys, on the MMA's 128-wide side
   static constexpr int KT = RT <= 64 ? 2 : 1;              // sub-tiles of a tile
   static constexpr int kKeys = KT * kSub;                  // keys of a tile
+  static constexpr int kTmaWarps = KT;                     // producer warps: one for every sub-tile of a tile
   static constexpr int CG = kRowLanes ? 32 : 16;           // rows of a softmax warp (keys, with a lane per row)
   static constexpr int kGroups = RT / CG;                  // groups of four warps
   static constexpr int NB = 2;                             // S and P buffers; S runs NB tiles ahead
   static constexpr int kSoftWarps = 4 * kGroups;
-  static constexpr int kTmaWarp = kSoftWarps, kMmaWarp = kTmaWarp + kTmaWarps, kPrepWarp = kMmaWarp + 1;
-  static constexpr int kWarps = kPrepWarp + 1;
+  // helper warps: warp w of the four writes TMEM lanes 32 w .. + 31 (those that a warp with this number modulo 4 reaches)
+  static constexpr int kHelpWarp = kSoftWarps, kTmaWarp = kHelpWarp + 4, kMmaWarp = kTmaWarp + kTmaWarps;
+  static constexpr int kWarps = kMmaWarp + 1;
   static constexpr int kThreads = kWarps * 32;
   static constexpr int kQTile = RT * 128;                  // q1 (or q2) at D = 128; [q1 | q2] at D = 64
   static constexpr int kQBuf = D == 128 ? 2 * kQTile : kQTile;
-  static constexpr int kPBlock = kSub * 128;               // 128-byte rows: 128 of N per key, or a row's 128 keys
-  static constexpr int kPBuf = RT > 64 ? 2 * kPBlock : kPBlock;  // p1 [RT] then p2 [RT] along N, of a sub-tile
+  // P V's operand in shared memory, halves: P^T of a sub-tile in rows of 128 bytes, a key each; with a lane per row V
+  // in blocks of 64 elements, rows of 128 bytes, a key each
+  static constexpr int kBlock = kSub * 128;
+  static constexpr int kHBuf = kRowLanes ? (D / 64) * kBlock : KT * kBlock;  // of a tile
   static constexpr int kSlot = kSub * D;                   // K or V of a sub-tile
-  static constexpr int kFixed = 2 * kQBuf + NB * KT * kPBuf;
+  static constexpr int kFixed = 2 * kQBuf + NB * kHBuf;
   static constexpr int kFit = (kSmemBudget - kFixed) / kSlot;
   static constexpr int kSlots = kFit > 16 ? 16 : kFit;
-  static constexpr int kQ = 0, kP = 2 * kQBuf, kRing = kFixed;
+  static constexpr int kQ = 0, kH = 2 * kQBuf, kRing = kFixed;
   static constexpr int kSmem = kFixed + kSlots * kSlot + 1024;
-  static constexpr int kOCol = NB * KT * RT;               // TMEM: NB x KT x S, then O1, O2
-  static constexpr uint32_t kCols = kOCol + 2 * (kRowLanes ? D : RT);
-  static constexpr uint32_t kTmem = kCols <= 64 ? 64 : (kCols <= 128 ? 128 : (kCols <= 256 ? 256 : 512));
-  static constexpr int kMeta = 16 / KT;                    // tiles whose block scales are held
+  // TMEM: NB x KT x S, O, and at its end P V's other operand in halves: V^T (as many buffers as there is room for), or P
+  static constexpr int kOCol = NB * KT * RT, kOCols = kRowLanes ? D : RT;
+  static constexpr int kACols = KT * (kSub / 2);           // of a tile
+  static constexpr int kABufs = kOCol + kOCols + NB * kACols <= 512 ? NB : 1;
+  static constexpr int kACol = 512 - kABufs * kACols;
+  static constexpr int kMeta = 24 / KT;                    // tiles whose block scales are held
   static_assert(kSmem + 13824 <= 227 * 1024, "shared memory with the static part");
   static_assert(kSlots >= (NB + 1) * KT, "S runs NB tiles ahead");
-  // A warp writes the scales of tile i before the wait of its load; its load before that lies at most kTmaWarps + 1
-  // loads back (KT = 1: K, V, and the other warps' pairs: 2 kTmaWarps - 1) and waited for the use of its slot, kSlots
-  // loads further back.  P V of tile i - NB is the last of a tile before the K loads of tile i.
-  static constexpr int kBack = kSlots + 2 * kTmaWarps + KT - 1;
-  static_assert(kMeta >= NB + (kBack + 2 * KT - 1) / (2 * KT), "block scales");
+  // A producer writes the scales of tiles i .. i + kBatch - 1 before the wait of tile i's K; its load before that waited for
+  // the use of its slot, kSlots + KT sub-tiles further back.  P V of tile i - NB is the last of a tile before K of tile i.
+  static_assert(kMeta >= NB + kBatch + (kSlots + KT + 2 * KT - 1) / (2 * KT), "block scales");
   static_assert(!kRowLanes || (RT == 128 && kGroups == 4), "a lane per row, a quarter of the keys per group");
-  static_assert(kRowLanes || (KT == 2 && CG == 16 && 2 * RT <= 128), "tiles of two sub-tiles, P in rows of 128 bytes");
-  static_assert(kCols <= 512 && RT % CG == 0 && kGroups <= 4, "rows");
+  static_assert(!kRowLanes || kABufs == NB, "P is written while the product before reads its own");
+  static_assert(kRowLanes || (KT == 2 && CG == 16 && RT <= 64), "tiles of two sub-tiles, P in rows of 128 bytes");
+  static_assert(kOCol + kOCols <= kACol && RT % CG == 0 && kGroups <= 4, "TMEM and rows");
 };
 
 // A segment's rows: q1, q2 into the operand tiles at qb, the row scales, and
@@ -526,16 +573,19 @@ __global__ void __launch_bounds__(Cfg<D, RT>::kThreads, 1)
   uint8_t *const smem =
       reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   __shared__ __align__(8) uint64_t full[NSLOT], empty[NSLOT];
-  __shared__ __align__(8) uint64_t sfull[NB], pfull[NB], pvdone[NB], qfull[2], qempty[2];
+  __shared__ __align__(8) uint64_t sfull[NB], pfull[NB], vfull[NB][KT], pvdone[NB], qfull[2], qempty[2];
   __shared__ uint32_t tmem_base;
   // a block's k_scale * scale * log2 e, v_scale (-1: hidden), log2 v_scale
   __shared__ __align__(16) float4 meta[kMeta][KT * kPages];
+  __shared__ __align__(16) int s_ids[C::kTmaWarps][kIds][kPages];  // block ids of a tile's sub-tile, -1 for none
+  __shared__ int s_row[C::kTmaWarps][kIds];                        // and its head's first row in a block
   __shared__ int par[2][kMaxNodes];
   __shared__ uint32_t anc[2][kMaxNodes][kMaxNodes / 32];    // per query: the nodes that it sees
   __shared__ float qs[2][RT];                               // row scales 2^e
   __shared__ __align__(16) float4 rowc[RT / 2];             // two rows: 2^e, 2^e, 4 - m, 4 - m
   __shared__ float s_m[RT], s_f[RT], red[4][RT];
-  __shared__ int s_nan[2];                                  // a tree node's v held NaN, by segment mod 2
+  __shared__ int s_nan[4];                                  // a tree node's v held NaN, by segment mod 4 (the helper
+                                                            // warps are in the segment behind the softmax warps' at most)
   __shared__ long long scan[32];
   __shared__ Piece s_piece;
   __shared__ volatile int s_abort;
@@ -552,20 +602,21 @@ __global__ void __launch_bounds__(Cfg<D, RT>::kThreads, 1)
     for (int u = 0; u < NB; ++u) {
       mbar_init(&sfull[u], 1);
       mbar_init(&pfull[u], 4 * C::kGroups);
+      for (int h = 0; h < KT; ++h) mbar_init(&vfull[u][h], 4);
       mbar_init(&pvdone[u], 1);
     }
     for (int u = 0; u < 2; ++u) {
-      mbar_init(&qfull[u], 1);
+      mbar_init(&qfull[u], 4);
       mbar_init(&qempty[u], 1 + C::kSoftWarps);
     }
     fence_mbar_init();
     s_abort = 0;
-    s_nan[0] = s_nan[1] = 0;
+    s_nan[0] = s_nan[1] = s_nan[2] = s_nan[3] = 0;
     s_piece.left = 0;
     s_piece.tiles = 0;
   }
   if (warp == C::kMmaWarp) {
-    tmem_alloc(&tmem_base, C::kTmem);
+    tmem_alloc(&tmem_base, 512);
     tmem_relinquish();
   }
   // the line of units: every thread sums some sequences' units, then the sums are scanned
@@ -626,175 +677,121 @@ __global__ void __launch_bounds__(Cfg<D, RT>::kThreads, 1)
     prepare_rows<D, RT>(a, sg, smem + C::kQ + buf * C::kQBuf, par[buf], anc[buf], qs[buf], w, n, bar);
   };
 
-  // V of tile i, sub-tile h (of segment seg, whose tiles end before `end`), this thread's key: hidden keys take no part whatever
-  // their v holds (0 * NaN): their rows become 0; a tree node's NaN becomes 0 too, and reaches the rows that see it at
-  // the segment's end; a prefix key stays.  False when the wait for V gave up.
-  auto void_rows = [&](int seg, int i, int end, bool gone, bool prefix, int h) -> bool {
-    const int load = (min(i + NB, end) + i) * KT + h;  // V's place in the order of loads
-    const bool ok = warp_wait(&full[load % NSLOT], (load / NSLOT) & 1);
-    if (prefix) return ok;
-    const int key = tid & 127;
-    uint8_t *const vt = smem + C::kRing + (load % NSLOT) * C::kSlot;
-#pragma unroll 1
-    for (int e = 0; e < D; e += 16) {
-      uint4 *const at = reinterpret_cast<uint4 *>(vt + (D == 128 ? sw128(key, e) : sw64(key, e)));
-      uint4 v = make_uint4(0, 0, 0, 0);
-      if (!gone) {
-        v = *at;
-        uint32_t any = 0;
-        auto clear = [&](uint32_t w) {
-          const uint32_t nan = ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;  // bytes 0x7F, 0xFF
-          any |= nan;
-          return w & ~((nan >> 7) * 0xFFu);
-        };
-        v = make_uint4(clear(v.x), clear(v.y), clear(v.z), clear(v.w));
-        if (any) s_nan[seg & 1] = 1;
-      }
-      *at = v;
-    }
-    return ok;
-  };
-
   Segments sg;
   if (warp >= C::kTmaWarp && warp < C::kMmaWarp) {
-    // ---------------- producers.  A load's fixed work costs its warp about 500 clocks and a copy 65 (the TMA unit's
-    // own pace for 2 KB), so a warp issues all eight copies of every second sub-tile.  Block ids and scales are
-    // fetched for kBatch of its sub-tiles at a time, one batch ahead (two dependent trips to memory for a batch):
-    // lane l holds block l % 8 of the batch's sub-tile l / 8.
+    // ---------------- producers: warp p loads sub-tile p of every tile, K and V.  A copy costs 45 clocks (the TMA unit's
+    // own pace for 2 KB).  Block ids and scales are fetched for kBatch tiles at a time, one batch ahead (two dependent
+    // trips to memory for a batch): lane l holds block l % 8 of the batch's tile l / 8.
     const int pw = warp - C::kTmaWarp, page = lane % kPages;
-    struct Batch {
-      int hk, blk;
-      float ks, vs;
-    };
     bool more = sg.first(a, piece);
-    int t = more ? sg.t0 * KT : 0;
-    auto advance = [&](int n) {  // this lane's place in the line of sub-tiles
+    int t = more ? sg.t0 : 0;
+    auto advance = [&](int n) {  // this lane's place in the line of tiles
       t += n;
-      while (more && t >= sg.t1 * KT) {
-        t -= sg.t1 * KT;
+      while (more && t >= sg.t1) {
+        t -= sg.t1;
         more = sg.step(a);
       }
     };
-    auto ids = [&](Batch &x) {
-      x.hk = more ? sg.hk : 0;
-      x.blk = -1;
-      x.vs = 0.f;
-      x.ks = -1.f;  // no block there
-      const int64_t lp = static_cast<int64_t>(t) * kPages + page;
+    int hk, blk;
+    float ks, vs;
+    auto ids = [&] {
+      hk = more ? sg.hk : 0;
+      blk = -1;
+      vs = 0.f;
+      ks = -1.f;  // no block there
+      const int64_t lp = (static_cast<int64_t>(t) * KT + pw) * kPages + page;
       if (more && lp < a.maxb && lp * kPage < sg.nkeys) {
-        x.blk = a.table[static_cast<int64_t>(sg.b) * a.maxb + lp];
-        x.ks = 0.f;
+        blk = a.table[static_cast<int64_t>(sg.b) * a.maxb + lp];
+        ks = 0.f;
       }
-      advance(kBatch * kTmaWarps);
+      advance(kBatch);
     };
-    auto scales = [&](Batch &x) {
-      if (x.blk >= 0 && x.blk < a.num_blocks) {
-        const int64_t unit = static_cast<int64_t>(x.blk) * a.Hkv + x.hk;
-        x.ks = __ldg(a.ks + unit);
-        x.vs = __ldg(a.vs + unit);
-      } else if (x.ks >= 0.f) {
+    auto scales = [&] {
+      if (blk >= 0 && blk < a.num_blocks) {
+        const int64_t unit = static_cast<int64_t>(blk) * a.Hkv + hk;
+        ks = __ldg(a.ks + unit);
+        vs = __ldg(a.vs + unit);
+      } else if (ks >= 0.f) {
         atomicOr(a.status, kFlagBadBlock);
-        x.blk = -1;
+        blk = -1;
       }
     };
-    Batch old, now, next;
-    advance(lane / kPages * kTmaWarps + pw);
-    ids(next);
-    scales(next);
-    now = old = next;
-    int slot = 0, mine = 0;  // `mine`: K sub-tiles that this warp has loaded
-    uint32_t phase = 1;      // of empty[slot]; the first round's slots are free
-    int issued = 0;          // loads so far, all warps'
-    uint32_t own = 0;        // bit k: the load k before the last was this warp's
+    advance(lane / kPages);
+    ids();
+    scales();
+    int slot = pw;
+    uint32_t phase = 1;  // of empty[slot]; the first round's slots are free
+    int c = 0;           // tiles of K and of V loaded so far
     bool ok = true;
-    auto next_slot = [&](bool mine) {
-      ++issued;
-      own = own << 1 | static_cast<uint32_t>(mine);
-      if (++slot == NSLOT) {
-        slot = 0;
-        phase ^= 1;
+    Order order;
+    order.start(a, piece);
+    for (int i = 0, j = 0; j < ntiles; ++c) {
+      const bool is_k = i - j < NB && i < order.end;  // K of tile i, or V of tile j
+      if (is_k) {
+        const int w = i % kBatch;
+        if (w == 0) {
+          if (blk >= 0 && !(good_scale(ks) && good_scale(vs))) {  // bad scales hide their block
+            atomicOr(a.status, kFlagBadValue);
+            blk = -1;
+          }
+          const float v = vs < kMinBlockScale ? 0.f : vs;
+          const int at = i + lane / kPages;
+          meta[at % kMeta][pw * kPages + page] =
+              blk >= 0 ? make_float4(ks * a.scale_log2, v, __log2f(fmaxf(v, kMinBlockScale)), 0.f)
+                       : make_float4(0.f, -1.f, 0.f, 0.f);
+          s_ids[pw][at % kIds][page] = blk;
+          if (page == 0) s_row[pw][at % kIds] = hk * kPage;
+          __syncwarp();
+          ids();
+        }
+        if (w == kBatch / 2) scales();
       }
-    };
-    // one load: sub-tile w of batch x into the next slot
-    auto load = [&](const Batch &x, int w, const CUtensorMap *map) {
-      const uint32_t which = __ballot_sync(0xffffffffu, x.blk >= 0) >> (w * kPages) & 0xFFu;
-      const int row = __shfl_sync(0xffffffffu, x.hk, w * kPages) * kPage;
-      int blk[kPages];
-#pragma unroll
-      for (int e = 0; e < kPages; ++e) blk[e] = __shfl_sync(0xffffffffu, x.blk, w * kPages + e);
-      ok = issued < NSLOT || warp_wait(&empty[slot], phase);
-      if (!ok) return;
+      const int x = (is_k ? i : j) % kIds;
+      const CUtensorMap *const map = is_k ? &kmap : &vmap;
+      const int row = s_row[pw][x];
+      const int4 lo = *reinterpret_cast<const int4 *>(s_ids[pw][x]), hi = *reinterpret_cast<const int4 *>(s_ids[pw][x] + 4);
+      const int e[kPages] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+      ok = c * KT + pw < NSLOT || warp_wait(&empty[slot], phase);
+      if (!ok) break;
       uint8_t *const dst = smem + C::kRing + slot * C::kSlot;
       if (elect_one()) {
-        mbar_arrive_expect_tx(&full[slot], __popc(which) * (kPage * D));
-        if (which == 0xFFu) {
+        if ((lo.x | lo.y | lo.z | lo.w | hi.x | hi.y | hi.z | hi.w) >= 0) {
+          mbar_arrive_expect_tx(&full[slot], C::kSlot);
 #pragma unroll
-          for (int e = 0; e < kPages; ++e) tma_load_3d(dst + e * (kPage * D), map, 0, row, blk[e], &full[slot]);
-        } else {
-#pragma unroll
-          for (int e = 0; e < kPages; ++e)
-            if ((which >> e) & 1u) tma_load_3d(dst + e * (kPage * D), map, 0, row, blk[e], &full[slot]);
+          for (int k = 0; k < kPages; ++k) tma_load_3d(dst + k * (kPage * D), map, 0, row, e[k], &full[slot]);
+        } else {  // some blocks are missing or bad
+          int n = 0;
+          for (int k = 0; k < kPages; ++k) n += s_ids[pw][x][k] >= 0;
+          mbar_arrive_expect_tx(&full[slot], n * (kPage * D));
+#pragma unroll 1
+          for (int k = 0; k < kPages; ++k)
+            if (s_ids[pw][x][k] >= 0) tma_load_3d(dst + k * (kPage * D), map, 0, row, s_ids[pw][x][k], &full[slot]);
         }
       }
       __syncwarp();
-    };
-    Order order;
-    order.start(a, piece);
-    for (int i = 0, j = 0; j < ntiles && ok;) {
-      if (i - j < NB && i < order.end) {  // K of tile i
-        for (int h = 0; h < KT && ok; ++h) {
-          const bool m = (i * KT + h) % kTmaWarps == pw;
-          if (m) {
-            const int w = mine++ % kBatch;
-            if (w == 0) {
-              old = now;
-              now = next;
-              if (now.blk >= 0 && !(good_scale(now.ks) && good_scale(now.vs))) {  // bad scales hide their block
-                atomicOr(a.status, kFlagBadValue);
-                now.blk = -1;
-              }
-              ids(next);
-            }
-            if (w == kBatch / 2) scales(next);
-            if (lane / kPages == w) {
-              const float v = now.vs < kMinBlockScale ? 0.f : now.vs;
-              meta[i % kMeta][h * kPages + page] =
-                  now.blk >= 0 ? make_float4(now.ks * a.scale_log2, v, __log2f(fmaxf(v, kMinBlockScale)), 0.f)
-                               : make_float4(0.f, -1.f, 0.f, 0.f);
-            }
-            load(now, w, &kmap);
-          }
-          next_slot(m && ok);
-        }
-        ++i;
-      } else {  // V of tile j
-        for (int h = 0; h < KT && ok; ++h) {
-          const int x = j * KT + h;
-          const bool m = x % kTmaWarps == pw;
-          if (m) {
-            const int k = x / kTmaWarps;  // its number among this warp's
-            load(k / kBatch == (mine - 1) / kBatch ? now : old, k % kBatch, &vmap);
-          }
-          next_slot(m && ok);
-        }
-        order.done(a, ++j);
+      slot += KT;
+      if (slot >= NSLOT) {
+        slot -= NSLOT;
+        phase ^= 1;
       }
+      if (is_k) ++i;
+      else order.done(a, ++j);
     }
     if (!ok) {
       s_abort = 1;
       // this warp's copies in flight land before the shared memory is given back
-      for (int k = 0, i = issued; k < NSLOT && --i >= 0; ++k)
-        if ((own >> k) & 1u) (void)warp_wait(&full[i % NSLOT], (i / NSLOT) & 1);
+      for (int k = 0; k < (NSLOT + KT - 1) / KT && --c >= 0; ++k) {
+        const int load = c * KT + pw;
+        (void)warp_wait(&full[load % NSLOT], (load / NSLOT) & 1);
+      }
     }
   } else if (warp == C::kMmaWarp) {
     // ---------------- MMA issue (one elected lane): S of up to NB tiles ahead, then P V and S in turn.  This loop
     // is one warp's chain of scalar work per tile, so what can be is kept in running words.
-    constexpr uint32_t idesc_s = idesc_f8(C::kRowLanes ? kSub : RT, 0);
-    constexpr uint32_t idesc_o = C::kRowLanes ? idesc_f8_kn(D) : idesc_f8(2 * RT, 1);
+    constexpr uint32_t idesc_s = idesc_f8(C::kRowLanes ? kSub : RT), idesc_o = idesc_f16(C::kRowLanes ? D : RT);
     constexpr uint32_t hi128 = desc_hi(1024, kSw128), hi64 = desc_hi(512, kSw64), hi_kv = D == 128 ? hi128 : hi64;
     const uint32_t base = smem_u32(smem);
-    const uint32_t ring_k = desc_lo(base + C::kRing, 16), ring_v = desc_lo(base + C::kRing, D == 128 ? 16 : 0);
-    const uint32_t p_lo = desc_lo(base + C::kP, C::kRowLanes ? 16 : C::kPBlock);
+    const uint32_t ring_k = desc_lo(base + C::kRing, 16), h_lo = desc_lo(base + C::kH, C::kBlock);
     bool ok = true;
     int slot = 0, seg = 0;
     uint32_t phase = 0;  // of full[slot]
@@ -856,24 +853,18 @@ __global__ void __launch_bounds__(Cfg<D, RT>::kThreads, 1)
         const uint32_t o = tmem + C::kOCol;
         const uint32_t later = j > order.begin;  // not the segment's first tile
         ok = warp_wait(&pfull[u], (j / NB) & 1);
-#pragma unroll
+        const uint32_t at = tmem + C::kACol + (j % C::kABufs) * C::kACols, b = h_lo + u * (C::kHBuf >> 4);
+#pragma unroll 1
         for (int h = 0; h < KT; ++h) {
-          ok = ok && warp_wait(&full[slot], phase);
+          ok = ok && warp_wait(&vfull[u][h], (j / NB) & 1);
           if (!ok) break;
           tc_fence_after();
-          const uint32_t v = ring_v + slot * (C::kSlot >> 4), p = p_lo + (u * KT + h) * (C::kPBuf >> 4);
           if (elect_one()) {
+            umma_commit(&empty[slot]);  // the helper warps have read V; given back in the order of the loads (S before)
 #pragma unroll
-            for (int kk = 0; kk < kSub / 32; ++kk) {  // 32 keys: four groups of 8 rows
-              const uint32_t vk = v + kk * ((32 * D) >> 4), more = (h > 0 || kk > 0) ? 1u : later;
-              if (C::kRowLanes) {
-                umma_f8(o, p + kk * 2, hi128, vk, hi_kv, idesc_o, more);
-                umma_f8(o + D, p + (C::kPBlock >> 4) + kk * 2, hi128, vk, hi_kv, idesc_o, more);
-              } else {
-                umma_f8(o, vk, hi_kv, p + kk * (4096 >> 4), hi128, idesc_o, more);
-              }
-            }
-            umma_commit(&empty[slot]);
+            for (int kk = 0; kk < kSub / 16; ++kk)  // 16 keys: two groups of 8 rows
+              umma_f16(o, at + h * (kSub / 2) + kk * 8, b + h * (C::kBlock >> 4) + kk * (2048 >> 4), hi128, idesc_o,
+                       kk > 0 || h > 0 ? 1u : later);
             if (h == KT - 1) umma_commit(&pvdone[u]);
           }
           __syncwarp();
@@ -883,25 +874,114 @@ __global__ void __launch_bounds__(Cfg<D, RT>::kThreads, 1)
       }
     }
     if (!ok) s_abort = 1;
-  } else if (warp == C::kPrepWarp) {
-    // ---------------- the rows of the segments after the first
-    bool more = sg.first(a, piece);
+  } else if (warp >= C::kHelpWarp && warp < C::kTmaWarp) {
+    // ---------------- helpers: V in halves, tile by tile, and the rows of the segments after the first, a segment ahead.
+    // They meet at named barriers, which have no limit, so a warp whose wait gave up goes on (its waits are over at once)
+    // until they leave together.
+    const int hw = warp - C::kHelpWarp;
+    bool ok = true, all = true, more = sg.first(a, piece);
     if (more) {
-      prepare(sg, 0, C::kSoftWarps, C::kSoftWarps + 1, 10);
-      bar_sync(10, (C::kSoftWarps + 1) * 32);
+      prepare(sg, 0, warp, C::kSoftWarps + 4, 10);
+      bar_sync(10, (C::kSoftWarps + 4) * 32);
       if (lane == 0) mbar_arrive1(&qfull[0]);
-      more = sg.step(a);
     }
-    for (int seg = 1; more; more = sg.step(a), ++seg) {
-      const int buf = seg & 1;
-      const bool ok = seg < 2 || warp_wait(&qempty[buf], ((seg >> 1) - 1) & 1);
-      if (!ok || __any_sync(0xffffffffu, s_abort != 0)) {
-        s_abort = 1;
-        break;
+    for (int i = 0, seg = 0; more; ++seg) {
+      const int n = sg.t1 - sg.t0, end = i + n;
+      Segments next = sg;
+      more = next.step(a);
+      if (more) {  // the next segment's rows, once the segment before this has left their buffer
+        const int buf = (seg + 1) & 1;
+        ok = ok && (seg < 1 || warp_wait(&qempty[buf], ((seg - 1) >> 1) & 1));
+        all = !bar_or(11, 128, !ok || s_abort);
+        if (!all) break;
+        prepare(next, buf, hw, 4, 11);
+        if (lane == 0) mbar_arrive1(&qfull[buf]);
       }
-      prepare(sg, buf, 0, 1, 11);
-      if (lane == 0) mbar_arrive1(&qfull[buf]);
+      for (int x = 0; x < n; ++x, ++i) {
+        const int t = sg.t0 + x, u = i % NB;
+        // S first: by then K of this tile has landed, and with it every load that used V's slots before; a wait for V's
+        // phase of a slot would not tell the phase two before from it
+        ok = ok && warp_wait(&sfull[u], (i / NB) & 1);
+        // the product that last read the buffer is done
+        if (i >= C::kABufs) ok = ok && warp_wait(&pvdone[(i - C::kABufs) % NB], ((i - C::kABufs) / NB) & 1);
+        tc_fence_after();
+        // hidden keys take no part whatever their v holds (0 * NaN): they become 0; a tree node's NaN becomes 0 too, and
+        // reaches the rows that see it at the segment's end
+        bool part = (t + 1) * C::kKeys > min(sg.L, sg.nkeys);
+        part = __any_sync(0xffffffffu, part || (lane < KT * kPages && meta[i % kMeta][lane].y < 0.f));
+        const int load0 = (min(i + NB, end) + i) * KT;  // V's place in the order of loads
+#pragma unroll 1
+        for (int h = 0; h < KT; ++h) {
+          const int slot = (load0 + h) % NSLOT;
+          ok = ok && warp_wait(&full[slot], ((load0 + h) / NSLOT) & 1);
+          if (!ok) break;
+          const uint8_t *const vt = smem + C::kRing + slot * C::kSlot;
+          uint32_t any = 0;
+          if constexpr (C::kRowLanes) {  // a lane per key
+            const int r = hw * 32 + lane, pos = t * kSub + r;
+            const bool gone = part && (meta[i % kMeta][r / kPage].y < 0.f || pos >= sg.nkeys);
+#pragma unroll
+            for (int c = 0; c < D / 16; ++c) {  // 16 codes
+              uint4 v = make_uint4(0, 0, 0, 0);
+              if (!gone) v = *reinterpret_cast<const uint4 *>(vt + (D == 128 ? sw128(r, c * 16) : sw64(r, c * 16)));
+              if (part && pos >= sg.L)
+                v = make_uint4(without_nan(v.x, ~0u, any), without_nan(v.y, ~0u, any), without_nan(v.z, ~0u, any),
+                               without_nan(v.w, ~0u, any));
+              uint32_t x[8];
+              halves_of(v.x, x[0], x[1]);
+              halves_of(v.y, x[2], x[3]);
+              halves_of(v.z, x[4], x[5]);
+              halves_of(v.w, x[6], x[7]);
+              uint8_t *const to = smem + C::kH + u * C::kHBuf + (c >> 2) * C::kBlock;
+              *reinterpret_cast<uint4 *>(to + sw128(r, (c & 3) * 32)) = make_uint4(x[0], x[1], x[2], x[3]);
+              *reinterpret_cast<uint4 *>(to + sw128(r, (c & 3) * 32 + 16)) = make_uint4(x[4], x[5], x[6], x[7]);
+            }
+            fence_proxy_async();  // V (generic writes) -> visible to the tensor cores
+          } else {  // V^T: 32 keys of this warp's 32 elements (at d = 64 the upper lanes repeat the lower ones) at a time
+            const int el = (D == 128 ? hw : hw & 1) * 32 + (lane >> 4) * 16;
+            const uint32_t from = smem_u32(vt) + (D == 128 ? sw128(lane & 15, el) : sw64(lane & 15, el));
+            const uint32_t to = tmem + C::kACol + (i % C::kABufs) * C::kACols + h * (kSub / 2) +
+                                (static_cast<uint32_t>(hw * 32) << 16);
+            // a rolled loop: the softmax warps' code has to stay in the instruction cache
+#pragma unroll 1
+            for (int k0 = 0; k0 < kSub; k0 += 32) {
+              uint32_t c[8];
+              load_columns(from + k0 * D, c);
+              load_columns(from + (k0 + 16) * D, c + 4);
+              if (part) {
+#pragma unroll
+                for (int b = 0; b < 2; ++b) {
+                  // this lane's four keys: those that are there, and those that are tree nodes
+                  const int key = h * kSub + k0 + b * 16, pos = t * C::kKeys + key + (lane & 3) * 4;
+                  auto first = [](int n) { return n <= 0 ? 0u : (n >= 4 ? ~0u : (1u << (8 * n)) - 1u); };
+                  const uint32_t there = meta[i % kMeta][key / kPage].y < 0.f ? 0u : first(sg.nkeys - pos);
+                  const uint32_t nodes = ~first(sg.L - pos);
+#pragma unroll
+                  for (int w = 0; w < 4; ++w) c[b * 4 + w] = without_nan(c[b * 4 + w] & there, nodes, any);
+                }
+              }
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {  // 16 elements each
+                uint32_t v[8];
+#pragma unroll
+                for (int b = 0; b < 2; ++b) {
+                  halves_of(c[b * 4 + e * 2], v[b * 4], v[b * 4 + 1]);
+                  halves_of(c[b * 4 + e * 2 + 1], v[b * 4 + 2], v[b * 4 + 3]);
+                }
+                tmem_st_16x16(to + k0 / 2 + (static_cast<uint32_t>(e * 16) << 16), v);
+              }
+            }
+            tmem_wait_st();
+            tc_fence_before();
+          }
+          if (any) s_nan[seg & 3] = 1;
+          __syncwarp();
+          if (lane == 0) mbar_arrive1(&vfull[u][h]);
+        }
+      }
+      sg = next;
     }
+    if (!ok || !all) s_abort = 1;
   } else if constexpr (C::kRowLanes) {
     // ---------------- softmax, a lane per row: group g has the keys g * 32 .. + 31 of every tile
     const int g = warp / 4, wg = warp & 3, r = tid & 127;
@@ -913,8 +993,8 @@ __global__ void __launch_bounds__(Cfg<D, RT>::kThreads, 1)
     bool dead = false;
     bool more = sg.first(a, piece);
     if (more) {
-      prepare(sg, 0, warp, C::kSoftWarps + 1, 10);
-      bar_sync(10, (C::kSoftWarps + 1) * 32);
+      prepare(sg, 0, warp, C::kSoftWarps + 4, 10);
+      bar_sync(10, (C::kSoftWarps + 4) * 32);
     }
     for (; more; more = sg.step(a), ++seg) {
       const int buf = seg & 1, n = sg.t1 - sg.t0, row = sg.mt * RT + r;
@@ -1017,8 +1097,8 @@ __global__ void __launch_bounds__(Cfg<D, RT>::kThreads, 1)
               l2[0] = mul2(l2[0], f2);
               l2[1] = mul2(l2[1], f2);
 #pragma unroll 1
-              for (int k = 0; k < 2 * (D / 64); ++k) {  // this group's quarter of both accumulators
-                const uint32_t at = tO + (k & 1) * D + (k >> 1) * 16;
+              for (int k = 0; k < D / 64; ++k) {  // this group's quarter of O
+                const uint32_t at = tO + k * 16;
                 float o[16];
                 tmem_ld16(at, o);
 #pragma unroll
@@ -1029,41 +1109,24 @@ __global__ void __launch_bounds__(Cfg<D, RT>::kThreads, 1)
           }
           if (dead) break;
           begin = false;
-          // the P buffer is free: S of this tile was issued behind P V of tile i - NB
-          uint8_t *const pb = smem + C::kP + u * C::kPBuf;
+          // P's and V's buffers are free: S of this tile was issued behind P V of tile i - NB
+          const uint64_t unit2 = pack2(kSumUnit, kSumUnit);
+          uint32_t hp[16];
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             const uint64_t w2 = pack2(wv[e], wv[e]);
-            uint32_t p1[4], p2[4];
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              uint16_t e1[2], e2[2];
-#pragma unroll
-              for (int k = 0; k < 2; ++k) {
-                const int j = e * 16 + q * 4 + k * 2;
-                const uint64_t p = pack2(ex2(y[j]), ex2(y[j + 1]));
-                l2[k] = ssd::add2(l2[k], p);
-                float a0, a1;
-                unpack2(mul2(p, w2), a0, a1);
-                const uint32_t hp = half2_of(a0, a1);
-                e1[k] = e4m3_of_half2(hp);
-                // 32 (p - p1) in halves: exact (p is at most 2^8, the difference has at most 11 bits)
-                e2[k] = e4m3_of_half2(hfma2(e4m3_to_half2(e1[k]), 0xD000D000u, hmul2(hp, 0x50005000u)));
-              }
-              p1[q] = pack16(e1[0], e1[1]);
-              p2[q] = pack16(e2[0], e2[1]);
+            for (int j = 0; j < 8; ++j) {
+              const uint64_t p = pack2(ex2(y[e * 16 + 2 * j]), ex2(y[e * 16 + 2 * j + 1]));
+              l2[j & 1] = fma2(p, unit2, l2[j & 1]);
+              float a0, a1;
+              unpack2(mul2(p, w2), a0, a1);
+              hp[e * 8 + j] = half2_of(a0, a1);
             }
-            const uint32_t at = sw128(r, g * 32 + e * 16);
-            *reinterpret_cast<uint4 *>(pb + at) = make_uint4(p1[0], p1[1], p1[2], p1[3]);
-            *reinterpret_cast<uint4 *>(pb + C::kPBlock + at) = make_uint4(p2[0], p2[1], p2[2], p2[3]);
           }
+          tmem_st16_async(tmem + C::kACol + u * C::kACols + g * 16 + lane_off, hp);
         }
-        if (part && g == 0) {
-          const int pos = t * kSub + r;  // here a lane has a key
-          const bool gone = meta[i % kMeta][r / kPage].y < 0.f || pos >= sg.nkeys;
-          ok = void_rows(seg, i, i0 + n, gone, !gone && pos < sg.L, 0) && ok;
-        }
-        fence_proxy_async();  // P and V (generic writes) -> visible to the tensor cores
+        tmem_wait_st();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive1(&pfull[u]);
@@ -1083,28 +1146,25 @@ __global__ void __launch_bounds__(Cfg<D, RT>::kThreads, 1)
         s_abort = 1;
         break;
       }
-      const bool whole = sg.t0 == 0 && sg.t1 == sg.nt, nan = s_nan[seg & 1] != 0;
-      if (tid == 0) s_nan[(seg + 1) & 1] = 0;
+      const bool whole = sg.t0 == 0 && sg.t1 == sg.nt, nan = s_nan[seg & 3] != 0;
+      if (tid == 0) s_nan[(seg + 2) & 3] = 0;
       if (some) {
         const int slot = blockIdx.x * 2 + (sg.t0 > 0 ? 0 : 1);
         const float L = __fadd_rn(__fadd_rn(red[0][r], red[1][r]), __fadd_rn(red[2][r], red[3][r]));
-        const float factor = L == 0.f ? 0.f : (whole ? 1.f / L : 1.f);
+        const float factor = L == 0.f ? 0.f : (whole ? 1.f / L : 1.f) * kSumUnit;
         const int64_t orow = (static_cast<int64_t>(sg.b) * a.Nq + qi) * a.Hq + sg.hk * a.group + (row - qi * a.group);
         if (live && g == 0) {
           if (!whole)
             a.part_ml[slot * RT + r] = make_float2(m, L);
           else if (a.lse)
-            a.lse[orow] = L == 0.f ? NEG_INF : (m - kBias + log2f(L)) * 0.69314718055994531f;
+            a.lse[orow] = L == 0.f ? NEG_INF : (m - kSumBias + log2f(L)) * 0.69314718055994531f;
         }
 #pragma unroll 1
         for (int j0 = 0; j0 < D / 4; j0 += 16) {
-          float o[16], o2[16];
-          tmem_ld16_async(tO + j0, o);
-          tmem_ld16_async(tO + D + j0, o2);
-          tmem_wait16(o);
-          tmem_wait16(o2);
+          float o[16];
+          tmem_ld16(tO + j0, o);
 #pragma unroll
-          for (int j = 0; j < 16; ++j) o[j] = fmaf(o2[j], 0.03125f, o[j]) * factor;
+          for (int j = 0; j < 16; ++j) o[j] *= factor;
           if (!live) continue;
           const int e0 = g * (D / 4) + j0;
           if (nan) {
@@ -1154,8 +1214,8 @@ __global__ void __launch_bounds__(Cfg<D, RT>::kThreads, 1)
     bool dead = false;
     bool more = sg.first(a, piece);
     if (more) {
-      prepare(sg, 0, warp, C::kSoftWarps + 1, 10);
-      bar_sync(10, (C::kSoftWarps + 1) * 32);
+      prepare(sg, 0, warp, C::kSoftWarps + 4, 10);
+      bar_sync(10, (C::kSoftWarps + 4) * 32);
     }
     for (; more; more = sg.step(a), ++seg) {
       const int buf = seg & 1, n = sg.t1 - sg.t0;
@@ -1288,55 +1348,35 @@ __global__ void __launch_bounds__(Cfg<D, RT>::kThreads, 1)
             if (moved) {
 #pragma unroll
               for (int j = 0; j < CG / 2; ++j) l2[j] = mul2(l2[j], pack2(s_f[col + 2 * j], s_f[col + 2 * j + 1]));
-#pragma unroll 1
-              for (int term = 0; term < 2; ++term) {
-                float o[CG];
-                tmem_ld16(tO + term * RT, o);
+              float o[CG];
+              tmem_ld16(tO, o);
 #pragma unroll
-                for (int j = 0; j < CG; ++j) o[j] *= s_f[col + j];
-                tmem_st16(tO + term * RT, o);
-              }
+              for (int j = 0; j < CG; ++j) o[j] *= s_f[col + j];
+              tmem_st16(tO, o);
             }
           }
         }
         if (dead) break;
         begin = false;
         // the P buffer is free: S of this tile was issued behind P V of tile i - NB
+        const uint64_t unit2 = pack2(kSumUnit, kSumUnit);
 #pragma unroll
         for (int h = 0; h < KT; ++h) {
-          uint8_t *const pb = smem + C::kP + (u * KT + h) * C::kPBuf;
           const uint64_t w2 = pack2(wv[h], wv[h]);
-          uint32_t p1[4], p2[4];
+          uint32_t hp[CG / 2];
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            uint16_t e1[2], e2[2];
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-              const int j = q * 4 + x * 2;
-              const uint64_t p = pack2(ex2(y[h][j]), ex2(y[h][j + 1]));
-              l2[j / 2] = add2(l2[j / 2], p);
-              float a0, a1;
-              unpack2(mul2(p, w2), a0, a1);
-              const uint32_t hp = half2_of(a0, a1);
-              e1[x] = e4m3_of_half2(hp);
-              // 32 (p - p1) in halves: exact (p is at most 2^8, the difference has at most 11 bits)
-              e2[x] = e4m3_of_half2(hfma2(e4m3_to_half2(e1[x]), 0xD000D000u, hmul2(hp, 0x50005000u)));
-            }
-            p1[q] = pack16(e1[0], e1[1]);
-            p2[q] = pack16(e2[0], e2[1]);
+          for (int j = 0; j < CG / 2; ++j) {
+            const uint64_t p = pack2(ex2(y[h][2 * j]), ex2(y[h][2 * j + 1]));
+            l2[j] = fma2(p, unit2, l2[j]);
+            float a0, a1;
+            unpack2(mul2(p, w2), a0, a1);
+            hp[j] = half2_of(a0, a1);
           }
-          // places along N: p1 of the group's rows, then p2
-          *reinterpret_cast<uint4 *>(pb + sw128(tg, col)) = make_uint4(p1[0], p1[1], p1[2], p1[3]);
-          *reinterpret_cast<uint4 *>(pb + sw128(tg, RT + col)) = make_uint4(p2[0], p2[1], p2[2], p2[3]);
+          uint8_t *const pb = smem + C::kH + u * C::kHBuf + h * C::kBlock;
+          *reinterpret_cast<uint4 *>(pb + sw128(tg, col * 2)) = make_uint4(hp[0], hp[1], hp[2], hp[3]);
+          *reinterpret_cast<uint4 *>(pb + sw128(tg, col * 2 + 16)) = make_uint4(hp[4], hp[5], hp[6], hp[7]);
         }
-        if (part && g == 0) {
-#pragma unroll 1
-          for (int h = 0; h < KT; ++h) {
-            const bool gone = h ? hidden[1] : hidden[0];
-            ok = void_rows(seg, i, i0 + n, gone, !gone && t * C::kKeys + h * kSub + tg < sg.L, h) && ok;
-          }
-        }
-        fence_proxy_async();  // P and V (generic writes) -> visible to the tensor cores
+        fence_proxy_async();  // P (generic writes) -> visible to the tensor cores
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive1(&pfull[u]);
@@ -1359,22 +1399,22 @@ __global__ void __launch_bounds__(Cfg<D, RT>::kThreads, 1)
       }
       const bool whole = sg.t0 == 0 && sg.t1 == sg.nt;
       const int slot = blockIdx.x * 2 + (sg.t0 > 0 ? 0 : 1);
-      if (tid == 0) s_nan[(seg + 1) & 1] = 0;
+      if (tid == 0) s_nan[(seg + 2) & 3] = 0;
       for (int r = tid; r < RT; r += kSoftThreads) {
         const float M = s_m[r], L = __fadd_rn(__fadd_rn(red[0][r], red[1][r]), __fadd_rn(red[2][r], red[3][r]));
-        s_f[r] = L == 0.f ? 0.f : (whole ? 1.f / L : 1.f);
+        s_f[r] = L == 0.f ? 0.f : (whole ? 1.f / L : 1.f) * kSumUnit;
         const int row = mt * RT + r;
         if (row < a.nrows) {
           if (!whole) a.part_ml[slot * RT + r] = make_float2(M, L);
           else if (a.lse) {
             const int qi = static_cast<int>((row * a.group_magic) >> 16), head = hk * a.group + (row - qi * a.group);
             a.lse[(static_cast<int64_t>(sg.b) * a.Nq + qi) * a.Hq + head] =
-                L == 0.f ? NEG_INF : (M - kBias + log2f(L)) * 0.69314718055994531f;
+                L == 0.f ? NEG_INF : (M - kSumBias + log2f(L)) * 0.69314718055994531f;
           }
         }
       }
       bar_sync(9, kSoftThreads);
-      const bool nan = s_nan[seg & 1] != 0;
+      const bool nan = s_nan[seg & 3] != 0;
       // four rows at a time; at d = 64 the upper 64 lanes of O repeat the lower ones and take half of the rows
       constexpr int kShares = C::kGroups * (128 / D);
       const int share = D == 128 ? g : g * 2 + (wg >> 1), el = tg & (D - 1);
@@ -1383,11 +1423,10 @@ __global__ void __launch_bounds__(Cfg<D, RT>::kThreads, 1)
       for (int j0 = share * 4; j0 < RT; j0 += kShares * 4) {
         const int r0 = mt * RT + j0;
         if (r0 >= a.nrows) break;
-        float o[4], o2[4];
-        const uint32_t at = tmem + C::kOCol + j0 + lane_off;
-        tmem_ld4(at, o, at + RT, o2);
+        float o[4];
+        tmem_ld4(tmem + C::kOCol + j0 + lane_off, o);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) o[j] = fmaf(o2[j], 0.03125f, o[j]) * s_f[j0 + j];
+        for (int j = 0; j < 4; ++j) o[j] *= s_f[j0 + j];
         if (nan) {
           // tree nodes of this segment whose v holds NaN at this thread's element
           const int from = sg.t0 * C::kKeys - sg.L, to = min(sg.nkeys, sg.t1 * C::kKeys) - sg.L;
@@ -1438,7 +1477,7 @@ __global__ void __launch_bounds__(Cfg<D, RT>::kThreads, 1)
   if (s_abort && tid == 0) atomicOr(a.status, kFlagWaitTimeout);
   if (warp == C::kMmaWarp) {
     tc_fence_after();
-    tmem_dealloc(tmem, C::kTmem);
+    tmem_dealloc(tmem, 512);
   }
 }
 
@@ -1481,7 +1520,7 @@ __global__ void __launch_bounds__(256) k_attn_q8_merge(const __grid_constant__ A
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(b2) : "f"(acc[e + 1] * inv), "f"(acc[e] * inv));
     dst[e / 2] = b2;
   }
-  if (a.lse && lane == 0) a.lse[orow] = l == 0.f ? NEG_INF : (M - kBias + log2f(l)) * 0.69314718055994531f;
+  if (a.lse && lane == 0) a.lse[orow] = l == 0.f ? NEG_INF : (M - kSumBias + log2f(l)) * 0.69314718055994531f;
 }
 
 }  // namespace q8
