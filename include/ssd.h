@@ -578,7 +578,8 @@ ssd_status_t ssd_tree_rope(const void *q, int64_t q_seq_stride, int64_t q_tok_st
  * row (b, i, h) at base + b*seq_stride + i*tok_stride + h*d (strides in
  * elements, multiples of 8; 16-byte aligned bases).  count [B] int32 (or
  * NULL: S): rows i >= count[b] are not written (a padded batch); a count
- * outside [0, S] is clamped and sets BAD_PREFIX.  Per block and head
+ * outside [0, S] is clamped and sets BAD_PREFIX; of a sequence with count 0 no
+ * block is read, written or reported.  Per block and head
  *   need = the smallest power of two s >= 2^-100 with max|finite new rows| <= 448 s,
  *   scale' = max(scale, need) if the block holds rows before the new ones
  *            (positions below prefix_len[b] + node0), else need;

@@ -85,7 +85,7 @@ __global__ void __launch_bounds__(kThreads) k_kv_append_q8(const __grid_constant
   const int64_t first = static_cast<int64_t>(L) + a.node0;  // position of row 0
   const int64_t page = first / kPage + win;
   const int64_t rel0 = page * kPage - first;  // row at the block's first position (negative: older positions)
-  if (rel0 >= count) {
+  if (count == 0 || rel0 >= count) {  // no new row here
     if (lane == 0 && flags && win == 0) atomicOr(a.status, flags);
     return;
   }
