@@ -505,6 +505,10 @@ ssd_status_t ssd_fallback_plan(const float *p_hit, const float *e_hit, int B, do
  * k_scale, v_scale [num_blocks, Hkv] fp32: a code c of block n and head h
  * stands for c * scale[n, h].  Scales are finite and >= 0; the ones that
  * ssd_kv_append_q8 writes are powers of two.
+ * A length or prefix_len of -1 is a slot of a fixed batch without a request
+ * (a finished one): the tables take its blocks back, rope and append leave its
+ * rows and its blocks alone, attention writes 0 and lse = -inf, and nothing
+ * about it is reported, whatever its other arguments hold.
  *
  * ssd_block_table_update: the block tables of B sequences grown or shrunk to
  * given lengths without a host round trip: room for a tree's nodes before a
@@ -559,7 +563,7 @@ ssd_status_t ssd_block_table_update(const int32_t *len, int reserve, int B, int3
  * with strides of their own; an output may be its input (same address and
  * strides), any other overlap is not allowed.  Hkv = 0 (k NULL) or Hq = 0 (q
  * NULL) leaves that operand out.  turns: DEVICE uint64[rot/2].  The angle is
- * reduced exactly, the rotation is fp32, rounded once.  A negative prefix counts
+ * reduced exactly, the rotation is fp32, rounded once.  A prefix below -1 counts
  * as 0 (BAD_PREFIX); a parent outside [-1, m-1] ends the path (BAD_TREE).
  * rot even, 2 <= rot <= d <= 512; node0 + S <= N <= 128 with a tree.
  */

@@ -316,13 +316,16 @@ struct Args {
 };
 
 SSD_DEV int keys_of(const Args &a, int b, int &L) {
-  L = max(a.prefix_len[b], 0);
+  const int prefix = a.prefix_len[b];
+  L = max(prefix, 0);
+  if (prefix == -1) return 0;  // a slot without a request
   const int64_t n = min(static_cast<int64_t>(L) + a.N, static_cast<int64_t>(a.maxb) * kPage);
   return static_cast<int>(min(n, static_cast<int64_t>(0x7fffffff - 2 * kSub)));
 }
+SSD_DEV int tiles_of(const Args &a, int nkeys) { return max(1, (nkeys + a.keys - 1) / a.keys); }
 SSD_DEV int units_of(const Args &a, int b) {  // of an item
   int L;
-  return (keys_of(a, b, L) + a.keys - 1) / a.keys + kEnd;
+  return tiles_of(a, keys_of(a, b, L)) + kEnd;
 }
 
 SSD_DEV long long quotient(long long x, int y) {  // x >= 0, y > 0; a 64-bit division takes ten times a 32-bit one's time
@@ -344,7 +347,7 @@ struct Segments {
   int b, hk, mt, nt, nkeys, L, t0, t1, left;
   SSD_DEV void sequence(const Args &a) {
     nkeys = keys_of(a, b, L);
-    nt = (nkeys + a.keys - 1) / a.keys;
+    nt = tiles_of(a, nkeys);
   }
   SSD_DEV bool first(const Args &a, const Piece &p) {
     if (p.left <= 0) return false;
@@ -468,12 +471,12 @@ __device__ __noinline__ void prepare_rows(const Args &a, const Segments sg, uint
   };
   uint4 x[V], next[V];
   fetch(w * 8 + (lane >> 2), x);
-  const bool tree = static_cast<int64_t>(sg.t1) * C::kKeys > sg.L;
+  const bool tree = sg.nkeys > 0 && static_cast<int64_t>(sg.t1) * C::kKeys > sg.L;
   if (tree)
     for (int m = w * 32 + lane; m < a.N; m += n * 32) par[m] = a.parent[static_cast<int64_t>(sg.b) * a.N + m];
   if (w == 0 && lane == 0) {
     const int L = a.prefix_len[sg.b];
-    if (L < 0 || static_cast<int64_t>(L) + a.N > static_cast<int64_t>(a.maxb) * kPage)
+    if (L < -1 || (L >= 0 && static_cast<int64_t>(L) + a.N > static_cast<int64_t>(a.maxb) * kPage))
       atomicOr(a.status, kFlagBadPrefix);
   }
   bar_sync(bar, n * 32);

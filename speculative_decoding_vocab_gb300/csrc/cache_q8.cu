@@ -79,7 +79,7 @@ __global__ void __launch_bounds__(kThreads) k_kv_append_q8(const __grid_constant
     if (c != count) flags |= kFlagBadPrefix;
   }
   if (L < 0) {
-    if (lane == 0 && win == 0) atomicOr(a.status, flags | kFlagBadPrefix);
+    if (L != -1 && lane == 0 && win == 0) atomicOr(a.status, flags | kFlagBadPrefix);  // -1: a slot without a request
     return;
   }
   const int64_t first = static_cast<int64_t>(L) + a.node0;  // position of row 0

@@ -157,6 +157,7 @@ __global__ void __launch_bounds__(kThreads) k_tree_rope(RopeArgs a) {
   Unit unit;
   if (tid < total) load(tid, unit);
   const int L = a.prefix_len[b];
+  if (L == -1) return;  // a slot without a request
   int64_t pos = static_cast<int64_t>(max(L, 0));
   if (L < 0 && tid == 0) atomicOr(a.status, kFlagBadPrefix);
   if (a.parent) {

@@ -46,3 +46,55 @@ def test_append_leaves_empty_sequences_alone(d):
         for got, want in zip(g, (codes[0], codes[1], scale[0], scale[1])):
             np.testing.assert_array_equal(got.cpu().numpy(), want)
         assert int(status.item()) == flags
+
+
+@pytest.mark.parametrize("d,Hq,Hkv,chains", [(64, 8, 2, 3), (128, 16, 1, 6)], ids=["32-rows", "112-rows"])
+def test_step_with_finished_requests(d, Hq, Hkv, chains):
+    """A fixed batch of which two requests have ended (length and prefix -1; their table rows, tree and queries hold
+    anything): the step's calls leave them out without a flag, and the others get what they get alone."""
+    rng = np.random.default_rng(d)
+    B, N, nb, maxb, idle = 5, 1 + chains, 60, 12, [1, 4]
+    live = [b for b in range(B) if b not in idle]
+    lengths = np.array([33, 70, 5, 150, 16], np.int32)
+    g = dict(table=torch.full((B, maxb), -1, dtype=torch.int32, device="cuda"),
+             pages=torch.zeros(B, dtype=torch.int32, device="cuda"), ring=torch.arange(nb, dtype=torch.int32, device="cuda"),
+             pool=torch.tensor([0, nb, 0, 0], dtype=torch.int32, device="cuda"))
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    slots = torch.empty(B, N, dtype=torch.int32, device="cuda")
+
+    def tables(length, reserve, s=None):
+        ssd.ssd_block_table_update(dev(length), reserve, g["table"], g["pages"], g["ring"], g["pool"], slots=s, status=status)
+    tables(lengths, N)
+    lengths[idle] = -1
+    for _ in range(2):  # the round in which they end, and the next
+        tables(lengths, N, slots)
+        assert (g["table"][idle] == -1).all() and (slots[idle] == -1).all()
+    codes = rng.integers(0, 0x7F, (2, nb, Hkv, 16, d)).astype(np.uint8)
+    scale = (2.0 ** rng.integers(-8, -4, (2, nb, Hkv))).astype(np.float32)
+    parent = np.zeros((B, N), np.int32)
+    parent[:, 0] = -1
+    parent[idle] = 999
+    x = torch.as_tensor(rng.standard_normal((B, N, Hq + 2 * Hkv, d)).astype(np.float32)).to(torch.bfloat16).cuda()
+    x[idle, :, :Hq] = math.nan
+    turns = ssd.ssd_rope_frequencies(d)[0].cuda()
+
+    def step(sel):
+        t, prefix, par = g["table"][sel].contiguous(), dev(lengths[sel]), dev(parent[sel])
+        y = x[sel].contiguous()
+        q, k, v = y[:, :, :Hq], y[:, :, Hq:Hq + Hkv], y[:, :, Hq + Hkv:]
+        qo, ko = torch.full((len(sel), N, Hq, d), 7.0, dtype=torch.bfloat16, device="cuda"), torch.full(
+            (len(sel), N, Hkv, d), 7.0, dtype=torch.bfloat16, device="cuda")
+        c = [dev(codes[0]), dev(codes[1]), dev(scale[0]), dev(scale[1])]
+        out, lse = torch.full_like(qo, 7.0), torch.full((len(sel), N, Hq), 7.0, device="cuda")
+        ssd.ssd_tree_rope(q, k, turns, d, prefix, qo, ko, parent=par, status=status)
+        ssd.ssd_kv_append_q8(ko, v, *c, t, prefix, 0, status=status)
+        ssd.ssd_branch_attention_q8(qo, *c, t, prefix, par, out, lse=lse, status=status)
+        return qo, ko, out, lse, c
+    whole, alone = step(list(range(B))), step(live)
+    for a, b in zip(whole[:4], alone[:4]):
+        assert torch.equal(a[live], b)
+    for a, b in zip(whole[4], alone[4]):
+        assert torch.equal(a, b)
+    assert (whole[0][idle] == 7).all() and (whole[1][idle] == 7).all()
+    assert (whole[2][idle] == 0).all() and (whole[3][idle] == -math.inf).all()
+    assert int(status.item()) == 0
