@@ -498,8 +498,17 @@ def _dense(x, dtype, shape, dev, what):
     return x.data_ptr()
 
 
+def _overlap(B, S, a, b, n):
+    """Whether two of the runs of n elements that start at i a + j b (i < B, j < S) meet."""
+    starts = sorted(i * a + j * b for i in range(B) for j in range(S))
+    return any(y - x < n for x, y in zip(starts, starts[1:]))
+
+
 def _rows(x, y, dtype, lead, dev, what):
-    """Addresses and (sequence, token) strides of [B, S, H, d] rows x and their output y, whose heads are dense."""
+    """Addresses and (sequence, token) strides of [B, S, H, d] rows x and their output y, whose heads are dense;
+    an output's tokens do not overlap."""
+    if y is None:
+        raise ValueError(f"{what}_out is missing")
     shape = x.shape
     B, S, H, d = shape
     a, b, h, e = x.stride()
@@ -514,6 +523,9 @@ def _rows(x, y, dtype, lead, dev, what):
         a = ya = 0
     if S == 1:
         b = yb = 0
+    n = H * d  # of a token
+    if ((yb < n and S > 1) or (ya < (S - 1) * yb + n and B > 1)) and _overlap(B, S, ya, yb, n):
+        raise ValueError(f"{what}_out: the tokens of an output must not overlap, got strides {y.stride()}")
     return x.data_ptr(), a, b, y.data_ptr(), ya, yb
 
 
