@@ -213,16 +213,17 @@ extern "C" ssd_status_t ssd_rope_frequencies(int rot, double base, double factor
   // the (fractional) pair that turns r times in original_len positions
   auto pair_of = [&](double r) { return rot * std::log(original_len / (r * tau)) / (2.0 * std::log(base)); };
   double lo = 0.0, hi = 0.0;
-  if (parts) {
+  const bool ramped = parts && pair_of(slow) > 0.0;
+  if (ramped) {
     lo = std::fmax(std::floor(pair_of(fast)), 0.0);
     hi = std::fmin(std::ceil(pair_of(slow)), rot - 1.0);
   }
   for (int i = 0; i < rot / 2; ++i) {
     double theta = std::pow(base, -2.0 * i / rot);
-    if (parts) {
+    if (ramped) {
       const double ramp = std::fmin(std::fmax((i - lo) / std::fmax(hi - lo, 1e-3), 0.0), 1.0);
       theta = theta / factor * ramp + theta * (1.0 - ramp);
-    } else {
+    } else {  // without parts, or no pair turns `slow` times
       theta /= factor;
     }
     turns[i] = static_cast<uint64_t>(std::nearbyint(theta / tau * 18446744073709551616.0));

@@ -46,3 +46,13 @@ def test_outputs_that_do_not_overlap_are_taken(shape, stride):
     q = torch.zeros(4096, dtype=bf).as_strided(shape, (0, 0, 64, 1))  # inputs may be broadcast
     with pytest.raises(ValueError, match="CUDA device"):
         call(q, torch.zeros(4096, dtype=bf).as_strided(shape, stride))
+
+
+@pytest.mark.parametrize("original", [1.0, 4.0, 6.0])
+def test_frequencies_below_the_slow_border(original):
+    """A context in which not even the fastest pair turns `slow` times: every pair is divided by the factor."""
+    from speculative_decoding_vocab_gb300 import build
+    build.build()
+    turns, m = ssd.ssd_rope_frequencies(64, 10000.0, 4.0, original)
+    whole, _ = ssd.ssd_rope_frequencies(64, 10000.0, 4.0)
+    assert torch.equal(turns, whole) and m > 1
