@@ -173,7 +173,7 @@ __global__ void __launch_bounds__(kThreads) k_tree_rope(RopeArgs a) {
       m = up;
     }
   } else {
-    pos += a.node0 + i;
+    pos += static_cast<int64_t>(a.node0) + i;
   }
   for (int j = tid; j < half; j += nt) {
     const uint64_t t = static_cast<uint64_t>(pos) * a.turns[j];

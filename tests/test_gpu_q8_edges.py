@@ -98,3 +98,21 @@ def test_step_with_finished_requests(d, Hq, Hkv, chains):
     assert (whole[0][idle] == 7).all() and (whole[1][idle] == 7).all()
     assert (whole[2][idle] == 0).all() and (whole[3][idle] == -math.inf).all()
     assert int(status.item()) == 0
+
+
+def test_rope_chain_behind_the_largest_node():
+    """A chain's node numbers pass 32 bits with the tokens: positions go on."""
+    S, d, node0 = 5, 64, 2 ** 31 - 3
+    x = torch.as_tensor(np.random.default_rng(1).standard_normal((1, S, 2, d)).astype(np.float32)).cuda()
+    turns = ssd.ssd_rope_frequencies(d)[0]
+    out, status = torch.empty_like(x), torch.zeros(1, dtype=torch.int32, device="cuda")
+    ssd.ssd_tree_rope(x, None, turns.cuda(), d, dev(np.array([9], np.int32)), out, None, node0=node0, status=status)
+    frac = np.array([[((9 + node0 + s) * int(t)) % 2 ** 64 / 2 ** 64 for t in turns.tolist()] for s in range(S)])
+    z = np.exp(2j * math.pi * frac)[None, :, None]
+    y = x.cpu().numpy().astype(np.float64)
+    w = (y[..., :32] + 1j * y[..., 32:]) * z
+    want = np.concatenate([w.real, w.imag], -1)
+    # the angle in half-turns rounded to 24 bits, sincospi, two products and a sum: below 2^-20 (|a| + |b|)
+    tol = 2.0 ** -20 * np.tile(np.abs(y[..., :32]) + np.abs(y[..., 32:]), 2)
+    assert (np.abs(out.cpu().numpy() - want) <= tol).all()
+    assert int(status.item()) == 0
