@@ -12,9 +12,9 @@
 //                 rot/2 rotations once for all Hq + Hkv heads.
 // Bound by HBM: every element is read and written once.  64 + 8 heads of 128
 // with 64 rotated, 16396 tokens (604 MB): 104 us, 5.8 TB/s (128 us
-// when the pieces were asked for after the rotations); 2 or 4 pieces per thread
-// at a time 107 and 110 us (fewer threads fit).  A decode step of 256 tokens:
-// 3 us, two dependent reads and a launch.
+// when the pieces were asked for after the rotations; with 2 or 4 pieces per thread
+// at a time 3 and 6 us more).  A decode step of 256 tokens: 2.9 us, two dependent
+// reads and a launch.
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
@@ -28,7 +28,9 @@ namespace {
 
 using namespace ssd;
 
-constexpr int kThreads = 192;  // at most; 128, 256, 384 and 640 threads: 99, 103, 108, 125 us for the prompts below
+// At most.  96, 128, 160, 192, 256 threads: the prompts above 102.9, 102.1, 103.6, 103.7, 104.7 us; in fp32, 3075 tokens
+// of 40 heads, 18.7, 19.4, 18.3, 18.3, 18.8 us; the decode step 3.2, 3.2, 2.9, 2.9, 2.9 us.
+constexpr int kThreads = 192;
 constexpr int kMaxNodes = 128;
 constexpr int kMaxD = 512;
 
