@@ -592,6 +592,11 @@ ssd_status_t ssd_tree_rope(const void *q, int64_t q_seq_stride, int64_t q_tok_st
  *   rows before the new ones: code = e4m3(code * scale / scale') when the
  *            scale grew (exact for powers of two but for underflow);
  *   rows behind the new ones: left as they were (their values are void).
+ * So while a block holds rows its scale only grows, and rows that were rejected
+ * since have had their say in it: one large element of a draft that is thrown
+ * away leaves the accepted rows of its block rounded to multiples of 2^-9 of
+ * the grown scale, and an append in two steps may round twice what one step
+ * rounds once.  Rows of normal codes at the grown scale keep their values.
  * BAD_PREFIX and BAD_BLOCK as in ssd_kv_append.  d in {64, 128}.  The blocks
  * that one call writes are distinct (a block belongs to one sequence).
  */

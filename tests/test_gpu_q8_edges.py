@@ -116,3 +116,37 @@ def test_rope_chain_behind_the_largest_node():
     tol = 2.0 ** -20 * np.tile(np.abs(y[..., :32]) + np.abs(y[..., 32:]), 2)
     assert (np.abs(out.cpu().numpy() - want) <= tol).all()
     assert int(status.item()) == 0
+
+
+@pytest.mark.parametrize("grow", [3, 8, 14])
+def test_append_after_a_rejected_row(grow):
+    """A row that is large by 2^grow is appended behind accepted rows, rejected, and written over by a small one: the
+    block keeps the grown scale, and its accepted rows are what rounding them to that scale leaves: unchanged while they
+    are e4m3's normal values there (2^-6 of the scale and more), else off by up to 2^-10 of it."""
+    rng = np.random.default_rng(grow)
+    H, d = 2, 64
+    rows = rng.uniform(0.25, 1, (1, 6, H, d)).astype(np.float32) * np.where(rng.random((1, 6, H, d)) < 0.5, -1, 1)
+    rows[0, 0, :, 0] = 1.75   # the scale: 448 = 1.75 * 2^8
+    x = torch.as_tensor(rows).to(torch.bfloat16)
+    big = (x[:, :1].float() * 2.0 ** grow).to(torch.bfloat16)
+    table, status = dev(np.array([[1]], np.int32)), torch.zeros(1, dtype=torch.int32, device="cuda")
+    c = [torch.zeros(2, H, 16, d, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    s = [torch.zeros(2, H, device="cuda") for _ in range(2)]
+
+    def append(rows, at):
+        y = rows.cuda()
+        ssd.ssd_kv_append_q8(y, y, *c, *s, table, dev(np.array([at], np.int32)), 0, status=status)
+    append(x[:, :5], 0)
+    before = ref.VALUES[c[0][1].cpu().numpy()][:, :5]
+    assert (s[0][1] == 2.0 ** -8).all()
+    append(big, 5)                # the draft
+    append(x[:, 5:], 5)           # it was rejected: the accepted token takes its place
+    assert int(status.item()) == 0
+    scale = 2.0 ** (grow - 8)
+    assert (s[0][1] == scale).all() and (s[1][1] == scale).all()
+    was, now = before * 2.0 ** -8, ref.VALUES[c[0][1].cpu().numpy()][:, :5] * scale
+    normal = np.abs(was) >= 2.0 ** -6 * scale
+    np.testing.assert_array_equal(now[normal], was[normal])
+    assert (np.abs(now - was) <= 2.0 ** -10 * scale).all()
+    assert normal.all() == (grow <= 12) and ((now == was).mean() < 0.6) == (grow > 12)
+    np.testing.assert_array_equal(c[0].cpu().numpy(), c[1].cpu().numpy())
