@@ -740,7 +740,7 @@ __global__ void __launch_bounds__(Cfg<D, RT>::kThreads, 1)
           const float v = vs < kMinBlockScale ? 0.f : vs;
           const int at = i + lane / kPages;
           meta[at % kMeta][pw * kPages + page] =
-              blk >= 0 ? make_float4(ks * a.scale_log2, v, __log2f(fmaxf(v, kMinBlockScale)), 0.f)
+              blk >= 0 ? make_float4(fminf(ks * a.scale_log2, 3e38f), v, __log2f(fmaxf(v, kMinBlockScale)), 0.f)
                        : make_float4(0.f, -1.f, 0.f, 0.f);
           s_ids[pw][at % kIds][page] = blk;
           if (page == 0) s_row[pw][at % kIds] = hk * kPage;

@@ -150,3 +150,26 @@ def test_append_after_a_rejected_row(grow):
     assert (np.abs(now - was) <= 2.0 ** -10 * scale).all()
     assert normal.all() == (grow <= 12) and ((now == was).mean() < 0.6) == (grow > 12)
     np.testing.assert_array_equal(c[0].cpu().numpy(), c[1].cpu().numpy())
+
+
+@pytest.mark.parametrize("Nq", [2, 5], ids=["32-rows", "80-rows"])
+@pytest.mark.parametrize("d", [64, 128])
+def test_attention_scale_at_the_end_of_fp32(d, Nq):
+    """A key scale near fp32's largest: a query of zeros has equal scores (0 times a factor past fp32's range is not 0)."""
+    rng = np.random.default_rng(d)
+    L, N, Hq = 90, Nq, 16
+    codes = rng.integers(0, 0x7F, (2, 6, 1, 16, d)).astype(np.uint8)
+    table, parent = np.arange(6, dtype=np.int32)[None], np.arange(-1, N - 1, dtype=np.int32)[None]
+    q = torch.zeros(1, N, Hq, d, dtype=torch.bfloat16, device="cuda")
+    out, lse = torch.empty_like(q), torch.empty(1, N, Hq, device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    ssd.ssd_branch_attention_q8(q, dev(codes[0]), dev(codes[1]), torch.full((6, 1), 3e38, device="cuda"),
+                                torch.full((6, 1), 0.25, device="cuda"), dev(table), dev(np.array([L], np.int32)), dev(parent),
+                                out, lse=lse, scale=2.0, status=status)
+    v = ref.VALUES[codes[1][:, 0].reshape(-1, d)] * 0.25
+    for i in range(N):
+        want = v[:L + i + 1].mean(0)
+        # P to 2^-11, the output to 2^-8, sums to 2^-20
+        assert (np.abs(out[0, i].double().cpu().numpy() - want) <= (2.0 ** -8 + 2.0 ** -10) * want).all()
+        assert (lse[0, i] - math.log(L + i + 1)).abs().max() <= 2.0 ** -18
+    assert int(status.item()) == 0
