@@ -56,3 +56,19 @@ def test_frequencies_below_the_slow_border(original):
     turns, m = ssd.ssd_rope_frequencies(64, 10000.0, 4.0, original)
     whole, _ = ssd.ssd_rope_frequencies(64, 10000.0, 4.0)
     assert torch.equal(turns, whole) and m > 1
+
+
+def test_binding_without_torchs_short_ways(monkeypatch):
+    """The binding loads, and finds stream and device, where torch does not have the private calls that it prefers."""
+    import importlib.util
+
+    class Stream:
+        cuda_stream = 77
+    for name in ("_cuda_getCurrentRawStream", "_cuda_getDevice"):
+        monkeypatch.delattr(torch._C, name, raising=False)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda dev: Stream)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 3)
+    spec = importlib.util.spec_from_file_location("speculative_decoding_vocab_gb300.binding_again", ssd.__file__)
+    again = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(again)
+    assert again._raw_stream(0) == 77 and again._current_device() == 3
