@@ -50,8 +50,8 @@
 // take together does not fit the SM's instruction cache: smaller code is
 // faster code here (loops that are not the softmax warps' are rolled).
 // 64 sequences of 8192 keys, 8 KV heads of 128 with 6 queries of 8 heads each
-// (1.08 GB): 194 us, 5.6 TB/s.  Ragged batch of 48 sequences up to 16384 keys, 64 rows
-// (411 MB): 98 us, 4.2 TB/s.  One sequence, 100003 keys, one query (205 MB): 44 us,
+// (1.08 GB): 191 us, 5.7 TB/s.  Ragged batch of 48 sequences up to 16384 keys, 64 rows
+// (411 MB): 95 us, 4.3 TB/s.  One sequence, 100003 keys, one query (205 MB): 44 us,
 // of which the set-up, the first tile and the merge take 12.  16 sequences of
 // 2048 keys with 256 rows (d 64): 60 us (66 with P in two e4m3 terms, which
 // two conversions and three packed operations a pair took).
@@ -89,13 +89,14 @@ constexpr int kPages = kSub / kPage;       // 8
 // thousands, and moving m costs about a tile's time.  l sums P / 2^7: with
 // v_scale down to 2^-100, P itself reaches 2^115, and thousands of those pass fp32.
 constexpr float kBias = 11.f, kMoved = 12.f, kGrow = 15.f, kSumUnit = 0x1p-7f, kSumBias = kBias - 7.f;
-// Keys of the smallest piece, and the longest table whose items are not cut: joining costs 3 us.  One query, 8 heads:
-// 2000 keys 14.2 us in pieces of 512, 15.9 of 1024, 17.2 whole; 1000 keys 13.3 in pieces of 512, 12.5 whole.
+// Keys of the smallest piece, and the longest table whose items are not cut: joining costs 2 to 3 us.  One query, 8 heads of
+// 128: 2000 keys 12.3 us in pieces of 512, 15.0 of 1024, 17.0 whole; 1000 keys 12.4 either way; 40 sequences of 900 keys,
+// 2 KV heads, 14.2 whole, 16.7 cut; 4 of 700 keys 11.0 and 12.3.
 constexpr int kMinKeys = 512, kWholeKeys = 1024;
-// An item's end costs its CTA a few tiles' time: O leaves TMEM, the next rows come in, the pipeline drains.  Ragged
-// batch of 1 to 16384 keys: 3: 99 us, 4: 95, 6: 92, 8: 95 (without ends in the split 131); 64 sequences of 100 to
-// 600 keys (draft): 97, 90, 88, 86; equal lengths: within 2%.
-constexpr int kEnd = 6;
+// An item's end costs its CTA a few tiles' time: O leaves TMEM, the next rows come in, the pipeline drains.  3, 4, 6, 8:
+// ragged batch of 1 to 16384 keys 98, 95, 96, 100 us; 256 sequences of up to 600 keys 76, 75, 76, 79; 64 of 100 to 600
+// (draft) 73, 76, 77, 80; equal lengths within 1%.
+constexpr int kEnd = 4;
 constexpr int kSmemBudget = 212 * 1024;
 constexpr int kBatch = 32 / kPages;        // tiles that a producer warp's lanes hold the blocks of
 constexpr int kIds = 4 * kBatch;           // tiles whose block ids are held in shared memory (K runs two tiles ahead of V)
@@ -1039,7 +1040,7 @@ __global__ void __launch_bounds__(Cfg<D, RT>::kThreads, 1)
             }
           }
           float y[32];
-          // y = x - m + 4 (x for a row without m); hidden keys -inf
+          // y = x - m + 11 (x for a row without m); hidden keys -inf
           auto scores = [&]() {
             tmem_ld16_async(tS + u * kSub, y);
             tmem_ld16_async(tS + u * kSub + 16, y + 16);
@@ -1242,15 +1243,15 @@ __global__ void __launch_bounds__(Cfg<D, RT>::kThreads, 1)
         sphase ^= 1u << u;  // the scales were there before K was
         tc_fence_after();
         // this thread's keys: their scales, and the rows that see them
-        float c[KT], wv[KT], lsv[KT];
+        float c[KT];
+        // what is used once a tile is read where it is used: at 64 rows the warps have 80 registers a thread
+        auto scale_of = [&](int h) -> const float4 & { return meta[i % kMeta][h * kPages + tg / kPage]; };
         uint32_t vis[KT];
         bool hidden[KT], part = false;
 #pragma unroll
         for (int h = 0; h < KT; ++h) {
-          const float4 sc = meta[i % kMeta][h * kPages + tg / kPage];
+          const float2 sc = *reinterpret_cast<const float2 *>(&scale_of(h));
           c[h] = sc.x;
-          wv[h] = fmaxf(sc.y, 0.f);
-          lsv[h] = sc.z;
           const int pos = t * C::kKeys + h * kSub + tg;
           hidden[h] = sc.y < 0.f || pos >= sg.nkeys;
           part = part || hidden[h] || pos >= sg.L;
@@ -1274,7 +1275,7 @@ __global__ void __launch_bounds__(Cfg<D, RT>::kThreads, 1)
           }
         }
         float y[KT][CG];
-        // y = x - m + 4 (x for a row without m); hidden keys -inf
+        // y = x - m + 11 (x for a row without m); hidden keys -inf
         auto scores = [&]() {
 #pragma unroll
           for (int h = 0; h < KT; ++h) tmem_ld16_async(tS + (u * KT + h) * RT, y[h]);
@@ -1306,14 +1307,14 @@ __global__ void __launch_bounds__(Cfg<D, RT>::kThreads, 1)
             float t4[4] = {y[h][0], y[h][1], y[h][2], y[h][3]};
 #pragma unroll
             for (int j = 4; j < CG; ++j) t4[j & 3] = fmaxf(t4[j & 3], y[h][j]);
-            top = fmaxf(top, fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3])) + lsv[h]);
+            top = fmaxf(top, fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3])) + scale_of(h).z);
           }
           if (!bar_or(bar, 128, top > kGrow || unset || !ok)) break;
           // the rows' largest log2 of P v_scale (of a row without a key so far: x + log2 v_scale) in this tile
           float big = NEG_INF;
 #pragma unroll
           for (int j = 0; j < CG; ++j) {
-            const float z = warp_top(fmaxf(y[0][j] + lsv[0], y[1][j] + lsv[1]));
+            const float z = warp_top(fmaxf(y[0][j] + scale_of(0).z, y[1][j] + scale_of(1).z));
             if (lane == j) big = z;
           }
           if (lane < CG) red[wg][col + lane] = big;
@@ -1365,7 +1366,8 @@ __global__ void __launch_bounds__(Cfg<D, RT>::kThreads, 1)
         const uint64_t unit2 = pack2(kSumUnit, kSumUnit);
 #pragma unroll
         for (int h = 0; h < KT; ++h) {
-          const uint64_t w2 = pack2(wv[h], wv[h]);
+          const float wv = fmaxf(scale_of(h).y, 0.f);
+          const uint64_t w2 = pack2(wv, wv);
           uint32_t hp[CG / 2];
 #pragma unroll
           for (int j = 0; j < CG / 2; ++j) {
