@@ -18,7 +18,7 @@
 // is subnormal, 2^-36 of the row's largest or less: a key that takes most of a row (an
 // attention sink) does not cost the row the thousands of others.  Two e4m3 terms
 // did: they end 2^-19 below the largest, and with 0.99 of a row on one of 8192
-// keys, its value 0, the output was off by 0.6 of itself.
+// keys, its value 0, the output was off by 0.7 of itself (halves: 0.002).
 // The product takes its A from TMEM, so that is where V^T (or P) goes in halves:
 // byte columns of a V sub-tile by ldmatrix, two codes per conversion, stored in the
 // lanes' fragment order.  With a lane per row P is there and V, as the B, in
@@ -89,17 +89,17 @@ constexpr int kPages = kSub / kPage;       // 8
 // thousands, and moving m costs about a tile's time.  l sums P / 2^7: with
 // v_scale down to 2^-100, P itself reaches 2^115, and thousands of those pass fp32.
 constexpr float kBias = 11.f, kMoved = 12.f, kGrow = 15.f, kSumUnit = 0x1p-7f, kSumBias = kBias - 7.f;
-// Keys of the smallest piece, and the longest table whose items are not cut: joining costs 2 to 3 us.  One query, 8 heads of
-// 128: 2000 keys 12.3 us in pieces of 512, 15.0 of 1024, 17.0 whole; 1000 keys 12.4 either way; 40 sequences of 900 keys,
-// 2 KV heads, 14.2 whole, 16.7 cut; 4 of 700 keys 11.0 and 12.3.
+// Keys of the smallest piece, and the longest table whose items are not cut: joining costs 2 to 3 us.  One query, 8
+// heads of 128: 2000 keys 12.3 us in pieces of 512, 15.0 of 1024, 17.0 whole; 1000 keys 12.4 either way; 40 sequences
+// of 900 keys, 2 KV heads, 14.2 whole, 16.7 cut; 4 of 700 keys 11.0 and 12.3.
 constexpr int kMinKeys = 512, kWholeKeys = 1024;
-// An item's end costs its CTA a few tiles' time: O leaves TMEM, the next rows come in, the pipeline drains.  3, 4, 6, 8:
-// ragged batch of 1 to 16384 keys 98, 95, 96, 100 us; 256 sequences of up to 600 keys 76, 75, 76, 79; 64 of 100 to 600
-// (draft) 73, 76, 77, 80; equal lengths within 1%.
+// An item's end costs its CTA a few tiles' time: O leaves TMEM, the next rows come in, the pipeline drains.  3, 4, 6,
+// 8: ragged batch of 1 to 16384 keys 98, 95, 96, 100 us; 256 sequences of up to 600 keys 76, 75, 76, 79; 64 of 100 to
+// 600 (draft) 73, 76, 77, 80; equal lengths within 1%.
 constexpr int kEnd = 4;
 constexpr int kSmemBudget = 212 * 1024;
 constexpr int kBatch = 32 / kPages;        // tiles that a producer warp's lanes hold the blocks of
-constexpr int kIds = 4 * kBatch;           // tiles whose block ids are held in shared memory (K runs two tiles ahead of V)
+constexpr int kIds = 4 * kBatch;           // tiles whose block ids are held in shared memory (K runs ahead of V)
 
 // D[tmem] (+)= A B of one 32-byte step of K; A and B by the low words of their
 // shared-memory descriptors (the high words are constants)
@@ -219,16 +219,16 @@ SSD_DEV void tmem_st16_async(uint32_t at, const uint32_t *v) {
       "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
       : "memory");
 }
-// 16 TMEM lanes x 16 columns: of columns 8 w .. + 7, lane l holds columns 2 (l % 4) and the next of TMEM lane l / 4 (v[4 w],
-// v[4 w + 1]) and of TMEM lane 8 + l / 4 (v[4 w + 2], v[4 w + 3])
+// 16 TMEM lanes x 16 columns: of columns 8 w .. + 7, lane l holds columns 2 (l % 4) and the next of TMEM lane l / 4
+// (v[4 w], v[4 w + 1]) and of TMEM lane 8 + l / 4 (v[4 w + 2], v[4 w + 3])
 SSD_DEV void tmem_st_16x16(uint32_t at, const uint32_t *v) {
   asm volatile("tcgen05.st.sync.aligned.16x256b.x2.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(at), "r"(v[0]),
                "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
                : "memory");
 }
 SSD_DEV void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-// Two 16 x 16 byte blocks, transposed: lane l gives the address of row l % 16 of block l / 16 and gets bytes 4 (l % 4) .. + 3
-// of columns l / 4 (c[2 b]) and 8 + l / 4 (c[2 b + 1]) of block b: four rows' bytes of one column
+// Two 16 x 16 byte blocks, transposed: lane l gives the address of row l % 16 of block l / 16 and gets bytes
+// 4 (l % 4) .. + 3 of columns l / 4 (c[2 b]) and 8 + l / 4 (c[2 b + 1]) of block b: four rows' bytes of one column
 SSD_DEV void load_columns(uint32_t saddr, uint32_t *c) {
   asm volatile("ldmatrix.sync.aligned.m16n16.x2.trans.shared.b8 {%0, %1, %2, %3}, [%4];"
                : "=r"(c[0]), "=r"(c[1]), "=r"(c[2]), "=r"(c[3])
@@ -414,7 +414,7 @@ struct Cfg {
   static constexpr int kGroups = RT / CG;                  // groups of four warps
   static constexpr int NB = 2;                             // S and P buffers; S runs NB tiles ahead
   static constexpr int kSoftWarps = 4 * kGroups;
-  // helper warps: warp w of the four writes TMEM lanes 32 w .. + 31 (those that a warp with this number modulo 4 reaches)
+  // helper warps: warp w of the four writes TMEM lanes 32 w .. + 31 (those that a warp of its number modulo 4 reaches)
   static constexpr int kHelpWarp = kSoftWarps, kTmaWarp = kHelpWarp + 4, kMmaWarp = kTmaWarp + kTmaWarps;
   static constexpr int kWarps = kMmaWarp + 1;
   static constexpr int kThreads = kWarps * 32;
@@ -430,7 +430,7 @@ struct Cfg {
   static constexpr int kSlots = kFit > 16 ? 16 : kFit;
   static constexpr int kQ = 0, kH = 2 * kQBuf, kRing = kFixed;
   static constexpr int kSmem = kFixed + kSlots * kSlot + 1024;
-  // TMEM: NB x KT x S, O, and at its end P V's other operand in halves: V^T (as many buffers as there is room for), or P
+  // TMEM: NB x KT x S, O, and at its end P V's other operand in halves: V^T (as many buffers as fit), or P
   static constexpr int kOCol = NB * KT * RT, kOCols = kRowLanes ? D : RT;
   static constexpr int kACols = KT * (kSub / 2);           // of a tile
   static constexpr int kABufs = kOCol + kOCols + NB * kACols <= 512 ? NB : 1;
@@ -438,8 +438,9 @@ struct Cfg {
   static constexpr int kMeta = 24 / KT;                    // tiles whose block scales are held
   static_assert(kSmem + 13824 <= 227 * 1024, "shared memory with the static part");
   static_assert(kSlots >= (NB + 1) * KT, "S runs NB tiles ahead");
-  // A producer writes the scales of tiles i .. i + kBatch - 1 before the wait of tile i's K; its load before that waited for
-  // the use of its slot, kSlots + KT sub-tiles further back.  P V of tile i - NB is the last of a tile before K of tile i.
+  // A producer writes the scales of tiles i .. i + kBatch - 1 before the wait of tile i's K; its load before that waited
+  // for the use of its slot, kSlots + KT sub-tiles further back.  P V of tile i - NB is the last of a tile before K of
+  // tile i.
   static_assert(kMeta >= NB + kBatch + (kSlots + KT + 2 * KT - 1) / (2 * KT), "block scales");
   static_assert(!kRowLanes || (RT == 128 && kGroups == 4), "a lane per row, a quarter of the keys per group");
   static_assert(!kRowLanes || kABufs == NB, "P is written while the product before reads its own");

@@ -4,7 +4,8 @@
 // theta_i is held as a 64-bit fraction of a turn, so n theta_i mod one turn is
 // one wrapping integer product: no position, however far, loses angle bits
 // (an fp32 product is off by 0.06 rad at a million positions).  The angle
-// then enters sincospi as half-turns in [-1, 1).
+// then enters sincospi as half-turns in [-1, 1), rounded to 24 bits: at most
+// 2^-25 pi rad, as much as the two products and the sum of an fp32 rotation round.
 //
 //   k_tree_rope   one CTA per token.  Its threads first ask for their pieces of
 //                 the heads; meanwhile they walk the token's ancestors in
