@@ -587,7 +587,7 @@ __global__ void __launch_bounds__(Cfg<D, RT>::kThreads, 1)
   __shared__ int par[2][kMaxNodes];
   __shared__ uint32_t anc[2][kMaxNodes][kMaxNodes / 32];    // per query: the nodes that it sees
   __shared__ float qs[2][RT];                               // row scales 2^e
-  __shared__ __align__(16) float4 rowc[RT / 2];             // two rows: 2^e, 2^e, 4 - m, 4 - m
+  __shared__ __align__(16) float4 rowc[RT / 2];             // two rows: 2^e, 2^e, 11 - m, 11 - m
   __shared__ float s_m[RT], s_f[RT], red[4][RT];
   __shared__ int s_nan[4];                                  // a tree node's v held NaN, by segment mod 4 (the helper
                                                             // warps are in the segment behind the softmax warps' at most)
@@ -1114,7 +1114,7 @@ __global__ void __launch_bounds__(Cfg<D, RT>::kThreads, 1)
           }
           if (dead) break;
           begin = false;
-          // P's and V's buffers are free: S of this tile was issued behind P V of tile i - NB
+          // the P buffer is free: S of this tile was issued behind P V of tile i - NB
           const uint64_t unit2 = pack2(kSumUnit, kSumUnit);
           uint32_t hp[16];
 #pragma unroll

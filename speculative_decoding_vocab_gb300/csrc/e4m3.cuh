@@ -7,8 +7,9 @@
 namespace ssd {
 
 constexpr float kE4m3Max = 448.f;
-// Block scales below this are not written, and count as 0 in values: it leaves
-// the sums of the attention 2^27 of room on either side of fp32's range.
+// Block scales below this are not written, and count as 0 in values: where all of
+// a row's v scales are this small the attention's sums reach 2^108 a key, which
+// leaves 2^19 keys of room in fp32's range.
 constexpr float kMinBlockScale = 0x1p-100f;
 
 // two fp32 -> two codes (nearest even, clamped to +-448; NaN -> 0x7F): lo in the low byte
