@@ -81,7 +81,9 @@ typedef enum { SSD_F32 = 0, SSD_BF16 = 1 } ssd_dtype_t;
                                   /* clamped into [0, 1], taken as 0                        */
 #define SSD_FLAG_BAD_VALUE 512u   /* 8-bit cache: a value that is not finite (stored as NaN), or a block   */
                                   /* scale that is negative or not finite (append: taken as 0; attention:  */
-                                  /* the block's keys are hidden)                                          */
+                                  /* the block's keys are hidden); 4-bit append: a value that is not       */
+                                  /* finite (its group is stored as NaN); log probabilities: a row without */
+                                  /* a distribution                                                        */
 #define SSD_FLAG_NO_BLOCKS 1024u  /* block tables: the free blocks do not suffice; the sequence keeps its  */
                                   /* blocks as they are                                                    */
 
@@ -631,6 +633,101 @@ ssd_status_t ssd_branch_attention_q8(const void *q, const void *k_cache, const v
                                      int Nq, int Hq, int Hkv, int d, float scale, void *out,
                                      float *lse, uint32_t *status, void *ws, size_t ws_bytes,
                                      ssd_stream_t s);
+
+/*
+ * The 4-bit cache of the branch decode
+ * ------------------------------------
+ * The same step with keys and values held in 4 bits, 0.53 of the 8-bit
+ * cache's bytes: e2m1 codes (bit 3 the sign; magnitudes 0, 0.5, 1, 1.5, 2, 3,
+ * 4, 6) with a scale byte b per 32 elements of a token and head, standing for
+ * 2^(b - 127), 255 for NaN.  Every token has scales of its own, so nothing that a
+ * cache holds is rounded again by a later append.  A cache is
+ *   k_cache [num_blocks, Hkv, 16, d/2]: byte (r, j) = elements 2j (low four
+ *           bits) and 2j + 1 of position r,
+ *   v_cache [num_blocks, Hkv, 8, d]: byte (p, e) = element e of positions 2p
+ *           (low four bits) and 2p + 1 (codes lie along the dimension that the
+ *           attention's product sums over),
+ *   k_scale, v_scale [num_blocks, Hkv, 16, d/32] bytes.
+ * Blocks, tables, positions and a prefix_len of -1 are as in the 8-bit calls
+ * (ssd_block_table_update and ssd_tree_rope serve both).  d in {64, 128}.
+ *
+ * ssd_kv_append_q4: the arguments of ssd_kv_append_q8.  Per token, head and
+ * group of 32 elements
+ *   scale = the smallest power of two in [2^-100, 2^125] with max|x| <= 6 scale
+ *           (2^125 where none is: larger values are clamped to 6 scale),
+ *   code  = e2m1(x / scale) to nearest even (the sign of zeros is kept);
+ * a group with a value that is not finite stands for NaN as a whole (byte 255,
+ * codes 0; BAD_VALUE).  Rows i >= count[b], other positions of the block and
+ * their codes in shared bytes stay as they were.  BAD_PREFIX and BAD_BLOCK as
+ * in ssd_kv_append_q8.  The blocks that one call writes are distinct.
+ */
+ssd_status_t ssd_kv_append_q4(const void *k_new, int64_t k_seq_stride, int64_t k_tok_stride,
+                              const void *v_new, int64_t v_seq_stride, int64_t v_tok_stride,
+                              void *k_cache, void *v_cache, uint8_t *k_scale, uint8_t *v_scale,
+                              const int32_t *block_table, int maxb, int64_t num_blocks,
+                              const int32_t *prefix_len, const int32_t *count, int node0, int B,
+                              int S, int Hkv, int d, uint32_t *status, ssd_stream_t s);
+
+/*
+ * ssd_kv_read_q4: rows of the 4-bit cache as values (a prefix moved into the
+ * bf16 cache, a layer that runs outside this library).  Row i < S of
+ * sequence b is position prefix_len[b] + node0 + i; k_out, v_out: row (b, i, h)
+ * at base + b*seq_stride + i*tok_stride + h*d, of type dt (strides in
+ * elements and bases multiples of 16 bytes); either may be NULL.  The values
+ * are exact in both types.  Rows i >= count[b] (count NULL: S), of a slot
+ * without a request, past the table (BAD_PREFIX) or of a bad block (BAD_BLOCK)
+ * are left as they were.  The rows of an output do not overlap.
+ */
+ssd_status_t ssd_kv_read_q4(const void *k_cache, const void *v_cache, const uint8_t *k_scale,
+                            const uint8_t *v_scale, const int32_t *block_table, int maxb,
+                            int64_t num_blocks, const int32_t *prefix_len, const int32_t *count,
+                            int node0, void *k_out, int64_t ko_seq_stride, int64_t ko_tok_stride,
+                            void *v_out, int64_t vo_seq_stride, int64_t vo_tok_stride, ssd_dtype_t dt,
+                            int B, int S, int Hkv, int d, uint32_t *status, ssd_stream_t s);
+
+/*
+ * ssd_branch_attention_q4: ssd_branch_attention over the 4-bit cache, same
+ * arguments, limits and flags otherwise.  A row that sees no key (its blocks
+ * are bad) gives 0 and lse = -inf.  A NaN scale of a key reaches the rows that
+ * see the key, in v only the 32 elements of its group; what hidden positions
+ * hold does not matter.  A query row with a value that is not finite gives NaN.
+ * v scales below 2^-100 (bytes below 27) count as 0.
+ * Workspace: ssd_attention_q4_workspace_size() bytes, 256-byte aligned, for
+ * splitting long key ranges; NULL or short: not split, the same result but for
+ * rounding, slower.
+ */
+size_t ssd_attention_q4_workspace_size(int B, int Nq, int Hq, int Hkv, int d);
+ssd_status_t ssd_branch_attention_q4(const void *q, const void *k_cache, const void *v_cache,
+                                     const uint8_t *k_scale, const uint8_t *v_scale,
+                                     const int32_t *block_table, int maxb, int64_t num_blocks,
+                                     const int32_t *prefix_len, const int32_t *parent, int B, int N,
+                                     int Nq, int Hq, int Hkv, int d, float scale, void *out,
+                                     float *lse, uint32_t *status, void *ws, size_t ws_bytes,
+                                     ssd_stream_t s);
+
+/*
+ * Log probabilities of given tokens: what a serving program reports of the
+ * tokens that a round emits, or of a prompt's.  logits [B, R, V] as above
+ * (element (b, r, i) at base + b*seq_stride + r*row_stride + i; any R);
+ * with p = softmax(z / T) of row (b, r) and t = tokens[b, r]:
+ *   logprob [B, R] fp32      = ln p(t)
+ *   rank    [B, R] int32     = tokens before t in the order (logit descending, index ascending)
+ *   entropy [B, R] fp32      = -sum p ln p
+ *   top_ids [B, R, n] int32, top_logprob [B, R, n] fp32 = the first n tokens of that order, and their ln p
+ * Every output may be NULL (logprob and rank need tokens; tokens NULL: every
+ * row is wanted).  t = -1 (the tail of ssd_verify's out_tokens): nothing of
+ * the row is read or written.  Another t outside [0, V): logprob NaN, rank -1
+ * (BAD_TOKEN), the rest of the row as usual.  Logits of -inf are tokens of
+ * probability 0; a row with a NaN or +inf, or with no finite logit, has no
+ * distribution: NaN, and -1 for rank and ids (BAD_VALUE).  T = 0: one-hot at the
+ * first token of the order (ln p = 0 there and -inf elsewhere, entropy 0).
+ * Sums are fp32 around the row's maximum.  0 <= n <= min(V, 64); T = 0 or T >=
+ * 2^-60; V * elem <= 4 MiB; B * R < 2^28.
+ */
+ssd_status_t ssd_token_logprobs(const void *logits, ssd_dtype_t dt, int64_t seq_stride, int64_t row_stride,
+                                int B, int R, int V, float T, const int32_t *tokens, float *logprob,
+                                int32_t *rank, float *entropy, int n, int32_t *top_ids, float *top_logprob,
+                                uint32_t *status, ssd_stream_t s);
 
 #ifdef __cplusplus
 }

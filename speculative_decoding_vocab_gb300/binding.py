@@ -36,7 +36,9 @@ EXPORTS = ("ssd_status_string", "ssd_fanout_split", "ssd_workspace_size", "ssd_s
            "ssd_attention_workspace_size", "ssd_branch_attention", "ssd_ngram_backup",
            "ssd_fallback_plan", "ssd_fill_sample", "ssd_kv_append", "ssd_tree_verify",
            "ssd_round_pipelined", "ssd_block_table_update", "ssd_rope_frequencies", "ssd_tree_rope",
-           "ssd_kv_append_q8", "ssd_attention_q8_workspace_size", "ssd_branch_attention_q8")
+           "ssd_kv_append_q8", "ssd_attention_q8_workspace_size", "ssd_branch_attention_q8",
+           "ssd_kv_append_q4", "ssd_kv_read_q4", "ssd_attention_q4_workspace_size", "ssd_branch_attention_q4",
+           "ssd_token_logprobs")
 
 _lib = None
 
@@ -144,6 +146,17 @@ def _declare(lib):
     lib.ssd_branch_attention_q8.argtypes = ([_vp] * 6 + [_i, _i64, _vp, _vp] + [_i] * 6
                                             + [_f, _vp, _vp, _vp, _vp, _sz, _vp])
     lib.ssd_branch_attention_q8.restype = _i
+    lib.ssd_kv_append_q4.argtypes = lib.ssd_kv_append_q8.argtypes
+    lib.ssd_kv_append_q4.restype = _i
+    lib.ssd_kv_read_q4.argtypes = ([_vp] * 5 + [_i, _i64, _vp, _vp, _i] + [_vp, _i64, _i64] * 2 + [_i] * 5
+                                   + [_vp, _vp])
+    lib.ssd_kv_read_q4.restype = _i
+    lib.ssd_attention_q4_workspace_size.argtypes = [_i] * 5
+    lib.ssd_attention_q4_workspace_size.restype = _sz
+    lib.ssd_branch_attention_q4.argtypes = lib.ssd_branch_attention_q8.argtypes
+    lib.ssd_branch_attention_q4.restype = _i
+    lib.ssd_token_logprobs.argtypes = ([_vp, _i, _i64, _i64, _i, _i, _i, _f] + [_vp] * 4 + [_i] + [_vp] * 4)
+    lib.ssd_token_logprobs.restype = _i
 
 
 # ---------------------------------------------------------------------------
@@ -683,3 +696,129 @@ def ssd_branch_attention_q8(q, k_cache, v_cache, k_scale, v_scale, block_table, 
             parent.data_ptr(), B, N, Nq, Hq, Hkv, d, float(scale), out.data_ptr(),
             _dense(lse, f32, (B, Nq, Hq), dev, "lse"), _dense(status, i32, (1,), dev, "status"),
             None if ws is None else _dense(ws, torch.uint8, (ws_bytes,), dev, "ws"), ws_bytes)
+
+
+# ---------------------------------------------------------------------------
+# the 4-bit cache of the branch decode
+# ---------------------------------------------------------------------------
+def _q4_cache(k_cache, v_cache, k_scale, v_scale, Hkv, d, dev):
+    """Checks the 4-bit cache's tensors; returns their addresses and the number of blocks."""
+    nb = k_cache.shape[0]
+    u8 = torch.uint8
+    return (_dense(k_cache, u8, (nb, Hkv, 16, d // 2), dev, "k_cache"), _dense(v_cache, u8, (nb, Hkv, 8, d), dev, "v_cache"),
+            _dense(k_scale, u8, (nb, Hkv, 16, d // 32), dev, "k_scale"),
+            _dense(v_scale, u8, (nb, Hkv, 16, d // 32), dev, "v_scale")), nb
+
+
+def q4_cache(num_blocks, Hkv, d, device="cuda"):
+    """An empty 4-bit cache: (k_cache, v_cache, k_scale, v_scale)."""
+    u8 = dict(dtype=torch.uint8, device=device)
+    return (torch.zeros(num_blocks, Hkv, 16, d // 2, **u8), torch.zeros(num_blocks, Hkv, 8, d, **u8),
+            torch.zeros(num_blocks, Hkv, 16, d // 32, **u8), torch.zeros(num_blocks, Hkv, 16, d // 32, **u8))
+
+
+def ssd_kv_append_q4(k_new, v_new, k_cache, v_cache, k_scale, v_scale, block_table, prefix_len, node0, count=None,
+                     status=None, stream=None):
+    """Quantise the rows ``k_new``/``v_new`` [B, S, Hkv, d] (bf16, heads
+    contiguous) into the 4-bit caches at tree nodes node0.. of every sequence
+    (rows i >= count[b] are left out)."""
+    rows = k_new.shape
+    B, S, Hkv, d = rows
+    maxb = block_table.shape[1]
+    dev = k_cache.get_device()
+    i32, bf16 = torch.int32, torch.bfloat16
+    kss, kts, khs, kes = k_new.stride()
+    vss, vts, vhs, ves = v_new.stride()
+    if k_new.dtype is not bf16 or v_new.dtype is not bf16 or v_new.shape != rows:
+        raise ValueError(f"k_new and v_new must be {bf16} tensors of one shape")
+    if (kes != 1 and d > 1) or (khs != d and Hkv > 1) or (ves != 1 and d > 1) or (vhs != d and Hkv > 1):
+        raise ValueError("k_new and v_new: the heads of a token must be contiguous")
+    if not (dev == k_new.get_device() == v_new.get_device()):
+        raise ValueError("all tensors of a call must live on one device")
+    cache, nb = _q4_cache(k_cache, v_cache, k_scale, v_scale, Hkv, d, dev)
+    _launch("ssd_kv_append_q4", dev, stream,
+            k_new.data_ptr(), kss if B > 1 else 0, kts if S > 1 else 0,
+            v_new.data_ptr(), vss if B > 1 else 0, vts if S > 1 else 0, *cache,
+            _dense(block_table, i32, (B, maxb), dev, "block_table"), maxb, nb,
+            _dense(prefix_len, i32, (B,), dev, "prefix_len"), _dense(count, i32, (B,), dev, "count"), int(node0),
+            B, S, Hkv, d, _dense(status, i32, (1,), dev, "status"))
+
+
+def ssd_kv_read_q4(k_cache, v_cache, k_scale, v_scale, block_table, prefix_len, node0, k_out, v_out, count=None,
+                   status=None, stream=None):
+    """Rows of the 4-bit caches at tree nodes node0.. of every sequence as
+    values: ``k_out``, ``v_out`` [B, S, Hkv, d] (bf16 or fp32, heads
+    contiguous; either may be None)."""
+    x = k_out if k_out is not None else v_out
+    rows = x.shape
+    B, S, Hkv, d = rows
+    maxb = block_table.shape[1]
+    dev = k_cache.get_device()
+    i32 = torch.int32
+    dt = SSD_F32 if x.dtype == torch.float32 else SSD_BF16
+    if dt == SSD_BF16 and x.dtype != torch.bfloat16:
+        raise ValueError(f"k_out and v_out must be float32 or bfloat16, got {x.dtype}")
+    cache, nb = _q4_cache(k_cache, v_cache, k_scale, v_scale, Hkv, d, dev)
+    outs = []
+    for y, what in ((k_out, "k"), (v_out, "v")):
+        # an output stands for its own input: the same checks of heads, device and overlap
+        outs += (None, 0, 0) if y is None else _rows(y, y, x.dtype, (B, S, d), dev, what)[3:]
+        if y is not None and y.shape != rows:
+            raise ValueError(f"k_out and v_out must have one shape, got {tuple(rows)} and {tuple(y.shape)}")
+    _launch("ssd_kv_read_q4", dev, stream, *cache, _dense(block_table, i32, (B, maxb), dev, "block_table"), maxb, nb,
+            _dense(prefix_len, i32, (B,), dev, "prefix_len"), _dense(count, i32, (B,), dev, "count"), int(node0),
+            *outs, dt, B, S, Hkv, d, _dense(status, i32, (1,), dev, "status"))
+
+
+def ssd_attention_q4_workspace_size(B, Nq, Hq, Hkv, d) -> int:
+    return int(load().ssd_attention_q4_workspace_size(int(B), int(Nq), int(Hq), int(Hkv), int(d)))
+
+
+def ssd_branch_attention_q4(q, k_cache, v_cache, k_scale, v_scale, block_table, prefix_len, parent, out, lse=None,
+                            scale=None, status=None, ws=None, stream=None):
+    """ssd_branch_attention over the 4-bit caches."""
+    rows = q.shape
+    B, Nq, Hq, d = rows
+    Hkv = k_cache.shape[1]
+    N = parent.shape[1]
+    maxb = block_table.shape[1]
+    i32, bf16 = torch.int32, torch.bfloat16
+    if scale is None:
+        scale = d ** -0.5
+    dev = q.get_device()
+    ws_bytes = 0 if ws is None else ws.numel()
+    cache, nb = _q4_cache(k_cache, v_cache, k_scale, v_scale, Hkv, d, dev)
+    _launch("ssd_branch_attention_q4", dev, stream, _dense(q, bf16, rows, dev, "q"), *cache,
+            _dense(block_table, i32, (B, maxb), dev, "block_table"), maxb, nb,
+            _dense(prefix_len, i32, (B,), dev, "prefix_len"), _dense(parent, i32, (B, N), dev, "parent"),
+            B, N, Nq, Hq, Hkv, d, float(scale), _dense(out, bf16, rows, dev, "out"),
+            _dense(lse, torch.float32, (B, Nq, Hq), dev, "lse"), _dense(status, i32, (1,), dev, "status"),
+            None if ws is None else _dense(ws, torch.uint8, (ws_bytes,), dev, "ws"), ws_bytes)
+
+
+# ---------------------------------------------------------------------------
+# log probabilities of given tokens
+# ---------------------------------------------------------------------------
+def ssd_token_logprobs(logits, V, T, tokens=None, logprob=None, rank=None, entropy=None, top_ids=None,
+                       top_logprob=None, status=None, stream=None):
+    """Log probability, rank, entropy and the n likeliest alternatives of the
+    rows of ``logits`` [B, R, V'] (the first V entries of each) for the tokens
+    [B, R] (int32; -1: the row is left out); ``top_ids``, ``top_logprob``
+    [B, R, n].  Every output may be None."""
+    dt, ss, rs = _logit_meta(logits)
+    B, R = logits.shape[:2]
+    if logits.numel() and logits.shape[2] < V:
+        raise ValueError(f"logits hold {logits.shape[2]} entries per row, V is {V}")
+    if B == 1 or logits.numel() == 0:
+        ss = 0
+    if R == 1 or logits.numel() == 0:
+        rs = 0
+    top = top_ids if top_ids is not None else top_logprob
+    n = 0 if top is None else top.shape[2]
+    dev = logits.get_device()
+    i32, f32 = torch.int32, torch.float32
+    _launch("ssd_token_logprobs", dev, stream, logits.data_ptr(), dt, ss, rs, B, R, int(V), float(T),
+            _dense(tokens, i32, (B, R), dev, "tokens"), _dense(logprob, f32, (B, R), dev, "logprob"),
+            _dense(rank, i32, (B, R), dev, "rank"), _dense(entropy, f32, (B, R), dev, "entropy"), n,
+            _dense(top_ids, i32, (B, R, n), dev, "top_ids"), _dense(top_logprob, f32, (B, R, n), dev, "top_logprob"),
+            _dense(status, i32, (1,), dev, "status"))
