@@ -47,7 +47,7 @@ using namespace line;
 
 constexpr int kSmemBudget = 214 * 1024;
 constexpr int kTiles = 4;     // tiles whose scales of v are held
-constexpr int kIds = 16;      // units whose block ids are held
+constexpr int kIds = 32;      // units whose block ids are held
 constexpr int kVShift = 13;
 constexpr float kOutUnit = kSumUnit * 0x1p-13f;
 constexpr int kQueryByte = 127 - 8;
@@ -108,16 +108,23 @@ struct Cfg {
   static constexpr int NB = 2;                             // S buffers; S runs NB tiles ahead
   static constexpr int kSoftWarps = 4 * kGroups;
   // helper warps: warp w of the four writes TMEM lanes 32 w .. + 31 (those that a warp of its number modulo 4 reaches)
-  static constexpr int kHelpWarp = kSoftWarps, kKWarp = kHelpWarp + 4, kVWarp = kKWarp + 1, kMmaWarp = kVWarp + 1;
+  static constexpr int kHelpWarp = kSoftWarps;
+  // two sets of helpers where the registers of 24 warps (80 a thread) allow them, a sub-tile each; and the producers
+  static constexpr int kSets = RT <= 48 ? 2 : 1, kHelpers = 4 * kSets, kTmaWarp = kHelpWarp + kHelpers;
+  static constexpr int kKWarps = RT <= 48 ? 2 : 2, kVWarps = RT <= 32 ? 2 : 1;
+  static constexpr int kMmaWarp = kTmaWarp + kKWarps + kVWarps;
   static constexpr int kWarps = kMmaWarp + 1;
   static constexpr int kThreads = kWarps * 32;
   // units of a tile; a unit's keys, its rows of 128 elements, its blocks
   static constexpr int kUnits = D == 128 ? KT : 1;
+  static constexpr bool kApart = kSets == 2 && kUnits == 2;  // a set has a unit of each tile for itself
+  static constexpr int kVHelp = kApart ? 4 : kHelpers;       // helper warps that turn a unit of V into halves
   static constexpr int kUKeys = kKeys / kUnits, kURows = kUKeys * D / 128, kUPages = kUKeys / kPage;
   static constexpr int kG = D / kQ4Group;                  // scales of a key
   static constexpr int kPageBytes = kPage * D / 2;         // codes of a block and head, K or V
   static constexpr int kScalePage = kPage * kG;
-  static constexpr int kBatch = 32 / kUPages;              // units that a producer warp's lanes hold the blocks of
+  static constexpr int kBatch = 32 / kUPages;              // units that a producer warp's lanes hold the blocks of, every
+                                                           // other one
   static constexpr int kQTile = RT * 128;                  // q1 (or q2) at D = 128; [q1 | q2] at D = 64
   static constexpr int kQBuf = D == 128 ? 2 * kQTile : kQTile;
   // P V's operand in shared memory, halves: P^T of a sub-tile in rows of 128 bytes, a key each; with a lane per row V
@@ -128,7 +135,9 @@ struct Cfg {
   static constexpr int kFactors = kURows * 8;              // of a unit: a half per key and group
   static constexpr int kFixed = 2 * kQBuf + NB * kHBuf + kTiles * kKeys * 8 + kTiles * kUnits * kFactors;
   static constexpr int kFit = (kSmemBudget - kFixed) / (kKSlot + kVSlot + kSSlot);
-  static constexpr int kSlots = kFit > 8 ? 8 : kFit;
+  // Sets that work apart may be two tiles from each other, and a barrier's parity tells a wait only the phase before
+  // from the one after: each set has slots of its own, every other one.
+  static constexpr int kSlots = (kFit > 8 ? 8 : kFit) & (kApart ? ~1 : ~0);
   static constexpr int kQ = 0, kH = 2 * kQBuf, kKRing = kH + NB * kHBuf, kVRing = kKRing + kSlots * kKSlot,
                        kSRing = kVRing + kSlots * kVSlot, kTop = kSRing + kSlots * kSSlot,
                        kFactor = kTop + kTiles * kKeys * 8;
@@ -142,12 +151,14 @@ struct Cfg {
   static constexpr int kVBufs = kRowLanes ? NB : kABufs;   // of V in halves, in shared memory or TMEM
   static constexpr int kSfCol = kOCol + kOCols;
   static constexpr int kSfFit = (kACol - kSfCol) / 4 - 1;
-  static constexpr int kSf = kSfFit > kSlots ? kSlots : kSfFit;
+  static constexpr int kSf = (kSfFit > kSlots ? kSlots : kSfFit) & (kApart ? ~1 : ~0);
   static_assert(kSmem + 13 * 1024 <= 227 * 1024, "shared memory with the static part");
   // The helpers write the scales of a tile NB tiles ahead of V, and the softmax warps are NB tiles behind S at most.
   static_assert(kTiles >= NB + 2, "scales of v");
   static_assert(kSlots >= (NB + 1) * kUnits || kSlots >= 4, "S runs ahead");
-  static_assert(kSf >= kUnits && kSf <= kSlots && kIds >= kSlots + 2 * kBatch, "scale bytes in TMEM, block ids");
+  static_assert(kSf >= kUnits && kSf <= kSlots && kIds >= kSlots + 4 * kBatch, "scale bytes in TMEM, block ids");
+  static_assert(!kApart || (kSlots % 2 == 0 && kSf % 2 == 0), "a set's slots are its own");
+  static_assert(kVWarps == 1 || kApart || kUnits == 1, "V's producers wait for units that one set gives back in order");
   static_assert(!kRowLanes || (RT == 128 && kGroups == 4), "a lane per row, a quarter of the keys per group");
   static_assert(kRowLanes || (KT == 2 && CG == 16 && RT <= 64), "tiles of two sub-tiles, P in rows of 128 bytes");
   static_assert(kKRing % 1024 == 0 && kVRing % 1024 == 0, "swizzled tiles");
@@ -161,16 +172,15 @@ __global__ void __launch_bounds__(Cfg<D, RT>::kThreads, 1)
   constexpr int CG = C::CG, NB = C::NB, NSLOT = C::kSlots, KT = C::KT, U = C::kUnits, UP = C::kUPages, G = C::kG;
   constexpr int kSoftThreads = C::kSoftWarps * 32;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
-  uint8_t *const smem =
-      reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t *const smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);  // by an offset: known to be shared memory
   // Of a tile, by the place of a key's scores (element h * 128 + lane of the S^T pair, or the column of S): t (-1: hidden),
   // then log2 t
   float *const top = reinterpret_cast<float *>(smem + C::kTop);
   __shared__ __align__(8) uint64_t kfull[NSLOT], kempty[NSLOT], vfull[NSLOT], vempty[NSLOT], kready[C::kSf];
   __shared__ __align__(8) uint64_t sfull[NB], pfull[NB], vready[NB][U], pvdone[NB], qfull[2], qempty[2];
   __shared__ uint32_t tmem_base;
-  __shared__ __align__(16) int s_ids[2][kIds][UP];          // block ids of a unit (K's and V's producer), -1 for none
-  __shared__ int s_row[2][kIds];                            // and its KV head
+  __shared__ __align__(16) int s_ids[2][kIds][UP];          // block ids of a unit (K's and V's producers), -1 for none
+  __shared__ int s_row[2][kIds];                            // and its head's first row in a block
   __shared__ uint32_t s_gone[kTiles][U * 4];                // missing blocks of a tile, by helper warp
   __shared__ int par[2][kMaxNodes];
   __shared__ uint32_t anc[2][kMaxNodes][kMaxNodes / 32];    // per query: the nodes that it sees
@@ -192,17 +202,17 @@ __global__ void __launch_bounds__(Cfg<D, RT>::kThreads, 1)
       mbar_init(&kfull[s], 33);
       mbar_init(&kempty[s], 1);
       mbar_init(&vfull[s], 1);
-      mbar_init(&vempty[s], 4);
+      mbar_init(&vempty[s], C::kVHelp);
     }
     for (int s = 0; s < C::kSf; ++s) mbar_init(&kready[s], 4);
     for (int u = 0; u < NB; ++u) {
       mbar_init(&sfull[u], 1);
       mbar_init(&pfull[u], 4 * C::kGroups);
-      for (int h = 0; h < U; ++h) mbar_init(&vready[u][h], 4);
+      for (int h = 0; h < U; ++h) mbar_init(&vready[u][h], C::kVHelp);
       mbar_init(&pvdone[u], 1);
     }
     for (int u = 0; u < 2; ++u) {
-      mbar_init(&qfull[u], 4);
+      mbar_init(&qfull[u], C::kHelpers);
       mbar_init(&qempty[u], 1 + C::kSoftWarps);
     }
     fence_mbar_init();
@@ -229,11 +239,13 @@ __global__ void __launch_bounds__(Cfg<D, RT>::kThreads, 1)
   };
 
   Segments sg;
-  if (warp == C::kKWarp || warp == C::kVWarp) {
-    // ---------------- producers: one warp for K's codes and both scales, one for V's codes.  Block ids are fetched for
-    // kBatch units at a time, one batch ahead: lane l holds block l % UP of the batch's unit l / UP.
-    const bool is_k = warp == C::kKWarp;
-    const int pw = is_k ? 0 : 1, page = lane % UP;
+  if (warp >= C::kTmaWarp && warp < C::kMmaWarp) {
+    // ---------------- producers: warps for K's codes and both scales, and for V's codes, a unit each in turn (a copy
+    // costs its warp 60 to 70 clocks).  Block ids are fetched for kBatch of a warp's units at a time, one batch ahead: lane l
+    // holds block l % UP of the batch's unit l / UP.
+    const bool is_k = warp < C::kTmaWarp + C::kKWarps;
+    const int pw = is_k ? 0 : 1, mine = warp - C::kTmaWarp - (is_k ? 0 : C::kKWarps), page = lane % UP;
+    const int step = is_k ? C::kKWarps : C::kVWarps;
     uint64_t *const full = is_k ? kfull : vfull, *const empty = is_k ? kempty : vempty;
     const CUtensorMap *const map = is_k ? &kmap : &vmap;
     constexpr int kKRows = kPage * D / 128;                // rows of a block and head: K, then V
@@ -249,9 +261,9 @@ __global__ void __launch_bounds__(Cfg<D, RT>::kThreads, 1)
         more = sg.step(a);
       }
     };
-    int hk, blk;
+    int row, blk;
     auto ids = [&] {
-      hk = more ? sg.hk : 0;
+      row = more ? sg.hk * rows : 0;
       blk = -1;
       const int64_t lp = static_cast<int64_t>(t) * UP + page;
       if (more && lp < a.maxb && lp * kPage < sg.nkeys) {
@@ -261,68 +273,69 @@ __global__ void __launch_bounds__(Cfg<D, RT>::kThreads, 1)
           blk = -1;
         }
       }
-      advance(C::kBatch);
+      advance(step * C::kBatch);
     };
-    advance(lane / UP);
+    advance(mine + step * (lane / UP));
     ids();
-    int slot = 0;
-    uint32_t phase = 1;  // of empty[slot]; the first round's slots are free
     const int nunits = ntiles * U;
+    int slot = mine, i = mine;
+    uint32_t phase = 1;  // of empty[slot]; the first round's slots are free
     bool ok = true;
-    int i = 0;
-    for (; i < nunits; ++i) {
-      if (i % C::kBatch == 0) {
-        const int at = (i + lane / UP) % kIds;
-        __syncwarp();
+    for (int n = 0; i < nunits; i += step, ++n) {
+      if (n % C::kBatch == 0) {
+        const int at = (i + step * (lane / UP)) % kIds;
         s_ids[pw][at][page] = blk;
-        if (page == 0) s_row[pw][at] = hk;
+        if (page == 0) s_row[pw][at] = row;
         __syncwarp();
         ids();
       }
-      const int x = i % kIds;
-      const int head = s_row[pw][x];
+      const int x = i % kIds, r = s_row[pw][x];
+      int e[UP], all = 0;
+#pragma unroll
+      for (int k = 0; k < UP; k += 4) {
+        const int4 v = *reinterpret_cast<const int4 *>(&s_ids[pw][x][k]);
+        e[k] = v.x, e[k + 1] = v.y, e[k + 2] = v.z, e[k + 3] = v.w;
+        all |= v.x | v.y | v.z | v.w;
+      }
       ok = i < NSLOT || warp_wait(&empty[slot], phase);
       if (!ok) break;
-      if (is_k) {  // the scales, 16 bytes a lane: K's, then V's (a unit's fill 512 bytes, or 256)
-        constexpr int kChunks = C::kScalePage / 16;
-        const int p = lane / kChunks;
-        if (p < UP) {
-          const int e = s_ids[0][x][p];
-          if (e >= 0) {
-            const int64_t from = (static_cast<int64_t>(e) * a.Hkv + head) * C::kScalePage + (lane % kChunks) * 16;
-            uint8_t *const to = smem + C::kSRing + slot * C::kSSlot + lane * 16;
-            cp_async16(to, a.ks + from);
-            cp_async16(to + 512, a.vs + from);
-          }
-        }
-        cp_async_arrive(&kfull[slot]);
-      }
       uint8_t *const dst = ring + slot * slot_bytes;
-      int there = 0;
-#pragma unroll
-      for (int k = 0; k < UP; ++k) there += s_ids[pw][x][k] >= 0;
       if (elect_one()) {
-        mbar_arrive_expect_tx(&full[slot], there * C::kPageBytes);
-        if (there == UP) {
+        if (all >= 0) {
+          mbar_arrive_expect_tx(&full[slot], UP * C::kPageBytes);
 #pragma unroll
-          for (int k = 0; k < UP; ++k) tma_load_3d(dst + k * pitch, map, 0, head * rows, s_ids[pw][x][k], &full[slot]);
+          for (int k = 0; k < UP; ++k) tma_load_3d(dst + k * pitch, map, 0, r, e[k], &full[slot]);
         } else {  // some blocks are missing or bad
+          int there = 0;
+          for (int k = 0; k < UP; ++k) there += s_ids[pw][x][k] >= 0;
+          mbar_arrive_expect_tx(&full[slot], there * C::kPageBytes);
 #pragma unroll 1
           for (int k = 0; k < UP; ++k)
-            if (s_ids[pw][x][k] >= 0)
-              tma_load_3d(dst + k * pitch, map, 0, head * rows, s_ids[pw][x][k], &full[slot]);
+            if (s_ids[pw][x][k] >= 0) tma_load_3d(dst + k * pitch, map, 0, r, s_ids[pw][x][k], &full[slot]);
         }
       }
       __syncwarp();
-      if (++slot == NSLOT) {
-        slot = 0;
+      if (is_k) {  // the scales, 16 bytes a lane: K's, then V's (a unit's fill 512 bytes, or 256)
+        constexpr int kChunks = C::kScalePage / 16;
+        const int p = lane / kChunks, b = p < UP ? s_ids[0][x][p] : -1;
+        if (b >= 0) {
+          const int64_t from = static_cast<int64_t>(b) * (a.Hkv * C::kScalePage) + r * (C::kScalePage / kKRows) + (lane % kChunks) * 16;
+          uint8_t *const to = smem + C::kSRing + slot * C::kSSlot + lane * 16;
+          cp_async16(to, a.ks + from);
+          cp_async16(to + 512, a.vs + from);
+        }
+        cp_async_arrive(&kfull[slot]);
+      }
+      slot += step;
+      if (slot >= NSLOT) {
+        slot -= NSLOT;
         phase ^= 1;
       }
     }
     if (!ok) {
       s_abort = 1;
       // this warp's copies in flight land before the shared memory is given back
-      for (int k = 0; k < NSLOT && --i >= 0; ++k) (void)warp_wait(&full[i % NSLOT], (i / NSLOT) & 1);
+      for (int k = 0; k < (NSLOT + step - 1) / step && (i -= step) >= 0; ++k) (void)warp_wait(&full[i % NSLOT], (i / NSLOT) & 1);
     }
     cp_async_wait_all();
   } else if (warp == C::kMmaWarp) {
@@ -416,30 +429,32 @@ __global__ void __launch_bounds__(Cfg<D, RT>::kThreads, 1)
       }
     }
     if (!ok) s_abort = 1;
-  } else if (warp >= C::kHelpWarp && warp < C::kKWarp) {
+  } else if (warp >= C::kHelpWarp && warp < C::kTmaWarp) {
     // ---------------- helpers, in the order of the MMAs.  They meet at named barriers, which have no limit, so a warp
     // whose wait gave up goes on (its waits are over at once) until they leave together.
-    const int hw = warp - C::kHelpWarp, r = hw * 32 + lane;
+    const int hw = warp & 3, set = (warp - C::kHelpWarp) >> 2, r = hw * 32 + lane;
+    constexpr int kStep = C::kApart ? 2 : 1;  // units from one of this warp's to the next
+    const int h0 = C::kApart ? set : 0, h1 = C::kApart ? set + 1 : U;
     const uint32_t quad = static_cast<uint32_t>(hw * 32) << 16;
     bool ok = true, all = true, more = sg.first(a, piece);
     if (more) {
       constexpr uint32_t q = kQueryByte * 0x01010101u;
-      tmem_st4(tmem + C::kSfCol + quad, q, q, q, q);
+      if (set == 0) tmem_st4(tmem + C::kSfCol + quad, q, q, q, q);
       tmem_wait_st();
       tc_fence_before();
-      prepare(sg, 0, warp, C::kSoftWarps + 4, 10);
-      bar_sync(10, (C::kSoftWarps + 4) * 32);
+      prepare(sg, 0, warp, C::kSoftWarps + C::kHelpers, 10);
+      bar_sync(10, (C::kSoftWarps + C::kHelpers) * 32);
       tc_fence_after();
       tc_fence_before();
       if (lane == 0) mbar_arrive1(&qfull[0]);
     }
-    int slot = 0, sf = 0, vslot = 0;
+    int slot = h0, sf = h0 % C::kSf, vslot = h0;
     uint32_t phase = 0, vphase = 0;  // of kfull[slot], vfull[vslot]
-    int nk = 0;                      // units of K so far
+    int nk = h0;                     // number of the unit of K
     // the scales of tile i (number t of the segment)
     auto scales = [&](int i, int t, int seg) {
 #pragma unroll 1
-      for (int h = 0; h < U; ++h, ++nk) {
+      for (int h = h0; h < h1; ++h, nk += kStep) {
         ok = ok && warp_wait(&kfull[slot], phase);
         // the unit whose scale bytes were there has been multiplied
         const int old = nk - C::kSf;
@@ -447,44 +462,75 @@ __global__ void __launch_bounds__(Cfg<D, RT>::kThreads, 1)
         tc_fence_after();
         const uint32_t *const sk = reinterpret_cast<const uint32_t *>(smem + C::kSRing + slot * C::kSSlot), *const sv = sk + 128;
         tmem_st4(tmem + C::kSfCol + 4 + sf * 4 + quad, sk[lane], sk[32 + lane], sk[64 + lane], sk[96 + lane]);
-        bool gone = false, nan = false;
-        if (C::kURows == 128 || r < C::kURows) {
-          const uint32_t word = sv[r];
-          uint16_t *const factor = reinterpret_cast<uint16_t *>(smem + C::kFactor + ((i % kTiles) * U + h) * C::kFactors);
-          constexpr int kOf = 128 / D;  // keys of a row of 128 elements
-          uint32_t f[4];
+        constexpr int kOf = 128 / D;  // keys of a row of 128 elements
+        const int first = t * C::kKeys + h * C::kUKeys + r * kOf;
+        const bool live = C::kURows == 128 || r < C::kURows;
+        const bool gone = live && s_ids[0][nk % kIds][(r * kOf / kPage) % UP] < 0;
+        const uint32_t word = live ? sv[r] : 0x7F7F7F7Fu;
+        // the usual case: factors 2^13 .. 2^-14, as halves of pairs of bytes
+        const uint32_t lo = __byte_perm(word, 0, 0x4140), hi = __byte_perm(word, 0, 0x4342);
+        uint32_t f[2], tb[kOf];
+        if (D == 128) {
+          const uint32_t m = max_u16x2(lo, hi);
+          tb[0] = max(m & 0xFFFFu, m >> 16);
+          f[0] = ((lo + 28u * 0x10001u) - tb[0] * 0x10001u) << 10;
+          f[1] = ((hi + 28u * 0x10001u) - tb[0] * 0x10001u) << 10;
+        } else {
+          tb[0] = max(lo & 0xFFFFu, lo >> 16);
+          tb[kOf - 1] = max(hi & 0xFFFFu, hi >> 16);
+          f[0] = ((lo + 28u * 0x10001u) - tb[0] * 0x10001u) << 10;
+          f[1] = ((hi + 28u * 0x10001u) - tb[kOf - 1] * 0x10001u) << 10;
+        }
+        float top_of[kOf], log_of[kOf];
 #pragma unroll
+        for (int w = 0; w < kOf; ++w) {
+          top_of[w] = __uint_as_float(tb[w] << 23);
+          log_of[w] = static_cast<float>(static_cast<int>(tb[w]) - 127);
+        }
+        const uint32_t least = min_u16x2(lo, hi), most = max(tb[0], tb[kOf - 1]);
+        bool nan = false;
+        if (__any_sync(0xffffffffu, gone || first + kOf > sg.nkeys || most == kNanScaleByte ||
+                                        min(least & 0xFFFFu, least >> 16) < max(kMinScaleByte + 0u, most - 27u))) {
+#pragma unroll 1
           for (int w = 0; w < kOf; ++w) {
-            const int key = r * kOf + w, pos = t * C::kKeys + h * C::kUKeys + key;
-            const bool missing = s_ids[0][nk % kIds][key / kPage] < 0;
-            const bool hidden = missing || pos >= sg.nkeys;
-            gone = gone || missing;
-            int b[G], tb = kMinScaleByte;
-#pragma unroll
+            const int pos = first + w;
+            const bool hidden = gone || pos >= sg.nkeys;
+            int big = kMinScaleByte;
             for (int g = 0; g < G; ++g) {
-              b[g] = (word >> ((w * G + g) * 8)) & 255;
-              if (b[g] != kNanScaleByte) tb = max(tb, b[g]);
+              const int b = (word >> ((w * G + g) * 8)) & 255;
+              if (b != kNanScaleByte) big = max(big, b);
             }
-#pragma unroll
+            uint32_t x[2] = {0, 0};
             for (int g = 0; g < G; ++g) {
-              uint32_t x = b[g] < kMinScaleByte ? 0u : half_pow2(b[g] - tb + kVShift + 15);
-              if (b[g] == kNanScaleByte) {  // of a tree node: 0 here, and reaches the rows that see it at the segment's end
-                x = pos >= sg.L ? 0u : 0x7E00u;
+              const int b = (word >> ((w * G + g) * 8)) & 255;
+              uint32_t y = b < kMinScaleByte ? 0u : half_pow2(b - big + kVShift + 15);
+              if (b == kNanScaleByte) {  // of a tree node: 0 here, and reaches the rows that see it at the segment's end
+                y = pos >= sg.L ? 0u : 0x7E00u;
                 nan = nan || (pos >= sg.L && !hidden);
               }
-              f[w * G + g] = hidden ? 0u : x;
+              if (!hidden) x[g >> 1] |= y << ((g & 1) * 16);
             }
-            const int at = (i % kTiles) * (2 * C::kKeys) + (D == 128 ? h * kSub + r : w * (C::kKeys / 2) + r);
-            top[at] = hidden ? -1.f : __uint_as_float(static_cast<uint32_t>(tb) << 23);
-            top[at + C::kKeys] = hidden ? 0.f : static_cast<float>(tb - 127);
+            const float big_of = hidden ? -1.f : __uint_as_float(static_cast<uint32_t>(big) << 23);
+            const float log = hidden ? 0.f : static_cast<float>(big - 127);
+            if (w == 0) top_of[0] = big_of, log_of[0] = log, f[0] = x[0];
+            else top_of[kOf - 1] = big_of, log_of[kOf - 1] = log, f[1] = x[0];
+            if (D == 128) f[1] = x[1];
+          }
+        }
+        if (live) {
+          uint16_t *const factor = reinterpret_cast<uint16_t *>(smem + C::kFactor + ((i % kTiles) * U + h) * C::kFactors);
+          float *const tops = top + (i % kTiles) * (2 * C::kKeys) + (D == 128 ? h * kSub : 0) + r;
+#pragma unroll
+          for (int w = 0; w < kOf; ++w) {
+            tops[w * (C::kKeys / 2)] = top_of[w];
+            tops[w * (C::kKeys / 2) + C::kKeys] = log_of[w];
           }
           if (D == 128) {
 #pragma unroll
-            for (int g = 0; g < 4; ++g) factor[g * C::kUKeys + r] = static_cast<uint16_t>(f[g]);
-          } else {
-#pragma unroll
-            for (int g = 0; g < 2; ++g)
-              reinterpret_cast<uint32_t *>(factor)[g * (C::kUKeys / 2) + r] = f[g] | f[2 + g] << 16;
+            for (int g = 0; g < 4; ++g) factor[g * C::kUKeys + r] = static_cast<uint16_t>(f[g >> 1] >> ((g & 1) * 16));
+          } else {  // two keys' halves of a group
+            reinterpret_cast<uint32_t *>(factor)[r] = __byte_perm(f[0], f[1], 0x5410);
+            reinterpret_cast<uint32_t *>(factor)[C::kUKeys / 2 + r] = __byte_perm(f[0], f[1], 0x7632);
           }
         }
         const uint32_t any = __ballot_sync(0xffffffffu, gone);
@@ -494,22 +540,24 @@ __global__ void __launch_bounds__(Cfg<D, RT>::kThreads, 1)
         tc_fence_before();
         __syncwarp();
         if (lane == 0 && ok) mbar_arrive1(&kready[sf]);
-        if (++slot == NSLOT) {
-          slot = 0;
+        slot += kStep;
+        if (slot >= NSLOT) {
+          slot -= NSLOT;
           phase ^= 1;
         }
-        if (++sf == C::kSf) sf = 0;
+        sf += kStep;
+        if (sf >= C::kSf) sf -= C::kSf;
       }
     };
     // V of tile i in halves
     auto values = [&](int i) {
       const int u = i % NB;
-      bar_sync(12, 128);  // the factors of all four warps
+      bar_sync(12 + (C::kApart ? set : 0), 32 * C::kVHelp);  // the factors of all four warps
       // the product that last read the buffer is done
       if (i >= C::kVBufs) ok = ok && warp_wait(&pvdone[(i - C::kVBufs) % NB], ((i - C::kVBufs) / NB) & 1);
       tc_fence_after();
 #pragma unroll 1
-      for (int h = 0; h < U; ++h) {
+      for (int h = h0; h < h1; ++h) {
         ok = ok && warp_wait(&vfull[vslot], vphase);
         if (!ok) break;
         const uint8_t *const vt = smem + C::kVRing + vslot * C::kVSlot;
@@ -550,15 +598,26 @@ __global__ void __launch_bounds__(Cfg<D, RT>::kThreads, 1)
           // columns of either 16x256b store, keys 4 (l % 4) .. + 3 (bits 3 and 4 of the key exchanged), and eight rows never meet in a bank.
           const int g = D == 128 ? hw : hw & 1, i16 = lane & 15;
           const int pair = (i16 & 9) | (i16 & 2) << 1 | (i16 & 4) >> 1, el = g * 32 + (lane >> 4) * 16;
-          uint32_t from = smem_u32(vt) + (D == 128 ? sw128(pair, el) : sw64(pair, el));
-          const uint8_t *f = factor + (g * C::kUKeys + (lane & 2) * 8 + (lane & 1) * 4) * 2;
-          uint32_t to = tmem + C::kACol + (i % C::kABufs) * C::kACols + h * (kSub / 2) + quad;
-          // a rolled loop: the softmax warps' code has to stay in the instruction cache
-#pragma unroll 1
-          for (int k0 = 0; k0 < C::kUKeys; k0 += 32, from += 16 * D, f += 64, to += 16) {
-            uint32_t c[4];
-            load_columns(from, c);
-            const uint2 m0 = *reinterpret_cast<const uint2 *>(f), m1 = *reinterpret_cast<const uint2 *>(f + 16);
+          // (two sets at D = 64: half of the unit's keys each)
+          constexpr int kMine = C::kUKeys * 4 / C::kVHelp;
+          const int key0 = C::kApart ? 0 : set * kMine;
+          uint32_t from = smem_u32(vt) + key0 / 2 * D + (D == 128 ? sw128(pair, el) : sw64(pair, el));
+          const uint8_t *f = factor + (g * C::kUKeys + key0 + (lane & 2) * 8 + (lane & 1) * 4) * 2;
+          uint32_t to = tmem + C::kACol + (i % C::kABufs) * C::kACols + h * (kSub / 2) + key0 / 2 + quad;
+          // a rolled loop: the softmax warps' code has to stay in the instruction cache; the next keys are read ahead
+          uint32_t c[4], next[4];
+          load_columns(from, c);
+          uint2 m0 = *reinterpret_cast<const uint2 *>(f), m1 = *reinterpret_cast<const uint2 *>(f + 16);
+#pragma unroll 2
+          for (int k0 = 0; k0 < kMine; k0 += 32, to += 16) {
+            uint2 n0 = m0, n1 = m1;
+            if (k0 + 32 < kMine) {
+              from += 16 * D;
+              f += 64;
+              load_columns(from, next);
+              n0 = *reinterpret_cast<const uint2 *>(f);
+              n1 = *reinterpret_cast<const uint2 *>(f + 16);
+            }
 #pragma unroll
             for (int e = 0; e < 2; ++e) {  // 16 elements each
               uint32_t x[4], y[4];
@@ -568,6 +627,10 @@ __global__ void __launch_bounds__(Cfg<D, RT>::kThreads, 1)
                                      hmul2(x[2], m1.x), hmul2(x[3], m1.y), hmul2(y[2], m1.x), hmul2(y[3], m1.y)};
               tmem_st_16x16(to + (static_cast<uint32_t>(e * 16) << 16), v);
             }
+#pragma unroll
+            for (int q = 0; q < 4; ++q) c[q] = next[q];
+            m0 = n0;
+            m1 = n1;
           }
           tmem_wait_st();
           tc_fence_before();
@@ -577,8 +640,9 @@ __global__ void __launch_bounds__(Cfg<D, RT>::kThreads, 1)
           mbar_arrive1(&vempty[vslot]);
           mbar_arrive1(&vready[u][h]);
         }
-        if (++vslot == NSLOT) {
-          vslot = 0;
+        vslot += kStep;
+        if (vslot >= NSLOT) {
+          vslot -= NSLOT;
           vphase ^= 1;
         }
       }
@@ -586,21 +650,23 @@ __global__ void __launch_bounds__(Cfg<D, RT>::kThreads, 1)
     for (int i0 = 0, seg = 0; more; ++seg) {
       const int n = sg.t1 - sg.t0;
       int x = 0;
-      for (; x < n && x < NB; ++x) scales(i0 + x, sg.t0 + x, seg);
+      const bool scaling = C::kApart || set == 0;
+      for (; x < n && x < NB; ++x)
+        if (scaling) scales(i0 + x, sg.t0 + x, seg);
       Segments next = sg;
       more = next.step(a);
       if (more) {  // the next segment's rows, once the segment before this has left their buffer
         const int buf = (seg + 1) & 1;
         ok = ok && (seg < 1 || warp_wait(&qempty[buf], ((seg - 1) >> 1) & 1));
-        all = !bar_or(11, 128, !ok || s_abort);
+        all = !bar_or(11, C::kHelpers * 32, !ok || s_abort);
         if (!all) break;
-        prepare(next, buf, hw, 4, 11);
+        prepare(next, buf, warp - C::kHelpWarp, C::kHelpers, 11);
         if (lane == 0) mbar_arrive1(&qfull[buf]);
       }
       for (int y = 0; y < n; ++y) {
         values(i0 + y);
         if (x < n) {
-          scales(i0 + x, sg.t0 + x, seg);
+          if (scaling) scales(i0 + x, sg.t0 + x, seg);
           ++x;
         }
       }
@@ -619,8 +685,8 @@ __global__ void __launch_bounds__(Cfg<D, RT>::kThreads, 1)
     bool dead = false;
     bool more = sg.first(a, piece);
     if (more) {
-      prepare(sg, 0, warp, C::kSoftWarps + 4, 10);
-      bar_sync(10, (C::kSoftWarps + 4) * 32);
+      prepare(sg, 0, warp, C::kSoftWarps + C::kHelpers, 10);
+      bar_sync(10, (C::kSoftWarps + C::kHelpers) * 32);
     }
     for (; more; more = sg.step(a), ++seg) {
       const int buf = seg & 1, n = sg.t1 - sg.t0, row = sg.mt * RT + r;
@@ -842,8 +908,8 @@ __global__ void __launch_bounds__(Cfg<D, RT>::kThreads, 1)
     bool dead = false;
     bool more = sg.first(a, piece);
     if (more) {
-      prepare(sg, 0, warp, C::kSoftWarps + 4, 10);
-      bar_sync(10, (C::kSoftWarps + 4) * 32);
+      prepare(sg, 0, warp, C::kSoftWarps + C::kHelpers, 10);
+      bar_sync(10, (C::kSoftWarps + C::kHelpers) * 32);
     }
     for (; more; more = sg.step(a), ++seg) {
       const int buf = seg & 1, n = sg.t1 - sg.t0;

@@ -161,6 +161,11 @@ SSD_DEV uint32_t max_u16x2(uint32_t x, uint32_t y) {  // lane-wise maximum of tw
   asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(y));
   return r;
 }
+SSD_DEV uint32_t min_u16x2(uint32_t x, uint32_t y) {
+  uint32_t r;
+  asm("min.u16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(y));
+  return r;
+}
 SSD_DEV uint32_t bmax2(uint32_t a, uint32_t b) {  // lane-wise maximum of two bf16 pairs
   uint32_t d;
   asm("max.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
