@@ -177,7 +177,7 @@ __global__ void __launch_bounds__(Cfg<D, RT>::kThreads, 1)
   // then log2 t
   float *const top = reinterpret_cast<float *>(smem + C::kTop);
   __shared__ __align__(8) uint64_t kfull[NSLOT], kempty[NSLOT], vfull[NSLOT], vempty[NSLOT], kready[C::kSf];
-  __shared__ __align__(8) uint64_t sfull[NB], pfull[NB], vready[NB][U], pvdone[NB], qfull[2], qempty[2];
+  __shared__ __align__(8) uint64_t sfull[NB], pfull[NB], vready[NB], pvdone[NB], qfull[2], qempty[2];
   __shared__ uint32_t tmem_base;
   __shared__ __align__(16) int s_ids[2][kIds][UP];          // block ids of a unit (K's and V's producers), -1 for none
   __shared__ int s_row[2][kIds];                            // and its head's first row in a block
@@ -208,7 +208,7 @@ __global__ void __launch_bounds__(Cfg<D, RT>::kThreads, 1)
     for (int u = 0; u < NB; ++u) {
       mbar_init(&sfull[u], 1);
       mbar_init(&pfull[u], 4 * C::kGroups);
-      for (int h = 0; h < U; ++h) mbar_init(&vready[u][h], C::kVHelp);
+      mbar_init(&vready[u], C::kHelpers);
       mbar_init(&pvdone[u], 1);
     }
     for (int u = 0; u < 2; ++u) {
@@ -379,8 +379,9 @@ __global__ void __launch_bounds__(Cfg<D, RT>::kThreads, 1)
         ok = ok && warp_wait(&kready[sf], sf_phase);  // K has landed, its scale bytes are in TMEM
         tc_fence_after();
         if (!ok) return;
+        const uint32_t dd = tmem + (u * KT + h) * (C::kRowLanes ? kSub : RT), kd = ring_k + slot * (C::kKSlot >> 4), qd = q, sd = sf_q + 4 + sf * 4;
         if (elect_one()) {
-          umma_s(tmem + (u * KT + h) * (C::kRowLanes ? kSub : RT), ring_k + slot * (C::kKSlot >> 4), q, sf_q + 4 + sf * 4);
+          umma_s(dd, kd, qd, sd);
           umma_commit(&kempty[slot]);
           if (h == U - 1) {
             umma_commit(&sfull[u]);
@@ -409,22 +410,21 @@ __global__ void __launch_bounds__(Cfg<D, RT>::kThreads, 1)
         const int u = j % NB;
         const uint32_t o = tmem + C::kOCol;
         const uint32_t later = j > order.begin;  // not the segment's first tile
-        ok = warp_wait(&pfull[u], (j / NB) & 1);
+        ok = warp_wait(&vready[u], (j / NB) & 1);
+        ok = ok && warp_wait(&pfull[u], (j / NB) & 1);
+        if (!ok) break;
+        tc_fence_after();
         const uint32_t at = tmem + C::kACol + (j % C::kABufs) * C::kACols, b = h_lo + u * (C::kHBuf >> 4);
-#pragma unroll 1
-        for (int h = 0; h < KT; ++h) {
-          if (h < U) ok = ok && warp_wait(&vready[u][h], (j / NB) & 1);
-          if (!ok) break;
-          tc_fence_after();
-          if (elect_one()) {
+        if (elect_one()) {
+#pragma unroll
+          for (int h = 0; h < KT; ++h)
 #pragma unroll
             for (int kk = 0; kk < kSub / 16; ++kk)  // 16 keys: two groups of 8 rows
               umma_f16(o, at + h * (kSub / 2) + kk * 8, b + h * (C::kBlock >> 4) + kk * (2048 >> 4), hi128, idesc_o,
                        kk > 0 || h > 0 ? 1u : later);
-            if (h == KT - 1) umma_commit(&pvdone[u]);
-          }
-          __syncwarp();
+          umma_commit(&pvdone[u]);
         }
+        __syncwarp();
         order.done(a, ++j);
       }
     }
@@ -457,8 +457,8 @@ __global__ void __launch_bounds__(Cfg<D, RT>::kThreads, 1)
       for (int h = h0; h < h1; ++h, nk += kStep) {
         ok = ok && warp_wait(&kfull[slot], phase);
         // the unit whose scale bytes were there has been multiplied
-        const int old = nk - C::kSf;
-        if (old >= 0) ok = ok && warp_wait(&kempty[old % NSLOT], (old / NSLOT) & 1);
+        const int old = nk - C::kSf;  // (with as many places for scale bytes as slots K's landing says so)
+        if (C::kSf < NSLOT && old >= 0) ok = ok && warp_wait(&kempty[old % NSLOT], (old / NSLOT) & 1);
         tc_fence_after();
         const uint32_t *const sk = reinterpret_cast<const uint32_t *>(smem + C::kSRing + slot * C::kSSlot), *const sv = sk + 128;
         tmem_st4(tmem + C::kSfCol + 4 + sf * 4 + quad, sk[lane], sk[32 + lane], sk[64 + lane], sk[96 + lane]);
@@ -608,7 +608,7 @@ __global__ void __launch_bounds__(Cfg<D, RT>::kThreads, 1)
           uint32_t c[4], next[4];
           load_columns(from, c);
           uint2 m0 = *reinterpret_cast<const uint2 *>(f), m1 = *reinterpret_cast<const uint2 *>(f + 16);
-#pragma unroll 2
+#pragma unroll (C::kSets == 2 ? 1 : 2)
           for (int k0 = 0; k0 < kMine; k0 += 32, to += 16) {
             uint2 n0 = m0, n1 = m1;
             if (k0 + 32 < kMine) {
@@ -638,7 +638,7 @@ __global__ void __launch_bounds__(Cfg<D, RT>::kThreads, 1)
         __syncwarp();
         if (lane == 0) {
           mbar_arrive1(&vempty[vslot]);
-          mbar_arrive1(&vready[u][h]);
+          if (h == h1 - 1) mbar_arrive1(&vready[u]);
         }
         vslot += kStep;
         if (vslot >= NSLOT) {
