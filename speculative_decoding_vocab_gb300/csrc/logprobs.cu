@@ -1,8 +1,26 @@
 // logprobs.cu -- log probabilities of given tokens, with their rank, the row's
-// entropy and its likeliest tokens.
+// entropy and its likeliest tokens, in one pass over the logits.
 //
-// One CTA per row: its maximum, then the sums around it, then the n first
-// tokens one after the other.
+// With c = log2(e) / T, m = max z, s = sum 2^((z - m) c), w = sum (z - m) c 2^((z - m) c):
+//   ln p(t) = ln2 ((z_t - m) c - log2 s),   entropy = ln2 (log2 s - w / s),
+//   rank(t) = #{z > z_t} + #{i < t: z_i = z_t}.
+// A thread keeps m, s and w of what it has read (s and w move to a new m when it
+// rises); parts meet in a fixed order.  (z - m) c is a difference first, so equal
+// large logits lose nothing, and is cut at -160, where the exponential is 0: tokens
+// of -inf cost no test.  A NaN reaches s.
+// The first n tokens: each CTA collects candidates in shared memory, those that its
+// threshold lets through.  The threshold starts from the first stage: each of
+// the 8 warps gives the k-th largest of its lanes' maxima, k = ceil(n / 8); at
+// least n elements reach the least of these.  From then on the n-th candidate so
+// far is the threshold, and only larger values pass (indices rise along the
+// part, and equal values rank by index).  Keys (value, ~index) are distinct, so their
+// ranks are counted, whatever order they came in.  Where a stage lets more through
+// than there is room for (ties, rising rows), the n-th key is searched bit by bit.
+//
+//   k_token_logprobs  a cluster of cw CTAs (256 threads) per row, a range of the row
+//       each, in stages of 16 KB that bulk copies bring into a ring of four; rank 0
+//       joins the parts through distributed shared memory.
+#include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
@@ -14,88 +32,412 @@ namespace {
 
 using namespace ssd;
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kMaxTop = 64;
+constexpr int kStageBytes = 16384, kStageVecs = kStageBytes / 16, kStages = 4;
+constexpr int kVecs = kStageVecs / kThreads;  // of a thread and stage
+constexpr int kRoom = 1024, kCompact = 512;   // candidates: room, and from when on they are reduced to n
+constexpr int kMaxCluster = 8;
+constexpr float kCut = -160.f;
 
 struct Args {
   const void *z;
   int64_t ss, rs;
-  int R, V, n;
-  float T;
+  int R, V, n, cw;
+  float c;
+  int greedy;
   const int32_t *tokens;
   float *logprob, *entropy, *top_logprob;
   int32_t *rank, *top_ids;
   uint32_t *status;
 };
 
+struct Part {
+  float m, s, w;
+  int before, count;
+};
+struct Shared {
+  uint64_t cand[kRoom], best[kMaxTop];
+  uint64_t full[kStages];
+  float red[kWarps][3];
+  uint32_t low[kWarps];
+  int before[kWarps];
+  int count, found;
+  Part part;
+  Part all[kMaxCluster];
+};
+
+SSD_DEV void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+SSD_DEV uint32_t peer_address(const void *p, unsigned rank) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(p)), "r"(rank));
+  return r;
+}
+SSD_DEV uint32_t peer_u32(uint32_t at) {
+  uint32_t v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
+  return v;
+}
+SSD_DEV uint64_t peer_u64(uint32_t at) {
+  uint64_t v;
+  asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(at) : "memory");
+  return v;
+}
+SSD_DEV float max_nan(float a, float b) {  // NaN if either is
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+SSD_DEV uint32_t ord(float x) { return f2ord(x + 0.f); }  // -0 and 0 rank alike
+// the next larger value of the type, as fp32
+template <class E>
+SSD_DEV float above(float x) {
+  const uint32_t step = 1u << (E::kSize == 2 ? 16 : 0);
+  const uint32_t b = __float_as_uint(x);
+  if (x == 0.f) return __uint_as_float(step);
+  return __uint_as_float(x > 0.f ? b + step : b - step);
+}
+
+// How many of a vector's elements are >= z2's, added to `acc` (bf16: a pair of small counts; fp32: a count)
+struct Counter {
+  __nv_bfloat162 pair;
+  int n;
+};
+template <class E>
+SSD_DEV void count_from(const uint4 &v, float z, Counter &k) {
+  if (E::kSize == 2) {
+    const __nv_bfloat162 z2 = __float2bfloat162_rn(z);  // z is a bf16 value
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      __nv_bfloat162 x;
+      *reinterpret_cast<uint32_t *>(&x) = w[j];
+      k.pair = __hadd2(k.pair, __hge2(x, z2));
+    }
+  } else {
+    k.n += (__uint_as_float(v.x) >= z) + (__uint_as_float(v.y) >= z) + (__uint_as_float(v.z) >= z) +
+           (__uint_as_float(v.w) >= z);
+  }
+}
+template <class E>
+SSD_DEV float vec_max(const uint4 &v) {
+  if (E::kSize == 2) {
+    const uint32_t m = bmax2(bmax2(v.x, v.y), bmax2(v.z, v.w));
+    return fmaxf(__uint_as_float(m << 16), __uint_as_float(m & 0xFFFF0000u));
+  }
+  return fmaxf(fmaxf(__uint_as_float(v.x), __uint_as_float(v.y)), fmaxf(__uint_as_float(v.z), __uint_as_float(v.w)));
+}
+
+// cand[0 .. c) -> its n largest, in order (all threads; c <= kRoom)
+SSD_DEV int keep_best(Shared &sh, int c, int n) {
+  __syncthreads();
+  for (int j = threadIdx.x; j < c; j += kThreads) {
+    const uint64_t key = sh.cand[j];
+    int r = 0;
+    for (int i = 0; i < c; ++i) r += sh.cand[i] > key;
+    if (r < n) sh.best[r] = key;
+  }
+  __syncthreads();
+  const int left = min(c, n);
+  if (threadIdx.x < left) sh.cand[threadIdx.x] = sh.best[threadIdx.x];
+  if (threadIdx.x == 0) sh.count = left;
+  __syncthreads();
+  return left;
+}
+
 template <class E>
 __global__ void __launch_bounds__(kThreads) k_token_logprobs(const __grid_constant__ Args a) {
-  __shared__ float red[kThreads / 32];
-  __shared__ uint64_t best[kThreads / 32];
-  const int64_t row = blockIdx.x;
-  const int tid = threadIdx.x;
+  extern __shared__ __align__(128) uint8_t ring[];
+  __shared__ __align__(16) Shared sh;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int64_t row = blockIdx.x / a.cw;
+  const int part = static_cast<int>(blockIdx.x - row * a.cw);
   const int t = a.tokens ? a.tokens[row] : 0;
-  if (t == -1) return;
-  const bool good = t >= 0 && t < a.V;
-  const char *const z = static_cast<const char *>(a.z) + ((row / a.R) * a.ss + (row % a.R) * a.rs) * E::kSize;
+  if (t == -1) return;  // the whole cluster
+  const bool given = a.tokens != nullptr, good = t >= 0 && t < a.V;
   const float INF = __int_as_float(0x7f800000), NAN_ = __int_as_float(0x7fc00000);
-  float m = -INF;
-  bool bad = false;
-  for (int i = tid; i < a.V; i += kThreads) {
-    const float x = E::ld(z, i);
-    bad |= !(x < INF);
-    m = fmaxf(m, x);
-  }
-  m = block_max<kThreads>(m, red);
-  bad = group_sync_or<kThreads>(bad) || m == -INF;
-  if (bad) {
-    if (tid == 0) {
-      if (a.logprob) a.logprob[row] = NAN_;
-      if (a.rank) a.rank[row] = -1;
-      if (a.entropy) a.entropy[row] = NAN_;
-      for (int j = 0; j < a.n; ++j) {
-        if (a.top_ids) a.top_ids[row * a.n + j] = -1;
-        if (a.top_logprob) a.top_logprob[row * a.n + j] = NAN_;
-      }
-      atomicOr(a.status, kFlagBadValue | (good ? 0u : kFlagBadToken));
-    }
-    return;
-  }
-  const float zt = good ? E::ld(z, t) : INF;
-  const float c = a.T == 0.f ? 0.f : 1.f / a.T;
-  float s = 0.f, w = 0.f, before = 0.f;
-  for (int i = tid; i < a.V; i += kThreads) {
-    const float x = E::ld(z, i), y = (x - m) * c, e = x == -INF ? 0.f : expf(y);
-    s += e;
-    w += e > 0.f ? e * y : 0.f;
-    before += (x > zt || (x == zt && i < t)) ? 1.f : 0.f;  // counts to 2^21: exact
-  }
-  s = block_sum<kThreads>(s, red);
-  w = block_sum<kThreads>(w, red);
-  before = block_sum<kThreads>(before, red);
-  const float ls = logf(s);
+  const char *const z = static_cast<const char *>(a.z) + ((row / a.R) * a.ss + (row % a.R) * a.rs) * E::kSize;
+  const int nv = a.V / E::kVec, per = (nv + a.cw - 1) / a.cw;
+  const int v0 = min(nv, part * per), v1 = min(nv, v0 + per), nst = (v1 - v0 + kStageVecs - 1) / kStageVecs;
+  auto load = [&](int st) {  // by thread 0
+    const int from = v0 + st * kStageVecs, bytes = min(kStageVecs, v1 - from) * 16;
+    mbar_arrive_expect_tx(&sh.full[st % kStages], bytes);
+    bulk_g2s(ring + (st % kStages) * kStageBytes, z + static_cast<int64_t>(from) * 16, bytes, &sh.full[st % kStages]);
+  };
   if (tid == 0) {
-    if (!good) atomicOr(a.status, kFlagBadToken);
-    if (a.rank) a.rank[row] = good ? static_cast<int>(before) : -1;
-    if (a.logprob)
-      a.logprob[row] = !good ? NAN_ : (a.T == 0.f ? (before == 0.f ? 0.f : -INF) : (zt - m) * c - ls);
-    if (a.entropy) a.entropy[row] = a.T == 0.f ? 0.f : ls - w / s;
+    for (int i = 0; i < kStages; ++i) mbar_init(&sh.full[i], 1);
+    fence_mbar_init();
+    fence_proxy_async();
+    for (int i = 0; i < min(kStages, nst); ++i) load(i);
+    sh.count = 0;
   }
-  uint64_t last = ~0ull;
-  for (int j = 0; j < a.n; ++j) {
-    uint64_t k = 0;
-    for (int i = tid; i < a.V; i += kThreads) {
-      const uint64_t key = cand_key(E::ld(z, i) + 0.f, i);
-      if (key < last && key > k) k = key;
+  const bool ranked = given && good && (a.rank || (a.logprob && a.greedy));
+  const float zt = given && good ? E::ld(z, t) : 0.f, zt_above = above<E>(zt);
+  const float c = a.c;
+  const uint64_t c2 = pack2(c, c);
+  float m = -INF;
+  uint64_t s2 = 0, w2 = 0, neg_m2 = 0;  // of a thread without a finite element m counts as 0
+  int before = 0;
+  auto rise = [&](float to) {  // a larger m
+    if (m != -INF) {
+      const float d = (m - to) * c, f = ex2(d);
+      const float dd = f == 0.f ? 0.f : d;
+      w2 = mul2(fma2(pack2(dd, dd), s2, w2), pack2(f, f));
+      s2 = mul2(s2, pack2(f, f));
     }
-    last = block_max_u64<kThreads>(k, best);
+    m = to;
+    neg_m2 = pack2(-to, -to);
+  };
+  auto add_pair = [&](uint64_t x) {
+    float y0, y1;
+    unpack2(mul2(add2(x, neg_m2), c2), y0, y1);
+    y0 = max_nan(y0, kCut);
+    y1 = max_nan(y1, kCut);
+    const uint64_t e = pack2(ex2(y0), ex2(y1));
+    s2 = add2(s2, e);
+    w2 = fma2(e, pack2(y0, y1), w2);
+  };
+  uint32_t least = 0;  // the order of the smallest value that passes
+  auto append = [&](float x, int i) {
+    const int at = atomicAdd(&sh.count, 1);
+    if (at < kRoom) sh.cand[at] = cand_key(x + 0.f, i);
+  };
+  auto append_vec = [&](const uint4 &v, int i0) {
+    float x[E::kVec];
+    E::unpack(v, x);
+#pragma unroll 1
+    for (int e = 0; e < E::kVec; ++e) {
+      float y = x[0];
+#pragma unroll
+      for (int k = 1; k < E::kVec; ++k) y = e == k ? x[k] : y;
+      if (ord(y) >= least) append(y, i0 + e);
+    }
+  };
+  __syncthreads();
+  if (part == a.cw - 1) {  // the elements behind the last whole vector: candidates in any case
+    const int i = nv * E::kVec + tid;
+    if (i < a.V) {
+      const float x = E::ld(z, i);
+      if (x > m) rise(x);
+      // the pair's other half adds nothing
+      float y = max_nan((x + (m == -INF ? 0.f : -m)) * c, kCut);
+      const float e = ex2(y);
+      s2 = add2(s2, pack2(e, 0.f));
+      w2 = fma2(pack2(e, 0.f), pack2(y, 0.f), w2);
+      if (ranked) before += i < t ? x >= zt : x > zt;
+      if (a.n > 0) append(x, i);
+    }
+  }
+  bool ok = true;
+  int kept = 0;  // candidates that the stages before left
+  __syncthreads();
+  for (int st = 0; st < nst; ++st) {
+    const int first = v0 + st * kStageVecs, count = min(kStageVecs, v1 - first);
+    const uint4 *const buf = reinterpret_cast<const uint4 *>(ring + (st % kStages) * kStageBytes);
+    ok = mbar_wait(&sh.full[st % kStages], (st / kStages) & 1) && ok;
+    if (a.n > 0) kept = sh.count;  // all threads, before the first candidate of this stage (a barrier ended the last one)
+    float top = -INF;  // of this thread's elements of the stage
+    bool any = false;
+    Counter k{__float2bfloat162_rn(0.f), 0};
+    if (a.n > 0 && st > 0) __syncthreads();
+#pragma unroll
+    for (int q = 0; q < kVecs; ++q) {
+      const int j = q * kThreads + tid;
+      if (j >= count) break;
+      const uint4 v = buf[j];
+      const float vm = vec_max<E>(v);
+      top = fmaxf(top, vm);
+      any = true;
+      if (vm > m) rise(vm);
+#pragma unroll
+      for (int h = 0; h < E::kPairs; ++h) add_pair(E::pair(v, h));
+      const int i0 = (first + j) * E::kVec;
+      if (ranked) count_from<E>(v, i0 + E::kVec <= t ? zt : zt_above, k);
+      if (st > 0 && a.n > 0 && ord(vm) >= least) append_vec(v, i0);
+    }
+    if (ranked)
+      before += k.n + static_cast<int>(__low2float(k.pair)) + static_cast<int>(__high2float(k.pair));
+    if (a.n > 0) {
+      if (st == 0) {  // the first threshold
+        uint32_t mine = any ? ord(top) : 0u, kth = 0;
+        const int rounds = (a.n + kWarps - 1) / kWarps;
+        for (int i = 0; i < rounds; ++i) {
+          kth = __reduce_max_sync(0xffffffffu, mine);
+          const uint32_t who = __ballot_sync(0xffffffffu, mine == kth);
+          if (lane == __ffs(who) - 1) mine = 0;
+        }
+        if (lane == 0) sh.low[warp] = kth;
+        __syncthreads();
+        least = sh.low[0];
+        for (int i = 1; i < kWarps; ++i) least = min(least, sh.low[i]);
+        for (int j = tid; j < count; j += kThreads) {
+          const uint4 v = buf[j];
+          if (ord(vec_max<E>(v)) >= least) append_vec(v, (first + j) * E::kVec);
+        }
+      }
+      __syncthreads();
+      int now = sh.count;
+      if (now > kRoom) {
+        // Too many: the n-th largest key of what was kept and this stage, from the highest bit down.  (The candidates of
+        // this stage are dropped and found again.)
+        uint64_t key = 0;
+        auto reach = [&](uint64_t from) {  // how many keys are >= from
+          int r = 0;
+          for (int j = tid; j < count * E::kVec; j += kThreads) {
+            const int i = first * E::kVec + j;
+            const float x = E::kSize == 2 ? __uint_as_float(static_cast<uint32_t>(reinterpret_cast<const uint16_t *>(buf)[j]) << 16)
+                                          : reinterpret_cast<const float *>(buf)[j];
+            r += cand_key(x + 0.f, i) >= from;
+          }
+          for (int j = tid; j < kept; j += kThreads) r += sh.cand[j] >= from;
+          if (tid == 0) sh.found = 0;
+          __syncthreads();
+          r = __reduce_add_sync(0xffffffffu, r);
+          if (lane == 0) atomicAdd(&sh.found, r);
+          __syncthreads();
+          const int all = sh.found;
+          __syncthreads();
+          return all;
+        };
+        for (int b = 63; b >= 0; --b) {
+          const uint64_t with = key | 1ull << b;
+          if (reach(with) >= a.n) key = with;
+        }
+        if (tid == 0) sh.count = kept;
+        __syncthreads();
+        for (int j = tid; j < count * E::kVec; j += kThreads) {
+          const int i = first * E::kVec + j;
+          const float x = E::kSize == 2 ? __uint_as_float(static_cast<uint32_t>(reinterpret_cast<const uint16_t *>(buf)[j]) << 16)
+                                        : reinterpret_cast<const float *>(buf)[j];
+          if (cand_key(x + 0.f, i) >= key) append(x, i);
+        }
+        __syncthreads();
+        now = sh.count;  // at most kept + n <= kRoom
+      }
+      if (st == 0 || now > kCompact) {
+        now = keep_best(sh, now, a.n);
+        // only larger values pass from here on; until there are n, all do
+        least = now == a.n ? static_cast<uint32_t>(sh.cand[a.n - 1] >> 32) + 1u : 0u;
+      }
+    }
+    __syncthreads();
+    if (tid == 0 && st + kStages < nst) load(st + kStages);
+  }
+  // equal logits before the token in its own vector, which was counted as if they ranked behind it
+  if (ranked && tid == 0) {
+    const int v = t / E::kVec;
+    if (v >= v0 && v < v1)
+      for (int i = v * E::kVec; i < t; ++i) before += E::ld(z, i) == zt;
+  }
+  // ---------------- the CTA's part
+  {
+    const float M = warp_max(m);
+    float s0, s1, w0, w1;
+    unpack2(s2, s0, s1);
+    unpack2(w2, w0, w1);
+    auto move = [&](float from, float to, float &s, float &w) {
+      if (from == -INF || from == to) return;
+      const float d = (from - to) * c, f = ex2(d);
+      w = f == 0.f ? 0.f : f * fmaf(d, s, w);
+      s = s * f;
+    };
+    float s = s0 + s1, w = w0 + w1;
+    move(m, M, s, w);
+    s = warp_sum(s);
+    w = warp_sum(w);
+    const int b = __reduce_add_sync(0xffffffffu, before);
+    if (lane == 0) {
+      sh.red[warp][0] = M;
+      sh.red[warp][1] = s;
+      sh.red[warp][2] = w;
+      sh.before[warp] = b;
+    }
+    __syncthreads();
     if (tid == 0) {
-      if (a.top_ids) a.top_ids[row * a.n + j] = cand_idx(last);
-      if (a.top_logprob)
-        a.top_logprob[row * a.n + j] =
-            a.T == 0.f ? (j == 0 ? 0.f : -INF) : (cand_val(last) - m) * c - ls;
+      Part p{-INF, 0.f, 0.f, 0, 0};
+      for (int i = 0; i < kWarps; ++i) p.m = fmaxf(p.m, sh.red[i][0]);
+      for (int i = 0; i < kWarps; ++i) {
+        float si = sh.red[i][1], wi = sh.red[i][2];
+        move(sh.red[i][0], p.m, si, wi);
+        p.s += si;
+        p.w += wi;
+        p.before += sh.before[i];
+      }
+      p.count = sh.count;
+      sh.part = p;
+    }
+    if (a.n > 0) {
+      const int left = keep_best(sh, sh.count, a.n);
+      if (tid == 0) sh.part.count = left;
+    }
+    __syncthreads();
+    // ---------------- the row, by rank 0
+    if (a.cw > 1) {
+      cluster_sync();
+      if (part == 0) {
+        if (tid < a.cw) {
+          const uint32_t from = peer_address(&sh.part, tid);
+          sh.all[tid] = Part{__uint_as_float(peer_u32(from)), __uint_as_float(peer_u32(from + 4)),
+                             __uint_as_float(peer_u32(from + 8)), static_cast<int>(peer_u32(from + 12)),
+                             static_cast<int>(peer_u32(from + 16))};
+        }
+        __syncthreads();
+        int at = sh.all[0].count;
+        for (int r = 1; r < a.cw; ++r) {
+          const uint32_t from = peer_address(sh.cand, r);
+          const int n = sh.all[r].count;
+          for (int j = tid; j < n; j += kThreads) sh.cand[at + j] = peer_u64(from + 8 * j);
+          at += n;
+        }
+        if (tid == 0) {
+          Part p{-INF, 0.f, 0.f, 0, 0};
+          for (int r = 0; r < a.cw; ++r) p.m = fmaxf(p.m, sh.all[r].m);
+          for (int r = 0; r < a.cw; ++r) {
+            move(sh.all[r].m, p.m, sh.all[r].s, sh.all[r].w);
+            p.s += sh.all[r].s;
+            p.w += sh.all[r].w;
+            p.before += sh.all[r].before;
+          }
+          sh.part = p;
+        }
+        if (a.n > 0) keep_best(sh, at, a.n);
+        __syncthreads();
+      }
     }
   }
+  if (part == 0) {
+    const Part p = sh.part;
+    const bool none = !(p.s == p.s) || p.m == INF || p.m == -INF;  // no distribution
+    const float ls = log2f(p.s), ln2 = 0.69314718055994531f;
+    if (tid == 0) {
+      const uint32_t flags = (none ? kFlagBadValue : 0u) | (good ? 0u : kFlagBadToken);
+      if (flags) atomicOr(a.status, flags);
+      if (a.logprob)
+        a.logprob[row] = none || !good ? NAN_ : (a.greedy ? (p.before == 0 ? 0.f : -INF) : ((zt - p.m) * c - ls) * ln2);
+      if (a.rank) a.rank[row] = none || !good ? -1 : p.before;
+      if (a.entropy) a.entropy[row] = none ? NAN_ : (a.greedy ? 0.f : (ls - p.w / p.s) * ln2);
+    }
+    if (tid < a.n) {
+      const uint64_t key = sh.cand[tid];
+      const int64_t at = row * a.n + tid;
+      if (a.top_ids) a.top_ids[at] = none ? -1 : cand_idx(key);
+      if (a.top_logprob)
+        a.top_logprob[at] =
+            none ? NAN_ : (a.greedy ? (tid == 0 ? 0.f : -INF) : ((cand_val(key) - p.m) * c - ls) * ln2);
+    }
+  }
+  if (!ok && tid == 0) atomicOr(a.status, kFlagWaitTimeout);
+  if (a.cw > 1) cluster_sync();  // no CTA leaves while rank 0 may still read its shared memory
+}
+
+// CTAs of a row: as many as fill the GPU once, so that a CTA's part is long.
+int cluster_of(int64_t rows, int V, int64_t size) {
+  const int64_t stages = (V * size + kStageBytes - 1) / kStageBytes;
+  int cw = 1;
+  while (cw < kMaxCluster && rows * cw < 304 && cw < stages) cw *= 2;
+  return cw;
 }
 
 }  // namespace
@@ -115,12 +457,38 @@ extern "C" ssd_status_t ssd_token_logprobs(const void *logits, ssd_dtype_t dt, i
   if (((reinterpret_cast<uintptr_t>(logits) | static_cast<uintptr_t>(seq_stride * size) |
         static_cast<uintptr_t>(row_stride * size)) & 15u))
     return SSD_ERR_UNSUPPORTED;
-  Args a{logits, seq_stride, row_stride, R, V, n, T, tokens, logprob, entropy, top_logprob, rank, top_ids, status};
-  const unsigned grid = static_cast<unsigned>(B * R);
-  cudaStream_t cs = reinterpret_cast<cudaStream_t>(s);
-  if (dt == SSD_BF16)
-    k_token_logprobs<EBF16><<<grid, kThreads, 0, cs>>>(a);
-  else
-    k_token_logprobs<EF32><<<grid, kThreads, 0, cs>>>(a);
-  return cudaGetLastError() == cudaSuccess ? SSD_OK : SSD_ERR_CUDA;
+  Args a{};
+  a.z = logits;
+  a.ss = seq_stride;
+  a.rs = row_stride;
+  a.R = R;
+  a.V = V;
+  a.n = top_ids || top_logprob ? n : 0;
+  a.cw = cluster_of(static_cast<int64_t>(B) * R, V, size);
+  a.greedy = T == 0.f;
+  a.c = a.greedy ? 1.f : static_cast<float>(1.4426950408889634 / T);
+  a.tokens = tokens;
+  a.logprob = logprob;
+  a.entropy = entropy;
+  a.top_logprob = top_logprob;
+  a.rank = rank;
+  a.top_ids = top_ids;
+  a.status = status;
+  constexpr int kRing = kStages * kStageBytes;
+  void (*const kernel)(Args) = dt == SSD_BF16 ? k_token_logprobs<EBF16> : k_token_logprobs<EF32>;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kRing) != cudaSuccess)
+    return SSD_ERR_CUDA;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(B * R * a.cw));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kRing;
+  cfg.stream = reinterpret_cast<cudaStream_t>(s);
+  cudaLaunchAttribute at;
+  at.id = cudaLaunchAttributeClusterDimension;
+  at.val.clusterDim.x = static_cast<unsigned>(a.cw);
+  at.val.clusterDim.y = 1;
+  at.val.clusterDim.z = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, a) == cudaSuccess ? SSD_OK : SSD_ERR_CUDA;
 }
