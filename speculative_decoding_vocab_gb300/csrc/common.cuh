@@ -188,6 +188,7 @@ struct EF32 {
   SSD_DEV static float ld(const void *base, int64_t i) {
     return __ldg(reinterpret_cast<const float *>(base) + i);
   }
+  SSD_DEV static uint4 nothing() { return make_uint4(0xFF800000u, 0xFF800000u, 0xFF800000u, 0xFF800000u); }  // -inf
   static constexpr int kPairs = 2;  // packed fp32 pairs per vector
   SSD_DEV static uint64_t pair(const uint4 &w, int h) {
     return h == 0 ? pack2(__uint_as_float(w.x), __uint_as_float(w.y)) : pack2(__uint_as_float(w.z), __uint_as_float(w.w));
@@ -211,6 +212,7 @@ struct EBF16 {
     uint16_t h = __ldg(reinterpret_cast<const unsigned short *>(base) + i);
     return __uint_as_float(static_cast<uint32_t>(h) << 16);
   }
+  SSD_DEV static uint4 nothing() { return make_uint4(0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u); }
   static constexpr int kPairs = 4;
   SSD_DEV static uint64_t pair(const uint4 &w, int h) {
     const uint32_t x = h == 0 ? w.x : (h == 1 ? w.y : (h == 2 ? w.z : w.w));

@@ -1,13 +1,16 @@
 // logprobs.cu -- log probabilities of given tokens, with their rank, the row's
 // entropy and its likeliest tokens, in one pass over the logits.
 //
-// With c = log2(e) / T, m = max z, s = sum 2^((z - m) c), w = sum (z - m) c 2^((z - m) c):
-//   ln p(t) = ln2 ((z_t - m) c - log2 s),   entropy = ln2 (log2 s - w / s),
+// With c = log2(e) / T, a number k near the largest z c, y = z c - k, s = sum 2^y, w = sum y 2^y:
+//   ln p(t) = ln2 (y_t - log2 s),   entropy = ln2 (log2 s - w / s),
 //   rank(t) = #{z > z_t} + #{i < t: z_i = z_t}.
-// A thread keeps m, s and w of what it has read (s and w move to a new m when it
-// rises); parts meet in a fixed order.  (z - m) c is a difference first, so equal
-// large logits lose nothing, and is cut at -160, where the exponential is 0: tokens
-// of -inf cost no test.  A NaN reaches s.
+// A thread keeps k, s and w of what it has read (k = m c rounded, m its largest
+// logit so far; s and w move with it); parts meet in a fixed order.  k is a
+// number like any other, so y = fma(z, c, -k) rounds once.  Logits are cut at
+// -1e30, where the exponential is 0 (0 * -inf would be NaN): tokens of -inf or of
+// the type's lowest value cost no test and are nobody's m.  A NaN reaches s.  A row
+// whose largest logit is itself below -1e29, or whose products would pass fp32's
+// range, is summed again by a loop that takes differences first.
 // The first n tokens: each CTA collects candidates in shared memory, those that its
 // threshold lets through.  The threshold starts from the first stage: each of
 // the 8 warps gives the k-th largest of its lanes' maxima, k = ceil(n / 8); at
@@ -34,11 +37,11 @@ using namespace ssd;
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kMaxTop = 64;
-constexpr int kStageBytes = 16384, kStageVecs = kStageBytes / 16, kStages = 4;
+constexpr int kStageBytes = 32768, kStageVecs = kStageBytes / 16, kStages = 2;
 constexpr int kVecs = kStageVecs / kThreads;  // of a thread and stage
-constexpr int kRoom = 1024, kCompact = 512;   // candidates: room, and from when on they are reduced to n
+constexpr int kRoom = 1024;  // of candidates
 constexpr int kMaxCluster = 8;
-constexpr float kCut = -160.f;
+constexpr float kCut = -1e30f, kLow = -1e29f, kHigh = 1e30f, kSteep = 1e7f;
 
 struct Args {
   const void *z;
@@ -53,16 +56,17 @@ struct Args {
 };
 
 struct Part {
-  float m, s, w;
+  float most, m, s, w;  // the largest logit; the largest above kLow, around which s and w are
   int before, count;
 };
 struct Shared {
   uint64_t cand[kRoom], best[kMaxTop];
   uint64_t full[kStages];
-  float red[kWarps][3];
+  float4 red[kWarps];
   uint32_t low[kWarps];
   int before[kWarps];
-  int count, found;
+  int count[3];  // candidates of a stage, by stage mod 3
+  int found;
   Part part;
   Part all[kMaxCluster];
 };
@@ -89,6 +93,21 @@ SSD_DEV float max_nan(float a, float b) {  // NaN if either is
   float r;
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
   return r;
+}
+SSD_DEV uint32_t max_nan2(uint32_t a, uint32_t b) {  // of bf16 pairs
+  uint32_t r;
+  asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+// a vector's elements, none below kCut
+template <class E>
+SSD_DEV uint4 cut(const uint4 &v) {
+  if (E::kSize == 2) {
+    const uint32_t low = 0xF149F149u;  // -1e30 in bf16
+    return make_uint4(max_nan2(v.x, low), max_nan2(v.y, low), max_nan2(v.z, low), max_nan2(v.w, low));
+  }
+  auto one = [](uint32_t x) { return __float_as_uint(max_nan(__uint_as_float(x), kCut)); };
+  return make_uint4(one(v.x), one(v.y), one(v.z), one(v.w));
 }
 SSD_DEV uint32_t ord(float x) { return f2ord(x + 0.f); }  // -0 and 0 rank alike
 // the next larger value of the type, as fp32
@@ -142,7 +161,6 @@ SSD_DEV int keep_best(Shared &sh, int c, int n) {
   __syncthreads();
   const int left = min(c, n);
   if (threadIdx.x < left) sh.cand[threadIdx.x] = sh.best[threadIdx.x];
-  if (threadIdx.x == 0) sh.count = left;
   __syncthreads();
   return left;
 }
@@ -171,48 +189,64 @@ __global__ void __launch_bounds__(kThreads) k_token_logprobs(const __grid_consta
     fence_mbar_init();
     fence_proxy_async();
     for (int i = 0; i < min(kStages, nst); ++i) load(i);
-    sh.count = 0;
+    sh.count[0] = sh.count[1] = sh.count[2] = 0;
   }
   const bool ranked = given && good && (a.rank || (a.logprob && a.greedy));
   const float zt = given && good ? E::ld(z, t) : 0.f, zt_above = above<E>(zt);
   const float c = a.c;
   const uint64_t c2 = pack2(c, c);
-  float m = -INF;
-  uint64_t s2 = 0, w2 = 0, neg_m2 = 0;  // of a thread without a finite element m counts as 0
+  float most = -INF, m = -INF, k = 0.f;  // the largest logit; the largest above kLow, and m c
+  uint64_t s2 = 0, w2 = 0, neg_k2 = 0;
   int before = 0;
   auto rise = [&](float to) {  // a larger m
+    const float kn = __fmul_rn(to, c);
     if (m != -INF) {
-      const float d = (m - to) * c, f = ex2(d);
-      const float dd = f == 0.f ? 0.f : d;
-      w2 = mul2(fma2(pack2(dd, dd), s2, w2), pack2(f, f));
+      const float d = k - kn, f = ex2(d);
       s2 = mul2(s2, pack2(f, f));
+      w2 = f == 0.f ? s2 : fma2(pack2(d, d), s2, mul2(w2, pack2(f, f)));  // d may be anything
     }
     m = to;
-    neg_m2 = pack2(-to, -to);
+    k = kn;
+    neg_k2 = pack2(-kn, -kn);
   };
   auto add_pair = [&](uint64_t x) {
+    const uint64_t y = fma2(x, c2, neg_k2);
     float y0, y1;
-    unpack2(mul2(add2(x, neg_m2), c2), y0, y1);
-    y0 = max_nan(y0, kCut);
-    y1 = max_nan(y1, kCut);
+    unpack2(y, y0, y1);
     const uint64_t e = pack2(ex2(y0), ex2(y1));
     s2 = add2(s2, e);
-    w2 = fma2(e, pack2(y0, y1), w2);
+    w2 = fma2(e, y, w2);
   };
-  uint32_t least = 0;  // the order of the smallest value that passes
+  float least = -INF;  // the smallest value that passes
+  int kept = 0, turn = 0;  // candidates of the stages before; which counter this one has
   auto append = [&](float x, int i) {
-    const int at = atomicAdd(&sh.count, 1);
+    const int at = kept + atomicAdd(&sh.count[turn], 1);
     if (at < kRoom) sh.cand[at] = cand_key(x + 0.f, i);
   };
-  auto append_vec = [&](const uint4 &v, int i0) {
-    float x[E::kVec];
-    E::unpack(v, x);
-#pragma unroll 1
-    for (int e = 0; e < E::kVec; ++e) {
-      float y = x[0];
+  // the elements of a vector that pass (element e at bit e, or pairs at bits e / 2 and 16 + e / 2), read again one by one
+  auto append_vec = [&](const uint4 &v, const uint4 *at, int i0) {
+    uint32_t mask = 0;
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    if (E::kSize == 2) {
+      const __nv_bfloat162 least2 = __float2bfloat162_rn(least);
 #pragma unroll
-      for (int k = 1; k < E::kVec; ++k) y = e == k ? x[k] : y;
-      if (ord(y) >= least) append(y, i0 + e);
+      for (int h = 0; h < 4; ++h) {
+        __nv_bfloat162 x;
+        *reinterpret_cast<uint32_t *>(&x) = w[h];
+        mask |= __hge2_mask(x, least2) & (0x00010001u << h);
+      }
+    } else {
+#pragma unroll
+      for (int h = 0; h < 4; ++h) mask |= (__uint_as_float(w[h]) >= least ? 1u : 0u) << h;
+    }
+    for (; mask; mask &= mask - 1) {
+      const int b = __ffs(mask) - 1;
+      if (E::kSize == 2) {
+        const int e = 2 * (b & 15) + (b >> 4);
+        append(__uint_as_float(static_cast<uint32_t>(reinterpret_cast<const uint16_t *>(at)[e]) << 16), i0 + e);
+      } else {
+        append(reinterpret_cast<const float *>(at)[b], i0 + b);
+      }
     }
   };
   __syncthreads();
@@ -220,45 +254,56 @@ __global__ void __launch_bounds__(kThreads) k_token_logprobs(const __grid_consta
     const int i = nv * E::kVec + tid;
     if (i < a.V) {
       const float x = E::ld(z, i);
-      if (x > m) rise(x);
-      // the pair's other half adds nothing
-      float y = max_nan((x + (m == -INF ? 0.f : -m)) * c, kCut);
-      const float e = ex2(y);
-      s2 = add2(s2, pack2(e, 0.f));
-      w2 = fma2(pack2(e, 0.f), pack2(y, 0.f), w2);
+      most = x;
+      if (x > kLow) rise(x);
+      add_pair(pack2(max_nan(x, kCut), kCut));  // the pair's other half adds nothing
       if (ranked) before += i < t ? x >= zt : x > zt;
       if (a.n > 0) append(x, i);
     }
   }
   bool ok = true;
-  int kept = 0;  // candidates that the stages before left
   __syncthreads();
+  if (a.n > 0) {
+    kept = sh.count[0];
+    turn = 1;
+  }
   for (int st = 0; st < nst; ++st) {
     const int first = v0 + st * kStageVecs, count = min(kStageVecs, v1 - first);
     const uint4 *const buf = reinterpret_cast<const uint4 *>(ring + (st % kStages) * kStageBytes);
     ok = mbar_wait(&sh.full[st % kStages], (st / kStages) & 1) && ok;
-    if (a.n > 0) kept = sh.count;  // all threads, before the first candidate of this stage (a barrier ended the last one)
+    uint4 v[kVecs];
     float top = -INF;  // of this thread's elements of the stage
-    bool any = false;
-    Counter k{__float2bfloat162_rn(0.f), 0};
-    if (a.n > 0 && st > 0) __syncthreads();
+    const bool whole = count == kStageVecs, any = tid < count;
 #pragma unroll
     for (int q = 0; q < kVecs; ++q) {
       const int j = q * kThreads + tid;
-      if (j >= count) break;
-      const uint4 v = buf[j];
-      const float vm = vec_max<E>(v);
-      top = fmaxf(top, vm);
-      any = true;
-      if (vm > m) rise(vm);
-#pragma unroll
-      for (int h = 0; h < E::kPairs; ++h) add_pair(E::pair(v, h));
-      const int i0 = (first + j) * E::kVec;
-      if (ranked) count_from<E>(v, i0 + E::kVec <= t ? zt : zt_above, k);
-      if (st > 0 && a.n > 0 && ord(vm) >= least) append_vec(v, i0);
+      v[q] = whole || j < count ? buf[j] : E::nothing();
+      top = fmaxf(top, vec_max<E>(v[q]));
     }
-    if (ranked)
-      before += k.n + static_cast<int>(__low2float(k.pair)) + static_cast<int>(__high2float(k.pair));
+    most = fmaxf(most, top);
+    if (top > m && top > kLow) rise(top);
+    if (ranked && top >= zt) {
+      Counter n{__float2bfloat162_rn(0.f), 0};
+#pragma unroll
+      for (int q = 0; q < kVecs; ++q) {
+        const int j = q * kThreads + tid, i0 = (first + j) * E::kVec;
+        if (whole || j < count) count_from<E>(v[q], i0 + E::kVec <= t ? zt : zt_above, n);
+      }
+      before += n.n + static_cast<int>(__low2float(n.pair)) + static_cast<int>(__high2float(n.pair));
+    }
+    if (a.n > 0 && st > 0 && top >= least) {
+#pragma unroll
+      for (int q = 0; q < kVecs; ++q) {
+        const int j = q * kThreads + tid;
+        if ((whole || j < count) && vec_max<E>(v[q]) >= least) append_vec(v[q], buf + j, (first + j) * E::kVec);
+      }
+    }
+#pragma unroll
+    for (int q = 0; q < kVecs; ++q) {
+      const uint4 x = cut<E>(v[q]);
+#pragma unroll
+      for (int h = 0; h < E::kPairs; ++h) add_pair(E::pair(x, h));
+    }
     if (a.n > 0) {
       if (st == 0) {  // the first threshold
         uint32_t mine = any ? ord(top) : 0u, kth = 0;
@@ -270,15 +315,18 @@ __global__ void __launch_bounds__(kThreads) k_token_logprobs(const __grid_consta
         }
         if (lane == 0) sh.low[warp] = kth;
         __syncthreads();
-        least = sh.low[0];
-        for (int i = 1; i < kWarps; ++i) least = min(least, sh.low[i]);
+        uint32_t low = sh.low[0];
+        for (int i = 1; i < kWarps; ++i) low = min(low, sh.low[i]);
+        least = low == 0 ? -INF : ord2f(low);  // 0: a lane without an element, all pass
         for (int j = tid; j < count; j += kThreads) {
           const uint4 v = buf[j];
-          if (ord(vec_max<E>(v)) >= least) append_vec(v, (first + j) * E::kVec);
+          if (vec_max<E>(v) >= least) append_vec(v, buf + j, (first + j) * E::kVec);
         }
       }
-      __syncthreads();
-      int now = sh.count;
+      __syncthreads();  // the only one of most stages: who is behind may still read this counter when the next stage's rises
+      int now = kept + sh.count[turn];
+      turn = turn == 2 ? 0 : turn + 1;
+      if (tid == 0) sh.count[turn == 2 ? 0 : turn + 1] = 0;  // the stage after next's
       if (now > kRoom) {
         // Too many: the n-th largest key of what was kept and this stage, from the highest bit down.  (The candidates of
         // this stage are dropped and found again.)
@@ -305,24 +353,26 @@ __global__ void __launch_bounds__(kThreads) k_token_logprobs(const __grid_consta
           const uint64_t with = key | 1ull << b;
           if (reach(with) >= a.n) key = with;
         }
-        if (tid == 0) sh.count = kept;
+        if (tid == 0) sh.found = 0;
         __syncthreads();
         for (int j = tid; j < count * E::kVec; j += kThreads) {
           const int i = first * E::kVec + j;
           const float x = E::kSize == 2 ? __uint_as_float(static_cast<uint32_t>(reinterpret_cast<const uint16_t *>(buf)[j]) << 16)
                                         : reinterpret_cast<const float *>(buf)[j];
-          if (cand_key(x + 0.f, i) >= key) append(x, i);
+          if (cand_key(x + 0.f, i) >= key) sh.cand[kept + atomicAdd(&sh.found, 1)] = cand_key(x + 0.f, i);
         }
         __syncthreads();
-        now = sh.count;  // at most kept + n <= kRoom
+        now = kept + sh.found;  // at most kept + n <= kRoom
       }
-      if (st == 0 || now > kCompact) {
+      if (st == 0 || now > 2 * a.n + 16) {
         now = keep_best(sh, now, a.n);
         // only larger values pass from here on; until there are n, all do
-        least = now == a.n ? static_cast<uint32_t>(sh.cand[a.n - 1] >> 32) + 1u : 0u;
+        least = now == a.n ? above<E>(cand_val(sh.cand[a.n - 1])) : -INF;
       }
+      kept = now;
+    } else {
+      __syncthreads();
     }
-    __syncthreads();
     if (tid == 0 && st + kStages < nst) load(st + kStages);
   }
   // equal logits before the token in its own vector, which was counted as if they ranked behind it
@@ -333,43 +383,40 @@ __global__ void __launch_bounds__(kThreads) k_token_logprobs(const __grid_consta
   }
   // ---------------- the CTA's part
   {
-    const float M = warp_max(m);
+    const float M = warp_max(most), W = warp_max(m);  // W: the warp's largest m
     float s0, s1, w0, w1;
     unpack2(s2, s0, s1);
     unpack2(w2, w0, w1);
-    auto move = [&](float from, float to, float &s, float &w) {
+    auto move = [&](float from, float to, float &s, float &w) {  // sums around `from` c to `to` c
       if (from == -INF || from == to) return;
-      const float d = (from - to) * c, f = ex2(d);
-      w = f == 0.f ? 0.f : f * fmaf(d, s, w);
+      const float d = __fmul_rn(from, c) - __fmul_rn(to, c), f = ex2(d);
       s = s * f;
+      w = f == 0.f ? s : fmaf(d, s, w * f);
     };
     float s = s0 + s1, w = w0 + w1;
-    move(m, M, s, w);
+    move(m, W, s, w);
     s = warp_sum(s);
     w = warp_sum(w);
     const int b = __reduce_add_sync(0xffffffffu, before);
     if (lane == 0) {
-      sh.red[warp][0] = M;
-      sh.red[warp][1] = s;
-      sh.red[warp][2] = w;
+      sh.red[warp] = make_float4(M, W, s, w);
       sh.before[warp] = b;
     }
     __syncthreads();
     if (tid == 0) {
-      Part p{-INF, 0.f, 0.f, 0, 0};
-      for (int i = 0; i < kWarps; ++i) p.m = fmaxf(p.m, sh.red[i][0]);
+      Part p{-INF, -INF, 0.f, 0.f, 0, 0};
+      for (int i = 0; i < kWarps; ++i) p.most = fmaxf(p.most, sh.red[i].x), p.m = fmaxf(p.m, sh.red[i].y);
       for (int i = 0; i < kWarps; ++i) {
-        float si = sh.red[i][1], wi = sh.red[i][2];
-        move(sh.red[i][0], p.m, si, wi);
+        float si = sh.red[i].z, wi = sh.red[i].w;
+        move(sh.red[i].y, p.m, si, wi);
         p.s += si;
         p.w += wi;
         p.before += sh.before[i];
       }
-      p.count = sh.count;
       sh.part = p;
     }
     if (a.n > 0) {
-      const int left = keep_best(sh, sh.count, a.n);
+      const int left = keep_best(sh, kept, a.n);
       if (tid == 0) sh.part.count = left;
     }
     __syncthreads();
@@ -379,9 +426,9 @@ __global__ void __launch_bounds__(kThreads) k_token_logprobs(const __grid_consta
       if (part == 0) {
         if (tid < a.cw) {
           const uint32_t from = peer_address(&sh.part, tid);
-          sh.all[tid] = Part{__uint_as_float(peer_u32(from)), __uint_as_float(peer_u32(from + 4)),
-                             __uint_as_float(peer_u32(from + 8)), static_cast<int>(peer_u32(from + 12)),
-                             static_cast<int>(peer_u32(from + 16))};
+          sh.all[tid] = Part{__uint_as_float(peer_u32(from)),      __uint_as_float(peer_u32(from + 4)),
+                             __uint_as_float(peer_u32(from + 8)),  __uint_as_float(peer_u32(from + 12)),
+                             static_cast<int>(peer_u32(from + 16)), static_cast<int>(peer_u32(from + 20))};
         }
         __syncthreads();
         int at = sh.all[0].count;
@@ -392,8 +439,8 @@ __global__ void __launch_bounds__(kThreads) k_token_logprobs(const __grid_consta
           at += n;
         }
         if (tid == 0) {
-          Part p{-INF, 0.f, 0.f, 0, 0};
-          for (int r = 0; r < a.cw; ++r) p.m = fmaxf(p.m, sh.all[r].m);
+          Part p{-INF, -INF, 0.f, 0.f, 0, 0};
+          for (int r = 0; r < a.cw; ++r) p.most = fmaxf(p.most, sh.all[r].most), p.m = fmaxf(p.m, sh.all[r].m);
           for (int r = 0; r < a.cw; ++r) {
             move(sh.all[r].m, p.m, sh.all[r].s, sh.all[r].w);
             p.s += sh.all[r].s;
@@ -409,15 +456,34 @@ __global__ void __launch_bounds__(kThreads) k_token_logprobs(const __grid_consta
   }
   if (part == 0) {
     const Part p = sh.part;
-    const bool none = !(p.s == p.s) || p.m == INF || p.m == -INF;  // no distribution
-    const float ls = log2f(p.s), ln2 = 0.69314718055994531f;
+    // the row's sums around its largest logit, or, where these are out of the loop's range, again
+    float total = p.s, moment = p.w, k_row = __fmul_rn(p.most, c);
+    const bool again = !(p.most > kLow) || !(fabsf(k_row) < kHigh) || !(c < kSteep);
+    if (again) {
+      float s = 0.f, w = 0.f;
+      for (int i = tid; i < a.V; i += kThreads) {
+        const float x = E::ld(z, i), y = max_nan((x - p.most) * c, -160.f), e = ex2(y);
+        s += e;
+        w = fmaf(e, y, w);
+      }
+      s = warp_sum(s);
+      w = warp_sum(w);
+      __syncthreads();
+      if (lane == 0) sh.red[warp] = make_float4(s, w, 0.f, 0.f);
+      __syncthreads();
+      total = moment = 0.f;
+      for (int i = 0; i < kWarps; ++i) total += sh.red[i].x, moment += sh.red[i].y;
+    }
+    auto log2_of = [&](float x) { return again ? (x - p.most) * c : fmaf(x, c, -k_row); };  // of its term
+    const bool none = !(total == total) || p.most == INF || p.most == -INF;  // no distribution
+    const float ls = log2f(total), ln2 = 0.69314718055994531f;
     if (tid == 0) {
       const uint32_t flags = (none ? kFlagBadValue : 0u) | (good ? 0u : kFlagBadToken);
       if (flags) atomicOr(a.status, flags);
       if (a.logprob)
-        a.logprob[row] = none || !good ? NAN_ : (a.greedy ? (p.before == 0 ? 0.f : -INF) : ((zt - p.m) * c - ls) * ln2);
+        a.logprob[row] = none || !good ? NAN_ : (a.greedy ? (p.before == 0 ? 0.f : -INF) : (log2_of(zt) - ls) * ln2);
       if (a.rank) a.rank[row] = none || !good ? -1 : p.before;
-      if (a.entropy) a.entropy[row] = none ? NAN_ : (a.greedy ? 0.f : (ls - p.w / p.s) * ln2);
+      if (a.entropy) a.entropy[row] = none ? NAN_ : (a.greedy ? 0.f : (ls - moment / total) * ln2);
     }
     if (tid < a.n) {
       const uint64_t key = sh.cand[tid];
@@ -425,7 +491,7 @@ __global__ void __launch_bounds__(kThreads) k_token_logprobs(const __grid_consta
       if (a.top_ids) a.top_ids[at] = none ? -1 : cand_idx(key);
       if (a.top_logprob)
         a.top_logprob[at] =
-            none ? NAN_ : (a.greedy ? (tid == 0 ? 0.f : -INF) : ((cand_val(key) - p.m) * c - ls) * ln2);
+            none ? NAN_ : (a.greedy ? (tid == 0 ? 0.f : -INF) : (log2_of(cand_val(key)) - ls) * ln2);
     }
   }
   if (!ok && tid == 0) atomicOr(a.status, kFlagWaitTimeout);
@@ -436,7 +502,7 @@ __global__ void __launch_bounds__(kThreads) k_token_logprobs(const __grid_consta
 int cluster_of(int64_t rows, int V, int64_t size) {
   const int64_t stages = (V * size + kStageBytes - 1) / kStageBytes;
   int cw = 1;
-  while (cw < kMaxCluster && rows * cw < 304 && cw < stages) cw *= 2;
+  while (cw < kMaxCluster && rows * cw < 608 && cw < stages) cw *= 2;
   return cw;
 }
 
