@@ -41,6 +41,7 @@ constexpr int kStageBytes = 32768, kStageVecs = kStageBytes / 16, kStages = 2;
 constexpr int kVecs = kStageVecs / kThreads;  // of a thread and stage
 constexpr int kRoom = 1024;  // of candidates
 constexpr int kMaxCluster = 8;
+static_assert(kMaxCluster <= kWarps, "a warp per CTA");
 constexpr float kCut = -1e30f, kLow = -1e29f, kHigh = 1e30f, kSteep = 1e7f;
 
 struct Args {
@@ -60,7 +61,7 @@ struct Part {
   int before, count;
 };
 struct Shared {
-  uint64_t cand[kRoom], best[kMaxTop];
+  uint64_t cand[kRoom + 8], best[kMaxTop];
   uint64_t full[kStages];
   float4 red[kWarps];
   uint32_t low[kWarps];
@@ -151,11 +152,15 @@ SSD_DEV float vec_max(const uint4 &v) {
 
 // cand[0 .. c) -> its n largest, in order (all threads; c <= kRoom)
 SSD_DEV int keep_best(Shared &sh, int c, int n) {
+  if (threadIdx.x < 8) sh.cand[c + threadIdx.x] = 0;  // smaller than any key
   __syncthreads();
   for (int j = threadIdx.x; j < c; j += kThreads) {
     const uint64_t key = sh.cand[j];
     int r = 0;
-    for (int i = 0; i < c; ++i) r += sh.cand[i] > key;
+    for (int i = 0; i < c; i += 8) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) r += sh.cand[i + k] > key;
+    }
     if (r < n) sh.best[r] = key;
   }
   __syncthreads();
@@ -219,12 +224,8 @@ __global__ void __launch_bounds__(kThreads) k_token_logprobs(const __grid_consta
   };
   float least = -INF;  // the smallest value that passes
   int kept = 0, turn = 0;  // candidates of the stages before; which counter this one has
-  auto append = [&](float x, int i) {
-    const int at = kept + atomicAdd(&sh.count[turn], 1);
-    if (at < kRoom) sh.cand[at] = cand_key(x + 0.f, i);
-  };
-  // the elements of a vector that pass (element e at bit e, or pairs at bits e / 2 and 16 + e / 2), read again one by one
-  auto append_vec = [&](const uint4 &v, const uint4 *at, int i0) {
+  // a vector's elements that pass: element e at bit e, or pairs at bits e / 2 and 16 + e / 2
+  auto passing = [&](const uint4 &v) {
     uint32_t mask = 0;
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
     if (E::kSize == 2) {
@@ -239,15 +240,7 @@ __global__ void __launch_bounds__(kThreads) k_token_logprobs(const __grid_consta
 #pragma unroll
       for (int h = 0; h < 4; ++h) mask |= (__uint_as_float(w[h]) >= least ? 1u : 0u) << h;
     }
-    for (; mask; mask &= mask - 1) {
-      const int b = __ffs(mask) - 1;
-      if (E::kSize == 2) {
-        const int e = 2 * (b & 15) + (b >> 4);
-        append(__uint_as_float(static_cast<uint32_t>(reinterpret_cast<const uint16_t *>(at)[e]) << 16), i0 + e);
-      } else {
-        append(reinterpret_cast<const float *>(at)[b], i0 + b);
-      }
-    }
+    return mask;
   };
   __syncthreads();
   if (part == a.cw - 1) {  // the elements behind the last whole vector: candidates in any case
@@ -258,9 +251,13 @@ __global__ void __launch_bounds__(kThreads) k_token_logprobs(const __grid_consta
       if (x > kLow) rise(x);
       add_pair(pack2(max_nan(x, kCut), kCut));  // the pair's other half adds nothing
       if (ranked) before += i < t ? x >= zt : x > zt;
-      if (a.n > 0) append(x, i);
+      if (a.n > 0) sh.cand[atomicAdd(&sh.count[0], 1)] = cand_key(x + 0.f, i);
     }
   }
+  auto element = [](const uint4 *buf, int j) {  // of a stage
+    return E::kSize == 2 ? __uint_as_float(static_cast<uint32_t>(reinterpret_cast<const uint16_t *>(buf)[j]) << 16)
+                         : reinterpret_cast<const float *>(buf)[j];
+  };
   bool ok = true;
   __syncthreads();
   if (a.n > 0) {
@@ -291,19 +288,6 @@ __global__ void __launch_bounds__(kThreads) k_token_logprobs(const __grid_consta
       }
       before += n.n + static_cast<int>(__low2float(n.pair)) + static_cast<int>(__high2float(n.pair));
     }
-    if (a.n > 0 && st > 0 && top >= least) {
-#pragma unroll
-      for (int q = 0; q < kVecs; ++q) {
-        const int j = q * kThreads + tid;
-        if ((whole || j < count) && vec_max<E>(v[q]) >= least) append_vec(v[q], buf + j, (first + j) * E::kVec);
-      }
-    }
-#pragma unroll
-    for (int q = 0; q < kVecs; ++q) {
-      const uint4 x = cut<E>(v[q]);
-#pragma unroll
-      for (int h = 0; h < E::kPairs; ++h) add_pair(E::pair(x, h));
-    }
     if (a.n > 0) {
       if (st == 0) {  // the first threshold
         uint32_t mine = any ? ord(top) : 0u, kth = 0;
@@ -318,11 +302,43 @@ __global__ void __launch_bounds__(kThreads) k_token_logprobs(const __grid_consta
         uint32_t low = sh.low[0];
         for (int i = 1; i < kWarps; ++i) low = min(low, sh.low[i]);
         least = low == 0 ? -INF : ord2f(low);  // 0: a lane without an element, all pass
-        for (int j = tid; j < count; j += kThreads) {
-          const uint4 v = buf[j];
-          if (vec_max<E>(v) >= least) append_vec(v, buf + j, (first + j) * E::kVec);
+      }
+      // one atomic per warp: its trip is what an append waits for
+      if (__any_sync(0xffffffffu, top >= least)) {
+        uint32_t mask[kVecs];
+        int mine = 0;
+#pragma unroll
+        for (int q = 0; q < kVecs; ++q) {
+          mask[q] = whole || q * kThreads + tid < count ? passing(v[q]) : 0u;
+          mine += __popc(mask[q]);
+        }
+        int upto = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int x = __shfl_up_sync(0xffffffffu, upto, o);
+          if (lane >= o) upto += x;
+        }
+        int at = 0;
+        if (lane == 31) at = atomicAdd(&sh.count[turn], upto);
+        at = kept + __shfl_sync(0xffffffffu, at, 31) + upto - mine;
+#pragma unroll
+        for (int q = 0; q < kVecs; ++q) {
+          const int j = q * kThreads + tid;
+          for (uint32_t left = mask[q]; left; left &= left - 1, ++at) {
+            const int b = __ffs(left) - 1, e = E::kSize == 2 ? 2 * (b & 15) + (b >> 4) : b;
+            const float x = element(buf, j * E::kVec + e);
+            if (at < kRoom) sh.cand[at] = cand_key(x + 0.f, (first + j) * E::kVec + e);
+          }
         }
       }
+    }
+#pragma unroll
+    for (int q = 0; q < kVecs; ++q) {
+      const uint4 x = cut<E>(v[q]);
+#pragma unroll
+      for (int h = 0; h < E::kPairs; ++h) add_pair(E::pair(x, h));
+    }
+    if (a.n > 0) {
       __syncthreads();  // the only one of most stages: who is behind may still read this counter when the next stage's rises
       int now = kept + sh.count[turn];
       turn = turn == 2 ? 0 : turn + 1;
@@ -335,8 +351,7 @@ __global__ void __launch_bounds__(kThreads) k_token_logprobs(const __grid_consta
           int r = 0;
           for (int j = tid; j < count * E::kVec; j += kThreads) {
             const int i = first * E::kVec + j;
-            const float x = E::kSize == 2 ? __uint_as_float(static_cast<uint32_t>(reinterpret_cast<const uint16_t *>(buf)[j]) << 16)
-                                          : reinterpret_cast<const float *>(buf)[j];
+            const float x = element(buf, j);
             r += cand_key(x + 0.f, i) >= from;
           }
           for (int j = tid; j < kept; j += kThreads) r += sh.cand[j] >= from;
@@ -357,8 +372,7 @@ __global__ void __launch_bounds__(kThreads) k_token_logprobs(const __grid_consta
         __syncthreads();
         for (int j = tid; j < count * E::kVec; j += kThreads) {
           const int i = first * E::kVec + j;
-          const float x = E::kSize == 2 ? __uint_as_float(static_cast<uint32_t>(reinterpret_cast<const uint16_t *>(buf)[j]) << 16)
-                                        : reinterpret_cast<const float *>(buf)[j];
+          const float x = element(buf, j);
           if (cand_key(x + 0.f, i) >= key) sh.cand[kept + atomicAdd(&sh.found, 1)] = cand_key(x + 0.f, i);
         }
         __syncthreads();
@@ -431,11 +445,11 @@ __global__ void __launch_bounds__(kThreads) k_token_logprobs(const __grid_consta
                              static_cast<int>(peer_u32(from + 16)), static_cast<int>(peer_u32(from + 20))};
         }
         __syncthreads();
-        int at = sh.all[0].count;
-        for (int r = 1; r < a.cw; ++r) {
-          const uint32_t from = peer_address(sh.cand, r);
+        int at = 0;  // a warp per CTA: one trip for all of them
+        for (int r = 0; r < a.cw; ++r) {
           const int n = sh.all[r].count;
-          for (int j = tid; j < n; j += kThreads) sh.cand[at + j] = peer_u64(from + 8 * j);
+          if (warp == r && r > 0)
+            for (int j = lane; j < n; j += 32) sh.cand[at + j] = peer_u64(peer_address(sh.cand, r) + 8 * j);
           at += n;
         }
         if (tid == 0) {
