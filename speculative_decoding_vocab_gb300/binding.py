@@ -701,13 +701,22 @@ def ssd_branch_attention_q8(q, k_cache, v_cache, k_scale, v_scale, block_table, 
 # ---------------------------------------------------------------------------
 # the 4-bit cache of the branch decode
 # ---------------------------------------------------------------------------
-def _q4_cache(k_cache, v_cache, k_scale, v_scale, Hkv, d, dev):
-    """Checks the 4-bit cache's tensors; returns their addresses and the number of blocks."""
-    nb = k_cache.shape[0]
+def _q4_misfit(k_cache, v_cache, k_scale, v_scale, nb, Hkv, d, dev):
+    """Whether a tensor of the 4-bit cache is not the dense uint8 tensor that its place asks for."""
     u8 = torch.uint8
-    return (_dense(k_cache, u8, (nb, Hkv, 16, d // 2), dev, "k_cache"), _dense(v_cache, u8, (nb, Hkv, 8, d), dev, "v_cache"),
-            _dense(k_scale, u8, (nb, Hkv, 16, d // 32), dev, "k_scale"),
-            _dense(v_scale, u8, (nb, Hkv, 16, d // 32), dev, "v_scale")), nb
+    scales = (nb, Hkv, 16, d >> 5)
+    return (k_cache.dtype is not u8 or k_cache.shape != (nb, Hkv, 16, d >> 1) or not k_cache.is_contiguous()
+            or v_cache.dtype is not u8 or v_cache.shape != (nb, Hkv, 8, d) or not v_cache.is_contiguous()
+            or k_scale.dtype is not u8 or k_scale.shape != scales or not k_scale.is_contiguous()
+            or v_scale.dtype is not u8 or v_scale.shape != scales or not v_scale.is_contiguous()
+            or not (dev == k_cache.get_device() == v_cache.get_device() == k_scale.get_device()
+                    == v_scale.get_device()))
+
+
+def _q4_tensors(k_cache, v_cache, k_scale, v_scale, nb, Hkv, d):
+    u8 = torch.uint8
+    return ((k_cache, u8, (nb, Hkv, 16, d // 2), "k_cache"), (v_cache, u8, (nb, Hkv, 8, d), "v_cache"),
+            (k_scale, u8, (nb, Hkv, 16, d // 32), "k_scale"), (v_scale, u8, (nb, Hkv, 16, d // 32), "v_scale"))
 
 
 def q4_cache(num_blocks, Hkv, d, device="cuda"):
@@ -724,23 +733,30 @@ def ssd_kv_append_q4(k_new, v_new, k_cache, v_cache, k_scale, v_scale, block_tab
     (rows i >= count[b] are left out)."""
     rows = k_new.shape
     B, S, Hkv, d = rows
+    nb = k_cache.shape[0]
     maxb = block_table.shape[1]
     dev = k_cache.get_device()
     i32, bf16 = torch.int32, torch.bfloat16
     kss, kts, khs, kes = k_new.stride()
     vss, vts, vhs, ves = v_new.stride()
-    if k_new.dtype is not bf16 or v_new.dtype is not bf16 or v_new.shape != rows:
-        raise ValueError(f"k_new and v_new must be {bf16} tensors of one shape")
+    # heads of a token contiguous
     if (kes != 1 and d > 1) or (khs != d and Hkv > 1) or (ves != 1 and d > 1) or (vhs != d and Hkv > 1):
         raise ValueError("k_new and v_new: the heads of a token must be contiguous")
-    if not (dev == k_new.get_device() == v_new.get_device()):
-        raise ValueError("all tensors of a call must live on one device")
-    cache, nb = _q4_cache(k_cache, v_cache, k_scale, v_scale, Hkv, d, dev)
+    if (k_new.dtype is not bf16 or v_new.dtype is not bf16 or v_new.shape != rows
+            or block_table.dtype is not i32 or block_table.shape[0] != B or not block_table.is_contiguous()
+            or prefix_len.dtype is not i32 or prefix_len.shape != (B,) or not prefix_len.is_contiguous()
+            or not (dev == k_new.get_device() == v_new.get_device() == block_table.get_device()
+                    == prefix_len.get_device())
+            or _q4_misfit(k_cache, v_cache, k_scale, v_scale, nb, Hkv, d, dev)):
+        if k_new.dtype != bf16 or v_new.dtype != bf16 or v_new.shape != rows:
+            raise ValueError(f"k_new and v_new must be {bf16} tensors of one shape")
+        _refuse(dev, *_q4_tensors(k_cache, v_cache, k_scale, v_scale, nb, Hkv, d),
+                (block_table, i32, (B, maxb), "block_table"), (prefix_len, i32, (B,), "prefix_len"))
     _launch("ssd_kv_append_q4", dev, stream,
             k_new.data_ptr(), kss if B > 1 else 0, kts if S > 1 else 0,
-            v_new.data_ptr(), vss if B > 1 else 0, vts if S > 1 else 0, *cache,
-            _dense(block_table, i32, (B, maxb), dev, "block_table"), maxb, nb,
-            _dense(prefix_len, i32, (B,), dev, "prefix_len"), _dense(count, i32, (B,), dev, "count"), int(node0),
+            v_new.data_ptr(), vss if B > 1 else 0, vts if S > 1 else 0,
+            k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+            block_table.data_ptr(), maxb, nb, prefix_len.data_ptr(), _dense(count, i32, (B,), dev, "count"), int(node0),
             B, S, Hkv, d, _dense(status, i32, (1,), dev, "status"))
 
 
@@ -752,21 +768,28 @@ def ssd_kv_read_q4(k_cache, v_cache, k_scale, v_scale, block_table, prefix_len, 
     x = k_out if k_out is not None else v_out
     rows = x.shape
     B, S, Hkv, d = rows
+    nb = k_cache.shape[0]
     maxb = block_table.shape[1]
     dev = k_cache.get_device()
     i32 = torch.int32
     dt = SSD_F32 if x.dtype == torch.float32 else SSD_BF16
     if dt == SSD_BF16 and x.dtype != torch.bfloat16:
         raise ValueError(f"k_out and v_out must be float32 or bfloat16, got {x.dtype}")
-    cache, nb = _q4_cache(k_cache, v_cache, k_scale, v_scale, Hkv, d, dev)
+    if (block_table.dtype is not i32 or block_table.shape[0] != B or not block_table.is_contiguous()
+            or prefix_len.dtype is not i32 or prefix_len.shape != (B,) or not prefix_len.is_contiguous()
+            or not (dev == block_table.get_device() == prefix_len.get_device())
+            or _q4_misfit(k_cache, v_cache, k_scale, v_scale, nb, Hkv, d, dev)):
+        _refuse(dev, *_q4_tensors(k_cache, v_cache, k_scale, v_scale, nb, Hkv, d),
+                (block_table, i32, (B, maxb), "block_table"), (prefix_len, i32, (B,), "prefix_len"))
     outs = []
     for y, what in ((k_out, "k"), (v_out, "v")):
         # an output stands for its own input: the same checks of heads, device and overlap
         outs += (None, 0, 0) if y is None else _rows(y, y, x.dtype, (B, S, d), dev, what)[3:]
         if y is not None and y.shape != rows:
             raise ValueError(f"k_out and v_out must have one shape, got {tuple(rows)} and {tuple(y.shape)}")
-    _launch("ssd_kv_read_q4", dev, stream, *cache, _dense(block_table, i32, (B, maxb), dev, "block_table"), maxb, nb,
-            _dense(prefix_len, i32, (B,), dev, "prefix_len"), _dense(count, i32, (B,), dev, "count"), int(node0),
+    _launch("ssd_kv_read_q4", dev, stream,
+            k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+            block_table.data_ptr(), maxb, nb, prefix_len.data_ptr(), _dense(count, i32, (B,), dev, "count"), int(node0),
             *outs, dt, B, S, Hkv, d, _dense(status, i32, (1,), dev, "status"))
 
 
@@ -779,7 +802,7 @@ def ssd_branch_attention_q4(q, k_cache, v_cache, k_scale, v_scale, block_table, 
     """ssd_branch_attention over the 4-bit caches."""
     rows = q.shape
     B, Nq, Hq, d = rows
-    Hkv = k_cache.shape[1]
+    nb, Hkv = k_cache.shape[:2]
     N = parent.shape[1]
     maxb = block_table.shape[1]
     i32, bf16 = torch.int32, torch.bfloat16
@@ -787,11 +810,21 @@ def ssd_branch_attention_q4(q, k_cache, v_cache, k_scale, v_scale, block_table, 
         scale = d ** -0.5
     dev = q.get_device()
     ws_bytes = 0 if ws is None else ws.numel()
-    cache, nb = _q4_cache(k_cache, v_cache, k_scale, v_scale, Hkv, d, dev)
-    _launch("ssd_branch_attention_q4", dev, stream, _dense(q, bf16, rows, dev, "q"), *cache,
-            _dense(block_table, i32, (B, maxb), dev, "block_table"), maxb, nb,
-            _dense(prefix_len, i32, (B,), dev, "prefix_len"), _dense(parent, i32, (B, N), dev, "parent"),
-            B, N, Nq, Hq, Hkv, d, float(scale), _dense(out, bf16, rows, dev, "out"),
+    if (q.dtype is not bf16 or not q.is_contiguous()
+            or out.dtype is not bf16 or out.shape != rows or not out.is_contiguous()
+            or block_table.dtype is not i32 or block_table.shape[0] != B or not block_table.is_contiguous()
+            or prefix_len.dtype is not i32 or prefix_len.shape != (B,) or not prefix_len.is_contiguous()
+            or parent.dtype is not i32 or parent.shape[0] != B or not parent.is_contiguous()
+            or not (dev == out.get_device() == block_table.get_device() == prefix_len.get_device()
+                    == parent.get_device())
+            or _q4_misfit(k_cache, v_cache, k_scale, v_scale, nb, Hkv, d, dev)):
+        _refuse(dev, (q, bf16, rows, "q"), (out, bf16, rows, "out"),
+                *_q4_tensors(k_cache, v_cache, k_scale, v_scale, nb, Hkv, d),
+                (block_table, i32, (B, maxb), "block_table"), (prefix_len, i32, (B,), "prefix_len"),
+                (parent, i32, (B, N), "parent"))
+    _launch("ssd_branch_attention_q4", dev, stream, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+            k_scale.data_ptr(), v_scale.data_ptr(), block_table.data_ptr(), maxb, nb, prefix_len.data_ptr(),
+            parent.data_ptr(), B, N, Nq, Hq, Hkv, d, float(scale), out.data_ptr(),
             _dense(lse, torch.float32, (B, Nq, Hq), dev, "lse"), _dense(status, i32, (1,), dev, "status"),
             None if ws is None else _dense(ws, torch.uint8, (ws_bytes,), dev, "ws"), ws_bytes)
 

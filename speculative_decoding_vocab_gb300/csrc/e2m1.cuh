@@ -41,10 +41,10 @@ SSD_DEV void e2m1_halves8(uint32_t w, uint32_t *h) {
 SSD_DEV float e8m0_value(uint32_t b) {
   return __uint_as_float(b == 0 ? 0x00400000u : (b == 255 ? 0x7fc00000u : b << 23));
 }
-// the scale byte of a group whose largest magnitude has these fp32 bits: 6 * 2^e = 1.5 * 2^(e + 2)
-SSD_DEV int e8m0_of(uint32_t amax_bits) {
-  const int b = static_cast<int>(amax_bits >> 23) - 2 + ((amax_bits & 0x7FFFFFu) > 0x400000u ? 1 : 0);
-  return min(max(b, kMinScaleByte), kMaxScaleByte);
+// the scale byte of a group whose largest magnitude has these bf16 bits: 6 * 2^e = 1.5 * 2^(e + 2), so the exponent - 2,
+// one more where the fraction is above a half (0x40)
+SSD_DEV uint32_t e8m0_of(uint32_t bits) {
+  return static_cast<uint32_t>(min(max(static_cast<int>((bits + 0x3Fu) >> 7) - 2, kMinScaleByte), kMaxScaleByte));
 }
 
 }  // namespace ssd
