@@ -107,14 +107,13 @@ struct Cfg {
   static constexpr int kGroups = RT / CG;                  // groups of four warps
   static constexpr int NB = 2;                             // S buffers; S runs NB tiles ahead
   static constexpr int kSoftWarps = 4 * kGroups;
-  // helper warps: warp w of the four writes TMEM lanes 32 w .. + 31 (those that a warp of its number modulo 4 reaches)
-  static constexpr int kHelpWarp = kSoftWarps;
-  // two sets of helpers where the registers of 24 warps (80 a thread) allow them, a sub-tile each; and the producers
-  static constexpr int kSets = RT <= 48 ? 2 : 1, kHelpers = 4 * kSets, kTmaWarp = kHelpWarp + kHelpers;
-  static constexpr int kKWarps = RT <= 48 ? 2 : 2, kVWarps = RT <= 32 ? 2 : 1;
-  static constexpr int kMmaWarp = kTmaWarp + kKWarps + kVWarps;
-  static constexpr int kWarps = kMmaWarp + 1;
-  static constexpr int kThreads = kWarps * 32;
+  // The MMA warp and the producers come first: the schedulers prefer older warps, and these few are what all others wait
+  // for.  Then the helpers (warp w of a set's four writes TMEM lanes 32 w .. + 31, those that a warp of its number modulo 4
+  // reaches), with the keys on the wide side in two sets, a sub-tile each, and the softmax warps.
+  static constexpr int kMmaWarp = 0, kTmaWarp = 1, kKWarps = 2, kVWarps = 1;
+  static constexpr int kSets = RT <= 64 ? 2 : 1, kHelpers = 4 * kSets, kHelpWarp = 4, kSoftWarp = kHelpWarp + kHelpers;
+  static constexpr int kWarps = kSoftWarp + kSoftWarps, kThreads = kWarps * 32;
+  static_assert(kTmaWarp + kKWarps + kVWarps == kHelpWarp, "roles");
   // units of a tile; a unit's keys, its rows of 128 elements, its blocks
   static constexpr int kUnits = D == 128 ? KT : 1;
   static constexpr bool kApart = kSets == 2 && kUnits == 2;  // a set has a unit of each tile for itself
@@ -239,7 +238,7 @@ __global__ void __launch_bounds__(Cfg<D, RT>::kThreads, 1)
   };
 
   Segments sg;
-  if (warp >= C::kTmaWarp && warp < C::kMmaWarp) {
+  if (warp >= C::kTmaWarp && warp < C::kHelpWarp) {
     // ---------------- producers: warps for K's codes and both scales, and for V's codes, a unit each in turn (a copy
     // costs its warp 60 to 70 clocks).  Block ids are fetched for kBatch of a warp's units at a time, one batch ahead: lane l
     // holds block l % UP of the batch's unit l / UP.
@@ -429,7 +428,7 @@ __global__ void __launch_bounds__(Cfg<D, RT>::kThreads, 1)
       }
     }
     if (!ok) s_abort = 1;
-  } else if (warp >= C::kHelpWarp && warp < C::kTmaWarp) {
+  } else if (warp >= C::kHelpWarp && warp < C::kSoftWarp) {
     // ---------------- helpers, in the order of the MMAs.  They meet at named barriers, which have no limit, so a warp
     // whose wait gave up goes on (its waits are over at once) until they leave together.
     const int hw = warp & 3, set = (warp - C::kHelpWarp) >> 2, r = hw * 32 + lane;
@@ -442,7 +441,7 @@ __global__ void __launch_bounds__(Cfg<D, RT>::kThreads, 1)
       if (set == 0) tmem_st4(tmem + C::kSfCol + quad, q, q, q, q);
       tmem_wait_st();
       tc_fence_before();
-      prepare(sg, 0, warp, C::kSoftWarps + C::kHelpers, 10);
+      prepare(sg, 0, warp - C::kHelpWarp, C::kSoftWarps + C::kHelpers, 10);
       bar_sync(10, (C::kSoftWarps + C::kHelpers) * 32);
       tc_fence_after();
       tc_fence_before();
@@ -676,7 +675,7 @@ __global__ void __launch_bounds__(Cfg<D, RT>::kThreads, 1)
     if (!ok || !all) s_abort = 1;
   } else if constexpr (C::kRowLanes) {
     // ---------------- softmax, a lane per row: group g has the keys g * 32 .. + 31 of every tile
-    const int g = warp / 4, wg = warp & 3, r = tid & 127;
+    const int g = (warp - C::kSoftWarp) / 4, wg = warp & 3, r = tid & 127;
     const uint32_t lane_off = static_cast<uint32_t>(wg * 32) << 16;
     const uint32_t tS = tmem + g * 32 + lane_off, tO = tmem + C::kOCol + g * (D / 4) + lane_off;
     const int bar = 1 + wg;  // the four warps that share 32 rows
@@ -685,7 +684,7 @@ __global__ void __launch_bounds__(Cfg<D, RT>::kThreads, 1)
     bool dead = false;
     bool more = sg.first(a, piece);
     if (more) {
-      prepare(sg, 0, warp, C::kSoftWarps + C::kHelpers, 10);
+      prepare(sg, 0, warp - C::kHelpWarp, C::kSoftWarps + C::kHelpers, 10);
       bar_sync(10, (C::kSoftWarps + C::kHelpers) * 32);
     }
     for (; more; more = sg.step(a), ++seg) {
@@ -843,7 +842,7 @@ __global__ void __launch_bounds__(Cfg<D, RT>::kThreads, 1)
         break;
       }
       const bool whole = sg.t0 == 0 && sg.t1 == sg.nt, nan = s_nan[seg & 3] != 0;
-      if (tid == 0) s_nan[(seg + 2) & 3] = 0;
+      if (tid == C::kSoftWarp * 32) s_nan[(seg + 2) & 3] = 0;
       if (some) {
         const int slot = blockIdx.x * 2 + (sg.t0 > 0 ? 0 : 1);
         const float L = __fadd_rn(__fadd_rn(red[0][r], red[1][r]), __fadd_rn(red[2][r], red[3][r]));
@@ -898,7 +897,7 @@ __global__ void __launch_bounds__(Cfg<D, RT>::kThreads, 1)
     }
   } else {
     // ---------------- softmax: group g of the rows, one thread per key
-    const int g = warp / 4, wg = warp & 3, tg = tid & 127;
+    const int g = (warp - C::kSoftWarp) / 4, wg = warp & 3, tg = tid & 127;
     const int col = g * CG;
     const uint32_t lane_off = static_cast<uint32_t>(wg * 32) << 16;
     const uint32_t tS = tmem + col + lane_off, tO = tmem + C::kOCol + col + lane_off;
@@ -908,7 +907,7 @@ __global__ void __launch_bounds__(Cfg<D, RT>::kThreads, 1)
     bool dead = false;
     bool more = sg.first(a, piece);
     if (more) {
-      prepare(sg, 0, warp, C::kSoftWarps + C::kHelpers, 10);
+      prepare(sg, 0, warp - C::kHelpWarp, C::kSoftWarps + C::kHelpers, 10);
       bar_sync(10, (C::kSoftWarps + C::kHelpers) * 32);
     }
     for (; more; more = sg.step(a), ++seg) {
@@ -1091,8 +1090,8 @@ __global__ void __launch_bounds__(Cfg<D, RT>::kThreads, 1)
       }
       const bool whole = sg.t0 == 0 && sg.t1 == sg.nt;
       const int slot = blockIdx.x * 2 + (sg.t0 > 0 ? 0 : 1);
-      if (tid == 0) s_nan[(seg + 2) & 3] = 0;
-      for (int r = tid; r < RT; r += kSoftThreads) {
+      if (tid == C::kSoftWarp * 32) s_nan[(seg + 2) & 3] = 0;
+      for (int r = tid - C::kSoftWarp * 32; r < RT; r += kSoftThreads) {
         const float M = s_m[r], L = __fadd_rn(__fadd_rn(red[0][r], red[1][r]), __fadd_rn(red[2][r], red[3][r]));
         s_f[r] = L == 0.f ? 0.f : (whole ? 1.f / L : 1.f) * kOutUnit;
         const int row = mt * RT + r;
