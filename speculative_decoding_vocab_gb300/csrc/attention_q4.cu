@@ -172,8 +172,8 @@ __global__ void __launch_bounds__(Cfg<D, RT>::kThreads, 1)
   constexpr int kSoftThreads = C::kSoftWarps * 32;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t *const smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);  // by an offset: known to be shared memory
-  // Of a tile, by the place of a key's scores (element h * 128 + lane of the S^T pair, or the column of S): t (-1: hidden),
-  // then log2 t
+  // Of a tile, by the place of a key's scores (element h * 128 + lane of the S^T pair, or the column of S): t, then log2 t
+  // (0 and -inf: hidden)
   float *const top = reinterpret_cast<float *>(smem + C::kTop);
   __shared__ __align__(8) uint64_t kfull[NSLOT], kempty[NSLOT], vfull[NSLOT], vempty[NSLOT], kready[C::kSf];
   __shared__ __align__(8) uint64_t sfull[NB], pfull[NB], vready[NB], pvdone[NB], qfull[2], qempty[2];
@@ -509,8 +509,8 @@ __global__ void __launch_bounds__(Cfg<D, RT>::kThreads, 1)
               }
               if (!hidden) x[g >> 1] |= y << ((g & 1) * 16);
             }
-            const float big_of = hidden ? -1.f : __uint_as_float(static_cast<uint32_t>(big) << 23);
-            const float log = hidden ? 0.f : static_cast<float>(big - 127);
+            const float big_of = hidden ? 0.f : __uint_as_float(static_cast<uint32_t>(big) << 23);
+            const float log = hidden ? NEG_INF : static_cast<float>(big - 127);
             if (w == 0) top_of[0] = big_of, log_of[0] = log, f[0] = x[0];
             else top_of[kOf - 1] = big_of, log_of[kOf - 1] = log, f[1] = x[0];
             if (D == 128) f[1] = x[1];
@@ -726,8 +726,8 @@ __global__ void __launch_bounds__(Cfg<D, RT>::kThreads, 1)
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
               const float4 s4 = tops[j];
-              vis &= ~((s4.x < 0.f ? 1u : 0u) << (4 * j) | (s4.y < 0.f ? 2u : 0u) << (4 * j) |
-                       (s4.z < 0.f ? 4u : 0u) << (4 * j) | (s4.w < 0.f ? 8u : 0u) << (4 * j));
+              vis &= ~((s4.x == 0.f ? 1u : 0u) << (4 * j) | (s4.y == 0.f ? 2u : 0u) << (4 * j) |
+                       (s4.z == 0.f ? 4u : 0u) << (4 * j) | (s4.w == 0.f ? 8u : 0u) << (4 * j));
             }
           }
           float y[32];
@@ -737,9 +737,9 @@ __global__ void __launch_bounds__(Cfg<D, RT>::kThreads, 1)
             tmem_ld16_async(tS + u * kSub + 16, y + 16);
             tmem_wait16(y);
             tmem_wait16(y + 16);
-            const uint64_t add2 = pack2(add, add), c2 = pack2(cq, cq);
+            const uint64_t off2 = pack2(add, add), c2 = pack2(cq, cq);
 #pragma unroll
-            for (int j = 0; j < 32; j += 2) unpack2(fma2(pack2(y[j], y[j + 1]), c2, add2), y[j], y[j + 1]);
+            for (int j = 0; j < 32; j += 2) unpack2(fma2(pack2(y[j], y[j + 1]), c2, off2), y[j], y[j + 1]);
             if (part) {
 #pragma unroll
               for (int j = 0; j < 32; ++j) y[j] = ((vis >> j) & 1u) ? y[j] : NEG_INF;
@@ -754,10 +754,11 @@ __global__ void __launch_bounds__(Cfg<D, RT>::kThreads, 1)
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
               const float4 l4 = logs[j];
-              t4[0] = fmaxf(t4[0], y[4 * j] + l4.x);
-              t4[1] = fmaxf(t4[1], y[4 * j + 1] + l4.y);
-              t4[2] = fmaxf(t4[2], y[4 * j + 2] + l4.z);
-              t4[3] = fmaxf(t4[3], y[4 * j + 3] + l4.w);
+              float z[4];
+              unpack2(add2(pack2(y[4 * j], y[4 * j + 1]), pack2(l4.x, l4.y)), z[0], z[1]);
+              unpack2(add2(pack2(y[4 * j + 2], y[4 * j + 3]), pack2(l4.z, l4.w)), z[2], z[3]);
+#pragma unroll
+              for (int k = 0; k < 4; ++k) t4[k] = fmaxf(t4[k], z[k]);
             }
             const float big = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
             if (!bar_or(bar, 128, big > kGrow || unset || !ok)) break;
@@ -806,7 +807,7 @@ __global__ void __launch_bounds__(Cfg<D, RT>::kThreads, 1)
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
             const float4 s4 = tops[j];
-            const uint64_t w2[2] = {pack2(fmaxf(s4.x, 0.f), fmaxf(s4.y, 0.f)), pack2(fmaxf(s4.z, 0.f), fmaxf(s4.w, 0.f))};
+            const uint64_t w2[2] = {pack2(s4.x, s4.y), pack2(s4.z, s4.w)};
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
               const uint64_t p = pack2(ex2(y[4 * j + 2 * k]), ex2(y[4 * j + 2 * k + 1]));
@@ -939,7 +940,7 @@ __global__ void __launch_bounds__(Cfg<D, RT>::kThreads, 1)
         bool hidden[KT], part = false;
 #pragma unroll
         for (int h = 0; h < KT; ++h) {
-          hidden[h] = tops[h * kSub] < 0.f;
+          hidden[h] = tops[h * kSub] == 0.f;
           part = part || hidden[h] || t * C::kKeys + key_of(h) >= sg.L;
         }
         part = __any_sync(0xffffffffu, part);
@@ -1051,7 +1052,7 @@ __global__ void __launch_bounds__(Cfg<D, RT>::kThreads, 1)
         const uint64_t unit2 = pack2(kSumUnit, kSumUnit);
 #pragma unroll
         for (int h = 0; h < KT; ++h) {
-          const float wv = fmaxf(tops[h * kSub], 0.f);
+          const float wv = tops[h * kSub];
           const uint64_t w2 = pack2(wv, wv);
           uint32_t hp[CG / 2];
 #pragma unroll
