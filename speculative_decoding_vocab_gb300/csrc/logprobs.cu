@@ -13,8 +13,8 @@
 // range, is summed again by a loop that takes differences first.
 // The first n tokens: each CTA collects candidates in shared memory, those that its
 // threshold lets through.  The threshold starts from the first stage: each of
-// the 8 warps gives the k-th largest of its lanes' maxima, k = ceil(n / 8); at
-// least n elements reach the least of these.  From then on the n-th candidate so
+// its (up to 8) whole warps gives the k-th largest of its lanes' maxima, k = ceil(n
+// / warps); at least n elements reach the least of these.  From then on the n-th candidate so
 // far is the threshold, and only larger values pass (indices rise along the
 // part, and equal values rank by index).  Keys (value, ~index) are distinct, so their
 // ranks are counted, whatever order they came in.  Where a stage lets more through
@@ -39,9 +39,9 @@ constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kMaxTop = 64;
 constexpr int kStageBytes = 32768, kStageVecs = kStageBytes / 16, kStages = 2;
 constexpr int kVecs = kStageVecs / kThreads;  // of a thread and stage
-constexpr int kRoom = 1024;  // of candidates
+constexpr int kRoom = 512;  // of candidates; at least kMaxCluster * kMaxTop
 constexpr int kMaxCluster = 8;
-static_assert(kMaxCluster <= kWarps, "a warp per CTA");
+static_assert(kMaxCluster <= kWarps && kMaxCluster * kMaxTop <= kRoom, "a warp per CTA, room for their candidates");
 constexpr float kCut = -1e30f, kLow = -1e29f, kHigh = 1e30f, kSteep = 1e7f;
 
 struct Args {
@@ -58,10 +58,10 @@ struct Args {
 
 struct Part {
   float most, m, s, w;  // the largest logit; the largest above kLow, around which s and w are
-  int before, count;
+  int before, count, buffer;  // buffer: which one holds its candidates
 };
 struct Shared {
-  uint64_t cand[kRoom + 8], best[kMaxTop];
+  uint64_t cand[2][kRoom];  // the current ones, and where the best of them go
   uint64_t full[kStages];
   float4 red[kWarps];
   uint32_t low[kWarps];
@@ -150,24 +150,22 @@ SSD_DEV float vec_max(const uint4 &v) {
   return fmaxf(fmaxf(__uint_as_float(v.x), __uint_as_float(v.y)), fmaxf(__uint_as_float(v.z), __uint_as_float(v.w)));
 }
 
-// cand[0 .. c) -> its n largest, in order (all threads; c <= kRoom)
-SSD_DEV int keep_best(Shared &sh, int c, int n) {
-  if (threadIdx.x < 8) sh.cand[c + threadIdx.x] = 0;  // smaller than any key
-  __syncthreads();
+// The n largest of cand[cur][0 .. c) -> the other buffer, in order (all threads; the candidates are written, c <= kRoom)
+SSD_DEV int keep_best(Shared &sh, int &cur, int c, int n) {
+  const uint64_t *const cand = sh.cand[cur];
   for (int j = threadIdx.x; j < c; j += kThreads) {
-    const uint64_t key = sh.cand[j];
-    int r = 0;
-    for (int i = 0; i < c; i += 8) {
+    const uint64_t key = cand[j];
+    int r = 0, i = 0;
+    for (; i + 8 <= c; i += 8) {
 #pragma unroll
-      for (int k = 0; k < 8; ++k) r += sh.cand[i + k] > key;
+      for (int k = 0; k < 8; ++k) r += cand[i + k] > key;
     }
-    if (r < n) sh.best[r] = key;
+    for (; i < c; ++i) r += cand[i] > key;
+    if (r < n) sh.cand[cur ^ 1][r] = key;
   }
   __syncthreads();
-  const int left = min(c, n);
-  if (threadIdx.x < left) sh.cand[threadIdx.x] = sh.best[threadIdx.x];
-  __syncthreads();
-  return left;
+  cur ^= 1;
+  return min(c, n);
 }
 
 template <class E>
@@ -223,7 +221,7 @@ __global__ void __launch_bounds__(kThreads) k_token_logprobs(const __grid_consta
     w2 = fma2(e, y, w2);
   };
   float least = -INF;  // the smallest value that passes
-  int kept = 0, turn = 0;  // candidates of the stages before; which counter this one has
+  int kept = 0, turn = 0, cur = 0;  // candidates of the stages before; which counter this one has; which buffer
   // a vector's elements that pass: element e at bit e, or pairs at bits e / 2 and 16 + e / 2
   auto passing = [&](const uint4 &v) {
     uint32_t mask = 0;
@@ -251,7 +249,7 @@ __global__ void __launch_bounds__(kThreads) k_token_logprobs(const __grid_consta
       if (x > kLow) rise(x);
       add_pair(pack2(max_nan(x, kCut), kCut));  // the pair's other half adds nothing
       if (ranked) before += i < t ? x >= zt : x > zt;
-      if (a.n > 0) sh.cand[atomicAdd(&sh.count[0], 1)] = cand_key(x + 0.f, i);
+      if (a.n > 0) sh.cand[0][atomicAdd(&sh.count[0], 1)] = cand_key(x + 0.f, i);
     }
   }
   auto element = [](const uint4 *buf, int j) {  // of a stage
@@ -270,7 +268,7 @@ __global__ void __launch_bounds__(kThreads) k_token_logprobs(const __grid_consta
     ok = mbar_wait(&sh.full[st % kStages], (st / kStages) & 1) && ok;
     uint4 v[kVecs];
     float top = -INF;  // of this thread's elements of the stage
-    const bool whole = count == kStageVecs, any = tid < count;
+    const bool whole = count == kStageVecs;
 #pragma unroll
     for (int q = 0; q < kVecs; ++q) {
       const int j = q * kThreads + tid;
@@ -290,18 +288,22 @@ __global__ void __launch_bounds__(kThreads) k_token_logprobs(const __grid_consta
     }
     if (a.n > 0) {
       if (st == 0) {  // the first threshold
-        uint32_t mine = any ? ord(top) : 0u, kth = 0;
-        const int rounds = (a.n + kWarps - 1) / kWarps;
-        for (int i = 0; i < rounds; ++i) {
-          kth = __reduce_max_sync(0xffffffffu, mine);
-          const uint32_t who = __ballot_sync(0xffffffffu, mine == kth);
-          if (lane == __ffs(who) - 1) mine = 0;
+        const int warps = min(kThreads, count) / 32;  // those of which every lane has an element
+        const int rounds = warps > 0 ? (a.n + warps - 1) / warps : 33;
+        if (rounds <= 32) {  // else at most 64 vectors: all pass
+          uint32_t mine = ord(top), kth = 0xffffffffu;
+          if (warp < warps)
+            for (int i = 0; i < rounds; ++i) {
+              kth = __reduce_max_sync(0xffffffffu, mine);
+              const uint32_t who = __ballot_sync(0xffffffffu, mine == kth);
+              if (lane == __ffs(who) - 1) mine = 0;
+            }
+          if (lane == 0) sh.low[warp] = kth;
+          __syncthreads();
+          uint32_t low = sh.low[0];
+          for (int i = 1; i < kWarps; ++i) low = min(low, sh.low[i]);
+          least = ord2f(low);
         }
-        if (lane == 0) sh.low[warp] = kth;
-        __syncthreads();
-        uint32_t low = sh.low[0];
-        for (int i = 1; i < kWarps; ++i) low = min(low, sh.low[i]);
-        least = low == 0 ? -INF : ord2f(low);  // 0: a lane without an element, all pass
       }
       // one atomic per warp: its trip is what an append waits for
       if (__any_sync(0xffffffffu, top >= least)) {
@@ -327,7 +329,7 @@ __global__ void __launch_bounds__(kThreads) k_token_logprobs(const __grid_consta
           for (uint32_t left = mask[q]; left; left &= left - 1, ++at) {
             const int b = __ffs(left) - 1, e = E::kSize == 2 ? 2 * (b & 15) + (b >> 4) : b;
             const float x = element(buf, j * E::kVec + e);
-            if (at < kRoom) sh.cand[at] = cand_key(x + 0.f, (first + j) * E::kVec + e);
+            if (at < kRoom) sh.cand[cur][at] = cand_key(x + 0.f, (first + j) * E::kVec + e);
           }
         }
       }
@@ -354,7 +356,7 @@ __global__ void __launch_bounds__(kThreads) k_token_logprobs(const __grid_consta
             const float x = element(buf, j);
             r += cand_key(x + 0.f, i) >= from;
           }
-          for (int j = tid; j < kept; j += kThreads) r += sh.cand[j] >= from;
+          for (int j = tid; j < kept; j += kThreads) r += sh.cand[cur][j] >= from;
           if (tid == 0) sh.found = 0;
           __syncthreads();
           r = __reduce_add_sync(0xffffffffu, r);
@@ -373,15 +375,15 @@ __global__ void __launch_bounds__(kThreads) k_token_logprobs(const __grid_consta
         for (int j = tid; j < count * E::kVec; j += kThreads) {
           const int i = first * E::kVec + j;
           const float x = element(buf, j);
-          if (cand_key(x + 0.f, i) >= key) sh.cand[kept + atomicAdd(&sh.found, 1)] = cand_key(x + 0.f, i);
+          if (cand_key(x + 0.f, i) >= key) sh.cand[cur][kept + atomicAdd(&sh.found, 1)] = cand_key(x + 0.f, i);
         }
         __syncthreads();
         now = kept + sh.found;  // at most kept + n <= kRoom
       }
       if (st == 0 || now > 2 * a.n + 16) {
-        now = keep_best(sh, now, a.n);
+        now = keep_best(sh, cur, now, a.n);
         // only larger values pass from here on; until there are n, all do
-        least = now == a.n ? above<E>(cand_val(sh.cand[a.n - 1])) : -INF;
+        least = now == a.n ? above<E>(cand_val(sh.cand[cur][a.n - 1])) : -INF;
       }
       kept = now;
     } else {
@@ -417,21 +419,30 @@ __global__ void __launch_bounds__(kThreads) k_token_logprobs(const __grid_consta
       sh.before[warp] = b;
     }
     __syncthreads();
-    if (tid == 0) {
-      Part p{-INF, -INF, 0.f, 0.f, 0, 0};
-      for (int i = 0; i < kWarps; ++i) p.most = fmaxf(p.most, sh.red[i].x), p.m = fmaxf(p.m, sh.red[i].y);
-      for (int i = 0; i < kWarps; ++i) {
-        float si = sh.red[i].z, wi = sh.red[i].w;
-        move(sh.red[i].y, p.m, si, wi);
-        p.s += si;
-        p.w += wi;
-        p.before += sh.before[i];
-      }
-      sh.part = p;
+    // a lane per part; their sums in the order of the exchanges
+    auto join = [&](Part p) {
+      Part all = p;
+      all.most = warp_max(p.most);
+      all.m = warp_max(p.m);
+      move(p.m, all.m, p.s, p.w);
+      all.s = warp_sum(p.s);
+      all.w = warp_sum(p.w);
+      all.before = __reduce_add_sync(0xffffffffu, p.before);
+      return all;
+    };
+    const Part nothing{-INF, -INF, 0.f, 0.f, 0, 0, 0};
+    if (warp == 0) {
+      Part p = nothing;
+      if (lane < kWarps) p = Part{sh.red[lane].x, sh.red[lane].y, sh.red[lane].z, sh.red[lane].w, sh.before[lane], 0, 0};
+      p = join(p);
+      if (lane == 0) sh.part = p;
     }
     if (a.n > 0) {
-      const int left = keep_best(sh, kept, a.n);
-      if (tid == 0) sh.part.count = left;
+      const int left = keep_best(sh, cur, kept, a.n);
+      if (tid == 0) {
+        sh.part.count = left;
+        sh.part.buffer = cur;
+      }
     }
     __syncthreads();
     // ---------------- the row, by rank 0
@@ -442,28 +453,23 @@ __global__ void __launch_bounds__(kThreads) k_token_logprobs(const __grid_consta
           const uint32_t from = peer_address(&sh.part, tid);
           sh.all[tid] = Part{__uint_as_float(peer_u32(from)),      __uint_as_float(peer_u32(from + 4)),
                              __uint_as_float(peer_u32(from + 8)),  __uint_as_float(peer_u32(from + 12)),
-                             static_cast<int>(peer_u32(from + 16)), static_cast<int>(peer_u32(from + 20))};
+                             static_cast<int>(peer_u32(from + 16)), static_cast<int>(peer_u32(from + 20)),
+                             static_cast<int>(peer_u32(from + 24))};
         }
         __syncthreads();
         int at = 0;  // a warp per CTA: one trip for all of them
         for (int r = 0; r < a.cw; ++r) {
           const int n = sh.all[r].count;
           if (warp == r && r > 0)
-            for (int j = lane; j < n; j += 32) sh.cand[at + j] = peer_u64(peer_address(sh.cand, r) + 8 * j);
+            for (int j = lane; j < n; j += 32) sh.cand[cur][at + j] = peer_u64(peer_address(sh.cand[sh.all[r].buffer], r) + 8 * j);
           at += n;
         }
-        if (tid == 0) {
-          Part p{-INF, -INF, 0.f, 0.f, 0, 0};
-          for (int r = 0; r < a.cw; ++r) p.most = fmaxf(p.most, sh.all[r].most), p.m = fmaxf(p.m, sh.all[r].m);
-          for (int r = 0; r < a.cw; ++r) {
-            move(sh.all[r].m, p.m, sh.all[r].s, sh.all[r].w);
-            p.s += sh.all[r].s;
-            p.w += sh.all[r].w;
-            p.before += sh.all[r].before;
-          }
-          sh.part = p;
+        if (warp == 0) {
+          const Part p = join(lane < a.cw ? sh.all[lane] : nothing);
+          if (lane == 0) sh.part = p;
         }
-        if (a.n > 0) keep_best(sh, at, a.n);
+        __syncthreads();
+        if (a.n > 0) keep_best(sh, cur, at, a.n);
         __syncthreads();
       }
     }
@@ -500,7 +506,7 @@ __global__ void __launch_bounds__(kThreads) k_token_logprobs(const __grid_consta
       if (a.entropy) a.entropy[row] = none ? NAN_ : (a.greedy ? 0.f : (ls - moment / total) * ln2);
     }
     if (tid < a.n) {
-      const uint64_t key = sh.cand[tid];
+      const uint64_t key = sh.cand[cur][tid];
       const int64_t at = row * a.n + tid;
       if (a.top_ids) a.top_ids[at] = none ? -1 : cand_idx(key);
       if (a.top_logprob)
@@ -554,14 +560,16 @@ extern "C" ssd_status_t ssd_token_logprobs(const void *logits, ssd_dtype_t dt, i
   a.rank = rank;
   a.top_ids = top_ids;
   a.status = status;
-  constexpr int kRing = kStages * kStageBytes;
+  // the ring, or a whole part where that is less
+  const int64_t part = ((V * size / 16 + a.cw - 1) / a.cw) * 16;
+  const int ring = static_cast<int>(part < kStages * kStageBytes ? (part + 127) / 128 * 128 : kStages * kStageBytes);
   void (*const kernel)(Args) = dt == SSD_BF16 ? k_token_logprobs<EBF16> : k_token_logprobs<EF32>;
-  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kRing) != cudaSuccess)
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kStages * kStageBytes) != cudaSuccess)
     return SSD_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(B * R * a.cw));
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = kRing;
+  cfg.dynamicSmemBytes = static_cast<size_t>(ring);
   cfg.stream = reinterpret_cast<cudaStream_t>(s);
   cudaLaunchAttribute at;
   at.id = cudaLaunchAttributeClusterDimension;
