@@ -659,7 +659,10 @@ ssd_status_t ssd_branch_attention_q8(const void *q, const void *k_cache, const v
  * a group with a value that is not finite stands for NaN as a whole (byte 255,
  * codes 0; BAD_VALUE).  Rows i >= count[b], other positions of the block and
  * their codes in shared bytes stay as they were.  BAD_PREFIX and BAD_BLOCK as
- * in ssd_kv_append_q8.  The blocks that one call writes are distinct.
+ * in ssd_kv_append_q8.  The blocks that one call writes are distinct, and two
+ * calls that write one block follow each other (neighbouring positions share
+ * bytes of v).  Rows, caches and scales start on 16-byte boundaries, strides are
+ * multiples of 16 bytes.
  */
 ssd_status_t ssd_kv_append_q4(const void *k_new, int64_t k_seq_stride, int64_t k_tok_stride,
                               const void *v_new, int64_t v_seq_stride, int64_t v_tok_stride,
@@ -691,10 +694,17 @@ ssd_status_t ssd_kv_read_q4(const void *k_cache, const void *v_cache, const uint
  * are bad) gives 0 and lse = -inf.  A NaN scale of a key reaches the rows that
  * see the key, in v only the 32 elements of its group; what hidden positions
  * hold does not matter.  A query row with a value that is not finite gives NaN.
- * v scales below 2^-100 (bytes below 27) count as 0.
+ * v scales below 2^-100 (bytes below 27) count as 0.  The caches start on
+ * 32-byte boundaries, q, out and the scales on 16-byte ones.
+ * Accuracy: the elements of q count down to 2^-17 of their row's largest.  With
+ * P = exp(score - max) * t, t the largest scale of a key's v, a key's P is
+ * rounded by up to 2^-11 of itself, or by 2^-36 of the row's largest P where
+ * that is more; elements of groups whose scale is below 2^-36 t count less
+ * exactly; sums are fp32.
  * Workspace: ssd_attention_q4_workspace_size() bytes, 256-byte aligned, for
  * splitting long key ranges; NULL or short: not split, the same result but for
- * rounding, slower.
+ * these roundings, slower.  Calls that may run at the same time need a workspace
+ * each.
  */
 size_t ssd_attention_q4_workspace_size(int B, int Nq, int Hq, int Hkv, int d);
 ssd_status_t ssd_branch_attention_q4(const void *q, const void *k_cache, const void *v_cache,

@@ -24,11 +24,19 @@
 // Scores are x = s * scale * 2^e, P = 2^(x - m + 11); m is the running maximum of x +
 // log2(t) as in the 8-bit kernel (kBias, kMoved, kGrow).
 //
-// CTA: softmax warps (groups of four: 16 rows of the tile each, or with a lane
-// per row a quarter of its keys), four helper warps (scale bytes to TMEM, t
-// and the factors of a key's groups, V into halves, the next segment's rows), a
-// producer warp for K and the scales, one for V, and an MMA warp.  A unit is what one K
-// slot holds: 128 rows of 128 elements.
+// CTA: an MMA warp, two producer warps for K and the scales, one for V, helper warps
+// (scale bytes to TMEM, t and the factors of a key's groups, V into halves, the
+// next segment's rows; two sets of four, with more than 64 rows one), softmax warps
+// (groups of four: 16 rows of the tile each, or with a lane per row a quarter of its
+// keys).  A unit is what one K slot holds: 128 rows of 128 elements; where a
+// tile has two, each set of helpers has one of them, a tile apart if it so happens.
+// Bound by the roles' chains in a CTA (issue slots 61 %, the tensor pipe 21 %, HBM a third), not by bytes; their
+// loops together miss the instruction cache (10 % of its requests).  Microseconds (bytes' floor): 64 sequences of 8192 keys, 6 rows of 8 per head, d 128: 186 (86); 16 of 2048, 68 rows of 4, d 64: 67
+// (4.0); one of 100003 keys, a token: 38 (16); 48 of up to 16384, 8 rows of 8: 96 (33); 64 of 8192, a token each: 144 (84).
+// The 8-bit kernel takes 190 / 62 / 45 / 97.  Measured and slower (first / last shape): S and P V issued by two
+// warps 232 / 174 instead of 198 / 168, scale warps of their own 201 / 155 instead of 190 / 147, waits with a suspend hint
+// 204 / 176 instead of 201 / 166, the loop over V's words unrolled by two 198 / 152 instead of 190 / 144; one set of
+// helpers at 64 rows 111 instead of 96 (the fourth).
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <math.h>

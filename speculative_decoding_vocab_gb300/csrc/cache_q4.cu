@@ -14,7 +14,7 @@
 //                 pair (an odd first or even last position) reads the byte first.
 //   k_read_q4     the same split the other way.
 // Bound by HBM and the issue slots for prompts, by the chain prefix -> block table -> block for a decode step.  8 prompts
-// of 4096 to 8191 tokens, 8 heads of 128: append (255 MB) 57 us, 4.5 TB/s, read back 51 us, 5.0 TB/s; 4 prefixes of 16384
+// of 4096 to 8191 tokens, 8 heads of 128: append (255 MB) 55 us, 4.6 TB/s, read back 51 us, 5.0 TB/s; 4 prefixes of 16384
 // tokens (340 MB) 64 us, 5.3 TB/s; a decode step of 256 tokens 2.5 and 2.9 us.
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -33,7 +33,7 @@ using namespace ssd;
 constexpr int kThreads = 256;
 constexpr int kPage = 16;
 // Reading takes two pairs a thread where there are many, for the loads in flight (prefix of 4 x 16384 tokens, 340 MB: 64 us,
-// 69 with one, 70 with four); appending, which has twice the bytes of a pair in flight, one (57 us, 59 with two).
+// 69 with one, 70 with four); appending, which has twice the bytes of a pair in flight, one (two took 2 us more).
 constexpr int64_t kFewItems = 1 << 15;
 
 struct Place {  // which rows, and where their blocks are

@@ -21,8 +21,12 @@
 // than there is room for (ties, rising rows), the n-th key is searched bit by bit.
 //
 //   k_token_logprobs  a cluster of cw CTAs (256 threads) per row, a range of the row
-//       each, in stages of 16 KB that bulk copies bring into a ring of four; rank 0
-//       joins the parts through distributed shared memory.
+//       each, in stages of 32 KB that bulk copies bring into a ring of two (8 or 16 KB,
+//       rings of three or four, and 64 to 512 threads were slower); rank 0 joins the
+//       parts through distributed shared memory.
+// Bound by the issue slots (11.5 instructions an element of bf16, IPC 2.3): 2048 rows of 151936 with 20 tokens and the
+// rank (622 MB) 170 us, 3.7 TB/s; without the first tokens 108, without the rank too 98 (6.4 TB/s).  384 rows of 128256,
+// 56 MB of them wanted, with 5 tokens 22 us.  Five fp32 rows: 12 us, the chain of one part's stages and the two joins.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <math.h>
@@ -518,7 +522,8 @@ __global__ void __launch_bounds__(kThreads) k_token_logprobs(const __grid_consta
   if (a.cw > 1) cluster_sync();  // no CTA leaves while rank 0 may still read its shared memory
 }
 
-// CTAs of a row: as many as fill the GPU once, so that a CTA's part is long.
+// CTAs of a row: as many as fill the GPU once (4 on each of 152 SMs), so that a CTA's part is long.  384 rows of 128256,
+// about half of them wanted: doubled while there are less than 304 CTAs 32 us, 608 22, 1216 28.
 int cluster_of(int64_t rows, int V, int64_t size) {
   const int64_t stages = (V * size + kStageBytes - 1) / kStageBytes;
   int cw = 1;

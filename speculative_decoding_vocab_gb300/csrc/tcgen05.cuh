@@ -1,5 +1,5 @@
 // tcgen05.cuh -- tensor-core and TMEM wrappers shared by the attention kernels
-// of the bf16 and the 8-bit cache.
+// of the bf16, the 8-bit and the 4-bit cache.
 #pragma once
 
 #include "common.cuh"
