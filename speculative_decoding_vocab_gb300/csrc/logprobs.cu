@@ -24,9 +24,9 @@
 //       each, in stages of 32 KB that bulk copies bring into a ring of two (8 or 16 KB,
 //       rings of three or four, and 64 to 512 threads were slower); rank 0 joins the
 //       parts through distributed shared memory.
-// Bound by the issue slots (11.5 instructions an element of bf16, IPC 2.3): 2048 rows of 151936 with 20 tokens and the
-// rank (622 MB) 170 us, 3.7 TB/s; without the first tokens 108, without the rank too 98 (6.4 TB/s).  384 rows of 128256,
-// 56 MB of them wanted, with 5 tokens 22 us.  Five fp32 rows: 12 us, the chain of one part's stages and the two joins.
+// Bound by the issue slots where the first tokens are asked for: 2048 rows of 151936 with 20 of them and the rank
+// (622 MB) 142 us, 4.4 TB/s; without the first tokens 103, without the rank too 98 (6.4 TB/s).  384 rows of 128256,
+// 56 MB of them wanted, with 5 tokens 19 us.  Five fp32 rows: 10 us, the chain of one part's stages and the two joins.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <math.h>
@@ -226,7 +226,7 @@ __global__ void __launch_bounds__(kThreads) k_token_logprobs(const __grid_consta
   };
   float least = -INF;  // the smallest value that passes
   int kept = 0, turn = 0, cur = 0;  // candidates of the stages before; which counter this one has; which buffer
-  // a vector's elements that pass: element e at bit e, or pairs at bits e / 2 and 16 + e / 2
+  // a vector's elements that pass: element e at bit e (of fp32), or e / 2 + 4 (e % 2)
   auto passing = [&](const uint4 &v) {
     uint32_t mask = 0;
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -238,6 +238,7 @@ __global__ void __launch_bounds__(kThreads) k_token_logprobs(const __grid_consta
         *reinterpret_cast<uint32_t *>(&x) = w[h];
         mask |= __hge2_mask(x, least2) & (0x00010001u << h);
       }
+      mask = (mask | mask >> 12) & 0xFFu;
     } else {
 #pragma unroll
       for (int h = 0; h < 4; ++h) mask |= (__uint_as_float(w[h]) >= least ? 1u : 0u) << h;
@@ -273,12 +274,16 @@ __global__ void __launch_bounds__(kThreads) k_token_logprobs(const __grid_consta
     uint4 v[kVecs];
     float top = -INF;  // of this thread's elements of the stage
     const bool whole = count == kStageVecs;
+    // `whole` is tested here alone, in a branch that the whole CTA takes: tested per vector it was a branch each time
+    if (whole) {
 #pragma unroll
-    for (int q = 0; q < kVecs; ++q) {
-      const int j = q * kThreads + tid;
-      v[q] = whole || j < count ? buf[j] : E::nothing();
-      top = fmaxf(top, vec_max<E>(v[q]));
+      for (int q = 0; q < kVecs; ++q) v[q] = buf[q * kThreads + tid];
+    } else {
+#pragma unroll
+      for (int q = 0; q < kVecs; ++q) v[q] = q * kThreads + tid < count ? buf[q * kThreads + tid] : E::nothing();
     }
+#pragma unroll
+    for (int q = 0; q < kVecs; ++q) top = fmaxf(top, vec_max<E>(v[q]));
     most = fmaxf(most, top);
     if (top > m && top > kLow) rise(top);
     if (ranked && top >= zt) {
@@ -286,7 +291,7 @@ __global__ void __launch_bounds__(kThreads) k_token_logprobs(const __grid_consta
 #pragma unroll
       for (int q = 0; q < kVecs; ++q) {
         const int j = q * kThreads + tid, i0 = (first + j) * E::kVec;
-        if (whole || j < count) count_from<E>(v[q], i0 + E::kVec <= t ? zt : zt_above, n);
+        count_from<E>(v[q], i0 + E::kVec <= t && j < count ? zt : zt_above, n);  // what is not there is above nothing
       }
       before += n.n + static_cast<int>(__low2float(n.pair)) + static_cast<int>(__high2float(n.pair));
     }
@@ -309,31 +314,22 @@ __global__ void __launch_bounds__(kThreads) k_token_logprobs(const __grid_consta
           least = ord2f(low);
         }
       }
-      // one atomic per warp: its trip is what an append waits for
       if (__any_sync(0xffffffffu, top >= least)) {
-        uint32_t mask[kVecs];
-        int mine = 0;
+        uint32_t mask[2] = {0, 0};  // kVec bits of each vector
 #pragma unroll
-        for (int q = 0; q < kVecs; ++q) {
-          mask[q] = whole || q * kThreads + tid < count ? passing(v[q]) : 0u;
-          mine += __popc(mask[q]);
+        for (int q = 0; q < kVecs; ++q) mask[q / 4] |= passing(v[q]) << (q % 4 * E::kVec);
+        if (!whole) {
+#pragma unroll
+          for (int q = 0; q < kVecs; ++q)
+            if (q * kThreads + tid >= count) mask[q / 4] &= ~(((1u << E::kVec) - 1u) << (q % 4 * E::kVec));
         }
-        int upto = mine;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const int x = __shfl_up_sync(0xffffffffu, upto, o);
-          if (lane >= o) upto += x;
-        }
-        int at = 0;
-        if (lane == 31) at = atomicAdd(&sh.count[turn], upto);
-        at = kept + __shfl_sync(0xffffffffu, at, 31) + upto - mine;
-#pragma unroll
-        for (int q = 0; q < kVecs; ++q) {
-          const int j = q * kThreads + tid;
-          for (uint32_t left = mask[q]; left; left &= left - 1, ++at) {
-            const int b = __ffs(left) - 1, e = E::kSize == 2 ? 2 * (b & 15) + (b >> 4) : b;
-            const float x = element(buf, j * E::kVec + e);
-            if (at < kRoom) sh.cand[cur][at] = cand_key(x + 0.f, (first + j) * E::kVec + e);
+        const int mine = __popc(mask[0]) + __popc(mask[1]);
+        if (mine) {  // few lanes: an atomic each is less than a scan of the warp
+          int at = kept + atomicAdd(&sh.count[turn], mine);
+          for (uint64_t left = static_cast<uint64_t>(mask[1]) << 32 | mask[0]; left; left &= left - 1, ++at) {
+            const int b = __ffsll(left) - 1, q = (b >> 5) * 4 + (b & 31) / E::kVec, p = (b & 31) % E::kVec;
+            const int j = q * kThreads + tid, e = E::kSize == 2 ? 2 * (p & 3) + (p >> 2) : p;
+            if (at < kRoom) sh.cand[cur][at] = cand_key(element(buf, j * E::kVec + e) + 0.f, (first + j) * E::kVec + e);
           }
         }
       }
