@@ -52,7 +52,7 @@ struct Args {
   const void *z;
   int64_t ss, rs;
   int R, V, n, cw;
-  float c;
+  float c, inv_t;  // log2(e) / T, 1 / T
   int greedy;
   const int32_t *tokens;
   float *logprob, *entropy, *top_logprob;
@@ -494,14 +494,17 @@ __global__ void __launch_bounds__(kThreads) k_token_logprobs(const __grid_consta
       total = moment = 0.f;
       for (int i = 0; i < kWarps; ++i) total += sh.red[i].x, moment += sh.red[i].y;
     }
-    auto log2_of = [&](float x) { return again ? (x - p.most) * c : fmaf(x, c, -k_row); };  // of its term
     const bool none = !(total == total) || p.most == INF || p.most == -INF;  // no distribution
     const float ls = log2f(total), ln2 = 0.69314718055994531f;
+    // ln p; of the logits that were cut, times c may pass fp32's range where ln p does not
+    auto ln_of = [&](float x) {
+      return again || x < kCut ? fmaf(-ls, ln2, (x - p.most) * a.inv_t) : (fmaf(x, c, -k_row) - ls) * ln2;
+    };
     if (tid == 0) {
       const uint32_t flags = (none ? kFlagBadValue : 0u) | (good ? 0u : kFlagBadToken);
       if (flags) atomicOr(a.status, flags);
       if (a.logprob)
-        a.logprob[row] = none || !good ? NAN_ : (a.greedy ? (p.before == 0 ? 0.f : -INF) : (log2_of(zt) - ls) * ln2);
+        a.logprob[row] = none || !good ? NAN_ : (a.greedy ? (p.before == 0 ? 0.f : -INF) : ln_of(zt));
       if (a.rank) a.rank[row] = none || !good ? -1 : p.before;
       if (a.entropy) a.entropy[row] = none ? NAN_ : (a.greedy ? 0.f : (ls - moment / total) * ln2);
     }
@@ -511,7 +514,7 @@ __global__ void __launch_bounds__(kThreads) k_token_logprobs(const __grid_consta
       if (a.top_ids) a.top_ids[at] = none ? -1 : cand_idx(key);
       if (a.top_logprob)
         a.top_logprob[at] =
-            none ? NAN_ : (a.greedy ? (tid == 0 ? 0.f : -INF) : (log2_of(cand_val(key)) - ls) * ln2);
+            none ? NAN_ : (a.greedy ? (tid == 0 ? 0.f : -INF) : ln_of(cand_val(key)));
     }
   }
   if (!ok && tid == 0) atomicOr(a.status, kFlagWaitTimeout);
@@ -554,6 +557,7 @@ extern "C" ssd_status_t ssd_token_logprobs(const void *logits, ssd_dtype_t dt, i
   a.cw = cluster_of(static_cast<int64_t>(B) * R, V, size);
   a.greedy = T == 0.f;
   a.c = a.greedy ? 1.f : static_cast<float>(1.4426950408889634 / T);
+  a.inv_t = a.greedy ? 1.f : 1.f / T;
   a.tokens = tokens;
   a.logprob = logprob;
   a.entropy = entropy;

@@ -139,6 +139,20 @@ def test_masked_and_extreme(dtype):
 
 
 @DT
+@pytest.mark.parametrize("T", [1.0, 1.5, 1e4])
+def test_lowest_value_as_the_token(dtype, T):
+    """ln p of a token at the type's lowest value is finite where T leaves it in fp32's range, given and among the first."""
+    V = 1003
+    z = logits(2, 3, V, dtype, 11)
+    low = torch.finfo(dtype).min
+    z[0, :, 5:V] = low                          # 5 tokens before them
+    z[1, 0, :V], z[1, 0, 7] = low, -1e30        # the largest logit far below 0
+    z[1, 1, 3::4] = low / 2
+    tokens = np.array([[5, 900, 1002], [8, 7, 12]], np.int32)
+    check(z, V, T, tokens, 20)
+
+
+@DT
 def test_rows_without_a_distribution(dtype):
     V, n = 3001, 5
     z = logits(2, 3, V, dtype, 4)
