@@ -46,6 +46,7 @@ constexpr int kVecs = kStageVecs / kThreads;  // of a thread and stage
 constexpr int kRoom = 512;  // of candidates; at least kMaxCluster * kMaxTop
 constexpr int kMaxCluster = 8;
 static_assert(kMaxCluster <= kWarps && kMaxCluster * kMaxTop <= kRoom, "a warp per CTA, room for their candidates");
+static_assert(2 * kMaxTop + 16 + 7 <= kRoom, "room for what is kept and the last elements");
 constexpr float kCut = -1e30f, kLow = -1e29f, kHigh = 1e30f, kSteep = 1e7f;
 
 struct Args {
@@ -246,27 +247,11 @@ __global__ void __launch_bounds__(kThreads) k_token_logprobs(const __grid_consta
     return mask;
   };
   __syncthreads();
-  if (part == a.cw - 1) {  // the elements behind the last whole vector: candidates in any case
-    const int i = nv * E::kVec + tid;
-    if (i < a.V) {
-      const float x = E::ld(z, i);
-      most = x;
-      if (x > kLow) rise(x);
-      add_pair(pack2(max_nan(x, kCut), kCut));  // the pair's other half adds nothing
-      if (ranked) before += i < t ? x >= zt : x > zt;
-      if (a.n > 0) sh.cand[0][atomicAdd(&sh.count[0], 1)] = cand_key(x + 0.f, i);
-    }
-  }
   auto element = [](const uint4 *buf, int j) {  // of a stage
     return E::kSize == 2 ? __uint_as_float(static_cast<uint32_t>(reinterpret_cast<const uint16_t *>(buf)[j]) << 16)
                          : reinterpret_cast<const float *>(buf)[j];
   };
   bool ok = true;
-  __syncthreads();
-  if (a.n > 0) {
-    kept = sh.count[0];
-    turn = 1;
-  }
   for (int st = 0; st < nst; ++st) {
     const int first = v0 + st * kStageVecs, count = min(kStageVecs, v1 - first);
     const uint4 *const buf = reinterpret_cast<const uint4 *>(ring + (st % kStages) * kStageBytes);
@@ -390,6 +375,19 @@ __global__ void __launch_bounds__(kThreads) k_token_logprobs(const __grid_consta
       __syncthreads();
     }
     if (tid == 0 && st + kStages < nst) load(st + kStages);
+  }
+  // The elements behind the last whole vector, which are candidates in any case.  They come last, as their indices do.
+  if (part == a.cw - 1) {
+    const int i = nv * E::kVec + tid;
+    if (i < a.V) {
+      const float x = E::ld(z, i);
+      most = fmaxf(most, x);
+      if (x > m && x > kLow) rise(x);
+      add_pair(pack2(max_nan(x, kCut), kCut));  // the pair's other half adds nothing
+      if (ranked) before += i < t ? x >= zt : x > zt;
+      if (a.n > 0) sh.cand[cur][kept + tid] = cand_key(x + 0.f, i);
+    }
+    kept += a.V - nv * E::kVec;
   }
   // equal logits before the token in its own vector, which was counted as if they ranked behind it
   if (ranked && tid == 0) {

@@ -139,6 +139,18 @@ def test_masked_and_extreme(dtype):
 
 
 @DT
+@pytest.mark.parametrize("n", [1, 3, 20])
+def test_ties_behind_the_last_whole_vector(dtype, n):
+    """Equal logits on both sides of a row's last whole vector rank by index like any others, also in rising rows."""
+    for V in (9, 4099, 16389, 200001):
+        z = logits(1, 3, V, dtype, V + n)
+        z[0, 0, V - 12:V] = 50.0
+        z[0, 1, :V] = torch.sort(z[0, 1, :V])[0].round()
+        z[0, 2, V - 1], z[0, 2, V // 2] = 50.0, 50.0
+        check(z, V, 1.0, np.array([[V - 1, V - 2, V // 2]], np.int32), min(n, V))
+
+
+@DT
 @pytest.mark.parametrize("T", [1.0, 1.5, 1e4])
 def test_lowest_value_as_the_token(dtype, T):
     """ln p of a token at the type's lowest value is finite where T leaves it in fp32's range, given and among the first."""
