@@ -8,9 +8,11 @@
 // logit so far; s and w move with it); parts meet in a fixed order.  k is a
 // number like any other, so y = fma(z, c, -k) rounds once.  Logits are cut at
 // -1e30, where the exponential is 0 (0 * -inf would be NaN): tokens of -inf or of
-// the type's lowest value cost no test and are nobody's m.  A NaN reaches s.  A row
-// whose largest logit is itself below -1e29, or whose products would pass fp32's
-// range, is summed again by a loop that takes differences first.
+// the type's lowest value cost no test and are nobody's m.  A NaN reaches s.  The
+// largest logit's own y is what the rounding of k left over, half a step of k: at most 1
+// below 2^25, past the exponential's range from 2^31 on.  A row whose largest logit is
+// that far from 0 for its c, or is itself below -1e29, or whose products would pass
+// fp32's range, is summed again by a loop that takes differences first.
 // The first n tokens: each CTA collects candidates in shared memory, those that its
 // threshold lets through.  The threshold starts from the first stage: each of
 // its (up to 8) whole warps gives the k-th largest of its lanes' maxima, k = ceil(n
@@ -47,7 +49,7 @@ constexpr int kRoom = 512;  // of candidates; at least kMaxCluster * kMaxTop
 constexpr int kMaxCluster = 8;
 static_assert(kMaxCluster <= kWarps && kMaxCluster * kMaxTop <= kRoom, "a warp per CTA, room for their candidates");
 static_assert(2 * kMaxTop + 16 + 7 <= kRoom, "room for what is kept and the last elements");
-constexpr float kCut = -1e30f, kLow = -1e29f, kHigh = 1e30f, kSteep = 1e7f;
+constexpr float kCut = -1e30f, kLow = -1e29f, kFar = 0x1p25f, kSteep = 1e7f;
 
 struct Args {
   const void *z;
@@ -476,7 +478,7 @@ __global__ void __launch_bounds__(kThreads) k_token_logprobs(const __grid_consta
     const Part p = sh.part;
     // the row's sums around its largest logit, or, where these are out of the loop's range, again
     float total = p.s, moment = p.w, k_row = __fmul_rn(p.most, c);
-    const bool again = !(p.most > kLow) || !(fabsf(k_row) < kHigh) || !(c < kSteep);
+    const bool again = !(p.most > kLow) || !(fabsf(k_row) < kFar) || !(c < kSteep);
     if (again) {
       float s = 0.f, w = 0.f;
       for (int i = tid; i < a.V; i += kThreads) {

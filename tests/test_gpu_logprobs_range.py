@@ -1,0 +1,28 @@
+"""Token log probabilities on the GPU where logits, masks or the temperature are large: results as in 64 bits
+(check of test_gpu_logprobs, its tolerances)."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from speculative_decoding_vocab_gb300 import binding as ssd
+from test_gpu_logprobs import DT, _lib, check, logits, outputs  # noqa: F401 (the fixture builds the library)
+
+pytestmark = pytest.mark.gpu
+
+
+@DT
+@pytest.mark.parametrize("T", [1.0, 0.3, 1e-6, 2e-7, 0.0])
+def test_large_row_maximum(dtype, T):
+    """Rows whose largest logit is far from 0 for their temperature: a forced token, all of a row at one value or near it."""
+    n = 20
+    for V in (9001, 128256):
+        for big in (400.0, 3e7, 3e9, 1e10, 1e15, 1e20):
+            z = logits(1, 5, V, dtype, 21)
+            z[0, 0, V // 3] = big
+            z[0, 1, :V] = -big
+            z[0, 2, :V] = big
+            z[0, 3, :V] = -big * (1 + torch.rand(V, generator=torch.Generator().manual_seed(3)) * 1e-2)
+            z[0, 4, :V] = big * (1 + torch.rand(V, generator=torch.Generator().manual_seed(4)) * 1e-6)
+            check(z, V, T, np.array([[V // 3, V - 1, 0, 17, V // 2]], np.int32), n)
