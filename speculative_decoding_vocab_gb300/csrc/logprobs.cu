@@ -12,7 +12,9 @@
 // largest logit's own y is what the rounding of k left over, half a step of k: at most 1
 // below 2^25, past the exponential's range from 2^31 on.  A row whose largest logit is
 // that far from 0 for its c, or is itself below -1e29, or whose products would pass
-// fp32's range, is summed again by a loop that takes differences first.
+// fp32's range, is summed again by a loop that takes differences first.  Of other rows
+// nothing below -2^26 / c is anyone's m (a finite mask, which may fill a thread's whole
+// part): it lies 2^25 below the row's largest, so its exponential is 0 around any k.
 // The first n tokens: each CTA collects candidates in shared memory, those that its
 // threshold lets through.  The threshold starts from the first stage: each of
 // its (up to 8) whole warps gives the k-th largest of its lanes' maxima, k = ceil(n
@@ -56,6 +58,7 @@ struct Args {
   int64_t ss, rs;
   int R, V, n, cw;
   float c, inv_t;  // log2(e) / T, 1 / T
+  float low;       // what is not above it is nobody's m
   int greedy;
   const int32_t *tokens;
   float *logprob, *entropy, *top_logprob;
@@ -64,7 +67,7 @@ struct Args {
 };
 
 struct Part {
-  float most, m, s, w;  // the largest logit; the largest above kLow, around which s and w are
+  float most, m, s, w;  // the largest logit; the largest above low, around which s and w are
   int before, count, buffer;  // buffer: which one holds its candidates
 };
 struct Shared {
@@ -205,7 +208,7 @@ __global__ void __launch_bounds__(kThreads) k_token_logprobs(const __grid_consta
   const float zt = given && good ? E::ld(z, t) : 0.f, zt_above = above<E>(zt);
   const float c = a.c;
   const uint64_t c2 = pack2(c, c);
-  float most = -INF, m = -INF, k = 0.f;  // the largest logit; the largest above kLow, and m c
+  float most = -INF, m = -INF, k = 0.f;  // the largest logit; the largest above a.low, and m c
   uint64_t s2 = 0, w2 = 0, neg_k2 = 0;
   int before = 0;
   auto rise = [&](float to) {  // a larger m
@@ -272,7 +275,7 @@ __global__ void __launch_bounds__(kThreads) k_token_logprobs(const __grid_consta
 #pragma unroll
     for (int q = 0; q < kVecs; ++q) top = fmaxf(top, vec_max<E>(v[q]));
     most = fmaxf(most, top);
-    if (top > m && top > kLow) rise(top);
+    if (top > m && top > a.low) rise(top);
     if (ranked && top >= zt) {
       Counter n{__float2bfloat162_rn(0.f), 0};
 #pragma unroll
@@ -384,7 +387,7 @@ __global__ void __launch_bounds__(kThreads) k_token_logprobs(const __grid_consta
     if (i < a.V) {
       const float x = E::ld(z, i);
       most = fmaxf(most, x);
-      if (x > m && x > kLow) rise(x);
+      if (x > m && x > a.low) rise(x);
       add_pair(pack2(max_nan(x, kCut), kCut));  // the pair's other half adds nothing
       if (ranked) before += i < t ? x >= zt : x > zt;
       if (a.n > 0) sh.cand[cur][kept + tid] = cand_key(x + 0.f, i);
@@ -558,6 +561,7 @@ extern "C" ssd_status_t ssd_token_logprobs(const void *logits, ssd_dtype_t dt, i
   a.greedy = T == 0.f;
   a.c = a.greedy ? 1.f : static_cast<float>(1.4426950408889634 / T);
   a.inv_t = a.greedy ? 1.f : 1.f / T;
+  a.low = fmaxf(kLow, -2.f * kFar / a.c);
   a.tokens = tokens;
   a.logprob = logprob;
   a.entropy = entropy;

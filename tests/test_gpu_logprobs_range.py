@@ -26,3 +26,26 @@ def test_large_row_maximum(dtype, T):
             z[0, 3, :V] = -big * (1 + torch.rand(V, generator=torch.Generator().manual_seed(3)) * 1e-2)
             z[0, 4, :V] = big * (1 + torch.rand(V, generator=torch.Generator().manual_seed(4)) * 1e-6)
             check(z, V, T, np.array([[V // 3, V - 1, 0, 17, V // 2]], np.int32), n)
+
+
+@DT
+@pytest.mark.parametrize("mask", [-1e9, -2e9, -1e10, -1e12, -1e15, -1e20, -1e28])
+def test_finite_masks(dtype, mask):
+    """A grammar's mask by a finite value: most of a row, whole stages, all but one token, a few scattered ones; the
+    token allowed or masked."""
+    n = 20
+    for V in (9001, 32000, 128256):
+        z = logits(1, 6, V, dtype, 22)
+        rng = np.random.default_rng(V)
+        few = torch.as_tensor(rng.permutation(V)[:10].copy(), device="cuda")
+        keep = z[0, 0, few].clone()
+        z[0, 0, :V] = mask
+        z[0, 0, few] = keep
+        z[0, 1, :V - 10] = mask         # the allowed tokens last
+        z[0, 2, 10:V] = mask            # first
+        z[0, 3, :V], z[0, 3, 4000] = mask, 1.5
+        z[0, 4, :V // 2] += mask        # added to the logits
+        z[0, 5, 3:V:2] = mask
+        tokens = np.array([[int(few[3]), 5, 3, 4000, V - 1, 4]], np.int32)
+        for T in (1.0, 0.7, 0.6, 0.3, 0.1, 0.05, 0.01, 0.0):
+            check(z, V, T, tokens, n)
