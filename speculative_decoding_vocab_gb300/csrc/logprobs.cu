@@ -11,8 +11,9 @@
 // the type's lowest value cost no test and are nobody's m.  A NaN reaches s.  The
 // largest logit's own y is what the rounding of k left over, half a step of k: at most 1
 // below 2^25, past the exponential's range from 2^31 on.  A row whose largest logit is
-// that far from 0 for its c, or is itself below -1e29, or whose products would pass
-// fp32's range, is summed again by a loop that takes differences first.  Of other rows
+// that far from 0 for its c, or is itself near -1e29, or whose products would pass
+// fp32's range, is summed again by a loop that takes differences first, and so is every row
+// where c is so small that the cut logits would count (T above 1.4e26).  Of other rows
 // nothing below -2^26 / c is anyone's m (a finite mask, which may fill a thread's whole
 // part): it lies 2^25 below the row's largest, so its exponential is 0 around any k.
 // The first n tokens: each CTA collects candidates in shared memory, those that its
@@ -51,7 +52,7 @@ constexpr int kRoom = 512;  // of candidates; at least kMaxCluster * kMaxTop
 constexpr int kMaxCluster = 8;
 static_assert(kMaxCluster <= kWarps && kMaxCluster * kMaxTop <= kRoom, "a warp per CTA, room for their candidates");
 static_assert(2 * kMaxTop + 16 + 7 <= kRoom, "room for what is kept and the last elements");
-constexpr float kCut = -1e30f, kLow = -1e29f, kFar = 0x1p25f, kSteep = 1e7f;
+constexpr float kCut = -1e30f, kLow = -1e29f, kFar = 0x1p25f, kFlat = 1e-26f, kSteep = 1e7f;
 
 struct Args {
   const void *z;
@@ -479,9 +480,10 @@ __global__ void __launch_bounds__(kThreads) k_token_logprobs(const __grid_consta
   }
   if (part == 0) {
     const Part p = sh.part;
-    // the row's sums around its largest logit, or, where these are out of the loop's range, again
+    // the row's sums around its largest logit, or, where these are out of the loop's range, again.  (With c >= kFlat the
+    // gap between kLow / 2 and kLow is 500 in y: what is not above kLow has the exponential 0, as it was counted.)
     float total = p.s, moment = p.w, k_row = __fmul_rn(p.most, c);
-    const bool again = !(p.most > kLow) || !(fabsf(k_row) < kFar) || !(c < kSteep);
+    const bool again = !(p.most > 0.5f * kLow) || !(fabsf(k_row) < kFar) || !(c >= kFlat && c < kSteep);
     if (again) {
       float s = 0.f, w = 0.f;
       for (int i = tid; i < a.V; i += kThreads) {

@@ -49,3 +49,16 @@ def test_finite_masks(dtype, mask):
         tokens = np.array([[int(few[3]), 5, 3, 4000, V - 1, 4]], np.int32)
         for T in (1.0, 0.7, 0.6, 0.3, 0.1, 0.05, 0.01, 0.0):
             check(z, V, T, tokens, n)
+
+
+@DT
+@pytest.mark.parametrize("T", [1e20, 1e26, 1e27, 1e28, 1e29, 1e30, 3e38])
+def test_large_temperature(dtype, T):
+    """Tokens of -inf have probability 0 at any temperature; what lies behind a row's end counts nothing."""
+    for V in (3, 9001, 32777):
+        z = logits(1, 4, V, dtype, 23)
+        z[0, 0, 1:V:2] = -math.inf
+        z[0, 1, 1:V] = -math.inf
+        z[0, 2, :V] *= 1e28
+        z[0, 3, :V] = z[0, 3, :V] * 1e29 - 2e29
+        check(z, V, T, np.array([[0, 1, V - 1, V // 2]], np.int32), min(V, 20))
