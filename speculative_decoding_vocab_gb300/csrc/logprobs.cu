@@ -483,11 +483,12 @@ __global__ void __launch_bounds__(kThreads) k_token_logprobs(const __grid_consta
     // the row's sums around its largest logit, or, where these are out of the loop's range, again.  (With c >= kFlat the
     // gap between kLow / 2 and kLow is 500 in y: what is not above kLow has the exponential 0, as it was counted.)
     float total = p.s, moment = p.w, k_row = __fmul_rn(p.most, c);
+    const float half_most = 0.5f * p.most;  // differences are taken of halves: those of logits may pass fp32's range
     const bool again = !(p.most > 0.5f * kLow) || !(fabsf(k_row) < kFar) || !(c >= kFlat && c < kSteep);
     if (again) {
       float s = 0.f, w = 0.f;
       for (int i = tid; i < a.V; i += kThreads) {
-        const float x = E::ld(z, i), y = max_nan((x - p.most) * c, -160.f), e = ex2(y);
+        const float x = E::ld(z, i), y = max_nan((0.5f * x - half_most) * (2.f * c), -160.f), e = ex2(y);
         s += e;
         w = fmaf(e, y, w);
       }
@@ -503,7 +504,7 @@ __global__ void __launch_bounds__(kThreads) k_token_logprobs(const __grid_consta
     const float ls = log2f(total), ln2 = 0.69314718055994531f;
     // ln p; of the logits that were cut, times c may pass fp32's range where ln p does not
     auto ln_of = [&](float x) {
-      return again || x < kCut ? fmaf(-ls, ln2, (x - p.most) * a.inv_t) : (fmaf(x, c, -k_row) - ls) * ln2;
+      return again || x < kCut ? fmaf(-ls, ln2, (0.5f * x - half_most) * (2.f * a.inv_t)) : (fmaf(x, c, -k_row) - ls) * ln2;
     };
     if (tid == 0) {
       const uint32_t flags = (none ? kFlagBadValue : 0u) | (good ? 0u : kFlagBadToken);

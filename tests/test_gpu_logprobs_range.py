@@ -62,3 +62,16 @@ def test_large_temperature(dtype, T):
         z[0, 2, :V] *= 1e28
         z[0, 3, :V] = z[0, 3, :V] * 1e29 - 2e29
         check(z, V, T, np.array([[0, 1, V - 1, V // 2]], np.int32), min(V, 20))
+
+
+@DT
+@pytest.mark.parametrize("T", [1e3, 1e30, 1e37, 3e38])
+def test_logits_whose_difference_passes_fp32(dtype, T):
+    """ln p where a logit less the row's largest is no fp32 number, but over T it is."""
+    V = 1003
+    z = logits(1, 3, V, dtype, 24)
+    top = torch.finfo(dtype).max
+    z[0, 0, :V], z[0, 0, 9] = -top, top
+    z[0, 1, :V:2], z[0, 1, 1:V:2] = top, -top
+    z[0, 2, :V] = z[0, 2, :V] * (top / 32)
+    check(z, V, T, np.array([[8, 9, V - 1]], np.int32), 20)
