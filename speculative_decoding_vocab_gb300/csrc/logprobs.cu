@@ -502,9 +502,12 @@ __global__ void __launch_bounds__(kThreads) k_token_logprobs(const __grid_consta
     }
     const bool none = !(total == total) || p.most == INF || p.most == -INF;  // no distribution
     const float ls = log2f(total), ln2 = 0.69314718055994531f;
-    // ln p; of the logits that were cut, times c may pass fp32's range where ln p does not
+    // ln p; of the logits that were cut, times c may pass fp32's range where ln p does not.  Where one token has all of
+    // the row, the roundings of ex2 and log2 leave it up to 1e-7 on either side of 0.
     auto ln_of = [&](float x) {
-      return again || x < kCut ? fmaf(-ls, ln2, (0.5f * x - half_most) * (2.f * a.inv_t)) : (fmaf(x, c, -k_row) - ls) * ln2;
+      const float ln = again || x < kCut ? fmaf(-ls, ln2, (0.5f * x - half_most) * (2.f * a.inv_t))
+                                         : (fmaf(x, c, -k_row) - ls) * ln2;
+      return fminf(ln, 0.f);
     };
     if (tid == 0) {
       const uint32_t flags = (none ? kFlagBadValue : 0u) | (good ? 0u : kFlagBadToken);
@@ -512,7 +515,7 @@ __global__ void __launch_bounds__(kThreads) k_token_logprobs(const __grid_consta
       if (a.logprob)
         a.logprob[row] = none || !good ? NAN_ : (a.greedy ? (p.before == 0 ? 0.f : -INF) : ln_of(zt));
       if (a.rank) a.rank[row] = none || !good ? -1 : p.before;
-      if (a.entropy) a.entropy[row] = none ? NAN_ : (a.greedy ? 0.f : (ls - moment / total) * ln2);
+      if (a.entropy) a.entropy[row] = none ? NAN_ : (a.greedy ? 0.f : fmaxf((ls - moment / total) * ln2, 0.f));
     }
     if (tid < a.n) {
       const uint64_t key = sh.cand[cur][tid];

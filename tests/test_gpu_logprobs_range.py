@@ -75,3 +75,23 @@ def test_logits_whose_difference_passes_fp32(dtype, T):
     z[0, 1, :V:2], z[0, 1, 1:V:2] = top, -top
     z[0, 2, :V] = z[0, 2, :V] * (top / 32)
     check(z, V, T, np.array([[8, 9, V - 1]], np.int32), 20)
+
+
+@DT
+@pytest.mark.parametrize("n", [0, 5])
+def test_no_probability_above_one(dtype, n):
+    """ln p <= 0 and entropy >= 0, also where one token has all of a row's probability."""
+    V, R = 3001, 512
+    z = logits(2, R, V, dtype, 25)
+    g = torch.Generator().manual_seed(5)
+    tokens = torch.randint(0, V, (2, R), generator=g, dtype=torch.int32).cuda()
+    tall = (30 + 70 * torch.rand(2, R, generator=g)).to("cuda", dtype)
+    z.scatter_(2, tokens.long()[..., None], tall[..., None])
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    for T in (1.0, 0.7, 0.3, 1e-2):
+        o = outputs(2, R, n)
+        ssd.ssd_token_logprobs(z, V, T, tokens=tokens, status=st, **o)
+        assert (o["logprob"] <= 0).all() and (o["logprob"] >= -1e-5).all(), (T, o["logprob"].max())
+        assert (o["entropy"] >= 0).all() and (o["entropy"] <= 1e-3).all(), (T, o["entropy"].min())
+        assert (o["top_logprob"] <= 0).all()
+    assert int(st.item()) == 0
