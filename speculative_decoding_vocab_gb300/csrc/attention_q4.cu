@@ -57,6 +57,8 @@ constexpr int kSmemBudget = 214 * 1024;
 constexpr int kTiles = 4;     // tiles whose scales of v are held
 constexpr int kIds = 32;      // units whose block ids are held
 constexpr int kVShift = 13;
+// O / L's unit.  It goes to O before 1 / L does: with v's smallest scales L passes 2^104 a key, and kOutUnit / L is
+// subnormal from 5 keys on; with its largest O / L passes fp32's range.
 constexpr float kOutUnit = kSumUnit * 0x1p-13f;
 constexpr int kQueryByte = 127 - 8;
 constexpr float kQueryUnit = 256.f;
@@ -861,7 +863,7 @@ __global__ void __launch_bounds__(Cfg<D, RT>::kThreads, 1)
       if (some) {
         const int slot = blockIdx.x * 2 + (sg.t0 > 0 ? 0 : 1);
         const float L = __fadd_rn(__fadd_rn(red[0][r], red[1][r]), __fadd_rn(red[2][r], red[3][r]));
-        const float factor = L == 0.f ? 0.f : (whole ? 1.f / L : 1.f) * kOutUnit;
+        const float factor = L == 0.f ? 0.f : (whole ? 1.f / L : 1.f);
         const int64_t orow = (static_cast<int64_t>(sg.b) * a.Nq + qi) * a.Hq + sg.hk * a.group + (row - qi * a.group);
         if (live && g == 0) {
           if (!whole)
@@ -874,7 +876,7 @@ __global__ void __launch_bounds__(Cfg<D, RT>::kThreads, 1)
           float o[16];
           tmem_ld16(tO + j0, o);
 #pragma unroll
-          for (int j = 0; j < 16; ++j) o[j] *= factor;
+          for (int j = 0; j < 16; ++j) o[j] = o[j] * kOutUnit * factor;
           if (!live) continue;
           const int e0 = g * (D / 4) + j0;
           if (nan) {
@@ -1108,7 +1110,7 @@ __global__ void __launch_bounds__(Cfg<D, RT>::kThreads, 1)
       if (tid == C::kSoftWarp * 32) s_nan[(seg + 2) & 3] = 0;
       for (int r = tid - C::kSoftWarp * 32; r < RT; r += kSoftThreads) {
         const float M = s_m[r], L = __fadd_rn(__fadd_rn(red[0][r], red[1][r]), __fadd_rn(red[2][r], red[3][r]));
-        s_f[r] = L == 0.f ? 0.f : (whole ? 1.f / L : 1.f) * kOutUnit;
+        s_f[r] = L == 0.f ? 0.f : (whole ? 1.f / L : 1.f);
         const int row = mt * RT + r;
         if (row < a.nrows) {
           if (!whole) a.part_ml[slot * RT + r] = make_float2(M, L);
@@ -1132,7 +1134,7 @@ __global__ void __launch_bounds__(Cfg<D, RT>::kThreads, 1)
         float o[4];
         tmem_ld4(tmem + C::kOCol + j0 + lane_off, o);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) o[j] *= s_f[j0 + j];
+        for (int j = 0; j < 4; ++j) o[j] = o[j] * kOutUnit * s_f[j0 + j];
         if (nan) {
           // tree nodes of this segment whose v has a NaN scale at this thread's element
           const int from = sg.t0 * C::kKeys - sg.L, to = min(sg.nkeys, sg.t1 * C::kKeys) - sg.L;
