@@ -764,16 +764,17 @@ def ssd_kv_read_q4(k_cache, v_cache, k_scale, v_scale, block_table, prefix_len, 
                    status=None, stream=None):
     """Rows of the 4-bit caches at tree nodes node0.. of every sequence as
     values: ``k_out``, ``v_out`` [B, S, Hkv, d] (bf16 or fp32, heads
-    contiguous; either may be None)."""
+    contiguous; either may be None, and with both nothing is read)."""
     x = k_out if k_out is not None else v_out
-    rows = x.shape
-    B, S, Hkv, d = rows
     nb = k_cache.shape[0]
+    # without an output: no rows, of the cache's heads
+    rows = x.shape if x is not None else (prefix_len.shape[0], 0, k_cache.shape[1], v_cache.shape[3])
+    B, S, Hkv, d = rows
     maxb = block_table.shape[1]
     dev = k_cache.get_device()
     i32 = torch.int32
-    dt = SSD_F32 if x.dtype == torch.float32 else SSD_BF16
-    if dt == SSD_BF16 and x.dtype != torch.bfloat16:
+    dt = SSD_F32 if x is not None and x.dtype == torch.float32 else SSD_BF16
+    if x is not None and dt == SSD_BF16 and x.dtype != torch.bfloat16:
         raise ValueError(f"k_out and v_out must be float32 or bfloat16, got {x.dtype}")
     if (block_table.dtype is not i32 or block_table.shape[0] != B or not block_table.is_contiguous()
             or prefix_len.dtype is not i32 or prefix_len.shape != (B,) or not prefix_len.is_contiguous()
