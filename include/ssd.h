@@ -679,7 +679,7 @@ ssd_status_t ssd_kv_append_q4(const void *k_new, int64_t k_seq_stride, int64_t k
  * elements and bases multiples of 16 bytes); either may be NULL.  The values
  * are exact in both types.  Rows i >= count[b] (count NULL: S), of a slot
  * without a request, past the table (BAD_PREFIX) or of a bad block (BAD_BLOCK)
- * are left as they were.  The rows of an output do not overlap.
+ * are left as they were.  The rows of the outputs do not overlap.
  */
 ssd_status_t ssd_kv_read_q4(const void *k_cache, const void *v_cache, const uint8_t *k_scale,
                             const uint8_t *v_scale, const int32_t *block_table, int maxb,

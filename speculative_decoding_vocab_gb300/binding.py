@@ -517,6 +517,23 @@ def _overlap(B, S, a, b, n):
     return any(y - x < n for x, y in zip(starts, starts[1:]))
 
 
+def _outputs_meet(B, S, n, size, ko, kss, kts, vo, vss, vts):
+    """Whether two outputs' runs of n elements (of `size` bytes) meet: addresses, (sequence, token) strides as of _rows."""
+    d = (vo - ko) // size
+    if d >= (B - 1) * kss + (S - 1) * kts + n or -d >= (B - 1) * vss + (S - 1) * vts + n:
+        return False  # one behind the other
+    if (kss, kts) == (vss, vts):
+        # interleaved in every token (heads of one buffer), or in every sequence
+        if kts > 0 and kss % kts == 0 and n <= d % kts <= kts - n:
+            return False
+        run = (S - 1) * kts + n
+        if kss > 0 and run <= d % kss <= kss - run:
+            return False
+    starts = [(i * kss + j * kts, 0) for i in range(B) for j in range(S)]
+    starts = sorted(starts + [(d + i * vss + j * vts, 1) for i in range(B) for j in range(S)])
+    return any(y[0] - x[0] < n for x, y in zip(starts, starts[1:]) if x[1] != y[1])
+
+
 def _rows(x, y, dtype, lead, dev, what):
     """Addresses and (sequence, token) strides of [B, S, H, d] rows x and their output y, whose heads are dense;
     an output's tokens do not overlap."""
@@ -788,6 +805,8 @@ def ssd_kv_read_q4(k_cache, v_cache, k_scale, v_scale, block_table, prefix_len, 
         outs += (None, 0, 0) if y is None else _rows(y, y, x.dtype, (B, S, d), dev, what)[3:]
         if y is not None and y.shape != rows:
             raise ValueError(f"k_out and v_out must have one shape, got {tuple(rows)} and {tuple(y.shape)}")
+    if k_out is not None and v_out is not None and _outputs_meet(B, S, Hkv * d, x.element_size(), *outs):
+        raise ValueError("k_out and v_out must not overlap")
     _launch("ssd_kv_read_q4", dev, stream,
             k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
             block_table.data_ptr(), maxb, nb, prefix_len.data_ptr(), _dense(count, i32, (B,), dev, "count"), int(node0),
