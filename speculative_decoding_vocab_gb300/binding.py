@@ -867,7 +867,7 @@ def ssd_token_logprobs(logits, V, T, tokens=None, logprob=None, rank=None, entro
     if R == 1 or logits.numel() == 0:
         rs = 0
     top = top_ids if top_ids is not None else top_logprob
-    n = 0 if top is None else top.shape[2]
+    n = 0 if top is None or top.dim() == 0 else top.shape[-1]
     dev = logits.get_device()
     i32, f32 = torch.int32, torch.float32
     _launch("ssd_token_logprobs", dev, stream, logits.data_ptr(), dt, ss, rs, B, R, int(V), float(T),
