@@ -486,11 +486,18 @@ __global__ void __launch_bounds__(kThreads) k_token_logprobs(const __grid_consta
     const float half_most = 0.5f * p.most;  // differences are taken of halves: those of logits may pass fp32's range
     const bool again = !(p.most > 0.5f * kLow) || !(fabsf(k_row) < kFar) || !(c >= kFlat && c < kSteep);
     if (again) {
-      float s = 0.f, w = 0.f;
+      // A thread adds up to 8192 terms here, often equal ones, whose additions round the same way each time: what each
+      // leaves goes to the next.
+      float s = 0.f, w = 0.f, s_left = 0.f, w_left = 0.f;
+      auto add = [](float &sum, float &left, float term) {
+        const float t = __fadd_rn(term, left), to = __fadd_rn(sum, t);
+        left = __fsub_rn(t, __fsub_rn(to, sum));
+        sum = to;
+      };
       for (int i = tid; i < a.V; i += kThreads) {
         const float x = E::ld(z, i), y = max_nan((0.5f * x - half_most) * (2.f * c), -160.f), e = ex2(y);
-        s += e;
-        w = fmaf(e, y, w);
+        add(s, s_left, e);
+        add(w, w_left, __fmul_rn(e, y));
       }
       s = warp_sum(s);
       w = warp_sum(w);

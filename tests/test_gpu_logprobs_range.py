@@ -95,3 +95,15 @@ def test_no_probability_above_one(dtype, n):
         assert (o["entropy"] >= 0).all() and (o["entropy"] <= 1e-3).all(), (T, o["entropy"].min())
         assert (o["top_logprob"] <= 0).all()
     assert int(st.item()) == 0
+
+
+@DT
+def test_long_rows_summed_by_differences(dtype):
+    """Rows of many equal terms, whose additions round the same way each time, at the largest sizes."""
+    top = 1 << (20 if dtype == torch.float32 else 21)
+    for V in (195115, top):
+        z = logits(1, 3, V, dtype, 26)
+        z[0, :, :V] = -1e30
+        z[0, 0, 100], z[0, 1, 100], z[0, 2, V - 1] = 0.7e30, 3e30, 9e30
+        for T in (2.9e29, 7e29):
+            check(z, V, T, np.array([[100, 5, V - 1]], np.int32), 20)
