@@ -621,6 +621,7 @@ ssd_status_t ssd_kv_append_q8(const void *k_new, int64_t k_seq_stride, int64_t k
  * to 2^-17 of their row's largest; with P = exp(score - max) * v_scale, a key's
  * P is rounded by up to 2^-11 of itself, or by 2^-36 of the row's largest P
  * where that is more (so n keys lose at most n * 2^-36 of it); sums are fp32.
+ * Scores, scale * q k, are below 2^24 in magnitude, as for the 4-bit cache.
  * Workspace: ssd_attention_q8_workspace_size() bytes, 256-byte aligned, for
  * splitting long key ranges; NULL or short: not split, the same result but for
  * these roundings, slower.
@@ -677,7 +678,8 @@ ssd_status_t ssd_kv_append_q4(const void *k_new, int64_t k_seq_stride, int64_t k
  * sequence b is position prefix_len[b] + node0 + i; k_out, v_out: row (b, i, h)
  * at base + b*seq_stride + i*tok_stride + h*d, of type dt (strides in
  * elements and bases multiples of 16 bytes); either may be NULL.  The values
- * are exact in both types.  Rows i >= count[b] (count NULL: S), of a slot
+ * are exact in both types (scale bytes 253 and 254, which the append does not
+ * write, give infinities where a code passes the types' range).  Rows i >= count[b] (count NULL: S), of a slot
  * without a request, past the table (BAD_PREFIX) or of a bad block (BAD_BLOCK)
  * are left as they were.  The rows of the outputs do not overlap.
  */
@@ -700,7 +702,9 @@ ssd_status_t ssd_kv_read_q4(const void *k_cache, const void *v_cache, const uint
  * P = exp(score - max) * t, t the largest scale of a key's v, a key's P is
  * rounded by up to 2^-11 of itself, or by 2^-36 of the row's largest P where
  * that is more; elements of groups whose scale is below 2^-36 t count less
- * exactly; sums are fp32.
+ * exactly; sums are fp32.  Scores, scale * q k, are below 2^24 in magnitude: above,
+ * their distances from the row's largest are lost to rounding, and a row may
+ * give 0, infinities or NaN without a flag.
  * Workspace: ssd_attention_q4_workspace_size() bytes, 256-byte aligned, for
  * splitting long key ranges; NULL or short: not split, the same result but for
  * these roundings, slower.  Calls that may run at the same time need a workspace
@@ -731,7 +735,8 @@ ssd_status_t ssd_branch_attention_q4(const void *q, const void *k_cache, const v
  * probability 0; a row with a NaN or +inf, or with no finite logit, has no
  * distribution: NaN, and -1 for rank and ids (BAD_VALUE).  T = 0: one-hot at the
  * first token of the order (ln p = 0 there and -inf elsewhere, entropy 0).
- * Sums are fp32 around the row's maximum.  0 <= n <= min(V, 64); T = 0 or T >=
+ * Sums are fp32 around the row's maximum, whatever its size; ln p <= 0 and
+ * entropy >= 0.  0 <= n <= min(V, 64); T = 0 or T >=
  * 2^-60; V * elem <= 4 MiB; B * R < 2^28.
  */
 ssd_status_t ssd_token_logprobs(const void *logits, ssd_dtype_t dt, int64_t seq_stride, int64_t row_stride,

@@ -23,7 +23,9 @@
 // far is the threshold, and only larger values pass (indices rise along the
 // part, and equal values rank by index).  Keys (value, ~index) are distinct, so their
 // ranks are counted, whatever order they came in.  Where a stage lets more through
-// than there is room for (ties, rising rows), the n-th key is searched bit by bit.
+// than there is room for, the n-th key is searched bit by bit, 64 passes over the stage: a
+// first stage in which a warp has fewer allowed tokens than it gives (a grammar's mask,
+// ties: 384 rows of 128256 with 10 allowed tokens 442 us, 40 unmasked), every stage of rising rows (1.6 ms).
 //
 //   k_token_logprobs  a cluster of cw CTAs (256 threads) per row, a range of the row
 //       each, in stages of 32 KB that bulk copies bring into a ring of two (8 or 16 KB,
@@ -537,8 +539,10 @@ __global__ void __launch_bounds__(kThreads) k_token_logprobs(const __grid_consta
   if (a.cw > 1) cluster_sync();  // no CTA leaves while rank 0 may still read its shared memory
 }
 
-// CTAs of a row: as many as fill the GPU once (4 on each of 152 SMs), so that a CTA's part is long.  384 rows of 128256,
-// about half of them wanted: doubled while there are less than 304 CTAs 32 us, 608 22, 1216 28.
+// CTAs of a row, doubled while there are less than 608 of them: few, so that a CTA's part is long.  (Three of 73 KB fit an
+// SM, 456 on 152.)  The call that it is chosen for, a round's emitted tokens (384 rows of 128256, about half of them
+// wanted): up to 304 32 us, 608 22, 1216 28.  Where all rows are wanted 304 is as fast or faster (384 bf16 rows of 128256 33
+// us instead of 40, of 32000 16 instead of 23; the same up to 64 rows and from 700 on), 1216 never.
 int cluster_of(int64_t rows, int V, int64_t size) {
   const int64_t stages = (V * size + kStageBytes - 1) / kStageBytes;
   int cw = 1;
